@@ -46,6 +46,15 @@ class CfMlaConfig(ctypes.Structure):
         ("rope_theta", ctypes.c_float), ("rms_eps", ctypes.c_float), ("dtype", ctypes.c_int32)]
 
 
+class CfPagedConfig(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "n_q_heads", "n_kv_heads", "head_dim", "page_size", "num_pages", "max_pages",
+        "max_batch", "max_tokens", "dtype", "layout")] + [
+        ("page_stride", ctypes.c_int64), ("rope_theta", ctypes.c_float),
+        ("rope_dim", ctypes.c_int32), ("rope_sections", ctypes.c_int32 * 3),
+        ("rope_interleaved", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
 class CfLaunchInfo(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in (
         "cluster_size", "batch_tile", "group", "rows_per_wtile", "pos_per_ktile",
@@ -103,6 +112,16 @@ SIGNATURES = {
     "cf_mla_launch_info": (ctypes.c_int, [_vp] + [ctypes.POINTER(ctypes.c_int32)] * 5),
     "cf_mla_destroy": (None, [_vp]),
     "cf_mla_set_timeline": (ctypes.c_int, [_vp, _vp]),
+    "cf_paged_create": (ctypes.c_int, [ctypes.POINTER(CfPagedConfig), ctypes.POINTER(_vp)]),
+    "cf_paged_append": (ctypes.c_int, [_vp, ctypes.c_int32, ctypes.c_int32] + [_vp] * 3
+                        + [ctypes.c_int64] * 2 + [_vp] * 7 + [ctypes.c_int64, _vp]),
+    "cf_paged_attention": (ctypes.c_int, [_vp] + [ctypes.c_int32] * 3 + [_vp, ctypes.c_int64]
+                           + [_vp] * 5 + [ctypes.c_int32] * 2 + [_vp] * 3),
+    "cf_paged_prefix_attention": (ctypes.c_int, [_vp] + [ctypes.c_int32] * 3
+                                  + [_vp, ctypes.c_int64] + [_vp] * 4 + [ctypes.c_int32]
+                                  + [_vp] * 5),
+    "cf_paged_get_status": (ctypes.c_int, [_vp]),
+    "cf_paged_destroy": (None, [_vp]),
 }
 
 TIMELINE_SLOTS = 32
@@ -478,6 +497,168 @@ class MlaBlock:
     def close(self) -> None:
         if getattr(self, "handle", None):
             lib().cf_mla_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+# ----------------------------------------------------------- paged KV cache --
+def cf_paged_create_rc(cfg: CfPagedConfig | None) -> tuple[int, int | None]:
+    """Return code and handle without raising (boundary tests)."""
+    h = _vp()
+    rc = lib().cf_paged_create(ctypes.byref(cfg) if cfg is not None else None, ctypes.byref(h))
+    return rc, h.value
+
+
+def make_paged_config(n_q_heads, n_kv_heads, head_dim, page_size, num_pages, max_pages, max_batch,
+                      max_tokens, dtype=CF_F16, layout=0, page_stride=0, rope_theta=1e4,
+                      rope_dim=0, rope_sections=None, rope_interleaved=False,
+                      scale=0.0) -> CfPagedConfig:
+    if isinstance(dtype, str):
+        dtype = {"f32": CF_F32, "f16": CF_F16, "bf16": CF_BF16}[dtype]
+    sec = (ctypes.c_int32 * 3)(*(int(x) for x in (rope_sections or (0, 0, 0))))
+    return CfPagedConfig(int(n_q_heads), int(n_kv_heads), int(head_dim), int(page_size),
+                         int(num_pages), int(max_pages), int(max_batch), int(max_tokens),
+                         int(dtype), int(layout), int(page_stride), float(rope_theta),
+                         int(rope_dim), sec, int(rope_interleaved), float(scale))
+
+
+class PagedKv:
+    """Owns one cf_paged_handle (include/cf_paged.h): appends to a paged KV
+    cache and attends over it.  Raises CfError on any non-zero return code.
+
+    Rows of q, k, v and q_out may be strided: a tensor's stride along dim 0 is
+    used, a raw address counts as dense unless the stride is given.  Tensors
+    are checked for dtype, device and dense inner dimensions; raw addresses
+    are taken as they are."""
+
+    def __init__(self, **cfg):
+        self.cfg = c = make_paged_config(**cfg)
+        rc, h = cf_paged_create_rc(c)
+        if rc != CF_OK:
+            raise CfError(rc, "cf_paged_create")
+        self.handle = h
+        self._qrow = c.n_q_heads * c.head_dim
+        self._kvrow = c.n_kv_heads * c.head_dim
+        import torch
+        self._dtype = {CF_F32: torch.float32, CF_F16: torch.float16, CF_BF16: torch.bfloat16}[
+            c.dtype]
+        self._int = torch.int32
+        self._f32 = torch.float32
+        self._dev = torch.cuda.current_device()
+        self._append = lib().cf_paged_append
+        self._attention = lib().cf_paged_attention
+        self._prefix = lib().cf_paged_prefix_attention
+
+    # Address of a tensor after checking it, or the address given.
+    def _at(self, x, dtype, numel, what):
+        if x is None or isinstance(x, int):
+            return x
+        if x.dtype is not dtype or x.get_device() != self._dev or not x.is_contiguous() or \
+                x.numel() < numel:
+            raise CfError(CF_ERR_INVALID_ARG, f"{what}: {x.dtype} {tuple(x.shape)} on {x.device}")
+        return x.data_ptr()
+
+    # Address and row stride of [n, heads, d] rows (or [n, heads * d]).
+    def _rows(self, x, n, row, stride, what):
+        if x is None or isinstance(x, int):
+            return x, int(stride) if stride else row
+        shape, st = x.shape, x.stride()
+        if x.dtype is not self._dtype or x.get_device() != self._dev or len(shape) < 2 or \
+                shape[0] < n or x.numel() != shape[0] * row or st[-1] != 1 or \
+                (len(shape) == 3 and st[1] != shape[2]) or len(shape) > 3:
+            raise CfError(CF_ERR_INVALID_ARG,
+                          f"{what}: {x.dtype} {tuple(shape)} strides {st} on {x.device}")
+        # the stride of a single row says nothing
+        return x.data_ptr(), int(stride) if stride else (st[0] if shape[0] > 1 else row)
+
+    # Address of a pool of num_pages pages.
+    def _pool(self, x, what):
+        if isinstance(x, int):
+            return x
+        c = self.cfg
+        page = c.page_size * self._kvrow
+        st = x.stride()
+        want = st[0] if x.dim() == 4 and x.shape[0] > 1 else (c.page_stride or page)
+        if x.dtype is not self._dtype or x.get_device() != self._dev or x.dim() != 4 or \
+                x.shape[0] != c.num_pages or x.numel() != c.num_pages * page or \
+                x.shape[3] != c.head_dim or st[3] != 1 or st[2] != c.head_dim or \
+                st[1] != x.shape[2] * c.head_dim or want != (c.page_stride or page) or \
+                x.shape[1] != (c.n_kv_heads if c.layout else c.page_size):
+            raise CfError(CF_ERR_INVALID_ARG,
+                          f"{what}: {x.dtype} {tuple(x.shape)} strides {st} on {x.device}")
+        return x.data_ptr()
+
+    def append(self, batch, n_tokens, q, k, v, q_start, kv_len, page_table, k_pages, v_pages,
+               q_out, rope_pos=None, q_stride=None, kv_stride=None, q_out_stride=None,
+               stream=None):
+        """Rotates q into q_out, and appends the rotated k and v (cf_paged_append)."""
+        c, i32 = self.cfg, self._int
+        qp, qs = self._rows(q, n_tokens, self._qrow, q_stride, "q")
+        kp, ks = self._rows(k, n_tokens, self._kvrow, kv_stride, "k")
+        vp, vs = self._rows(v, n_tokens, self._kvrow, kv_stride, "v")
+        op, os_ = self._rows(q_out, n_tokens, self._qrow, q_out_stride, "q_out")
+        if ks != vs and n_tokens > 1:
+            raise CfError(CF_ERR_INVALID_ARG, "k and v have different row strides")
+        axes = 3 if any(c.rope_sections) else 1
+        rc = self._append(
+            self.handle, batch, n_tokens, qp, kp, vp, qs, ks,
+            self._at(q_start, i32, batch + 1, "q_start"), self._at(kv_len, i32, batch, "kv_len"),
+            self._at(rope_pos, i32, axes * n_tokens, "rope_pos"),
+            self._at(page_table, i32, batch * c.max_pages, "page_table"),
+            self._pool(k_pages, "k_pages"), self._pool(v_pages, "v_pages"), op, os_,
+            _stream(stream))
+        if rc != CF_OK:
+            raise CfError(rc, "cf_paged_append")
+        return q_out
+
+    def attention(self, batch, n_tokens, max_q, q, q_start, kv_len, page_table, k_pages, v_pages,
+                  out, lse=None, window=0, n_sinks=0, q_stride=None, stream=None):
+        """Causal attention over the sequences' pages (cf_paged_attention)."""
+        c, i32 = self.cfg, self._int
+        qp, qs = self._rows(q, n_tokens, self._qrow, q_stride, "q")
+        rc = self._attention(
+            self.handle, batch, n_tokens, max_q, qp, qs,
+            self._at(q_start, i32, batch + 1, "q_start"), self._at(kv_len, i32, batch, "kv_len"),
+            self._at(page_table, i32, batch * c.max_pages, "page_table"),
+            self._pool(k_pages, "k_pages"), self._pool(v_pages, "v_pages"), window, n_sinks,
+            self._at(out, self._dtype, n_tokens * self._qrow, "out"),
+            self._at(lse, self._f32, n_tokens * c.n_q_heads, "lse"), _stream(stream))
+        if rc != CF_OK:
+            raise CfError(rc, "cf_paged_attention")
+        return out
+
+    def prefix_attention(self, batch, n_tokens, max_q, q, q_start, kv_len, page_table,
+                         prefix_table, prefix_len, k_pages, v_pages, out, lse=None, q_stride=None,
+                         stream=None):
+        """Attention over a prefix shared by the batch and the sequences' own
+        pages (cf_paged_prefix_attention)."""
+        c, i32 = self.cfg, self._int
+        qp, qs = self._rows(q, n_tokens, self._qrow, q_stride, "q")
+        rc = self._prefix(
+            self.handle, batch, n_tokens, max_q, qp, qs,
+            self._at(q_start, i32, batch + 1, "q_start"), self._at(kv_len, i32, batch, "kv_len"),
+            self._at(page_table, i32, batch * c.max_pages, "page_table"),
+            self._at(prefix_table, i32, -(-prefix_len // c.page_size), "prefix_table"),
+            prefix_len, self._pool(k_pages, "k_pages"), self._pool(v_pages, "v_pages"),
+            self._at(out, self._dtype, n_tokens * self._qrow, "out"),
+            self._at(lse, self._f32, n_tokens * c.n_q_heads, "lse"), _stream(stream))
+        if rc != CF_OK:
+            raise CfError(rc, "cf_paged_prefix_attention")
+        return out
+
+    def status(self) -> int:
+        import torch
+        torch.cuda.synchronize()
+        return lib().cf_paged_get_status(self.handle)
+
+    def close(self) -> None:
+        if getattr(self, "handle", None):
+            lib().cf_paged_destroy(self.handle)
             self.handle = None
 
     def __del__(self):
