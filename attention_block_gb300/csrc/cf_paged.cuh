@@ -103,7 +103,107 @@ __device__ __forceinline__ int64_t paged_offset(const int* table, int j, const P
   return (int64_t)page * g.page_stride + (int64_t)(j & g.page_mask) * g.slot_stride;
 }
 
+// How a kernel's work is cut over its blocks.  The units (key tiles) of all
+// items (a sequence or row tile and a KV head) form one line; block c takes
+// units [c * upc, (c + 1) * upc).  An item that lies in several blocks leaves
+// one partial state (o not normalised, running maximum in base 2, sum) per
+// block, in slot 2c where it is the block's first item and in 2c + 1 else.
+struct PagedParts {
+  float* o;     // [slots][rows][D]
+  float2* ml;   // [slots][rows]
+  int* tickets; // one per item: partial states written so far (0 between calls)
+};
+
+// The shared prefix's partial states, as the kernel that reads the sequences'
+// own keys finds them: row R = token * G + (head in the KV head's group) is
+// row R % rows of tile R / rows, and item tile * nkv + kv head has `tiles`
+// units.  rows == 0: there is no prefix.
+struct PagedPrefixParts {
+  const float* o;
+  const float2* ml;
+  int rows;
+  int tiles;
+  long long upc;
+};
+
+__device__ __forceinline__ void pdl_wait() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void pdl_trigger() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// Partial states of one item: the blocks first .. first + n - 1.
+struct PagedItemParts {
+  long long i0, upc, first;
+  int n;
+  __device__ __forceinline__ PagedItemParts(long long i0_, long long tiles, long long upc_)
+      : i0(i0_), upc(upc_), first(i0_ / upc_), n((int)((i0_ + tiles - 1) / upc_ - i0_ / upc_) + 1) {}
+  __device__ __forceinline__ long long slot(int k) const {
+    const long long c = first + k;
+    return 2 * c + (c * upc >= i0 ? 0 : 1);
+  }
+};
+
+// Softmax state of 4 columns of a row, joined with another one.
+struct PagedState4 {
+  float m, l;
+  float4 o;
+  __device__ __forceinline__ void join(float m2, float l2, const float4& o2) {
+    const float mn = fmaxf(m, m2);
+    if (mn == -INFINITY) return;
+    const float a = exp2f(m - mn), b = exp2f(m2 - mn);
+    m = mn;
+    l = l * a + l2 * b;
+    o.x = o.x * a + o2.x * b;
+    o.y = o.y * a + o2.y * b;
+    o.z = o.z * a + o2.z * b;
+    o.w = o.w * a + o2.w * b;
+  }
+};
+
+// Joins the prefix's states of one row's 4 columns at `col` into s.
+template <int D>
+__device__ __forceinline__ void paged_join_prefix(PagedState4& s, const PagedPrefixParts& x,
+                                                  long long R, int kvh, int nkv, int col) {
+  const long long tile = R / x.rows;
+  const int row = (int)(R - tile * x.rows);
+  const PagedItemParts parts((tile * nkv + kvh) * x.tiles, x.tiles, x.upc);
+#pragma unroll 4
+  for (int k = 0; k < parts.n; ++k) {
+    const long long at = parts.slot(k) * x.rows + row;
+    const float2 ml = __ldcg(x.ml + at);
+    const float4 o = __ldcg(reinterpret_cast<const float4*>(x.o + at * D + col));
+    s.join(ml.x, ml.y, o);
+  }
+}
+
+// Normalises and stores 4 columns of a row, and its lse.
+template <typename T, int D>
+__device__ __forceinline__ void paged_store4(const PagedState4& s, void* out, float* lse,
+                                             long long row, int col) {
+  const float inv = s.l == 0.f ? 0.f : 1.f / s.l;
+  const float f[4] = {s.o.x * inv, s.o.y * inv, s.o.z * inv, s.o.w * inv};
+  store4<T>(static_cast<T*>(out) + row * D + col, f);
+  if (lse && col == 0)
+    lse[row] = s.m == -INFINITY ? -INFINITY : (s.m + log2f(s.l)) * 0.69314718055994531f;
+}
+
 // Host launchers (one translation unit each); false: the launch failed.
+struct PagedSplit {  // one kernel's part of a handle's workspace
+  float* o = nullptr;
+  float2* ml = nullptr;
+  int* tickets = nullptr;
+  int grid = 0;  // resident blocks the kernel is cut for
+};
+// Rows (tokens x grouped heads) and resident blocks of the few-row kernel.
+constexpr int kFewRows = 16;
+int paged_few_grid(int dtype, int head_dim, int sm_count);
+// prefix: the call's tokens against the prefix alone, partial states only.
+bool paged_few_launch(int dtype, const PagedAttnParams& p, const PagedSplit& ws, bool prefix,
+                      const PagedPrefixParts& pre, cudaStream_t st);
+// How the few-row kernel cuts the prefix.
+PagedPrefixParts paged_few_prefix(const PagedAttnParams& p, const PagedSplit& ws);
 bool paged_append_launch(int dtype, const PagedAppendParams& p, int sm_count, cudaStream_t st);
 bool paged_attn_simple_launch(int dtype, const PagedAttnParams& p, cudaStream_t st);
 

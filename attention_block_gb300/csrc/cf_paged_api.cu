@@ -22,6 +22,7 @@ struct cf_paged_handle {
   float scale_log2 = 0.f;
   void* ws = nullptr;
   int* errflag = nullptr;
+  PagedSplit few, few_prefix;
 };
 
 namespace {
@@ -137,7 +138,25 @@ int attention(cf_paged_handle* h, int32_t batch, int32_t n_tokens, int32_t max_q
   p.n_sinks = n_sinks;
   p.scale_log2 = h->scale_log2;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (!paged_attn_simple_launch(c.dtype, p, st)) {
+  // fp32 has no tensor-core form.  Up to 16 rows per KV head (tokens of one
+  // sequence x grouped heads) share a tile of the few-row kernel.
+  const int G = p.g.G;
+  const bool tensor = c.dtype != CF_F32;
+  bool ok;
+  if (tensor && (int64_t)max_q * G <= kFewRows &&
+      (prefix_len == 0 || (int64_t)n_tokens * G <= kFewRows)) {
+    PagedPrefixParts pre;
+    std::memset(&pre, 0, sizeof(pre));
+    ok = true;
+    if (prefix_len > 0) {
+      pre = paged_few_prefix(p, h->few_prefix);
+      ok = paged_few_launch(c.dtype, p, h->few_prefix, true, pre, st);
+    }
+    ok = ok && paged_few_launch(c.dtype, p, h->few, false, pre, st);
+  } else {
+    ok = paged_attn_simple_launch(c.dtype, p, st);
+  }
+  if (!ok) {
     cudaGetLastError();
     return CF_ERR_CUDA;
   }
@@ -218,17 +237,45 @@ int cf_paged_create(const cf_paged_config* cfg, cf_paged_handle** out) {
     cudaGetLastError();
     return fail(CF_ERR_CUDA);
   }
-  const size_t bytes = 256;
+  // Workspace: the words that start at zero (error word, tickets), then the
+  // kernels' partial states.
+  size_t bytes = 256;
+  auto take = [&](size_t n) {
+    const size_t at = bytes;
+    bytes += (n + 255) & ~(size_t)255;
+    return at;
+  };
+  size_t zero = bytes, few_t = 0, few_at[2] = {0, 0};
+  const size_t row = (size_t)(c.head_dim + 2) * 4;  // o, m and l of a row
+  int few_grid = 0;
+  if (c.dtype != CF_F32) {
+    few_grid = paged_few_grid(c.dtype, c.head_dim, h->sm_count);
+    if (few_grid == 0) return fail(CF_ERR_CUDA);
+    few_t = take((size_t)c.max_batch * c.n_kv_heads * 4);
+    zero = bytes;
+    for (size_t& at : few_at) at = take((size_t)few_grid * 2 * kFewRows * row);
+  }
   if (cudaMalloc(&h->ws, bytes) != cudaSuccess) {
     cudaGetLastError();
     h->ws = nullptr;
     return fail(CF_ERR_CUDA);
   }
-  if (cudaMemset(h->ws, 0, bytes) != cudaSuccess) {
+  if (cudaMemset(h->ws, 0, zero) != cudaSuccess) {
     cudaGetLastError();
     return fail(CF_ERR_CUDA);
   }
-  h->errflag = static_cast<int*>(h->ws);
+  uint8_t* ws = static_cast<uint8_t*>(h->ws);
+  h->errflag = reinterpret_cast<int*>(ws);
+  auto split = [&](size_t at, int grid, int rows, int* tickets) {
+    PagedSplit s;
+    s.o = reinterpret_cast<float*>(ws + at);
+    s.ml = reinterpret_cast<float2*>(s.o + (size_t)grid * 2 * rows * c.head_dim);
+    s.tickets = tickets;
+    s.grid = grid;
+    return s;
+  };
+  h->few = split(few_at[0], few_grid, kFewRows, reinterpret_cast<int*>(ws + few_t));
+  h->few_prefix = split(few_at[1], few_grid, kFewRows, nullptr);
   *out = h;
   return CF_OK;
 }

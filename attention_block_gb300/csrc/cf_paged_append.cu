@@ -18,11 +18,11 @@ using namespace cf;
 
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kAppendThreads = 128;
 constexpr int kMaxTok = 4;  // tokens per block
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kAppendThreads)
     paged_append_kernel(const __grid_constant__ PagedAppendParams p, int tok_per_block) {
   constexpr int W = 16 / sizeof(T);
   __shared__ float2 s_cs[kMaxTok][kMaxPairs];
@@ -35,7 +35,7 @@ __global__ void __launch_bounds__(kThreads)
   if (tid < kMaxTok) s_seq[tid] = p.q_start ? -1 : t_lo + tid;
   __syncthreads();
   if (p.q_start) {
-    for (int b = tid; b < p.batch; b += kThreads) {
+    for (int b = tid; b < p.batch; b += kAppendThreads) {
       const int a = max(p.q_start[b], t_lo), e = min(p.q_start[b + 1], t_lo + nt);
       for (int t = a; t < e; ++t) s_seq[t - t_lo] = b;
     }
@@ -62,7 +62,7 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
   for (int i = 0; i < kMaxTok; ++i) {
     if (i >= nt || slot[i] < 0) continue;
-    for (int c = tid; c < half; c += kThreads) {
+    for (int c = tid; c < half; c += kAppendThreads) {
       const int P = p.rope_pos ? p.rope_pos[(int64_t)p.axis[c] * p.n_tokens + t_lo + i] : pos[i];
       const uint64_t f = (uint64_t)(int64_t)P * p.turn[c];
       const float turns = (float)(int32_t)(uint32_t)(f >> 32) * 0x1p-32f;
@@ -80,7 +80,7 @@ __global__ void __launch_bounds__(kThreads)
   for (int i = 0; i < kMaxTok; ++i) {
     if (i >= nt || slot[i] < 0) continue;
     const int64_t t = t_lo + i;
-    for (int u = blockIdx.y * kThreads + tid; u < per_tok; u += gridDim.y * kThreads) {
+    for (int u = blockIdx.y * kAppendThreads + tid; u < per_tok; u += gridDim.y * kAppendThreads) {
       const int h = u / upd, c = u - h * upd;
       const T* src;
       T* dst;
@@ -132,11 +132,11 @@ bool launch(const PagedAppendParams& p, int sm_count, cudaStream_t st) {
   // Few tokens: a token's heads are spread over several blocks, one unit per
   // thread; many: four tokens per block.
   const int units = (p.g.nq + 2 * p.g.nkv) * (p.g.D / (2 * W));
-  const int need = (units + kThreads - 1) / kThreads;
+  const int need = (units + kAppendThreads - 1) / kAppendThreads;
   const int tpb = p.n_tokens >= 16 * sm_count ? kMaxTok : 1;
   const int gx = (p.n_tokens + tpb - 1) / tpb;
   const int gy = gx >= 16 * sm_count ? 1 : need;
-  paged_append_kernel<T><<<dim3(gx, gy), kThreads, 0, st>>>(p, tpb);
+  paged_append_kernel<T><<<dim3(gx, gy), kAppendThreads, 0, st>>>(p, tpb);
   return cudaGetLastError() == cudaSuccess;
 }
 

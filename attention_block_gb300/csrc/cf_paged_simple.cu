@@ -16,16 +16,16 @@ using namespace cf;
 
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kSimpleWarps = 4;
 
 template <typename T, int D>
-__global__ void __launch_bounds__(kWarps * 32)
+__global__ void __launch_bounds__(kSimpleWarps * 32)
     paged_attn_simple_kernel(const __grid_constant__ PagedAttnParams p) {
   constexpr int E = D / 32;       // columns of a lane
   constexpr int W = 16 / sizeof(T);
   __shared__ float s_q[D];
-  __shared__ float s_o[kWarps][D];
-  __shared__ float s_m[kWarps], s_l[kWarps];
+  __shared__ float s_o[kSimpleWarps][D];
+  __shared__ float s_m[kSimpleWarps], s_l[kSimpleWarps];
   __shared__ int s_seq;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int64_t t = blockIdx.x;
@@ -34,13 +34,13 @@ __global__ void __launch_bounds__(kWarps * 32)
   if (tid == 0) s_seq = p.q_start ? -1 : (int)t;
   __syncthreads();
   if (p.q_start) {
-    for (int b = tid; b < p.batch; b += kWarps * 32)
+    for (int b = tid; b < p.batch; b += kSimpleWarps * 32)
       if (p.q_start[b] <= t && t < p.q_start[b + 1]) s_seq = b;
     __syncthreads();
   }
   const int b = s_seq;
   if (b < 0) return;  // behind the last sequence
-  for (int i = tid; i < D; i += kWarps * 32)
+  for (int i = tid; i < D; i += kSimpleWarps * 32)
     s_q[i] = Elem<T>::to_f(
         static_cast<const T*>(p.q)[t * p.q_stride + (int64_t)h * D + i]);
   __syncthreads();
@@ -59,7 +59,7 @@ __global__ void __launch_bounds__(kWarps * 32)
   float m = -INFINITY, l = 0.f, o[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = 0.f;
-  for (int base = warp * 32; base < total; base += kWarps * 32) {
+  for (int base = warp * 32; base < total; base += kSimpleWarps * 32) {
     int idx = base + lane;
     int64_t off = -1;
     if (idx < total) {
@@ -116,17 +116,17 @@ __global__ void __launch_bounds__(kWarps * 32)
   __syncthreads();
   float mt = -INFINITY;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) mt = fmaxf(mt, s_m[w]);
+  for (int w = 0; w < kSimpleWarps; ++w) mt = fmaxf(mt, s_m[w]);
   const float ref = mt == -INFINITY ? 0.f : mt;
   float lt = 0.f;
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) lt += s_l[w] * exp2f(s_m[w] - ref);
+  for (int w = 0; w < kSimpleWarps; ++w) lt += s_l[w] * exp2f(s_m[w] - ref);
   const float inv = lt == 0.f ? 0.f : 1.f / lt;
   T* out = static_cast<T*>(p.out) + (t * p.g.nq + h) * D;
-  for (int i = tid; i < D; i += kWarps * 32) {
+  for (int i = tid; i < D; i += kSimpleWarps * 32) {
     float v = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) v += s_o[w][i] * exp2f(s_m[w] - ref);
+    for (int w = 0; w < kSimpleWarps; ++w) v += s_o[w][i] * exp2f(s_m[w] - ref);
     out[i] = Elem<T>::from_f(v * inv);
   }
   if (p.lse && tid == 0)
@@ -138,9 +138,9 @@ template <typename T>
 bool launch(const PagedAttnParams& p, cudaStream_t st) {
   const dim3 grid(p.n_tokens, p.g.nq);
   if (p.g.D == 64)
-    paged_attn_simple_kernel<T, 64><<<grid, kWarps * 32, 0, st>>>(p);
+    paged_attn_simple_kernel<T, 64><<<grid, kSimpleWarps * 32, 0, st>>>(p);
   else
-    paged_attn_simple_kernel<T, 128><<<grid, kWarps * 32, 0, st>>>(p);
+    paged_attn_simple_kernel<T, 128><<<grid, kSimpleWarps * 32, 0, st>>>(p);
   return cudaGetLastError() == cudaSuccess;
 }
 
