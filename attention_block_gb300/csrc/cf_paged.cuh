@@ -103,6 +103,46 @@ __device__ __forceinline__ int64_t paged_offset(const int* table, int j, const P
   return (int64_t)page * g.page_stride + (int64_t)(j & g.page_mask) * g.slot_stride;
 }
 
+// The tiles of TK positions that hold a range: sink tiles from 0, then the
+// tiles of [lo, hi); always at least one.
+template <int TK>
+struct PagedTiles {
+  int sink, lo, hi;
+  int ns, skip;  // sink tiles, and tiles between them and the window's first
+  int tiles;
+  __device__ __forceinline__ void set(const PagedRange& r) {
+    sink = r.sink;
+    lo = r.lo;
+    hi = r.hi;
+    if (hi <= lo) {  // no key
+      sink = ns = skip = 0;
+      tiles = 1;
+      return;
+    }
+    const int f = lo / TK, e = (hi + TK - 1) / TK;
+    ns = (sink + TK - 1) / TK;
+    skip = max(0, f - ns);
+    if (skip == 0) ns = 0;
+    tiles = e - skip;
+  }
+  __device__ __forceinline__ int base(int tile) const {
+    return (tile < ns ? tile : tile + skip) * TK;
+  }
+  __device__ __forceinline__ bool sees(int j) const { return (j >= lo && j < hi) || j < sink; }
+};
+
+// 16 bytes global -> shared, asynchronously; zeros where there is no source.
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+               "r"(there ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
 // How a kernel's work is cut over its blocks.  The units (key tiles) of all
 // items (a sequence or row tile and a KV head) form one line; block c takes
 // units [c * upc, (c + 1) * upc).  An item that lies in several blocks leaves
@@ -194,6 +234,7 @@ struct PagedSplit {  // one kernel's part of a handle's workspace
   float* o = nullptr;
   float2* ml = nullptr;
   int* tickets = nullptr;
+  void* meta = nullptr;
   int grid = 0;  // resident blocks the kernel is cut for
 };
 // Rows (tokens x grouped heads) and resident blocks of the few-row kernel.
@@ -206,5 +247,13 @@ bool paged_few_launch(int dtype, const PagedAttnParams& p, const PagedSplit& ws,
 PagedPrefixParts paged_few_prefix(const PagedAttnParams& p, const PagedSplit& ws);
 bool paged_append_launch(int dtype, const PagedAppendParams& p, int sm_count, cudaStream_t st);
 bool paged_attn_simple_launch(int dtype, const PagedAttnParams& p, cudaStream_t st);
+
+// The tensor-core kernel for many rows; the arguments as above.
+constexpr int kTcRows = 256;
+int paged_tc_grid(int dtype, int head_dim, int sm_count);
+size_t paged_tc_meta_bytes(int grid);
+bool paged_tc_launch(int dtype, const PagedAttnParams& p, const PagedSplit& ws, bool prefix,
+                     const PagedPrefixParts& pre, cudaStream_t st);
+PagedPrefixParts paged_tc_prefix(const PagedAttnParams& p, const PagedSplit& ws);
 
 }  // namespace cf

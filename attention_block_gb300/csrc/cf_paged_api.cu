@@ -22,7 +22,7 @@ struct cf_paged_handle {
   float scale_log2 = 0.f;
   void* ws = nullptr;
   int* errflag = nullptr;
-  PagedSplit few, few_prefix;
+  PagedSplit few, few_prefix, tc, tc_prefix;
 };
 
 namespace {
@@ -139,22 +139,27 @@ int attention(cf_paged_handle* h, int32_t batch, int32_t n_tokens, int32_t max_q
   p.scale_log2 = h->scale_log2;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   // fp32 has no tensor-core form.  Up to 16 rows per KV head (tokens of one
-  // sequence x grouped heads) share a tile of the few-row kernel.
-  const int G = p.g.G;
-  const bool tensor = c.dtype != CF_F32;
+  // sequence x grouped heads) share a tile of the few-row kernel; more go to
+  // the tensor-core kernel.  For the prefix the rows are the whole call's.
   bool ok;
-  if (tensor && (int64_t)max_q * G <= kFewRows &&
-      (prefix_len == 0 || (int64_t)n_tokens * G <= kFewRows)) {
+  if (c.dtype == CF_F32) {
+    ok = paged_attn_simple_launch(c.dtype, p, st);
+  } else {
     PagedPrefixParts pre;
     std::memset(&pre, 0, sizeof(pre));
     ok = true;
     if (prefix_len > 0) {
-      pre = paged_few_prefix(p, h->few_prefix);
-      ok = paged_few_launch(c.dtype, p, h->few_prefix, true, pre, st);
+      if ((int64_t)n_tokens * p.g.G <= kFewRows) {
+        pre = paged_few_prefix(p, h->few_prefix);
+        ok = paged_few_launch(c.dtype, p, h->few_prefix, true, pre, st);
+      } else {
+        pre = paged_tc_prefix(p, h->tc_prefix);
+        ok = paged_tc_launch(c.dtype, p, h->tc_prefix, true, pre, st);
+      }
     }
-    ok = ok && paged_few_launch(c.dtype, p, h->few, false, pre, st);
-  } else {
-    ok = paged_attn_simple_launch(c.dtype, p, st);
+    if (ok)
+      ok = (int64_t)max_q * p.g.G <= kFewRows ? paged_few_launch(c.dtype, p, h->few, false, pre, st)
+                                              : paged_tc_launch(c.dtype, p, h->tc, false, pre, st);
   }
   if (!ok) {
     cudaGetLastError();
@@ -247,13 +252,20 @@ int cf_paged_create(const cf_paged_config* cfg, cf_paged_handle** out) {
   };
   size_t zero = bytes, few_t = 0, few_at[2] = {0, 0};
   const size_t row = (size_t)(c.head_dim + 2) * 4;  // o, m and l of a row
-  int few_grid = 0;
+  int few_grid = 0, tc_grid = 0;
+  size_t tc_at[2] = {0, 0}, meta_at = 0;
   if (c.dtype != CF_F32) {
     few_grid = paged_few_grid(c.dtype, c.head_dim, h->sm_count);
     if (few_grid == 0) return fail(CF_ERR_CUDA);
     few_t = take((size_t)c.max_batch * c.n_kv_heads * 4);
     zero = bytes;
     for (size_t& at : few_at) at = take((size_t)few_grid * 2 * kFewRows * row);
+    if ((int64_t)c.max_tokens * h->geom.G > kFewRows) {
+      tc_grid = paged_tc_grid(c.dtype, c.head_dim, h->sm_count);
+      if (tc_grid == 0) return fail(CF_ERR_CUDA);
+      for (size_t& at : tc_at) at = take((size_t)tc_grid * 2 * kTcRows * row);
+      meta_at = take(paged_tc_meta_bytes(tc_grid));
+    }
   }
   if (cudaMalloc(&h->ws, bytes) != cudaSuccess) {
     cudaGetLastError();
@@ -276,6 +288,9 @@ int cf_paged_create(const cf_paged_config* cfg, cf_paged_handle** out) {
   };
   h->few = split(few_at[0], few_grid, kFewRows, reinterpret_cast<int*>(ws + few_t));
   h->few_prefix = split(few_at[1], few_grid, kFewRows, nullptr);
+  h->tc = split(tc_at[0], tc_grid, kTcRows, nullptr);
+  h->tc.meta = ws + meta_at;
+  h->tc_prefix = split(tc_at[1], tc_grid, kTcRows, nullptr);
   *out = h;
   return CF_OK;
 }

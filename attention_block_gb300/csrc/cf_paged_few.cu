@@ -44,44 +44,11 @@ struct Shape {
   static_assert(kBlocksPerSm * (SMEM + 2048) <= 228 * 1024, "two blocks on an SM");
 };
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool there) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
-               "r"(there ? 16 : 0)
-               : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-// A sequence's rows and the tiles of positions that they see: sink tiles from
-// 0, then the tiles of [lo, hi).
+// A sequence's tokens and its key tiles; at least one tile where there are
+// tokens: rows that see nothing are written too.
 template <int TK>
-struct Work {
+struct Work : PagedTiles<TK> {
   int t0, n, p0;  // tokens, position of the first
-  int sink, lo, hi;
-  int ns, skip;   // sink tiles, and tiles between them and the window's first
-  int tiles;      // at least 1 where there are tokens: rows that see nothing are written too
-  __device__ __forceinline__ void set_ranges(const PagedRange& r) {
-    sink = r.sink;
-    lo = r.lo;
-    hi = r.hi;
-    const int f = lo / TK, e = (hi + TK - 1) / TK;
-    ns = (sink + TK - 1) / TK;
-    skip = max(0, f - ns);
-    if (skip == 0) ns = 0;
-    tiles = max(1, e - skip);
-    if (hi <= lo) {  // no key
-      ns = skip = 0;
-      tiles = 1;
-      sink = 0;
-    }
-  }
-  __device__ __forceinline__ int base(int tile) const {
-    return (tile < ns ? tile : tile + skip) * TK;
-  }
-  __device__ __forceinline__ bool sees(int j) const { return (j >= lo && j < hi) || j < sink; }
 };
 
 template <int TK, bool PRE>
@@ -91,7 +58,7 @@ __device__ __forceinline__ Work<TK> work_of(const PagedAttnParams& p, int b) {
     w.t0 = 0;
     w.n = p.n_tokens;
     w.p0 = p.prefix_len;
-    w.set_ranges(PagedRange{0, 0, p.prefix_len});
+    w.set(PagedRange{0, 0, p.prefix_len});
   } else {
     const PagedSeq s = paged_seq(p.q_start, p.kv_len, b, p.n_tokens, p.max_q, p.g, p.errflag);
     w.t0 = s.t0;
@@ -101,7 +68,7 @@ __device__ __forceinline__ Work<TK> work_of(const PagedAttnParams& p, int b) {
       w.n = w.tiles = 0;
       return w;
     }
-    w.set_ranges(paged_range(max(w.p0, 0), s.len - 1, s.len, p.window, p.n_sinks));
+    w.set(paged_range(max(w.p0, 0), s.len - 1, s.len, p.window, p.n_sinks));
   }
   return w;
 }
@@ -230,7 +197,7 @@ __global__ void __launch_bounds__(kFewThreads, kBlocksPerSm)
   };
   auto issue = [&](int stage) {
     if (ld.u < u1) {
-      int64_t off = -1;
+      int64_t off = -1;  // no copy: zeros
       if (ld_pos >= 0) {
         if ((unsigned)ld_page >= (unsigned)p.g.num_pages)
           atomicOr(p.errflag, kDevErrPosRange);
@@ -239,7 +206,7 @@ __global__ void __launch_bounds__(kFewThreads, kBlocksPerSm)
                  (int64_t)(ld_pos & p.g.page_mask) * p.g.slot_stride +
                  (int64_t)ld.h * p.g.head_stride) * 2;
       }
-      const uint32_t valid = __ballot_sync(~0u, off >= 0);
+      const uint32_t valid = __ballot_sync(~0u, ld_pos >= 0);
       if (lane == 0) s_valid[warp][stage] = valid;
       const uint32_t dst = ring_s + stage * S::STAGE;
       if (valid) {

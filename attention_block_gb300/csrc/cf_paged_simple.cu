@@ -61,8 +61,10 @@ __global__ void __launch_bounds__(kSimpleWarps * 32)
   for (int e = 0; e < E; ++e) o[e] = 0.f;
   for (int base = warp * 32; base < total; base += kSimpleWarps * 32) {
     int idx = base + lane;
-    int64_t off = -1;
+    int64_t off = -1;  // no page: zeros stand for the key and the value
+    float sc = -INFINITY;
     if (idx < total) {
+      sc = 0.f;
       if (idx < pre) {
         off = paged_offset(p.prefix_table, idx, p.g, p.errflag);
       } else {
@@ -70,7 +72,6 @@ __global__ void __launch_bounds__(kSimpleWarps * 32)
         off = paged_offset(table, idx < r.sink ? idx : r.lo + idx - r.sink, p.g, p.errflag);
       }
     }
-    float sc = -INFINITY;
     if (off >= 0) {
       off += (int64_t)kvh * p.g.head_stride;
       const T* k = static_cast<const T*>(p.k_pages) + off;

@@ -1,0 +1,865 @@
+// cf_paged_tc.cu -- attention over the paged cache for many rows per KV head:
+// prompts, long drafts, and a whole batch against its shared prefix, fp16 or
+// bf16, on the fifth-generation tensor cores.
+//
+// A KV head's rows are the packed (token, grouped head) pairs, so grouped
+// heads share every key tile.  An item is 256 rows (two halves of 128, the
+// tensor core's M) of one KV head; its units are tiles of 128 positions.  All
+// items' units form one line that the blocks, one per SM, share evenly
+// (PagedParts): causal triangles, windows, ragged batches and few long items
+// all fill the GPU.  An item that lies in several blocks leaves partial
+// states, joined by a second small kernel.
+//
+// Roles of a block's 16 warps:
+//   0-3, 4-7  softmax of half 0 / 1, a thread per row: S from TMEM, mask,
+//             running maximum, exp2, P (16 bits) back into TMEM over S, sum
+//             of P before its rounding; the final o
+//   8-11      copy Q, K and V through the page table into shared memory
+//             (cp.async; positions that no row sees become zeros, so what
+//             lies there reaches no product), in the 128-byte swizzle
+//   12        one thread issues S = Q K^T (operands in shared memory) and
+//             O += P V (P from TMEM, V as an N-major operand)
+// The halves alternate: while one is in its softmax the tensor core works on
+// the other.  TMEM: S (or P) and O of both halves, 512 columns.
+//
+// O is rescaled only where a row's maximum grew by more than 2^8 since its
+// last rescale: P then stays below 2^8 and keeps its relative precision in
+// 16-bit floating point, and most tiles pass without touching O.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstring>
+
+#include "cf_paged.cuh"
+#include "cf_tc05.cuh"
+
+using namespace cf;
+
+namespace {
+
+constexpr int kTcThreads = 512;
+constexpr int kHalf = 128;     // rows of a half
+constexpr int kBN = 128;       // positions of a tile
+constexpr float kGrow = 8.0f;  // log2 of the growth that forces a rescale
+
+template <int D>
+struct TcShape {
+  static constexpr int TILE = kBN * D * 2;                   // bytes of a K, V or Q tile
+  static constexpr int SLOTS = D == 128 ? 5 : 10;            // K and V tiles in flight
+  static constexpr int SMEM = (2 + SLOTS) * TILE + 1024;     // + alignment
+  static constexpr uint32_t S_COL = 0, O_COL = 2 * kBN;      // TMEM columns
+};
+
+// Element offset inside a tile: slabs of 64 columns, rows of 128 bytes, the
+// 16-byte chunks of a row swizzled.
+__device__ __forceinline__ uint32_t tile_at(int row, int chunk) {
+  return (uint32_t)((chunk >> 3) * (kBN * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4));
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, "
+      "%30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, "
+      "%10, %11, %12, %13, %14, %15};" ::"r"(r[0]),
+      "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+      "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() {
+  asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+
+// D[tmem] (+)= A[tmem] . B[bdesc] for one K step of 16.
+__device__ __forceinline__ void tc05_mma_f16_ts(uint32_t dtmem, uint32_t atmem, uint64_t bdesc,
+                                                uint32_t idesc, bool accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(dtmem),
+      "r"(atmem), "l"(bdesc), "r"(idesc), "r"((uint32_t)accumulate)
+      : "memory");
+}
+
+// mbar_wait without a call: a called function would need registers that
+// setmaxnreg moves.  Bounded like it, and as quick to give up once any wait
+// has recorded a timeout.
+__device__ __forceinline__ void wait_bar(uint64_t* bar, uint32_t parity, int* err) {
+  const uint32_t a = smem_u32(bar);
+  if (mbar_try_wait_cta(a, parity)) return;
+  const long long t0 = clock64();
+  for (uint32_t spins = 1; !mbar_try_wait_cta(a, parity); ++spins) {
+    if ((spins & 1023u) != 0) continue;
+    if (*reinterpret_cast<volatile int*>(err) & kDevErrTimeout) return;
+    if (clock64() - t0 > kWaitLimitCycles) {
+      atomicOr(err, kDevErrTimeout);
+      return;
+    }
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float a, float b);
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <typename T>
+constexpr bool kIsBf16 = false;
+template <>
+constexpr bool kIsBf16<__nv_bfloat16> = true;
+
+template <int N>
+__device__ __forceinline__ void set_regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void set_regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// A row tile (256 rows of a sequence, or of the whole call for the prefix)
+// and its key tiles.  Row tile j of sequence b has the number
+// t0 * G / 256 + b + j: unique, increasing, below T * G / 256 + batch.
+struct RowTile : PagedTiles<kBN> {
+  int b, j, jn;        // sequence, row tile, row tiles of the sequence
+  int t0, p0, rows;    // first token, its position, rows of the sequence
+  PagedRange half[2];  // what each half's rows see together
+  int plo[2], phi[2];  // positions of a half's first and last row
+};
+
+template <bool PRE>
+__device__ __forceinline__ void seq_of(const PagedAttnParams& p, int b, RowTile& t) {
+  t.b = b;
+  if constexpr (PRE) {
+    t.t0 = t.p0 = 0;
+    t.rows = p.n_tokens * p.g.G;
+  } else {
+    const PagedSeq s = paged_seq(p.q_start, p.kv_len, b, p.n_tokens, p.max_q, p.g, p.errflag);
+    t.t0 = s.t0;
+    t.p0 = s.len - s.n;
+    t.rows = s.n * p.g.G;
+  }
+  t.jn = (t.rows + 2 * kHalf - 1) / (2 * kHalf);
+}
+
+// Fills in row tile j of the sequence that seq_of() set.
+template <bool PRE>
+__device__ __forceinline__ void tile_of(const PagedAttnParams& p, int j, RowTile& t) {
+  t.j = j;
+  PagedRange u{0, 0, 0};
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const int r0 = j * 2 * kHalf + h * kHalf, r1 = min(r0 + kHalf, t.rows) - 1;
+    t.half[h] = PagedRange{0, 0, 0};
+    t.plo[h] = t.phi[h] = 0;
+    if (r0 > r1) continue;
+    if constexpr (PRE) {
+      t.half[h].hi = p.prefix_len;
+    } else {
+      t.plo[h] = t.p0 + r0 / p.g.G;
+      t.phi[h] = t.p0 + r1 / p.g.G;
+      // p0 + tokens is the sequence's length: no row sees past it
+      t.half[h] = paged_range(max(t.plo[h], 0), t.phi[h], t.phi[h] + 1, p.window, p.n_sinks);
+    }
+    if (h == 0) {
+      u = t.half[0];
+    } else {
+      // half 1 has the later rows: it sees as far or farther, and its window
+      // starts as late or later
+      const PagedRange a = t.half[0], c = t.half[1];
+      u = a.hi <= a.lo ? c : PagedRange{max(a.sink, min(c.sink, a.lo)), a.lo, c.hi};
+    }
+  }
+  t.set(u);
+}
+
+// Whether a half has rows that see part of the tile at `base`.
+__device__ __forceinline__ bool tile_active(const PagedRange& r, int base) {
+  return r.hi > r.lo && ((base < r.hi && base + kBN > r.lo) || base < r.sink);
+}
+
+// A walk over a block's units: row tiles, KV heads, key tiles.
+template <bool PRE>
+struct TcCursor {
+  RowTile t;
+  int h, tile;
+  long long u, i0;
+  // true when the unit left was the last of its item in this walk
+  __device__ __forceinline__ bool next(const PagedAttnParams& p, long long end) {
+    ++u;
+    if (++tile < t.tiles) return u >= end;
+    tile = 0;
+    i0 = u;
+    if (++h < p.g.nkv) return true;
+    h = 0;
+    if (u >= end) return true;
+    int j = t.j + 1;
+    while (j >= t.jn) {
+      if (PRE || t.b + 1 >= p.batch) {  // starts that contradict themselves: stop
+        u = end;
+        return true;
+      }
+      seq_of<PRE>(p, t.b + 1, t);
+      j = 0;
+    }
+    tile_of<PRE>(p, j, t);
+    return true;
+  }
+};
+
+// A split item, for the kernel that joins its parts: written by the block
+// that begins it.
+struct alignas(16) TcMeta {
+  long long i0, upc;
+  int tiles;  // 0: this block begins no split item
+  int t0, p0, rows, j, h;
+};
+
+struct TcArgs {
+  PagedAttnParams p;
+  PagedPrefixParts pre;
+  float* o;
+  float2* ml;
+  TcMeta* meta;
+  int slots;  // upper bound on the row tiles' numbers
+};
+
+template <typename T, int D, bool PRE>
+__global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const __grid_constant__ TcArgs a) {
+  using S = TcShape<D>;
+  constexpr int C = D / 8;  // 16-byte chunks of a row
+  const PagedAttnParams& p = a.p;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ long long s_scan[kTcThreads / 32];
+  __shared__ TcCursor<PRE> s_cur;
+  __shared__ TcCursor<PRE> s_wcur[8];  // each softmax warp's place: too much for its registers
+  __shared__ __align__(8) uint64_t s_full[S::SLOTS], s_empty[S::SLOTS];
+  __shared__ __align__(8) uint64_t s_qfull, s_qempty, s_done;
+  __shared__ __align__(8) uint64_t s_sfull[2], s_pfull[2], s_ofull[2];
+  __shared__ uint32_t s_tmem;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                           ~uintptr_t(1023));
+  const uint32_t sq = smem_u32(sm);                   // Q, two tiles
+  const uint32_t skv = sq + 2 * S::TILE;              // K and V slots
+  int* err = p.errflag;
+
+  if (tid == 0) {
+    for (int i = 0; i < S::SLOTS; ++i) {
+      mbar_init(&s_full[i], 4);
+      mbar_init(&s_empty[i], 1);
+    }
+    mbar_init(&s_qfull, 4);
+    mbar_init(&s_qempty, 1);
+    mbar_init(&s_done, 1);
+    for (int h = 0; h < 2; ++h) {
+      mbar_init(&s_sfull[h], 1);
+      mbar_init(&s_pfull[h], 4);
+      mbar_init(&s_ofull[h], 1);
+    }
+    fence_mbar_init_cluster();
+  }
+  pdl_wait();
+  pdl_trigger();
+
+  // ---- this block's units
+  const int nslots = PRE ? (p.n_tokens * p.g.G + 255) / 256 : a.slots;
+  const int per = (nslots + kTcThreads - 1) / kTcThreads;
+  const int s_lo = min(nslots, tid * per), s_hi = min(nslots, s_lo + per);
+  // Calls f(tile) for the row tiles numbered s_lo .. s_hi - 1, in order, until it says stop.
+  auto walk = [&](auto&& f) {
+    if (s_lo >= s_hi) return;
+    RowTile t;
+    if constexpr (PRE) {
+      seq_of<PRE>(p, 0, t);
+      for (int j = s_lo; j < s_hi; ++j) {
+        tile_of<PRE>(p, j, t);
+        if (f(t)) return;
+      }
+    } else {
+      // the last sequence whose first number is <= s_lo
+      int lo = 0, hi = p.batch - 1;
+      auto first_no = [&](int b) {
+        const int t0 = p.q_start ? min(max(p.q_start[b], 0), p.n_tokens) : b;
+        return (int)((long long)t0 * p.g.G / (2 * kHalf)) + b;
+      };
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (first_no(mid) <= s_lo)
+          lo = mid;
+        else
+          hi = mid - 1;
+      }
+      for (int b = lo; b < p.batch; ++b) {
+        const int no = first_no(b);
+        if (no >= s_hi) return;
+        seq_of<PRE>(p, b, t);
+        for (int j = max(0, s_lo - no); j < t.jn && no + j < s_hi; ++j) {
+          tile_of<PRE>(p, j, t);
+          if (f(t)) return;
+        }
+      }
+    }
+  };
+  long long mine = 0;
+  walk([&](const RowTile& t) {
+    mine += (long long)t.tiles * p.g.nkv;
+    return false;
+  });
+  long long incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long v = __shfl_up_sync(~0u, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) s_scan[warp] = incl;
+  __syncthreads();
+  long long before = incl - mine, total = 0;
+#pragma unroll
+  for (int w = 0; w < kTcThreads / 32; ++w) {
+    if (w < warp) before += s_scan[w];
+    total += s_scan[w];
+  }
+  const long long upc = PRE ? a.pre.upc : (total + gridDim.x - 1) / gridDim.x;
+  const long long u0 = blockIdx.x * upc, u1 = min(total, u0 + upc);
+  if (!PRE && tid == 0) a.meta[blockIdx.x].tiles = 0;
+  if (u0 >= u1) return;
+  if (before <= u0 && u0 < before + mine) {
+    long long at = before;
+    walk([&](const RowTile& t) {
+      const long long n = (long long)t.tiles * p.g.nkv;
+      if (u0 < at + n) {
+        TcCursor<PRE> c;
+        c.t = t;
+        c.u = u0;
+        c.h = (int)((u0 - at) / t.tiles);
+        c.tile = (int)((u0 - at) - (long long)c.h * t.tiles);
+        c.i0 = u0 - c.tile;
+        s_cur = c;
+        return true;
+      }
+      at += n;
+      return false;
+    });
+  }
+  if (warp == 12) {
+    tmem_alloc(&s_tmem, 512);
+    tmem_relinquish();
+  }
+  tc05_fence_before();
+  __syncthreads();
+  tc05_fence_after();
+  const uint32_t tmem = s_tmem;
+
+  if (warp < 8) {
+    // ------------------------------------------------------------ softmax --
+    set_regs_up<184>();
+    const int hf = warp >> 2;                   // half
+    const int r = (warp & 3) * 32 + lane;       // row of the half = TMEM lane
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + lanes + S::S_COL + hf * kBN;
+    const uint32_t to = tmem + lanes + S::O_COL + hf * D;
+    const float sc = p.scale_log2;
+    TcCursor<PRE>& cur = s_wcur[warp];
+    if (lane == 0) cur = s_cur;
+    __syncwarp();
+    uint32_t n_tiles = 0;  // active tiles so far: parity of the barriers
+    while (cur.u < u1) {
+      const RowTile& t = cur.t;
+      const int gr = t.j * 2 * kHalf + hf * kHalf + r;  // row of the sequence
+      const int pos = PRE ? 0 : t.p0 + gr / p.g.G;
+      const PagedRange rng = t.half[hf];
+      const int plo = t.plo[hf], phi = t.phi[hf];
+      const int first = cur.tile, count = (int)min((long long)(t.tiles - first), u1 - cur.u);
+      const int ns = t.ns, skip = t.skip;
+      float m = -INFINITY, l = 0.f;
+      bool some = false;  // O holds something
+#pragma unroll 1
+      for (int tile = first; tile < first + count; ++tile) {
+        const int base = (tile < ns ? tile : tile + skip) * kBN;
+        if (tile_active(rng, base)) {
+          wait_bar(&s_sfull[hf], n_tiles & 1, err);
+          tc05_fence_after();
+          float s[kBN];
+#pragma unroll
+          for (int k = 0; k < kBN / 32; ++k) tmem_ld32(ts + 32 * k, s + 32 * k);
+          tmem_wait_ld();
+          // all rows of the half see the whole tile?
+          bool full;
+          if constexpr (PRE)
+            full = base + kBN <= p.prefix_len;
+          else
+            full = base + kBN - 1 <= plo &&
+                   (p.window == 0 || phi - base < p.window || base + kBN <= p.n_sinks);
+          if (!full) {
+#pragma unroll
+            for (int k = 0; k < kBN; ++k) {
+              const bool see = PRE ? base + k < p.prefix_len
+                                   : paged_visible(pos, base + k, p.window, p.n_sinks);
+              if (!see) s[k] = -INFINITY;
+            }
+          }
+          float mx = s[0];
+#pragma unroll
+          for (int k = 1; k < kBN; ++k) mx = fmaxf(mx, s[k]);
+          const float m_new = fmaxf(m, mx);
+          const bool grow = (m_new - m) * sc > kGrow;  // also from -inf
+          if (__any_sync(~0u, grow)) {
+            const float corr = m_new == -INFINITY ? 1.f : ex2((m - m_new) * sc);
+            if (some) {
+              wait_bar(&s_ofull[hf], (n_tiles - 1) & 1, err);
+              tc05_fence_after();
+#pragma unroll 1
+              for (int c = 0; c < D; c += 16) {
+                uint32_t o[16];
+                tmem_ld_32x32b_x16_nowait(to + c, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * corr);
+                tmem_st16(to + c, o);
+              }
+            }
+            l *= corr;
+            m = m_new;
+          }
+          const float ref = m == -INFINITY ? 0.f : m * sc;
+#pragma unroll
+          for (int k = 0; k < kBN / 32; ++k) {
+            uint32_t w[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              const float x = ex2(fmaf(s[32 * k + 2 * e], sc, -ref));
+              const float y = ex2(fmaf(s[32 * k + 2 * e + 1], sc, -ref));
+              l += x + y;
+              w[e] = pack2<T>(x, y);
+            }
+            tmem_st16(ts + 16 * k, w);
+          }
+          tmem_wait_st();
+          tc05_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s_pfull[hf]);
+          some = true;
+          ++n_tiles;
+        }
+      }
+      // ---- the block's part of the item
+      const bool whole = first == 0 && count == t.tiles;
+      if (some) {
+        wait_bar(&s_ofull[hf], (n_tiles - 1) & 1, err);
+        tc05_fence_after();
+      }
+      const bool mine_row = gr < t.rows;
+      const float m2 = m * sc;  // base 2
+      const PagedItemParts parts(cur.i0, t.tiles, upc);
+      if (PRE || !whole) {
+        const long long at = parts.slot((int)(blockIdx.x - parts.first)) * (2 * kHalf) +
+                             hf * kHalf + r;
+        if (mine_row) __stcg(a.ml + at, make_float2(m2, l));
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k) {
+          float o[32];
+          if (some) {
+            tmem_ld32(to + 32 * k, o);
+            tmem_wait_ld();
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = 0.f;
+          }
+          if (mine_row) {
+            float4* dst = reinterpret_cast<float4*>(a.o + at * D + 32 * k);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              __stcg(dst + e, make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]));
+          }
+        }
+        if (!PRE && first == 0 && warp == 0 && lane == 0) {
+          TcMeta x;
+          x.i0 = cur.i0;
+          x.upc = upc;
+          x.tiles = t.tiles;
+          x.t0 = t.t0;
+          x.p0 = t.p0;
+          x.rows = t.rows;
+          x.j = t.j;
+          x.h = cur.h;
+          a.meta[blockIdx.x] = x;
+        }
+      } else {
+        const int i = gr / p.g.G, g = gr - i * p.g.G;
+        const long long tok = t.t0 + i;
+        float mt = m2, lt = l, own = 1.f;
+        const long long R = tok * p.g.G + g;
+        const long long ptile = a.pre.rows ? R / a.pre.rows : 0;
+        const PagedItemParts pp(a.pre.rows ? (ptile * p.g.nkv + cur.h) * a.pre.tiles : 0,
+                                a.pre.rows ? a.pre.tiles : 1, a.pre.rows ? a.pre.upc : 1);
+        const int prow = a.pre.rows ? (int)(R - ptile * a.pre.rows) : 0;
+        const int np = a.pre.rows && mine_row && t.p0 + i >= 0 ? pp.n : 0;
+        for (int k = 0; k < np; ++k) mt = fmaxf(mt, __ldcg(a.pre.ml + pp.slot(k) * a.pre.rows + prow).x);
+        if (np) {
+          own = mt == -INFINITY ? 1.f : ex2(m2 - mt);
+          lt = l * own;
+          for (int k = 0; k < np; ++k) {
+            const float2 ml = __ldcg(a.pre.ml + pp.slot(k) * a.pre.rows + prow);
+            if (mt != -INFINITY) lt += ml.y * ex2(ml.x - mt);
+          }
+        }
+        const float inv = lt == 0.f ? 0.f : 1.f / lt;
+        const long long orow = tok * p.g.nq + cur.h * p.g.G + g;
+#pragma unroll
+        for (int k = 0; k < D / 32; ++k) {
+          float o[32];
+          if (some) {
+            tmem_ld32(to + 32 * k, o);
+            tmem_wait_ld();
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = 0.f;
+          }
+          if (np && mt != -INFINITY) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] *= own;
+            for (int x = 0; x < np; ++x) {
+              const long long at = pp.slot(x) * a.pre.rows + prow;
+              const float f = ex2(__ldcg(a.pre.ml + at).x - mt);
+              const float4* src = reinterpret_cast<const float4*>(a.pre.o + at * D + 32 * k);
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                const float4 v = __ldcg(src + e);
+                o[4 * e] = fmaf(v.x, f, o[4 * e]);
+                o[4 * e + 1] = fmaf(v.y, f, o[4 * e + 1]);
+                o[4 * e + 2] = fmaf(v.z, f, o[4 * e + 2]);
+                o[4 * e + 3] = fmaf(v.w, f, o[4 * e + 3]);
+              }
+            }
+          }
+          if (mine_row) {
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(p.out) + orow * D + 32 * k);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              dst[e] = make_uint4(pack2<T>(o[8 * e] * inv, o[8 * e + 1] * inv),
+                                  pack2<T>(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
+                                  pack2<T>(o[8 * e + 4] * inv, o[8 * e + 5] * inv),
+                                  pack2<T>(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
+          }
+        }
+        if (mine_row && p.lse)
+          p.lse[orow] = mt == -INFINITY ? -INFINITY : (mt + log2f(lt)) * 0.69314718055994531f;
+      }
+      tc05_fence_before();  // O is read before the next item's first product
+      __syncwarp();
+      if (lane == 0) {
+        cur.u += count - 1;
+        cur.tile += count - 1;
+        cur.next(p, u1);
+      }
+      __syncwarp();
+    }
+  } else if (warp < 12) {
+    // ------------------------------------------------------------- copies --
+    set_regs_down<80>();
+    const int lw = warp - 8;
+    TcCursor<PRE> cur = s_cur;
+    // Up to three tiles are in flight before the oldest is announced.
+    uint64_t *b0 = nullptr, *b1 = nullptr, *b2 = nullptr;
+    auto announce = [&](uint64_t* bar) {
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar);
+    };
+    auto push = [&](uint64_t* bar) {
+      cp_commit();
+      if (b2) {
+        cp_wait<3>();
+        announce(b2);
+      }
+      b2 = b1;
+      b1 = b0;
+      b0 = bar;
+    };
+    auto flush = [&]() {
+      if (b2) {
+        cp_wait<2>();
+        announce(b2);
+      }
+      if (b1) {
+        cp_wait<1>();
+        announce(b1);
+      }
+      cp_wait<0>();
+      if (b0) announce(b0);
+      b0 = b1 = b2 = nullptr;
+    };
+    // Waits for a slot; what is in flight is announced before it blocks.
+    auto acquire = [&](uint64_t* bar, uint32_t parity) {
+      bool ok = mbar_try_wait_cta(smem_u32(bar), parity);
+      if (!__all_sync(~0u, ok)) {
+        flush();
+        wait_bar(bar, parity, err);
+      }
+    };
+    const char* kbase = static_cast<const char*>(p.k_pages);
+    const char* vbase = static_cast<const char*>(p.v_pages);
+    const char* qbase = static_cast<const char*>(p.q);
+    RingPos ring(0, S::SLOTS);
+    uint32_t use = 0;  // slots taken so far
+    uint32_t items = 0;
+    bool fresh = true;
+    while (cur.u < u1) {
+      const RowTile& t = cur.t;
+      if (fresh) {
+        if (items) acquire(&s_qempty, (items - 1) & 1);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const int row = lw * 32 + lane;
+          const int gr = t.j * 2 * kHalf + h * kHalf + row;
+          const int i = gr / p.g.G;
+          int64_t off = -1;
+          if (gr < t.rows)
+            off = ((int64_t)(t.t0 + i) * p.q_stride + (int64_t)(cur.h * p.g.G + gr - i * p.g.G) * D) * 2;
+          if (__any_sync(~0u, off >= 0)) {
+#pragma unroll 4
+            for (int x = 0; x < C; ++x) {
+              const int rr = x * (32 / C) + lane / C, c = lane % C;
+              const int64_t o = __shfl_sync(~0u, off, rr);
+              cp16(sq + h * S::TILE + tile_at(lw * 32 + rr, c), qbase + (o >= 0 ? o + c * 16 : 0),
+                   o >= 0);
+            }
+          } else {
+#pragma unroll 4
+            for (int x = 0; x < C; ++x)
+              cp16(sq + h * S::TILE + tile_at(lw * 32 + x * (32 / C) + lane / C, lane % C), qbase,
+                   false);
+          }
+        }
+        push(&s_qfull);
+        ++items;
+        fresh = false;
+      }
+      const int j = t.base(cur.tile) + lw * 32 + lane;
+      int64_t off = -1;
+      if (t.sees(j)) {
+        const int* table = PRE ? p.prefix_table : p.page_table + (int64_t)t.b * p.g.max_pages;
+        off = paged_offset(table, j, p.g, err);
+        if (off >= 0) off = (off + (int64_t)cur.h * p.g.head_stride) * 2;
+      }
+#pragma unroll
+      for (int kv = 0; kv < 2; ++kv) {
+        if (use >= S::SLOTS) acquire(&s_empty[ring.slot], ring.phase ^ 1u);
+        const uint32_t dst = skv + ring.slot * S::TILE;
+        const char* src = kv ? vbase : kbase;
+#pragma unroll 4
+        for (int x = 0; x < C; ++x) {
+          const int rr = x * (32 / C) + lane / C, c = lane % C;
+          const int64_t o = __shfl_sync(~0u, off, rr);
+          cp16(dst + tile_at(lw * 32 + rr, c), src + (o >= 0 ? o + c * 16 : 0), o >= 0);
+        }
+        push(&s_full[ring.slot]);
+        ring.next(S::SLOTS);
+        ++use;
+      }
+      fresh = cur.next(p, u1);
+    }
+    flush();
+  } else {
+    // ---------------------------------------------------------------- mma --
+    set_regs_down<64>();
+    if (warp == 12 && lane == 0) {
+      constexpr uint32_t id_s = idesc_kind_f16(kIsBf16<T>, kHalf, kBN);
+      constexpr uint32_t id_o = idesc_kind_f16(kIsBf16<T>, kHalf, D) | (1u << 16);  // B is N-major
+      TcCursor<PRE> cur = s_cur;
+      RingPos ring(0, S::SLOTS);
+      uint32_t items = 0, n_tiles[2] = {0, 0};
+      bool acc[2] = {false, false};
+      bool fresh = true;
+      bool pend = false;  // half 1's O += P V of the last tile is still to come
+      int pend_slot = 0;
+      auto scores = [&](int h, int slot) {
+        const uint32_t k0 = skv + slot * S::TILE, q0 = sq + h * S::TILE;
+#pragma unroll
+        for (int x = 0; x < D / 16; ++x) {
+          const uint32_t off = (x >> 2) * (kBN * 128) + (x & 3) * 32;
+          tc05_mma_f16(tmem + S::S_COL + h * kBN, smem_desc_k_sw128(q0 + off, 1024),
+                       smem_desc_k_sw128(k0 + off, 1024), id_s, x > 0);
+        }
+        tc05_commit(&s_sfull[h]);
+      };
+      auto values = [&](int h, int slot) {
+        wait_bar(&s_pfull[h], n_tiles[h] & 1, err);
+        tc05_fence_after();
+        const uint32_t v0 = skv + slot * S::TILE;
+#pragma unroll
+        for (int x = 0; x < kBN / 16; ++x)
+          tc05_mma_f16_ts(tmem + S::O_COL + h * D, tmem + S::S_COL + h * kBN + x * 8,
+                          smem_desc_mn_sw128(v0 + x * 16 * 128, kBN * 128, 1024), id_o,
+                          acc[h] || x > 0);
+        acc[h] = true;
+        ++n_tiles[h];
+        tc05_commit(&s_ofull[h]);
+      };
+      while (cur.u < u1) {
+        const int base = cur.t.base(cur.tile);
+        const bool act0 = tile_active(cur.t.half[0], base), act1 = tile_active(cur.t.half[1], base);
+        if (fresh) {
+          wait_bar(&s_qfull, items & 1, err);
+          acc[0] = acc[1] = false;
+          ++items;
+        }
+        const int kslot = ring.slot;
+        wait_bar(&s_full[kslot], ring.phase, err);
+        tc05_fence_after();
+        ring.next(S::SLOTS);
+        if (act0) scores(0, kslot);
+        if (pend) {
+          values(1, pend_slot);
+          tc05_commit(&s_empty[pend_slot]);
+          pend = false;
+        }
+        if (act1) scores(1, kslot);
+        tc05_commit(&s_empty[kslot]);
+        const int vslot = ring.slot;
+        wait_bar(&s_full[vslot], ring.phase, err);
+        tc05_fence_after();
+        ring.next(S::SLOTS);
+        fresh = cur.next(p, u1);
+        if (fresh) tc05_commit(&s_qempty);
+        if (act0) values(0, vslot);
+        if (act1 && !fresh) {
+          pend = true;
+          pend_slot = vslot;
+        } else {
+          if (act1) values(1, vslot);
+          tc05_commit(&s_empty[vslot]);
+        }
+      }
+      tc05_commit(&s_done);
+      wait_bar(&s_done, 0, err);
+    }
+  }
+  __syncthreads();
+  if (warp == 12) tmem_dealloc(tmem, 512);
+}
+
+// Joins the parts of the item that block x of the main kernel began, if that
+// was split: a thread per row and 4 columns.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) paged_tc_join_kernel(const __grid_constant__ TcArgs a) {
+  pdl_wait();
+  pdl_trigger();
+  const TcMeta x = a.meta[blockIdx.x];
+  if (x.tiles == 0) return;
+  const PagedAttnParams& p = a.p;
+  constexpr int C4 = D / 4;
+  const int rows = min(2 * kHalf, x.rows - x.j * 2 * kHalf);
+  const PagedItemParts parts(x.i0, x.tiles, x.upc);
+  for (int e = blockIdx.y * 256 + threadIdx.x; e < rows * C4; e += gridDim.y * 256) {
+    const int r = e / C4, col = (e - r * C4) * 4;
+    PagedState4 s{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+#pragma unroll 4
+    for (int k = 0; k < parts.n; ++k) {
+      const long long at = parts.slot(k) * (2 * kHalf) + r;
+      const float2 ml = __ldcg(a.ml + at);
+      s.join(ml.x, ml.y, __ldcg(reinterpret_cast<const float4*>(a.o + at * D + col)));
+    }
+    const int gr = x.j * 2 * kHalf + r, i = gr / p.g.G, g = gr - i * p.g.G;
+    const long long t = x.t0 + i;
+    if (a.pre.rows && x.p0 + i >= 0)
+      paged_join_prefix<D>(s, a.pre, t * p.g.G + g, x.h, p.g.nkv, col);
+    paged_store4<T, D>(s, p.out, p.lse, t * p.g.nq + x.h * p.g.G + g, col);
+  }
+}
+
+struct TcFns {
+  const void *main, *join;
+  int smem;
+};
+template <typename T, int D>
+TcFns fns_td(bool prefix) {
+  return TcFns{prefix ? (const void*)&paged_tc_kernel<T, D, true>
+                      : (const void*)&paged_tc_kernel<T, D, false>,
+               (const void*)&paged_tc_join_kernel<T, D>, TcShape<D>::SMEM};
+}
+TcFns tc_fns(int dtype, int d, bool prefix) {
+  if (dtype == CF_F16) return d == 64 ? fns_td<__half, 64>(prefix) : fns_td<__half, 128>(prefix);
+  return d == 64 ? fns_td<__nv_bfloat16, 64>(prefix) : fns_td<__nv_bfloat16, 128>(prefix);
+}
+
+bool launch_pdl(const void* fn, dim3 grid, int threads, int smem, cudaStream_t st, void** args) {
+  cudaLaunchConfig_t lc = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  lc.gridDim = grid;
+  lc.blockDim = dim3(threads, 1, 1);
+  lc.dynamicSmemBytes = smem;
+  lc.stream = st;
+  lc.attrs = attr;
+  lc.numAttrs = 1;
+  return cudaLaunchKernelExC(&lc, fn, args) == cudaSuccess;
+}
+
+}  // namespace
+
+int cf::paged_tc_grid(int dtype, int head_dim, int sm_count) {
+  for (int prefix = 0; prefix < 2; ++prefix) {
+    const TcFns f = tc_fns(dtype, head_dim, prefix != 0);
+    if (cudaFuncSetAttribute(f.main, cudaFuncAttributeMaxDynamicSharedMemorySize, f.smem) !=
+        cudaSuccess) {
+      cudaGetLastError();
+      return 0;
+    }
+  }
+  return sm_count;
+}
+
+size_t cf::paged_tc_meta_bytes(int grid) { return (size_t)grid * sizeof(TcMeta); }
+
+PagedPrefixParts cf::paged_tc_prefix(const PagedAttnParams& p, const PagedSplit& ws) {
+  PagedPrefixParts x;
+  x.o = ws.o;
+  x.ml = ws.ml;
+  x.rows = kTcRows;
+  x.tiles = (p.prefix_len + kBN - 1) / kBN;
+  const long long row_tiles = ((long long)p.n_tokens * p.g.G + kTcRows - 1) / kTcRows;
+  x.upc = std::max<long long>(1, (row_tiles * p.g.nkv * x.tiles + ws.grid - 1) / ws.grid);
+  return x;
+}
+
+bool cf::paged_tc_launch(int dtype, const PagedAttnParams& p, const PagedSplit& ws, bool prefix,
+                         const PagedPrefixParts& pre, cudaStream_t st) {
+  const TcFns f = tc_fns(dtype, p.g.D, prefix);
+  TcArgs a;
+  a.p = p;
+  a.pre = pre;
+  a.o = ws.o;
+  a.ml = ws.ml;
+  a.meta = static_cast<TcMeta*>(ws.meta);
+  a.slots = (int)((long long)p.n_tokens * p.g.G / kTcRows) + p.batch;
+  void* args[] = {&a};
+  if (!launch_pdl(f.main, dim3(ws.grid), kTcThreads, f.smem, st, args)) return false;
+  return prefix || launch_pdl(f.join, dim3(ws.grid, 8), 256, 0, st, args);
+}

@@ -60,8 +60,8 @@
  *   - a kv_len outside [0, max_pages * page_size] or more tokens in a sequence
  *     than max_q: the sequence's rows get o = 0, lse = -infinity and nothing
  *     is appended for it;
- *   - a needed page number outside [0, num_pages): its positions count as not
- *     visible, and nothing is appended to it;
+ *   - a needed page number outside [0, num_pages): keys and values of zero
+ *     stand for its positions, and nothing is appended to it;
  *   - an appended token with p < 0 is skipped (its q_out row too);
  *   - q_start values that decrease or leave [0, n_tokens]: such a sequence
  *     has no tokens.
@@ -106,7 +106,7 @@ typedef struct cf_paged_config {
 typedef struct cf_paged_handle cf_paged_handle; /* opaque */
 
 /* Validate cfg and allocate the handle's workspace (partial results of split
- * sequences, at most about 45 MB, and an error word) on the current device.
+ * sequences, at most about 90 MB, and an error word) on the current device.
  * On failure nothing stays allocated and *out is NULL.  Errors: INVALID_ARG
  * (NULL, sizes, strides, sections that do not add up), UNSUPPORTED
  * (head_dim, page_size), CUDA. */
