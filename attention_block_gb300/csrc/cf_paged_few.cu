@@ -234,6 +234,7 @@ __global__ void __launch_bounds__(kFewThreads, kBlocksPerSm)
   int stage = 0;
   uint32_t qf[D / 16][4];
   float o[NO][4], m[2], l[2];
+  int pos[2];  // positions of this thread's two rows
   bool fresh = true;
   int first_tile = cur.tile;
 
@@ -245,6 +246,7 @@ __global__ void __launch_bounds__(kFewThreads, kBlocksPerSm)
       for (int r = 0; r < 2; ++r) {
         const int row = gq + 8 * r;
         const int i = row / p.g.G;
+        pos[r] = cur.w.p0 + i;
         const T* src = static_cast<const T*>(p.q) + (int64_t)(cur.w.t0 + i) * p.q_stride +
                        (int64_t)(cur.h * p.g.G + row - i * p.g.G) * D + 2 * tq;
 #pragma unroll
@@ -290,8 +292,7 @@ __global__ void __launch_bounds__(kFewThreads, kBlocksPerSm)
           const int jj = nt * 8 + 2 * tq + (e & 1);
           bool see = (valid >> jj) & 1;
           if (!PRE && cur.w.n > 1)
-            see = see && paged_visible(cur.w.p0 + (gq + 8 * (e >> 1)) / p.g.G, j0 + jj, p.window,
-                                       p.n_sinks);
+            see = see && paged_visible(pos[e >> 1], j0 + jj, p.window, p.n_sinks);
           c[nt][e] = see ? c[nt][e] * p.scale_log2 : -INFINITY;
           mx[e >> 1] = fmaxf(mx[e >> 1], c[nt][e]);
         }

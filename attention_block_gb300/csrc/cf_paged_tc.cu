@@ -16,7 +16,8 @@
 //             of P before its rounding; the final o
 //   8-11      copy Q, K and V through the page table into shared memory
 //             (cp.async; positions that no row sees become zeros, so what
-//             lies there reaches no product), in the 128-byte swizzle
+//             lies there reaches no product): tiles of 64-column slabs, rows
+//             of 128 bytes, the 16-byte chunks of a row swizzled
 //   12        one thread issues S = Q K^T (operands in shared memory) and
 //             O += P V (P from TMEM, V as an N-major operand)
 // The halves alternate: while one is in its softmax the tensor core works on
@@ -38,6 +39,7 @@ using namespace cf;
 namespace {
 
 constexpr int kTcThreads = 512;
+constexpr int kCopyThreads = 128;
 constexpr int kHalf = 128;     // rows of a half
 constexpr int kBN = 128;       // positions of a tile
 constexpr float kGrow = 8.0f;  // log2 of the growth that forces a rescale
@@ -50,16 +52,45 @@ struct TcShape {
   static constexpr uint32_t S_COL = 0, O_COL = 2 * kBN;      // TMEM columns
 };
 
-// Element offset inside a tile: slabs of 64 columns, rows of 128 bytes, the
-// 16-byte chunks of a row swizzled.
-__device__ __forceinline__ uint32_t tile_at(int row, int chunk) {
-  return (uint32_t)((chunk >> 3) * (kBN * 128) + row * 128 + (((chunk & 7) ^ (row & 7)) << 4));
-}
-
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 ra, rb, rc, rd;\n\t"
+      "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\tmov.b64 rc, {%6, %7};\n\t"
+      "fma.rn.f32x2 rd, ra, rb, rc;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 ra, rb, rd;\n\t"
+      "mov.b64 ra, {%2, %3};\n\tmov.b64 rb, {%4, %5};\n\t"
+      "add.rn.f32x2 rd, ra, rb;\n\tmov.b64 {%0, %1}, rd;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+// The lowest n bits, n any number.
+__device__ __forceinline__ uint32_t low_bits(int n) {
+  return n <= 0 ? 0u : (n >= 32 ? ~0u : (1u << n) - 1u);
+}
+// Arrives on bar when this thread's copies so far have landed (the barrier's
+// count includes the arrival).
+__device__ __forceinline__ void cp_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar))
+               : "memory");
 }
 
 __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
@@ -270,10 +301,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const __grid_co
 
   if (tid == 0) {
     for (int i = 0; i < S::SLOTS; ++i) {
-      mbar_init(&s_full[i], 4);
+      mbar_init(&s_full[i], kCopyThreads);
       mbar_init(&s_empty[i], 1);
     }
-    mbar_init(&s_qfull, 4);
+    mbar_init(&s_qfull, kCopyThreads);
     mbar_init(&s_qempty, 1);
     mbar_init(&s_done, 1);
     for (int h = 0; h < 2; ++h) {
@@ -417,15 +448,25 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const __grid_co
                    (p.window == 0 || phi - base < p.window || base + kBN <= p.n_sinks);
           if (!full) {
 #pragma unroll
-            for (int k = 0; k < kBN; ++k) {
-              const bool see = PRE ? base + k < p.prefix_len
-                                   : paged_visible(pos, base + k, p.window, p.n_sinks);
-              if (!see) s[k] = -INFINITY;
+            for (int c = 0; c < kBN / 32; ++c) {
+              // bit k: this row sees position base + 32 c + k
+              const int j0 = base + 32 * c;
+              uint32_t see = low_bits((PRE ? p.prefix_len : pos + 1) - j0);
+              if (!PRE && p.window != 0)
+                see &= ~low_bits(pos - p.window + 1 - j0) | low_bits(p.n_sinks - j0);
+#pragma unroll
+              for (int k = 0; k < 32; ++k)
+                if (!((see >> k) & 1u)) s[32 * c + k] = -INFINITY;
             }
           }
-          float mx = s[0];
+          float mx4[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-          for (int k = 1; k < kBN; ++k) mx = fmaxf(mx, s[k]);
+          for (int k = 4; k < kBN - 4; k += 8)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) mx4[e] = max3(mx4[e], s[k + e], s[k + 4 + e]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) mx4[e] = fmaxf(mx4[e], s[kBN - 4 + e]);
+          const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
           const float m_new = fmaxf(m, mx);
           const bool grow = (m_new - m) * sc > kGrow;  // also from -inf
           if (__any_sync(~0u, grow)) {
@@ -447,18 +488,22 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const __grid_co
             m = m_new;
           }
           const float ref = m == -INFINITY ? 0.f : m * sc;
+          const float2 sc2 = make_float2(sc, sc), ref2 = make_float2(-ref, -ref);
+          float2 sum[2] = {make_float2(l, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
           for (int k = 0; k < kBN / 32; ++k) {
             uint32_t w[16];
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
-              const float x = ex2(fmaf(s[32 * k + 2 * e], sc, -ref));
-              const float y = ex2(fmaf(s[32 * k + 2 * e + 1], sc, -ref));
-              l += x + y;
-              w[e] = pack2<T>(x, y);
+              float2 x = fma2(make_float2(s[32 * k + 2 * e], s[32 * k + 2 * e + 1]), sc2, ref2);
+              x.x = ex2(x.x);
+              x.y = ex2(x.y);
+              sum[e & 1] = add2(sum[e & 1], x);
+              w[e] = pack2<T>(x.x, x.y);
             }
             tmem_st16(ts + 16 * k, w);
           }
+          l = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
           tmem_wait_st();
           tc05_fence_before();
           __syncwarp();
@@ -582,109 +627,90 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const __grid_co
   } else if (warp < 12) {
     // ------------------------------------------------------------- copies --
     set_regs_down<80>();
-    const int lw = warp - 8;
+    const int lw = warp - 8;  // rows 32 lw .. 32 lw + 31 of every tile
     TcCursor<PRE> cur = s_cur;
-    // Up to three tiles are in flight before the oldest is announced.
-    uint64_t *b0 = nullptr, *b1 = nullptr, *b2 = nullptr;
-    auto announce = [&](uint64_t* bar) {
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar);
-    };
-    auto push = [&](uint64_t* bar) {
-      cp_commit();
-      if (b2) {
-        cp_wait<3>();
-        announce(b2);
-      }
-      b2 = b1;
-      b1 = b0;
-      b0 = bar;
-    };
-    auto flush = [&]() {
-      if (b2) {
-        cp_wait<2>();
-        announce(b2);
-      }
-      if (b1) {
-        cp_wait<1>();
-        announce(b1);
-      }
-      cp_wait<0>();
-      if (b0) announce(b0);
-      b0 = b1 = b2 = nullptr;
-    };
-    // Waits for a slot; what is in flight is announced before it blocks.
-    auto acquire = [&](uint64_t* bar, uint32_t parity) {
-      bool ok = mbar_try_wait_cta(smem_u32(bar), parity);
-      if (!__all_sync(~0u, ok)) {
-        flush();
-        wait_bar(bar, parity, err);
+    constexpr int RP = 32 / C;                      // rows of one copy instruction
+    const int r0 = lane / C, c0 = lane % C;
+    const uint32_t d0 = (uint32_t)((c0 >> 3) * (kBN * 128) + (lw * 32 + r0) * 128);
+    const uint32_t x0 = (uint32_t)(((c0 & 7) ^ r0) << 4);
+    const int64_t ss = p.g.slot_stride * 2;
+    // Copies 32 rows; lane i holds row i's byte offset in src, or -1 (zeros).
+    auto copy = [&](uint32_t dst, const char* src, int64_t off, bool octets) {
+      if (octets && __all_sync(~0u, off >= 0)) {
+        // eight consecutive positions lie in one page: one lookup serves them
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          const char* at = src + __shfl_sync(~0u, off, 8 * y) + r0 * ss + c0 * 16;
+#pragma unroll
+          for (int z = 0; z < 8 / RP; ++z) {
+            cp16(dst + d0 + (8 * y + z * RP) * 128 + (x0 ^ ((z * RP) << 4)), at);
+            at += RP * ss;
+          }
+        }
+      } else {
+#pragma unroll 4
+        for (int x = 0; x < C; ++x) {
+          const int64_t o = __shfl_sync(~0u, off, x * RP + r0);
+          cp16(dst + d0 + x * RP * 128 + (x0 ^ (((x * RP) & 7) << 4)),
+               src + (o >= 0 ? o + c0 * 16 : 0), o >= 0);
+        }
       }
     };
     const char* kbase = static_cast<const char*>(p.k_pages);
     const char* vbase = static_cast<const char*>(p.v_pages);
     const char* qbase = static_cast<const char*>(p.q);
+    const bool octets = p.g.page_shift >= 3;
+    // The page of this lane's position, looked up one tile ahead of its copies.
+    int f_pos = -1, f_page = 0;
+    auto look_up = [&]() {
+      const int j = cur.t.base(cur.tile) + lw * 32 + lane;
+      f_pos = -1;
+      if (cur.u >= u1 || !cur.t.sees(j)) return;
+      f_pos = j;
+      f_page = __ldg((PRE ? p.prefix_table : p.page_table + (int64_t)cur.t.b * p.g.max_pages) +
+                     (j >> p.g.page_shift));
+    };
     RingPos ring(0, S::SLOTS);
     uint32_t use = 0;  // slots taken so far
     uint32_t items = 0;
     bool fresh = true;
+    look_up();
     while (cur.u < u1) {
-      const RowTile& t = cur.t;
       if (fresh) {
-        if (items) acquire(&s_qempty, (items - 1) & 1);
-#pragma unroll
+        const RowTile& t = cur.t;
+        if (items) wait_bar(&s_qempty, (items - 1) & 1, err);
+#pragma unroll 1
         for (int h = 0; h < 2; ++h) {
-          const int row = lw * 32 + lane;
-          const int gr = t.j * 2 * kHalf + h * kHalf + row;
+          const int gr = t.j * 2 * kHalf + h * kHalf + lw * 32 + lane;
           const int i = gr / p.g.G;
           int64_t off = -1;
           if (gr < t.rows)
             off = ((int64_t)(t.t0 + i) * p.q_stride + (int64_t)(cur.h * p.g.G + gr - i * p.g.G) * D) * 2;
-          if (__any_sync(~0u, off >= 0)) {
-#pragma unroll 4
-            for (int x = 0; x < C; ++x) {
-              const int rr = x * (32 / C) + lane / C, c = lane % C;
-              const int64_t o = __shfl_sync(~0u, off, rr);
-              cp16(sq + h * S::TILE + tile_at(lw * 32 + rr, c), qbase + (o >= 0 ? o + c * 16 : 0),
-                   o >= 0);
-            }
-          } else {
-#pragma unroll 4
-            for (int x = 0; x < C; ++x)
-              cp16(sq + h * S::TILE + tile_at(lw * 32 + x * (32 / C) + lane / C, lane % C), qbase,
-                   false);
-          }
+          copy(sq + h * S::TILE, qbase, off, false);
         }
-        push(&s_qfull);
+        cp_arrive(&s_qfull);
         ++items;
-        fresh = false;
       }
-      const int j = t.base(cur.tile) + lw * 32 + lane;
       int64_t off = -1;
-      if (t.sees(j)) {
-        const int* table = PRE ? p.prefix_table : p.page_table + (int64_t)t.b * p.g.max_pages;
-        off = paged_offset(table, j, p.g, err);
-        if (off >= 0) off = (off + (int64_t)cur.h * p.g.head_stride) * 2;
+      if (f_pos >= 0) {
+        if ((unsigned)f_page >= (unsigned)p.g.num_pages)
+          atomicOr(err, kDevErrPosRange);
+        else
+          off = ((int64_t)f_page * p.g.page_stride +
+                 (int64_t)(f_pos & p.g.page_mask) * p.g.slot_stride +
+                 (int64_t)cur.h * p.g.head_stride) * 2;
       }
-#pragma unroll
+      fresh = cur.next(p, u1);
+      look_up();
+#pragma unroll 1
       for (int kv = 0; kv < 2; ++kv) {
-        if (use >= S::SLOTS) acquire(&s_empty[ring.slot], ring.phase ^ 1u);
-        const uint32_t dst = skv + ring.slot * S::TILE;
-        const char* src = kv ? vbase : kbase;
-#pragma unroll 4
-        for (int x = 0; x < C; ++x) {
-          const int rr = x * (32 / C) + lane / C, c = lane % C;
-          const int64_t o = __shfl_sync(~0u, off, rr);
-          cp16(dst + tile_at(lw * 32 + rr, c), src + (o >= 0 ? o + c * 16 : 0), o >= 0);
-        }
-        push(&s_full[ring.slot]);
+        if (use >= S::SLOTS) wait_bar(&s_empty[ring.slot], ring.phase ^ 1u, err);
+        copy(skv + ring.slot * S::TILE, kv ? vbase : kbase, off, octets);
+        cp_arrive(&s_full[ring.slot]);
         ring.next(S::SLOTS);
         ++use;
       }
-      fresh = cur.next(p, u1);
     }
-    flush();
   } else {
     // ---------------------------------------------------------------- mma --
     set_regs_down<64>();
@@ -726,11 +752,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const __grid_co
         const bool act0 = tile_active(cur.t.half[0], base), act1 = tile_active(cur.t.half[1], base);
         if (fresh) {
           wait_bar(&s_qfull, items & 1, err);
+          fence_proxy_async_smem();  // the copies wrote as ordinary stores
           acc[0] = acc[1] = false;
           ++items;
         }
         const int kslot = ring.slot;
         wait_bar(&s_full[kslot], ring.phase, err);
+        fence_proxy_async_smem();
         tc05_fence_after();
         ring.next(S::SLOTS);
         if (act0) scores(0, kslot);
@@ -743,6 +771,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const __grid_co
         tc05_commit(&s_empty[kslot]);
         const int vslot = ring.slot;
         wait_bar(&s_full[vslot], ring.phase, err);
+        fence_proxy_async_smem();
         tc05_fence_after();
         ring.next(S::SLOTS);
         fresh = cur.next(p, u1);
