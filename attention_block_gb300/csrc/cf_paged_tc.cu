@@ -114,6 +114,46 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t* r) {
       "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(taddr)
       : "memory");
 }
+// 32 columns of 16 TMEM lanes as mma accumulator fragments: of column octet b,
+// r[4b], r[4b+1] are row lane / 4, columns 2 (lane % 4) and + 1, and r[4b+2],
+// r[4b+3] the same of row lane / 4 + 8.
+__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, float (&v)[16]) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(v);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
+}
+// Transposes w over a quad of lanes: lane q ends with word q of lanes 0..3.
+__device__ __forceinline__ void quad_transpose(uint32_t (&w)[4], int q) {
+  const bool a = q & 1, b = q & 2;
+#pragma unroll
+  for (int i = 0; i < 4; i += 2) {  // pairs (0, 1) and (2, 3)
+    const uint32_t x = __shfl_xor_sync(~0u, a ? w[i] : w[i + 1], 1);
+    if (a)
+      w[i] = x;
+    else
+      w[i + 1] = x;
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {  // pairs (0, 2) and (1, 3)
+    const uint32_t x = __shfl_xor_sync(~0u, b ? w[i] : w[i + 2], 2);
+    if (b)
+      w[i] = x;
+    else
+      w[i + 2] = x;
+  }
+}
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(p));
+  return p != 0;
+}
 __device__ __forceinline__ void tmem_wait_st() {
   asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
@@ -162,6 +202,12 @@ template <typename T>
 constexpr bool kIsBf16 = false;
 template <>
 constexpr bool kIsBf16<__nv_bfloat16> = true;
+
+// Starts a load into L1 without waiting for it.
+__device__ __forceinline__ void prefetch_line(const int* at) {
+  int v;
+  asm volatile("ld.global.ca.u32 %0, [%1];" : "=r"(v) : "l"(at));
+}
 
 template <int N>
 __device__ __forceinline__ void set_regs_up() {
@@ -287,7 +333,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const __grid_co
   extern __shared__ uint8_t smem_raw[];
   __shared__ long long s_scan[kTcThreads / 32];
   __shared__ TcCursor<PRE> s_cur;
-  __shared__ TcCursor<PRE> s_wcur[8];  // each softmax warp's place: too much for its registers
+  __shared__ TcCursor<PRE> s_wcur[9];  // places of the softmax warps and of the issuing one
   __shared__ __align__(8) uint64_t s_full[S::SLOTS], s_empty[S::SLOTS];
   __shared__ __align__(8) uint64_t s_qfull, s_qempty, s_done;
   __shared__ __align__(8) uint64_t s_sfull[2], s_pfull[2], s_ofull[2];
@@ -318,6 +364,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const __grid_co
   pdl_trigger();
 
   // ---- this block's units
+  if constexpr (!PRE)  // the lookups below depend on one another: have their lines on the way
+    for (int b = tid; b < p.batch; b += kTcThreads) {
+      if (p.q_start) prefetch_line(p.q_start + b + 1);
+      prefetch_line(p.kv_len + b);
+    }
   const int nslots = PRE ? (p.n_tokens * p.g.G + 255) / 256 : a.slots;
   const int per = (nslots + kTcThreads - 1) / kTcThreads;
   const int s_lo = min(nslots, tid * per), s_hi = min(nslots, s_lo + per);
@@ -454,6 +505,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const __grid_co
               uint32_t see = low_bits((PRE ? p.prefix_len : pos + 1) - j0);
               if (!PRE && p.window != 0)
                 see &= ~low_bits(pos - p.window + 1 - j0) | low_bits(p.n_sinks - j0);
+              if (__all_sync(~0u, see == ~0u)) continue;
 #pragma unroll
               for (int k = 0; k < 32; ++k)
                 if (!((see >> k) & 1u)) s[32 * c + k] = -INFINITY;
@@ -518,102 +570,127 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const __grid_co
         wait_bar(&s_ofull[hf], (n_tiles - 1) & 1, err);
         tc05_fence_after();
       }
-      const bool mine_row = gr < t.rows;
       const float m2 = m * sc;  // base 2
       const PagedItemParts parts(cur.i0, t.tiles, upc);
-      if (PRE || !whole) {
-        const long long at = parts.slot((int)(blockIdx.x - parts.first)) * (2 * kHalf) +
-                             hf * kHalf + r;
-        if (mine_row) __stcg(a.ml + at, make_float2(m2, l));
+      const bool part = PRE || !whole;
+      const long long prow0 =
+          part ? parts.slot((int)(blockIdx.x - parts.first)) * (2 * kHalf) + hf * kHalf : 0;
+      if (part && gr < t.rows) __stcg(a.ml + prow0 + r, make_float2(m2, l));
+      const int q4 = lane & 3;
+#pragma unroll 1
+      for (int hh = 0; hh < 2; ++hh) {  // 16 rows of the warp at a time
+        float own[2], inv[2], mt[2];
+        int row[2], np[2];
+        long long orow[2];
 #pragma unroll
-        for (int k = 0; k < D / 32; ++k) {
-          float o[32];
-          if (some) {
-            tmem_ld32(to + 32 * k, o);
-            tmem_wait_ld();
-          } else {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = 0.f;
-          }
-          if (mine_row) {
-            float4* dst = reinterpret_cast<float4*>(a.o + at * D + 32 * k);
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-              __stcg(dst + e, make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]));
-          }
-        }
-        if (!PRE && first == 0 && warp == 0 && lane == 0) {
-          TcMeta x;
-          x.i0 = cur.i0;
-          x.upc = upc;
-          x.tiles = t.tiles;
-          x.t0 = t.t0;
-          x.p0 = t.p0;
-          x.rows = t.rows;
-          x.j = t.j;
-          x.h = cur.h;
-          a.meta[blockIdx.x] = x;
-        }
-      } else {
-        const int i = gr / p.g.G, g = gr - i * p.g.G;
-        const long long tok = t.t0 + i;
-        float mt = m2, lt = l, own = 1.f;
-        const long long R = tok * p.g.G + g;
-        const long long ptile = a.pre.rows ? R / a.pre.rows : 0;
-        const PagedItemParts pp(a.pre.rows ? (ptile * p.g.nkv + cur.h) * a.pre.tiles : 0,
-                                a.pre.rows ? a.pre.tiles : 1, a.pre.rows ? a.pre.upc : 1);
-        const int prow = a.pre.rows ? (int)(R - ptile * a.pre.rows) : 0;
-        const int np = a.pre.rows && mine_row && t.p0 + i >= 0 ? pp.n : 0;
-        for (int k = 0; k < np; ++k) mt = fmaxf(mt, __ldcg(a.pre.ml + pp.slot(k) * a.pre.rows + prow).x);
-        if (np) {
-          own = mt == -INFINITY ? 1.f : ex2(m2 - mt);
-          lt = l * own;
-          for (int k = 0; k < np; ++k) {
-            const float2 ml = __ldcg(a.pre.ml + pp.slot(k) * a.pre.rows + prow);
-            if (mt != -INFINITY) lt += ml.y * ex2(ml.x - mt);
-          }
-        }
-        const float inv = lt == 0.f ? 0.f : 1.f / lt;
-        const long long orow = tok * p.g.nq + cur.h * p.g.G + g;
-#pragma unroll
-        for (int k = 0; k < D / 32; ++k) {
-          float o[32];
-          if (some) {
-            tmem_ld32(to + 32 * k, o);
-            tmem_wait_ld();
-          } else {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = 0.f;
-          }
-          if (np && mt != -INFINITY) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] *= own;
-            for (int x = 0; x < np; ++x) {
-              const long long at = pp.slot(x) * a.pre.rows + prow;
-              const float f = ex2(__ldcg(a.pre.ml + at).x - mt);
-              const float4* src = reinterpret_cast<const float4*>(a.pre.o + at * D + 32 * k);
-#pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                const float4 v = __ldcg(src + e);
-                o[4 * e] = fmaf(v.x, f, o[4 * e]);
-                o[4 * e + 1] = fmaf(v.y, f, o[4 * e + 1]);
-                o[4 * e + 2] = fmaf(v.z, f, o[4 * e + 2]);
-                o[4 * e + 3] = fmaf(v.w, f, o[4 * e + 3]);
-              }
+        for (int e = 0; e < 2; ++e) {
+          const int src = hh * 16 + e * 8 + (lane >> 2);  // lane that has this row's state
+          const float rm = __shfl_sync(~0u, m2, src);
+          float rl = __shfl_sync(~0u, l, src);
+          row[e] = (warp & 3) * 32 + src;
+          const int rg = t.j * 2 * kHalf + hf * kHalf + row[e];
+          const bool there = rg < t.rows;
+          if (!there) row[e] = -1;
+          own[e] = 1.f;
+          mt[e] = rm;
+          np[e] = 0;
+          const int i = rg / p.g.G;
+          orow[e] = ((long long)t.t0 + i) * p.g.nq + cur.h * p.g.G + rg - i * p.g.G;
+          if (!part && a.pre.rows && there && t.p0 + i >= 0) {
+            const long long R = (long long)t.t0 * p.g.G + rg, pt = R / a.pre.rows;
+            const PagedItemParts pp((pt * p.g.nkv + cur.h) * a.pre.tiles, a.pre.tiles, a.pre.upc);
+            const int pr = (int)(R - pt * a.pre.rows);
+            np[e] = pp.n;
+            for (int k = 0; k < pp.n; ++k)
+              mt[e] = fmaxf(mt[e], __ldcg(a.pre.ml + pp.slot(k) * a.pre.rows + pr).x);
+            const float ref = mt[e] == -INFINITY ? 0.f : mt[e];
+            own[e] = ex2(rm - ref);
+            rl *= own[e];
+            for (int k = 0; k < pp.n; ++k) {
+              const float2 ml = __ldcg(a.pre.ml + pp.slot(k) * a.pre.rows + pr);
+              rl += ml.y * ex2(ml.x - ref);
             }
           }
-          if (mine_row) {
-            uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(p.out) + orow * D + 32 * k);
+          inv[e] = part ? 1.f : (rl == 0.f ? 0.f : 1.f / rl);
+          if (!part && p.lse && there && q4 == 0)
+            p.lse[orow[e]] =
+                mt[e] == -INFINITY ? -INFINITY : (mt[e] + log2f(rl)) * 0.69314718055994531f;
+        }
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          float o[16];
+          if (some) {
+            tmem_ld_frag(to + ((uint32_t)(16 * hh) << 16) + c, o);
+            tmem_wait_ld();
+          } else {
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              dst[e] = make_uint4(pack2<T>(o[8 * e] * inv, o[8 * e + 1] * inv),
-                                  pack2<T>(o[8 * e + 2] * inv, o[8 * e + 3] * inv),
-                                  pack2<T>(o[8 * e + 4] * inv, o[8 * e + 5] * inv),
-                                  pack2<T>(o[8 * e + 6] * inv, o[8 * e + 7] * inv));
+            for (int x = 0; x < 16; ++x) o[x] = 0.f;
+          }
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            if (part) {
+              // of two octets A, B the even lanes of a quad store A's words, the
+              // odd ones B's, 16 bytes each
+#pragma unroll
+              for (int b2 = 0; b2 < 2; ++b2) {
+                const float A0 = o[8 * b2 + 2 * e], A1 = o[8 * b2 + 2 * e + 1];
+                const float B0 = o[8 * b2 + 4 + 2 * e], B1 = o[8 * b2 + 5 + 2 * e];
+                const bool odd = q4 & 1;
+                const float g0 = __shfl_xor_sync(~0u, odd ? A0 : B0, 1);
+                const float g1 = __shfl_xor_sync(~0u, odd ? A1 : B1, 1);
+                if (row[e] >= 0)
+                  __stcg(reinterpret_cast<float4*>(a.o + (prow0 + row[e]) * D + c + 16 * b2 +
+                                                   8 * (q4 & 1) + 4 * (q4 >> 1)),
+                         odd ? make_float4(g0, g1, B0, B1) : make_float4(A0, A1, g0, g1));
+              }
+            } else {
+              if (np[e]) {
+                const long long R = (long long)t.t0 * p.g.G + t.j * 2 * kHalf + hf * kHalf + row[e];
+                const long long pt = R / a.pre.rows;
+                const PagedItemParts pp((pt * p.g.nkv + cur.h) * a.pre.tiles, a.pre.tiles,
+                                        a.pre.upc);
+                const int pr = (int)(R - pt * a.pre.rows);
+                const float ref = mt[e] == -INFINITY ? 0.f : mt[e];
+#pragma unroll
+                for (int b = 0; b < 4; ++b) {
+                  o[4 * b + 2 * e] *= own[e];
+                  o[4 * b + 2 * e + 1] *= own[e];
+                }
+                for (int k = 0; k < np[e]; ++k) {
+                  const long long at = pp.slot(k) * a.pre.rows + pr;
+                  const float f = ex2(__ldcg(a.pre.ml + at).x - ref);
+#pragma unroll
+                  for (int b = 0; b < 4; ++b) {
+                    const float2 v =
+                        __ldcg(reinterpret_cast<const float2*>(a.pre.o + at * D + c + 8 * b + 2 * q4));
+                    o[4 * b + 2 * e] = fmaf(v.x, f, o[4 * b + 2 * e]);
+                    o[4 * b + 2 * e + 1] = fmaf(v.y, f, o[4 * b + 2 * e + 1]);
+                  }
+                }
+              }
+              uint32_t w[4];
+#pragma unroll
+              for (int b = 0; b < 4; ++b)
+                w[b] = pack2<T>(o[4 * b + 2 * e] * inv[e], o[4 * b + 2 * e + 1] * inv[e]);
+              quad_transpose(w, q4);  // lane q: the 8 columns of octet q
+              if (row[e] >= 0)
+                *reinterpret_cast<uint4*>(static_cast<T*>(p.out) + orow[e] * D + c + 8 * q4) =
+                    make_uint4(w[0], w[1], w[2], w[3]);
+            }
           }
         }
-        if (mine_row && p.lse)
-          p.lse[orow] = mt == -INFINITY ? -INFINITY : (mt + log2f(lt)) * 0.69314718055994531f;
+      }
+      if (!PRE && !whole && first == 0 && tid == 0) {
+        TcMeta x;
+        x.i0 = cur.i0;
+        x.upc = upc;
+        x.tiles = t.tiles;
+        x.t0 = t.t0;
+        x.p0 = t.p0;
+        x.rows = t.rows;
+        x.j = t.j;
+        x.h = cur.h;
+        a.meta[blockIdx.x] = x;
       }
       tc05_fence_before();  // O is read before the next item's first product
       __syncwarp();
@@ -714,78 +791,108 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const __grid_co
   } else {
     // ---------------------------------------------------------------- mma --
     set_regs_down<64>();
-    if (warp == 12 && lane == 0) {
+    // The whole warp walks (its operands then lie in uniform registers); one
+    // elected thread issues.
+    if (__shfl_sync(~0u, warp, 0) == 12) {
       constexpr uint32_t id_s = idesc_kind_f16(kIsBf16<T>, kHalf, kBN);
       constexpr uint32_t id_o = idesc_kind_f16(kIsBf16<T>, kHalf, D) | (1u << 16);  // B is N-major
-      TcCursor<PRE> cur = s_cur;
+      TcCursor<PRE>& cur = s_wcur[8];
+      if (lane == 0) cur = s_cur;
+      __syncwarp();
+      const bool leader = elect_one();
+      // descriptors of slot 0 and of Q; addresses count in 16 bytes
+      const uint64_t dk0 = smem_desc_k_sw128(skv, 1024), dq0 = smem_desc_k_sw128(sq, 1024);
+      const uint64_t dv0 = smem_desc_mn_sw128(skv, kBN * 128, 1024);
       RingPos ring(0, S::SLOTS);
       uint32_t items = 0, n_tiles[2] = {0, 0};
-      bool acc[2] = {false, false};
-      bool fresh = true;
-      bool pend = false;  // half 1's O += P V of the last tile is still to come
-      int pend_slot = 0;
       auto scores = [&](int h, int slot) {
-        const uint32_t k0 = skv + slot * S::TILE, q0 = sq + h * S::TILE;
+        if (leader) {
+          const uint64_t dk = dk0 + slot * (S::TILE / 16), dq = dq0 + h * (S::TILE / 16);
 #pragma unroll
-        for (int x = 0; x < D / 16; ++x) {
-          const uint32_t off = (x >> 2) * (kBN * 128) + (x & 3) * 32;
-          tc05_mma_f16(tmem + S::S_COL + h * kBN, smem_desc_k_sw128(q0 + off, 1024),
-                       smem_desc_k_sw128(k0 + off, 1024), id_s, x > 0);
+          for (int x = 0; x < D / 16; ++x) {
+            const uint32_t off = ((x >> 2) * (kBN * 128) + (x & 3) * 32) / 16;
+            tc05_mma_f16(tmem + S::S_COL + h * kBN, dq + off, dk + off, id_s, x > 0);
+          }
+          tc05_commit(&s_sfull[h]);
         }
-        tc05_commit(&s_sfull[h]);
+        __syncwarp();
       };
-      auto values = [&](int h, int slot) {
+      // O of half h (+)= P V; frees the slot where it is V's last reader
+      auto values = [&](int h, int slot, bool acc, bool free_slot) {
         wait_bar(&s_pfull[h], n_tiles[h] & 1, err);
-        tc05_fence_after();
-        const uint32_t v0 = skv + slot * S::TILE;
-#pragma unroll
-        for (int x = 0; x < kBN / 16; ++x)
-          tc05_mma_f16_ts(tmem + S::O_COL + h * D, tmem + S::S_COL + h * kBN + x * 8,
-                          smem_desc_mn_sw128(v0 + x * 16 * 128, kBN * 128, 1024), id_o,
-                          acc[h] || x > 0);
-        acc[h] = true;
         ++n_tiles[h];
-        tc05_commit(&s_ofull[h]);
+        tc05_fence_after();
+        if (leader) {
+          const uint64_t dv = dv0 + slot * (S::TILE / 16);
+#pragma unroll
+          for (int x = 0; x < kBN / 16; ++x)
+            tc05_mma_f16_ts(tmem + S::O_COL + h * D, tmem + S::S_COL + h * kBN + x * 8,
+                            dv + x * (16 * 128 / 16), id_o, acc || x > 0);
+          tc05_commit(&s_ofull[h]);
+          if (free_slot) tc05_commit(&s_empty[slot]);
+        }
+        __syncwarp();
       };
       while (cur.u < u1) {
-        const int base = cur.t.base(cur.tile);
-        const bool act0 = tile_active(cur.t.half[0], base), act1 = tile_active(cur.t.half[1], base);
-        if (fresh) {
-          wait_bar(&s_qfull, items & 1, err);
-          fence_proxy_async_smem();  // the copies wrote as ordinary stores
-          acc[0] = acc[1] = false;
-          ++items;
+        const PagedRange h0 = cur.t.half[0], h1 = cur.t.half[1];
+        const int ns = cur.t.ns, skip = cur.t.skip, first = cur.tile;
+        const int count = (int)min((long long)(cur.t.tiles - first), u1 - cur.u);
+        wait_bar(&s_qfull, items & 1, err);
+        ++items;
+        fence_proxy_async_smem();  // the copies wrote as ordinary stores
+        bool acc0 = false, acc1 = false;
+        bool pend = false;  // half 1's O += P V of the last tile is still to come
+        int pend_slot = 0;
+#pragma unroll 1
+        for (int tile = first; tile < first + count; ++tile) {
+          const int base = (tile < ns ? tile : tile + skip) * kBN;
+          const bool act0 = tile_active(h0, base), act1 = tile_active(h1, base);
+          const bool last = tile + 1 == first + count;
+          const int kslot = ring.slot;
+          wait_bar(&s_full[kslot], ring.phase, err);
+          ring.next(S::SLOTS);
+          fence_proxy_async_smem();
+          tc05_fence_after();
+          if (act0) scores(0, kslot);
+          if (pend) {
+            values(1, pend_slot, acc1, true);
+            acc1 = true;
+            pend = false;
+          }
+          if (act1) scores(1, kslot);
+          if (leader) {
+            tc05_commit(&s_empty[kslot]);
+            if (last) tc05_commit(&s_qempty);
+          }
+          __syncwarp();
+          const int vslot = ring.slot;
+          wait_bar(&s_full[vslot], ring.phase, err);
+          ring.next(S::SLOTS);
+          fence_proxy_async_smem();
+          tc05_fence_after();
+          if (act0) {
+            values(0, vslot, acc0, !act1);
+            acc0 = true;
+          }
+          if (act1 && !last) {
+            pend = true;
+            pend_slot = vslot;
+          } else if (act1) {
+            values(1, vslot, acc1, true);
+          } else if (!act0) {
+            if (leader) tc05_commit(&s_empty[vslot]);
+            __syncwarp();
+          }
         }
-        const int kslot = ring.slot;
-        wait_bar(&s_full[kslot], ring.phase, err);
-        fence_proxy_async_smem();
-        tc05_fence_after();
-        ring.next(S::SLOTS);
-        if (act0) scores(0, kslot);
-        if (pend) {
-          values(1, pend_slot);
-          tc05_commit(&s_empty[pend_slot]);
-          pend = false;
+        if (lane == 0) {
+          cur.u += count - 1;
+          cur.tile += count - 1;
+          cur.next(p, u1);
         }
-        if (act1) scores(1, kslot);
-        tc05_commit(&s_empty[kslot]);
-        const int vslot = ring.slot;
-        wait_bar(&s_full[vslot], ring.phase, err);
-        fence_proxy_async_smem();
-        tc05_fence_after();
-        ring.next(S::SLOTS);
-        fresh = cur.next(p, u1);
-        if (fresh) tc05_commit(&s_qempty);
-        if (act0) values(0, vslot);
-        if (act1 && !fresh) {
-          pend = true;
-          pend_slot = vslot;
-        } else {
-          if (act1) values(1, vslot);
-          tc05_commit(&s_empty[vslot]);
-        }
+        __syncwarp();
       }
-      tc05_commit(&s_done);
+      if (leader) tc05_commit(&s_done);
+      __syncwarp();
       wait_bar(&s_done, 0, err);
     }
   }
@@ -890,5 +997,5 @@ bool cf::paged_tc_launch(int dtype, const PagedAttnParams& p, const PagedSplit& 
   a.slots = (int)((long long)p.n_tokens * p.g.G / kTcRows) + p.batch;
   void* args[] = {&a};
   if (!launch_pdl(f.main, dim3(ws.grid), kTcThreads, f.smem, st, args)) return false;
-  return prefix || launch_pdl(f.join, dim3(ws.grid, 8), 256, 0, st, args);
+  return prefix || launch_pdl(f.join, dim3(ws.grid, 16), 256, 0, st, args);
 }
