@@ -150,23 +150,12 @@ __device__ __forceinline__ void cp_wait() {
 // items (a sequence or row tile and a KV head) form one line; block c takes
 // units [c * upc, (c + 1) * upc).  An item that lies in several blocks leaves
 // one partial state (o not normalised, running maximum in base 2, sum) per
-// block, in slot 2c where it is the block's first item and in 2c + 1 else.
+// block, in slot 2c where it began in an earlier block and in 2c + 1 where it
+// begins in this one.
 struct PagedParts {
   float* o;     // [slots][rows][D]
   float2* ml;   // [slots][rows]
   int* tickets; // one per item: partial states written so far (0 between calls)
-};
-
-// The shared prefix's partial states, as the kernel that reads the sequences'
-// own keys finds them: row R = token * G + (head in the KV head's group) is
-// row R % rows of tile R / rows, and item tile * nkv + kv head has `tiles`
-// units.  rows == 0: there is no prefix.
-struct PagedPrefixParts {
-  const float* o;
-  const float2* ml;
-  int rows;
-  int tiles;
-  long long upc;
 };
 
 __device__ __forceinline__ void pdl_wait() {
@@ -176,15 +165,38 @@ __device__ __forceinline__ void pdl_trigger() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 }
 
+// a / b, in 32 bits where both fit (a 64-bit division is a long chain).
+__device__ __forceinline__ long long div_units(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return (long long)((uint32_t)a / (uint32_t)b);
+  return a / b;
+}
+
 // Partial states of one item: the blocks first .. first + n - 1.
 struct PagedItemParts {
   long long i0, upc, first;
   int n;
   __device__ __forceinline__ PagedItemParts(long long i0_, long long tiles, long long upc_)
-      : i0(i0_), upc(upc_), first(i0_ / upc_), n((int)((i0_ + tiles - 1) / upc_ - i0_ / upc_) + 1) {}
+      : i0(i0_), upc(upc_), first(div_units(i0_, upc_)) {
+    n = (int)(div_units(i0_ + tiles - 1, upc_) - first) + 1;
+  }
   __device__ __forceinline__ long long slot(int k) const {
     const long long c = first + k;
     return 2 * c + (c * upc >= i0 ? 0 : 1);
+  }
+};
+
+// The shared prefix's partial states, as the kernel that reads the sequences'
+// own keys finds them: row R = token * G + (head in the KV head's group) is
+// row R % rows of tile R / rows, and item tile * nkv + kv head has `tiles`
+// units behind item_cost empty ones.  rows == 0: there is no prefix.
+struct PagedPrefixParts {
+  const float* o;
+  const float2* ml;
+  int rows;
+  int tiles, item_cost;
+  long long upc;
+  __device__ __forceinline__ PagedItemParts item(long long index) const {
+    return PagedItemParts(index * (tiles + item_cost) + item_cost, tiles, upc);
   }
 };
 
@@ -209,9 +221,9 @@ struct PagedState4 {
 template <int D>
 __device__ __forceinline__ void paged_join_prefix(PagedState4& s, const PagedPrefixParts& x,
                                                   long long R, int kvh, int nkv, int col) {
-  const long long tile = R / x.rows;
+  const long long tile = div_units(R, x.rows);
   const int row = (int)(R - tile * x.rows);
-  const PagedItemParts parts((tile * nkv + kvh) * x.tiles, x.tiles, x.upc);
+  const PagedItemParts parts(x.item(tile * nkv + kvh));
 #pragma unroll 4
   for (int k = 0; k < parts.n; ++k) {
     const long long at = parts.slot(k) * x.rows + row;

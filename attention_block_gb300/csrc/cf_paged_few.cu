@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(kFewThreads, kBlocksPerSm)
     total += s_scan[w];
     top = max(top, s_max[w]);
   }
-  const long long upc = max((total + max_blocks - 1) / max_blocks,
+  const long long upc = max(div_units(total + max_blocks - 1, max_blocks),
                             (long long)((top + kMaxParts - 1) / kMaxParts));
   const long long u0 = blockIdx.x * upc, u1 = min(total, u0 + upc);
   if (u0 >= u1) return;
@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(kFewThreads, kBlocksPerSm)
   cur.u = u0;
   {
     const long long off = u0 - s_start_i0;
-    cur.h = (int)(off / cur.w.tiles);
+    cur.h = (int)div_units(off, cur.w.tiles);
     cur.tile = (int)(off - (long long)cur.h * cur.w.tiles);
     cur.i0 = u0 - cur.tile;
   }
@@ -471,6 +471,7 @@ PagedPrefixParts cf::paged_few_prefix(const PagedAttnParams& p, const PagedSplit
   x.ml = ws.ml;
   x.rows = kFewRows;
   x.tiles = (p.prefix_len + TK - 1) / TK;
+  x.item_cost = 0;
   const long long total = (long long)x.tiles * p.g.nkv;
   x.upc = std::max((total + ws.grid - 1) / ws.grid,
                    (long long)((x.tiles + kMaxParts - 1) / kMaxParts));

@@ -42,6 +42,7 @@ constexpr int kTcThreads = 512;
 constexpr int kCopyThreads = 128;
 constexpr int kHalf = 128;     // rows of a half
 constexpr int kBN = 128;       // positions of a tile
+constexpr int kItemCost = 3;   // what an item costs beside its tiles, in tiles
 constexpr float kGrow = 8.0f;  // log2 of the growth that forces a rescale
 
 template <int D>
@@ -205,8 +206,7 @@ constexpr bool kIsBf16<__nv_bfloat16> = true;
 
 // Starts a load into L1 without waiting for it.
 __device__ __forceinline__ void prefetch_line(const int* at) {
-  int v;
-  asm volatile("ld.global.ca.u32 %0, [%1];" : "=r"(v) : "l"(at));
+  asm volatile("{\n\t.reg .u32 v;\n\tld.global.ca.u32 v, [%0];\n\t}" ::"l"(at));
 }
 
 template <int N>
@@ -279,17 +279,20 @@ __device__ __forceinline__ bool tile_active(const PagedRange& r, int base) {
   return r.hi > r.lo && ((base < r.hi && base + kBN > r.lo) || base < r.sink);
 }
 
-// A walk over a block's units: row tiles, KV heads, key tiles.
+// A walk over a block's units: row tiles, KV heads, key tiles.  On the line of
+// units an item has kItemCost empty ones before its tiles, so that blocks with
+// many small items get fewer of them.
 template <bool PRE>
 struct TcCursor {
   RowTile t;
   int h, tile;
-  long long u, i0;
+  long long u, i0;  // this unit, the item's first
   // true when the unit left was the last of its item in this walk
   __device__ __forceinline__ bool next(const PagedAttnParams& p, long long end) {
     ++u;
     if (++tile < t.tiles) return u >= end;
     tile = 0;
+    u += kItemCost;
     i0 = u;
     if (++h < p.g.nkv) return true;
     h = 0;
@@ -325,15 +328,20 @@ struct TcArgs {
   int slots;  // upper bound on the row tiles' numbers
 };
 
-template <typename T, int D, bool PRE>
+// What a launch attends to: the sequences' own keys; the shared prefix; own
+// keys, with the prefix's partial states joined to the results.
+enum TcMode { kOwn = 0, kPrefix = 1, kOwnAfterPrefix = 2 };
+
+template <typename T, int D, int MODE>
 __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const __grid_constant__ TcArgs a) {
+  constexpr bool PRE = MODE == kPrefix, JOIN = MODE == kOwnAfterPrefix;
   using S = TcShape<D>;
   constexpr int C = D / 8;  // 16-byte chunks of a row
   const PagedAttnParams& p = a.p;
   extern __shared__ uint8_t smem_raw[];
   __shared__ long long s_scan[kTcThreads / 32];
   __shared__ TcCursor<PRE> s_cur;
-  __shared__ TcCursor<PRE> s_wcur[9];  // places of the softmax warps and of the issuing one
+  __shared__ TcCursor<PRE> s_wcur[13];  // each working warp's place: too much for registers
   __shared__ __align__(8) uint64_t s_full[S::SLOTS], s_empty[S::SLOTS];
   __shared__ __align__(8) uint64_t s_qfull, s_qempty, s_done;
   __shared__ __align__(8) uint64_t s_sfull[2], s_pfull[2], s_ofull[2];
@@ -409,7 +417,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const __grid_co
   };
   long long mine = 0;
   walk([&](const RowTile& t) {
-    mine += (long long)t.tiles * p.g.nkv;
+    mine += (long long)(t.tiles + kItemCost) * p.g.nkv;
     return false;
   });
   long long incl = mine;
@@ -426,21 +434,22 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const __grid_co
     if (w < warp) before += s_scan[w];
     total += s_scan[w];
   }
-  const long long upc = PRE ? a.pre.upc : (total + gridDim.x - 1) / gridDim.x;
+  const long long upc = PRE ? a.pre.upc : div_units(total + gridDim.x - 1, gridDim.x);
   const long long u0 = blockIdx.x * upc, u1 = min(total, u0 + upc);
   if (!PRE && tid == 0) a.meta[blockIdx.x].tiles = 0;
   if (u0 >= u1) return;
   if (before <= u0 && u0 < before + mine) {
     long long at = before;
     walk([&](const RowTile& t) {
-      const long long n = (long long)t.tiles * p.g.nkv;
+      const int len = t.tiles + kItemCost;
+      const long long n = (long long)len * p.g.nkv;
       if (u0 < at + n) {
         TcCursor<PRE> c;
         c.t = t;
-        c.u = u0;
-        c.h = (int)((u0 - at) / t.tiles);
-        c.tile = (int)((u0 - at) - (long long)c.h * t.tiles);
-        c.i0 = u0 - c.tile;
+        c.h = (int)div_units(u0 - at, len);
+        c.i0 = at + (long long)c.h * len + kItemCost;
+        c.tile = (int)max(0LL, u0 - c.i0);
+        c.u = c.i0 + c.tile;
         s_cur = c;
         return true;
       }
@@ -555,11 +564,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const __grid_co
             }
             tmem_st16(ts + 16 * k, w);
           }
-          l = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
           tmem_wait_st();
           tc05_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&s_pfull[hf]);
+          l = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
           some = true;
           ++n_tiles;
         }
@@ -571,10 +580,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const __grid_co
         tc05_fence_after();
       }
       const float m2 = m * sc;  // base 2
-      const PagedItemParts parts(cur.i0, t.tiles, upc);
       const bool part = PRE || !whole;
+      // this block's slot for the item (PagedParts)
       const long long prow0 =
-          part ? parts.slot((int)(blockIdx.x - parts.first)) * (2 * kHalf) + hf * kHalf : 0;
+          (2 * (long long)blockIdx.x + (u0 >= cur.i0 ? 0 : 1)) * (2 * kHalf) + hf * kHalf;
       if (part && gr < t.rows) __stcg(a.ml + prow0 + r, make_float2(m2, l));
       const int q4 = lane & 3;
 #pragma unroll 1
@@ -596,9 +605,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const __grid_co
           np[e] = 0;
           const int i = rg / p.g.G;
           orow[e] = ((long long)t.t0 + i) * p.g.nq + cur.h * p.g.G + rg - i * p.g.G;
-          if (!part && a.pre.rows && there && t.p0 + i >= 0) {
-            const long long R = (long long)t.t0 * p.g.G + rg, pt = R / a.pre.rows;
-            const PagedItemParts pp((pt * p.g.nkv + cur.h) * a.pre.tiles, a.pre.tiles, a.pre.upc);
+          if (JOIN && !part && there && t.p0 + i >= 0) {
+            const long long R = (long long)t.t0 * p.g.G + rg, pt = div_units(R, a.pre.rows);
+            const PagedItemParts pp(a.pre.item(pt * p.g.nkv + cur.h));
             const int pr = (int)(R - pt * a.pre.rows);
             np[e] = pp.n;
             for (int k = 0; k < pp.n; ++k)
@@ -617,15 +626,20 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const __grid_co
                 mt[e] == -INFINITY ? -INFINITY : (mt[e] + log2f(rl)) * 0.69314718055994531f;
         }
 #pragma unroll 1
-        for (int c = 0; c < D; c += 32) {
-          float o[16];
-          if (some) {
-            tmem_ld_frag(to + ((uint32_t)(16 * hh) << 16) + c, o);
-            tmem_wait_ld();
-          } else {
+        for (int c64 = 0; c64 < D; c64 += 64) {
+        float o2[2][16];
+        if (some) {
+          tmem_ld_frag(to + ((uint32_t)(16 * hh) << 16) + c64, o2[0]);
+          tmem_ld_frag(to + ((uint32_t)(16 * hh) << 16) + c64 + 32, o2[1]);
+          tmem_wait_ld();
+        } else {
 #pragma unroll
-            for (int x = 0; x < 16; ++x) o[x] = 0.f;
-          }
+          for (int x = 0; x < 32; ++x) o2[x >> 4][x & 15] = 0.f;
+        }
+#pragma unroll
+        for (int y = 0; y < 2; ++y) {
+          const int c = c64 + 32 * y;
+          float(&o)[16] = o2[y];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             if (part) {
@@ -644,11 +658,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const __grid_co
                          odd ? make_float4(g0, g1, B0, B1) : make_float4(A0, A1, g0, g1));
               }
             } else {
-              if (np[e]) {
+              if (JOIN && np[e]) {
                 const long long R = (long long)t.t0 * p.g.G + t.j * 2 * kHalf + hf * kHalf + row[e];
-                const long long pt = R / a.pre.rows;
-                const PagedItemParts pp((pt * p.g.nkv + cur.h) * a.pre.tiles, a.pre.tiles,
-                                        a.pre.upc);
+                const long long pt = div_units(R, a.pre.rows);
+                const PagedItemParts pp(a.pre.item(pt * p.g.nkv + cur.h));
                 const int pr = (int)(R - pt * a.pre.rows);
                 const float ref = mt[e] == -INFINITY ? 0.f : mt[e];
 #pragma unroll
@@ -679,6 +692,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const __grid_co
             }
           }
         }
+        }
       }
       if (!PRE && !whole && first == 0 && tid == 0) {
         TcMeta x;
@@ -705,7 +719,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const __grid_co
     // ------------------------------------------------------------- copies --
     set_regs_down<80>();
     const int lw = warp - 8;  // rows 32 lw .. 32 lw + 31 of every tile
-    TcCursor<PRE> cur = s_cur;
+    TcCursor<PRE>& cur = s_wcur[warp];
+    if (lane == 0) cur = s_cur;
+    __syncwarp();
     constexpr int RP = 32 / C;                      // rows of one copy instruction
     const int r0 = lane / C, c0 = lane % C;
     const uint32_t d0 = (uint32_t)((c0 >> 3) * (kBN * 128) + (lw * 32 + r0) * 128);
@@ -725,7 +741,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const __grid_co
           }
         }
       } else {
-#pragma unroll 4
+#pragma unroll 8
         for (int x = 0; x < C; ++x) {
           const int64_t o = __shfl_sync(~0u, off, x * RP + r0);
           cp16(dst + d0 + x * RP * 128 + (x0 ^ (((x * RP) & 7) << 4)),
@@ -753,20 +769,19 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const __grid_co
     bool fresh = true;
     look_up();
     while (cur.u < u1) {
-      if (fresh) {
+      // a new item's Q: this lane's rows
+      int64_t qoff[2] = {-1, -1};
+      const bool new_q = fresh;
+      if (new_q) {
         const RowTile& t = cur.t;
-        if (items) wait_bar(&s_qempty, (items - 1) & 1, err);
-#pragma unroll 1
+#pragma unroll
         for (int h = 0; h < 2; ++h) {
           const int gr = t.j * 2 * kHalf + h * kHalf + lw * 32 + lane;
           const int i = gr / p.g.G;
-          int64_t off = -1;
           if (gr < t.rows)
-            off = ((int64_t)(t.t0 + i) * p.q_stride + (int64_t)(cur.h * p.g.G + gr - i * p.g.G) * D) * 2;
-          copy(sq + h * S::TILE, qbase, off, false);
+            qoff[h] =
+                ((int64_t)(t.t0 + i) * p.q_stride + (int64_t)(cur.h * p.g.G + gr - i * p.g.G) * D) * 2;
         }
-        cp_arrive(&s_qfull);
-        ++items;
       }
       int64_t off = -1;
       if (f_pos >= 0) {
@@ -777,7 +792,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const __grid_co
                  (int64_t)(f_pos & p.g.page_mask) * p.g.slot_stride +
                  (int64_t)cur.h * p.g.head_stride) * 2;
       }
-      fresh = cur.next(p, u1);
+      __syncwarp();
+      if (lane == 0) fresh = cur.next(p, u1);
+      fresh = __shfl_sync(~0u, fresh, 0);
       look_up();
 #pragma unroll 1
       for (int kv = 0; kv < 2; ++kv) {
@@ -786,6 +803,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const __grid_co
         cp_arrive(&s_full[ring.slot]);
         ring.next(S::SLOTS);
         ++use;
+      }
+      // Q last: its buffer is free only when the previous item's scores are done
+      if (new_q) {
+        if (items) wait_bar(&s_qempty, (items - 1) & 1, err);
+        copy(sq, qbase, qoff[0], false);
+        copy(sq + S::TILE, qbase, qoff[1], false);
+        cp_arrive(&s_qfull);
+        ++items;
       }
     }
   } else {
@@ -796,7 +821,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const __grid_co
     if (__shfl_sync(~0u, warp, 0) == 12) {
       constexpr uint32_t id_s = idesc_kind_f16(kIsBf16<T>, kHalf, kBN);
       constexpr uint32_t id_o = idesc_kind_f16(kIsBf16<T>, kHalf, D) | (1u << 16);  // B is N-major
-      TcCursor<PRE>& cur = s_wcur[8];
+      TcCursor<PRE>& cur = s_wcur[12];
       if (lane == 0) cur = s_cur;
       __syncwarp();
       const bool leader = elect_one();
@@ -820,7 +845,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const __grid_co
       // O of half h (+)= P V; frees the slot where it is V's last reader
       auto values = [&](int h, int slot, bool acc, bool free_slot) {
         wait_bar(&s_pfull[h], n_tiles[h] & 1, err);
-        ++n_tiles[h];
         tc05_fence_after();
         if (leader) {
           const uint64_t dv = dv0 + slot * (S::TILE / 16);
@@ -832,6 +856,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const __grid_co
           if (free_slot) tc05_commit(&s_empty[slot]);
         }
         __syncwarp();
+        ++n_tiles[h];
       };
       while (cur.u < u1) {
         const PagedRange h0 = cur.t.half[0], h1 = cur.t.half[1];
@@ -915,7 +940,7 @@ __global__ void __launch_bounds__(256) paged_tc_join_kernel(const __grid_constan
   for (int e = blockIdx.y * 256 + threadIdx.x; e < rows * C4; e += gridDim.y * 256) {
     const int r = e / C4, col = (e - r * C4) * 4;
     PagedState4 s{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-#pragma unroll 4
+#pragma unroll 8
     for (int k = 0; k < parts.n; ++k) {
       const long long at = parts.slot(k) * (2 * kHalf) + r;
       const float2 ml = __ldcg(a.ml + at);
@@ -934,14 +959,15 @@ struct TcFns {
   int smem;
 };
 template <typename T, int D>
-TcFns fns_td(bool prefix) {
-  return TcFns{prefix ? (const void*)&paged_tc_kernel<T, D, true>
-                      : (const void*)&paged_tc_kernel<T, D, false>,
-               (const void*)&paged_tc_join_kernel<T, D>, TcShape<D>::SMEM};
+TcFns fns_td(int mode) {
+  const void* main = mode == kPrefix ? (const void*)&paged_tc_kernel<T, D, kPrefix>
+                     : mode == kOwn  ? (const void*)&paged_tc_kernel<T, D, kOwn>
+                                     : (const void*)&paged_tc_kernel<T, D, kOwnAfterPrefix>;
+  return TcFns{main, (const void*)&paged_tc_join_kernel<T, D>, TcShape<D>::SMEM};
 }
-TcFns tc_fns(int dtype, int d, bool prefix) {
-  if (dtype == CF_F16) return d == 64 ? fns_td<__half, 64>(prefix) : fns_td<__half, 128>(prefix);
-  return d == 64 ? fns_td<__nv_bfloat16, 64>(prefix) : fns_td<__nv_bfloat16, 128>(prefix);
+TcFns tc_fns(int dtype, int d, int mode) {
+  if (dtype == CF_F16) return d == 64 ? fns_td<__half, 64>(mode) : fns_td<__half, 128>(mode);
+  return d == 64 ? fns_td<__nv_bfloat16, 64>(mode) : fns_td<__nv_bfloat16, 128>(mode);
 }
 
 bool launch_pdl(const void* fn, dim3 grid, int threads, int smem, cudaStream_t st, void** args) {
@@ -961,8 +987,8 @@ bool launch_pdl(const void* fn, dim3 grid, int threads, int smem, cudaStream_t s
 }  // namespace
 
 int cf::paged_tc_grid(int dtype, int head_dim, int sm_count) {
-  for (int prefix = 0; prefix < 2; ++prefix) {
-    const TcFns f = tc_fns(dtype, head_dim, prefix != 0);
+  for (int mode = kOwn; mode <= kOwnAfterPrefix; ++mode) {
+    const TcFns f = tc_fns(dtype, head_dim, mode);
     if (cudaFuncSetAttribute(f.main, cudaFuncAttributeMaxDynamicSharedMemorySize, f.smem) !=
         cudaSuccess) {
       cudaGetLastError();
@@ -980,14 +1006,15 @@ PagedPrefixParts cf::paged_tc_prefix(const PagedAttnParams& p, const PagedSplit&
   x.ml = ws.ml;
   x.rows = kTcRows;
   x.tiles = (p.prefix_len + kBN - 1) / kBN;
+  x.item_cost = kItemCost;
   const long long row_tiles = ((long long)p.n_tokens * p.g.G + kTcRows - 1) / kTcRows;
-  x.upc = std::max<long long>(1, (row_tiles * p.g.nkv * x.tiles + ws.grid - 1) / ws.grid);
+  x.upc = std::max<long long>(1, (row_tiles * p.g.nkv * (x.tiles + kItemCost) + ws.grid - 1) / ws.grid);
   return x;
 }
 
 bool cf::paged_tc_launch(int dtype, const PagedAttnParams& p, const PagedSplit& ws, bool prefix,
                          const PagedPrefixParts& pre, cudaStream_t st) {
-  const TcFns f = tc_fns(dtype, p.g.D, prefix);
+  const TcFns f = tc_fns(dtype, p.g.D, prefix ? kPrefix : pre.rows ? kOwnAfterPrefix : kOwn);
   TcArgs a;
   a.p = p;
   a.pre = pre;
@@ -997,5 +1024,5 @@ bool cf::paged_tc_launch(int dtype, const PagedAttnParams& p, const PagedSplit& 
   a.slots = (int)((long long)p.n_tokens * p.g.G / kTcRows) + p.batch;
   void* args[] = {&a};
   if (!launch_pdl(f.main, dim3(ws.grid), kTcThreads, f.smem, st, args)) return false;
-  return prefix || launch_pdl(f.join, dim3(ws.grid, 16), 256, 0, st, args);
+  return prefix || launch_pdl(f.join, dim3(ws.grid, 32), 256, 0, st, args);
 }
