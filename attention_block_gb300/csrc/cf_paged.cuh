@@ -146,18 +146,26 @@ __device__ __forceinline__ void cp_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// How a kernel's work is cut over its blocks.  The units (key tiles) of all
-// items (a sequence or row tile and a KV head) form one line; block c takes
-// units [c * upc, (c + 1) * upc).  An item that lies in several blocks leaves
+// How a kernel's work is cut.  The units (key tiles) of all items (a sequence
+// or row tile and a KV head) form one line, cut into pieces: piece c takes
+// units [c * upc, (c + 1) * upc).  An item that lies in several pieces leaves
 // one partial state (o not normalised, running maximum in base 2, sum) per
-// block, in slot 2c where it began in an earlier block and in 2c + 1 where it
-// begins in this one.
+// piece, in slot 2c where it began in an earlier piece and in 2c + 1 where it
+// begins in this one.  Where states are wanted of every item (a prefix's, and
+// own keys' before the prefix is joined), one that lies within a piece has
+// rows of its own from state_base on: the prefix's at token * nq + head; own
+// ones too, or at 16 rows per (sequence, KV head) where those are fewer.
 struct PagedParts {
-  float* o;     // [slots][rows][D]
-  float2* ml;   // [slots][rows]
-  int* tickets; // one per item: partial states written so far (0 between calls)
+  float* o;              // [rows][D]: slots of a fixed number of rows, then single rows
+  float2* ml;            // [rows]
+  long long state_base;
+  int by_token;
 };
 
+// Starts a load into L1 without waiting for it.
+__device__ __forceinline__ void prefetch_line(const void* at) {
+  asm volatile("{\n\t.reg .u32 v;\n\tld.global.ca.u32 v, [%0];\n\t}" ::"l"(at));
+}
 __device__ __forceinline__ void pdl_wait() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
@@ -171,7 +179,7 @@ __device__ __forceinline__ long long div_units(long long a, long long b) {
   return a / b;
 }
 
-// Partial states of one item: the blocks first .. first + n - 1.
+// Partial states of one item: the pieces first .. first + n - 1.
 struct PagedItemParts {
   long long i0, upc, first;
   int n;
@@ -185,29 +193,48 @@ struct PagedItemParts {
   }
 };
 
-// The shared prefix's partial states, as the kernel that reads the sequences'
-// own keys finds them: row R = token * G + (head in the KV head's group) is
-// row R % rows of tile R / rows, and item tile * nkv + kv head has `tiles`
-// units behind item_cost empty ones.  rows == 0: there is no prefix.
+// The shared prefix's states, as the kernels that join them to the sequences'
+// own find them: row R = token * G + (head in the KV head's group) is row
+// R % rows of tile R / rows, and item tile * nkv + kv head has `tiles` units
+// behind item_cost empty ones.  rows == 0: there is no prefix.
 struct PagedPrefixParts {
   const float* o;
   const float2* ml;
+  long long state_base;
   int rows;
   int tiles, item_cost;
   long long upc;
-  __device__ __forceinline__ PagedItemParts item(long long index) const {
-    return PagedItemParts(index * (tiles + item_cost) + item_cost, tiles, upc);
+};
+
+// Where one row's states of an item lie: row() of the arrays for part k < n.
+struct PagedRowParts {
+  PagedItemParts parts;
+  int rows, r, n;
+  long long state;
+  __device__ __forceinline__ PagedRowParts(const PagedItemParts& p, int rows_, int r_,
+                                           long long state_)
+      : parts(p), rows(rows_), r(r_), n(p.n), state(state_) {}
+  __device__ __forceinline__ long long row(int k) const {
+    return n == 1 ? state : parts.slot(k) * rows + r;
   }
 };
+__device__ __forceinline__ PagedRowParts paged_prefix_row(const PagedPrefixParts& x,
+                                                          const PagedGeom& g, long long token,
+                                                          int kvh, int gi) {
+  const long long R = token * g.G + gi, tile = div_units(R, x.rows);
+  const long long index = tile * g.nkv + kvh;
+  return PagedRowParts(
+      PagedItemParts(index * (x.tiles + x.item_cost) + x.item_cost, x.tiles, x.upc), x.rows,
+      (int)(R - tile * x.rows), x.state_base + token * g.nq + kvh * g.G + gi);
+}
 
 // Softmax state of 4 columns of a row, joined with another one.
 struct PagedState4 {
   float m, l;
   float4 o;
   __device__ __forceinline__ void join(float m2, float l2, const float4& o2) {
-    const float mn = fmaxf(m, m2);
-    if (mn == -INFINITY) return;
-    const float a = exp2f(m - mn), b = exp2f(m2 - mn);
+    const float mn = fmaxf(m, m2), ref = mn == -INFINITY ? 0.f : mn;
+    const float a = exp2f(m - ref), b = exp2f(m2 - ref);
     m = mn;
     l = l * a + l2 * b;
     o.x = o.x * a + o2.x * b;
@@ -217,19 +244,39 @@ struct PagedState4 {
   }
 };
 
-// Joins the prefix's states of one row's 4 columns at `col` into s.
+// Joins a row's states into s: the D / 4 lanes that share the row call it
+// together, each for its 4 columns at `col`.  Each lane fetches one part's
+// maximum and sum, so all parts' values are on their way at once.
 template <int D>
-__device__ __forceinline__ void paged_join_prefix(PagedState4& s, const PagedPrefixParts& x,
-                                                  long long R, int kvh, int nkv, int col) {
-  const long long tile = div_units(R, x.rows);
-  const int row = (int)(R - tile * x.rows);
-  const PagedItemParts parts(x.item(tile * nkv + kvh));
-#pragma unroll 4
-  for (int k = 0; k < parts.n; ++k) {
-    const long long at = parts.slot(k) * x.rows + row;
-    const float2 ml = __ldcg(x.ml + at);
-    const float4 o = __ldcg(reinterpret_cast<const float4*>(x.o + at * D + col));
-    s.join(ml.x, ml.y, o);
+__device__ __forceinline__ void paged_join_row(PagedState4& s, const float* o, const float2* ml,
+                                               const PagedRowParts& x, int col) {
+  constexpr int W = D / 4;
+  const int lane = threadIdx.x & 31, gl = lane % W;
+  const uint32_t mask = W == 32 ? ~0u : 0xffffu << (lane & 16);
+  for (int k0 = 0; k0 < x.n; k0 += W) {
+    float2 v = make_float2(-INFINITY, 0.f);
+    if (k0 + gl < x.n) v = __ldcg(ml + x.row(k0 + gl));
+    float mx = v.x;
+#pragma unroll
+    for (int d = W / 2; d >= 1; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(mask, mx, d));
+    const float mn = fmaxf(s.m, mx), ref = mn == -INFINITY ? 0.f : mn;
+    const float a = exp2f(s.m - ref), w = exp2f(v.x - ref);
+    float l = v.y * w;
+#pragma unroll
+    for (int d = W / 2; d >= 1; d >>= 1) l += __shfl_xor_sync(mask, l, d);
+    s.m = mn;
+    s.l = s.l * a + l;
+    s.o = make_float4(s.o.x * a, s.o.y * a, s.o.z * a, s.o.w * a);
+    const int n = min(W, x.n - k0);
+#pragma unroll 8
+    for (int k = 0; k < n; ++k) {
+      const float wk = __shfl_sync(mask, w, k, W);
+      const float4 y = __ldcg(reinterpret_cast<const float4*>(o + x.row(k0 + k) * D + col));
+      s.o.x = fmaf(y.x, wk, s.o.x);
+      s.o.y = fmaf(y.y, wk, s.o.y);
+      s.o.z = fmaf(y.z, wk, s.o.z);
+      s.o.w = fmaf(y.w, wk, s.o.w);
+    }
   }
 }
 
@@ -244,31 +291,74 @@ __device__ __forceinline__ void paged_store4(const PagedState4& s, void* out, fl
     lse[row] = s.m == -INFINITY ? -INFINITY : (s.m + log2f(s.l)) * 0.69314718055994531f;
 }
 
-// Host launchers (one translation unit each); false: the launch failed.
-struct PagedSplit {  // one kernel's part of a handle's workspace
-  float* o = nullptr;
-  float2* ml = nullptr;
-  int* tickets = nullptr;
-  void* meta = nullptr;
-  int grid = 0;  // resident blocks the kernel is cut for
+// Transposes w over a quad of lanes: lane q ends with word q of lanes 0..3.
+__device__ __forceinline__ void quad_transpose(uint32_t (&w)[4], int q) {
+  const bool a = q & 1, b = q & 2;
+#pragma unroll
+  for (int i = 0; i < 4; i += 2) {  // pairs (0, 1) and (2, 3)
+    const uint32_t x = __shfl_xor_sync(~0u, a ? w[i] : w[i + 1], 1);
+    if (a)
+      w[i] = x;
+    else
+      w[i + 1] = x;
+  }
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {  // pairs (0, 2) and (1, 3)
+    const uint32_t x = __shfl_xor_sync(~0u, b ? w[i] : w[i + 2], 2);
+    if (b)
+      w[i] = x;
+    else
+      w[i + 2] = x;
+  }
+}
+
+template <typename T>
+__device__ __forceinline__ uint32_t pack2(float a, float b);
+template <>
+__device__ __forceinline__ uint32_t pack2<__half>(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+template <>
+__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// What a launch attends to: the sequences' own keys; the shared prefix (it
+// leaves states only); own keys, joined with the prefix's states.
+enum PagedMode { kOwn = 0, kPrefix = 1, kOwnAfterPrefix = 2 };
+
+// An attention kernel's part of a handle's workspace.
+struct PagedSplit {
+  PagedParts parts;
+  void* list = nullptr;    // items whose parts a second kernel joins
+  int* counter = nullptr;  // words that are zero between calls
+  int grid = 0;            // resident blocks
 };
-// Rows (tokens x grouped heads) and resident blocks of the few-row kernel.
-constexpr int kFewRows = 16;
-int paged_few_grid(int dtype, int head_dim, int sm_count);
-// prefix: the call's tokens against the prefix alone, partial states only.
-bool paged_few_launch(int dtype, const PagedAttnParams& p, const PagedSplit& ws, bool prefix,
-                      const PagedPrefixParts& pre, cudaStream_t st);
-// How the few-row kernel cuts the prefix.
-PagedPrefixParts paged_few_prefix(const PagedAttnParams& p, const PagedSplit& ws);
+
+// Host launchers (one translation unit each); false: the launch failed.
 bool paged_append_launch(int dtype, const PagedAppendParams& p, int sm_count, cudaStream_t st);
 bool paged_attn_simple_launch(int dtype, const PagedAttnParams& p, cudaStream_t st);
 
-// The tensor-core kernel for many rows; the arguments as above.
+// The kernel for few rows (tokens x grouped heads), and the one on the fifth
+// generation's tensor cores for many.  grid: resident blocks, 0 on failure;
+// part_rows and list_bytes: workspace; launch with kPrefix: the call's tokens
+// against the prefix alone; prefix: how such a launch cuts it.
+constexpr int kFewRows = 16;
+int paged_few_grid(int dtype, int head_dim, int sm_count);
+long long paged_few_part_rows(int grid);
+size_t paged_few_list_bytes(long long items);
+PagedPrefixParts paged_few_prefix(const PagedAttnParams& p, const PagedSplit& ws);
+bool paged_few_launch(int dtype, const PagedAttnParams& p, const PagedSplit& ws, PagedMode mode,
+                      const PagedPrefixParts& pre, cudaStream_t st);
+
 constexpr int kTcRows = 256;
 int paged_tc_grid(int dtype, int head_dim, int sm_count);
-size_t paged_tc_meta_bytes(int grid);
-bool paged_tc_launch(int dtype, const PagedAttnParams& p, const PagedSplit& ws, bool prefix,
-                     const PagedPrefixParts& pre, cudaStream_t st);
+long long paged_tc_part_rows(int grid);
+size_t paged_tc_list_bytes(int grid);
 PagedPrefixParts paged_tc_prefix(const PagedAttnParams& p, const PagedSplit& ws);
+bool paged_tc_launch(int dtype, const PagedAttnParams& p, const PagedSplit& ws, PagedMode mode,
+                     const PagedPrefixParts& pre, cudaStream_t st);
 
 }  // namespace cf

@@ -2,6 +2,7 @@
 // handle and its workspace, and which kernel a call launches.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 #include <new>
@@ -147,19 +148,21 @@ int attention(cf_paged_handle* h, int32_t batch, int32_t n_tokens, int32_t max_q
   } else {
     PagedPrefixParts pre;
     std::memset(&pre, 0, sizeof(pre));
+    PagedMode mode = kOwn;
     ok = true;
     if (prefix_len > 0) {
+      mode = kOwnAfterPrefix;
       if ((int64_t)n_tokens * p.g.G <= kFewRows) {
         pre = paged_few_prefix(p, h->few_prefix);
-        ok = paged_few_launch(c.dtype, p, h->few_prefix, true, pre, st);
+        ok = paged_few_launch(c.dtype, p, h->few_prefix, kPrefix, pre, st);
       } else {
         pre = paged_tc_prefix(p, h->tc_prefix);
-        ok = paged_tc_launch(c.dtype, p, h->tc_prefix, true, pre, st);
+        ok = paged_tc_launch(c.dtype, p, h->tc_prefix, kPrefix, pre, st);
       }
     }
     if (ok)
-      ok = (int64_t)max_q * p.g.G <= kFewRows ? paged_few_launch(c.dtype, p, h->few, false, pre, st)
-                                              : paged_tc_launch(c.dtype, p, h->tc, false, pre, st);
+      ok = (int64_t)max_q * p.g.G <= kFewRows ? paged_few_launch(c.dtype, p, h->few, mode, pre, st)
+                                              : paged_tc_launch(c.dtype, p, h->tc, mode, pre, st);
   }
   if (!ok) {
     cudaGetLastError();
@@ -242,29 +245,37 @@ int cf_paged_create(const cf_paged_config* cfg, cf_paged_handle** out) {
     cudaGetLastError();
     return fail(CF_ERR_CUDA);
   }
-  // Workspace: the words that start at zero (error word, tickets), then the
-  // kernels' partial states.
   size_t bytes = 256;
   auto take = [&](size_t n) {
     const size_t at = bytes;
     bytes += (n + 255) & ~(size_t)255;
     return at;
   };
-  size_t zero = bytes, few_t = 0, few_at[2] = {0, 0};
-  const size_t row = (size_t)(c.head_dim + 2) * 4;  // o, m and l of a row
-  int few_grid = 0, tc_grid = 0;
-  size_t tc_at[2] = {0, 0}, meta_at = 0;
+  // The words that start at zero, then the lists, then two sets of states:
+  // of the sequences' own keys and of the prefix.  A call uses one attention
+  // kernel for each, so the kernels share them.
+  const size_t counters = take(16 * 4);
+  const size_t zero = bytes;
+  const int64_t all_rows = (int64_t)c.max_tokens * c.n_q_heads;
+  size_t few_list = 0, tc_list = 0, at_o[2] = {0, 0}, at_ml[2] = {0, 0};
+  const int64_t few_rows = (int64_t)c.max_batch * c.n_kv_heads * kFewRows;
+  int64_t slot_rows = 0;
   if (c.dtype != CF_F32) {
-    few_grid = paged_few_grid(c.dtype, c.head_dim, h->sm_count);
-    if (few_grid == 0) return fail(CF_ERR_CUDA);
-    few_t = take((size_t)c.max_batch * c.n_kv_heads * 4);
-    zero = bytes;
-    for (size_t& at : few_at) at = take((size_t)few_grid * 2 * kFewRows * row);
+    h->few.grid = paged_few_grid(c.dtype, c.head_dim, h->sm_count);
+    if (h->few.grid == 0) return fail(CF_ERR_CUDA);
+    few_list = take(paged_few_list_bytes((long long)c.max_batch * c.n_kv_heads));
+    slot_rows = paged_few_part_rows(h->few.grid);
     if ((int64_t)c.max_tokens * h->geom.G > kFewRows) {
-      tc_grid = paged_tc_grid(c.dtype, c.head_dim, h->sm_count);
-      if (tc_grid == 0) return fail(CF_ERR_CUDA);
-      for (size_t& at : tc_at) at = take((size_t)tc_grid * 2 * kTcRows * row);
-      meta_at = take(paged_tc_meta_bytes(tc_grid));
+      h->tc.grid = paged_tc_grid(c.dtype, c.head_dim, h->sm_count);
+      if (h->tc.grid == 0) return fail(CF_ERR_CUDA);
+      tc_list = take(paged_tc_list_bytes(h->tc.grid));
+      slot_rows = std::max<int64_t>(slot_rows, paged_tc_part_rows(h->tc.grid));
+    }
+    // single rows: a prefix call's, and the few-row kernel's own
+    const int64_t rows[2] = {slot_rows + std::min(all_rows, few_rows), slot_rows + all_rows};
+    for (int i = 0; i < 2; ++i) {
+      at_o[i] = take((size_t)rows[i] * c.head_dim * 4);
+      at_ml[i] = take((size_t)rows[i] * 8);
     }
   }
   if (cudaMalloc(&h->ws, bytes) != cudaSuccess) {
@@ -278,19 +289,20 @@ int cf_paged_create(const cf_paged_config* cfg, cf_paged_handle** out) {
   }
   uint8_t* ws = static_cast<uint8_t*>(h->ws);
   h->errflag = reinterpret_cast<int*>(ws);
-  auto split = [&](size_t at, int grid, int rows, int* tickets) {
-    PagedSplit s;
-    s.o = reinterpret_cast<float*>(ws + at);
-    s.ml = reinterpret_cast<float2*>(s.o + (size_t)grid * 2 * rows * c.head_dim);
-    s.tickets = tickets;
-    s.grid = grid;
-    return s;
-  };
-  h->few = split(few_at[0], few_grid, kFewRows, reinterpret_cast<int*>(ws + few_t));
-  h->few_prefix = split(few_at[1], few_grid, kFewRows, nullptr);
-  h->tc = split(tc_at[0], tc_grid, kTcRows, nullptr);
-  h->tc.meta = ws + meta_at;
-  h->tc_prefix = split(tc_at[1], tc_grid, kTcRows, nullptr);
+  const PagedParts own = {reinterpret_cast<float*>(ws + at_o[0]),
+                          reinterpret_cast<float2*>(ws + at_ml[0]), slot_rows,
+                          all_rows <= few_rows};
+  const PagedParts prefix = {reinterpret_cast<float*>(ws + at_o[1]),
+                             reinterpret_cast<float2*>(ws + at_ml[1]), slot_rows, 1};
+  int* words = reinterpret_cast<int*>(ws + counters);
+  h->few.parts = h->tc.parts = own;
+  h->few.list = ws + few_list;
+  h->few.counter = words;
+  h->tc.list = ws + tc_list;
+  h->few_prefix.parts = h->tc_prefix.parts = prefix;
+  h->few_prefix.grid = h->few.grid;
+  h->few_prefix.counter = words + 4;
+  h->tc_prefix.grid = h->tc.grid;
   *out = h;
   return CF_OK;
 }

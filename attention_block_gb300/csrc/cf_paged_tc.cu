@@ -128,26 +128,6 @@ __device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, float (&v)[16]) {
         "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
 }
-// Transposes w over a quad of lanes: lane q ends with word q of lanes 0..3.
-__device__ __forceinline__ void quad_transpose(uint32_t (&w)[4], int q) {
-  const bool a = q & 1, b = q & 2;
-#pragma unroll
-  for (int i = 0; i < 4; i += 2) {  // pairs (0, 1) and (2, 3)
-    const uint32_t x = __shfl_xor_sync(~0u, a ? w[i] : w[i + 1], 1);
-    if (a)
-      w[i] = x;
-    else
-      w[i + 1] = x;
-  }
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {  // pairs (0, 2) and (1, 3)
-    const uint32_t x = __shfl_xor_sync(~0u, b ? w[i] : w[i + 2], 2);
-    if (b)
-      w[i] = x;
-    else
-      w[i + 2] = x;
-  }
-}
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
   asm volatile(
@@ -188,26 +168,9 @@ __device__ __forceinline__ void wait_bar(uint64_t* bar, uint32_t parity, int* er
 }
 
 template <typename T>
-__device__ __forceinline__ uint32_t pack2(float a, float b);
-template <>
-__device__ __forceinline__ uint32_t pack2<__half>(float a, float b) {
-  const __half2 h = __floats2half2_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-template <>
-__device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-template <typename T>
 constexpr bool kIsBf16 = false;
 template <>
 constexpr bool kIsBf16<__nv_bfloat16> = true;
-
-// Starts a load into L1 without waiting for it.
-__device__ __forceinline__ void prefetch_line(const int* at) {
-  asm volatile("{\n\t.reg .u32 v;\n\tld.global.ca.u32 v, [%0];\n\t}" ::"l"(at));
-}
 
 template <int N>
 __device__ __forceinline__ void set_regs_up() {
@@ -322,15 +285,10 @@ struct alignas(16) TcMeta {
 struct TcArgs {
   PagedAttnParams p;
   PagedPrefixParts pre;
-  float* o;
-  float2* ml;
+  PagedParts ws;
   TcMeta* meta;
   int slots;  // upper bound on the row tiles' numbers
 };
-
-// What a launch attends to: the sequences' own keys; the shared prefix; own
-// keys, with the prefix's partial states joined to the results.
-enum TcMode { kOwn = 0, kPrefix = 1, kOwnAfterPrefix = 2 };
 
 template <typename T, int D, int MODE>
 __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const __grid_constant__ TcArgs a) {
@@ -580,11 +538,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const __grid_co
         tc05_fence_after();
       }
       const float m2 = m * sc;  // base 2
-      const bool part = PRE || !whole;
+      const bool part = PRE || !whole;  // leaves a state, not a result
       // this block's slot for the item (PagedParts)
       const long long prow0 =
           (2 * (long long)blockIdx.x + (u0 >= cur.i0 ? 0 : 1)) * (2 * kHalf) + hf * kHalf;
-      if (part && gr < t.rows) __stcg(a.ml + prow0 + r, make_float2(m2, l));
       const int q4 = lane & 3;
 #pragma unroll 1
       for (int hh = 0; hh < 2; ++hh) {  // 16 rows of the warp at a time
@@ -605,18 +562,22 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const __grid_co
           np[e] = 0;
           const int i = rg / p.g.G;
           orow[e] = ((long long)t.t0 + i) * p.g.nq + cur.h * p.g.G + rg - i * p.g.G;
+          if (part) {
+            orow[e] = whole ? a.ws.state_base + orow[e] : prow0 + row[e];
+            if (there && q4 == 0) __stcg(a.ws.ml + orow[e], make_float2(rm, rl));
+          }
           if (JOIN && !part && there && t.p0 + i >= 0) {
-            const long long R = (long long)t.t0 * p.g.G + rg, pt = div_units(R, a.pre.rows);
-            const PagedItemParts pp(a.pre.item(pt * p.g.nkv + cur.h));
-            const int pr = (int)(R - pt * a.pre.rows);
+            const PagedRowParts pp =
+                paged_prefix_row(a.pre, p.g, (long long)t.t0 + i, cur.h, rg - i * p.g.G);
             np[e] = pp.n;
-            for (int k = 0; k < pp.n; ++k)
-              mt[e] = fmaxf(mt[e], __ldcg(a.pre.ml + pp.slot(k) * a.pre.rows + pr).x);
+#pragma unroll 4
+            for (int k = 0; k < pp.n; ++k) mt[e] = fmaxf(mt[e], __ldcg(a.pre.ml + pp.row(k)).x);
             const float ref = mt[e] == -INFINITY ? 0.f : mt[e];
             own[e] = ex2(rm - ref);
             rl *= own[e];
+#pragma unroll 4
             for (int k = 0; k < pp.n; ++k) {
-              const float2 ml = __ldcg(a.pre.ml + pp.slot(k) * a.pre.rows + pr);
+              const float2 ml = __ldcg(a.pre.ml + pp.row(k));
               rl += ml.y * ex2(ml.x - ref);
             }
           }
@@ -653,24 +614,24 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const __grid_co
                 const float g0 = __shfl_xor_sync(~0u, odd ? A0 : B0, 1);
                 const float g1 = __shfl_xor_sync(~0u, odd ? A1 : B1, 1);
                 if (row[e] >= 0)
-                  __stcg(reinterpret_cast<float4*>(a.o + (prow0 + row[e]) * D + c + 16 * b2 +
-                                                   8 * (q4 & 1) + 4 * (q4 >> 1)),
+                  __stcg(reinterpret_cast<float4*>(a.ws.o + orow[e] * D + c + 16 * b2 + 8 * (q4 & 1) +
+                                                   4 * (q4 >> 1)),
                          odd ? make_float4(g0, g1, B0, B1) : make_float4(A0, A1, g0, g1));
               }
             } else {
               if (JOIN && np[e]) {
-                const long long R = (long long)t.t0 * p.g.G + t.j * 2 * kHalf + hf * kHalf + row[e];
-                const long long pt = div_units(R, a.pre.rows);
-                const PagedItemParts pp(a.pre.item(pt * p.g.nkv + cur.h));
-                const int pr = (int)(R - pt * a.pre.rows);
+                const int rg = t.j * 2 * kHalf + hf * kHalf + row[e], i = rg / p.g.G;
+                const PagedRowParts pp =
+                    paged_prefix_row(a.pre, p.g, (long long)t.t0 + i, cur.h, rg - i * p.g.G);
                 const float ref = mt[e] == -INFINITY ? 0.f : mt[e];
 #pragma unroll
                 for (int b = 0; b < 4; ++b) {
                   o[4 * b + 2 * e] *= own[e];
                   o[4 * b + 2 * e + 1] *= own[e];
                 }
+#pragma unroll 2
                 for (int k = 0; k < np[e]; ++k) {
-                  const long long at = pp.slot(k) * a.pre.rows + pr;
+                  const long long at = pp.row(k);
                   const float f = ex2(__ldcg(a.pre.ml + at).x - ref);
 #pragma unroll
                   for (int b = 0; b < 4; ++b) {
@@ -940,16 +901,11 @@ __global__ void __launch_bounds__(256) paged_tc_join_kernel(const __grid_constan
   for (int e = blockIdx.y * 256 + threadIdx.x; e < rows * C4; e += gridDim.y * 256) {
     const int r = e / C4, col = (e - r * C4) * 4;
     PagedState4 s{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-#pragma unroll 8
-    for (int k = 0; k < parts.n; ++k) {
-      const long long at = parts.slot(k) * (2 * kHalf) + r;
-      const float2 ml = __ldcg(a.ml + at);
-      s.join(ml.x, ml.y, __ldcg(reinterpret_cast<const float4*>(a.o + at * D + col)));
-    }
     const int gr = x.j * 2 * kHalf + r, i = gr / p.g.G, g = gr - i * p.g.G;
     const long long t = x.t0 + i;
+    paged_join_row<D>(s, a.ws.o, a.ws.ml, PagedRowParts(parts, 2 * kHalf, r, 0), col);
     if (a.pre.rows && x.p0 + i >= 0)
-      paged_join_prefix<D>(s, a.pre, t * p.g.G + g, x.h, p.g.nkv, col);
+      paged_join_row<D>(s, a.pre.o, a.pre.ml, paged_prefix_row(a.pre, p.g, t, x.h, g), col);
     paged_store4<T, D>(s, p.out, p.lse, t * p.g.nq + x.h * p.g.G + g, col);
   }
 }
@@ -998,31 +954,34 @@ int cf::paged_tc_grid(int dtype, int head_dim, int sm_count) {
   return sm_count;
 }
 
-size_t cf::paged_tc_meta_bytes(int grid) { return (size_t)grid * sizeof(TcMeta); }
+long long cf::paged_tc_part_rows(int grid) { return 2LL * grid * kTcRows; }
+
+size_t cf::paged_tc_list_bytes(int grid) { return (size_t)grid * sizeof(TcMeta); }
 
 PagedPrefixParts cf::paged_tc_prefix(const PagedAttnParams& p, const PagedSplit& ws) {
   PagedPrefixParts x;
-  x.o = ws.o;
-  x.ml = ws.ml;
+  x.o = ws.parts.o;
+  x.ml = ws.parts.ml;
+  x.state_base = ws.parts.state_base;
   x.rows = kTcRows;
   x.tiles = (p.prefix_len + kBN - 1) / kBN;
   x.item_cost = kItemCost;
   const long long row_tiles = ((long long)p.n_tokens * p.g.G + kTcRows - 1) / kTcRows;
-  x.upc = std::max<long long>(1, (row_tiles * p.g.nkv * (x.tiles + kItemCost) + ws.grid - 1) / ws.grid);
+  x.upc = std::max<long long>(
+      1, (row_tiles * p.g.nkv * (x.tiles + kItemCost) + ws.grid - 1) / ws.grid);
   return x;
 }
 
-bool cf::paged_tc_launch(int dtype, const PagedAttnParams& p, const PagedSplit& ws, bool prefix,
+bool cf::paged_tc_launch(int dtype, const PagedAttnParams& p, const PagedSplit& ws, PagedMode mode,
                          const PagedPrefixParts& pre, cudaStream_t st) {
-  const TcFns f = tc_fns(dtype, p.g.D, prefix ? kPrefix : pre.rows ? kOwnAfterPrefix : kOwn);
+  const TcFns f = tc_fns(dtype, p.g.D, mode);
   TcArgs a;
   a.p = p;
   a.pre = pre;
-  a.o = ws.o;
-  a.ml = ws.ml;
-  a.meta = static_cast<TcMeta*>(ws.meta);
+  a.ws = ws.parts;
+  a.meta = static_cast<TcMeta*>(ws.list);
   a.slots = (int)((long long)p.n_tokens * p.g.G / kTcRows) + p.batch;
   void* args[] = {&a};
   if (!launch_pdl(f.main, dim3(ws.grid), kTcThreads, f.smem, st, args)) return false;
-  return prefix || launch_pdl(f.join, dim3(ws.grid, 32), 256, 0, st, args);
+  return mode == kPrefix || launch_pdl(f.join, dim3(ws.grid, 32), 256, 0, st, args);
 }

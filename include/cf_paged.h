@@ -106,7 +106,8 @@ typedef struct cf_paged_config {
 typedef struct cf_paged_handle cf_paged_handle; /* opaque */
 
 /* Validate cfg and allocate the handle's workspace (partial results of split
- * sequences, at most about 90 MB, and an error word) on the current device.
+ * sequences, and an error word: about 130 MB
+ * plus, per token of max_tokens, up to 2 * nq * (d + 2) fp32 values) on the current device.
  * On failure nothing stays allocated and *out is NULL.  Errors: INVALID_ARG
  * (NULL, sizes, strides, sections that do not add up), UNSUPPORTED
  * (head_dim, page_size), CUDA. */
