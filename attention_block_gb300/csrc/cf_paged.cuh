@@ -312,6 +312,13 @@ __device__ __forceinline__ void quad_transpose(uint32_t (&w)[4], int q) {
   }
 }
 
+// 2^x, off by 2 ulp; results below 2^-126 are 0.
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 template <typename T>
 __device__ __forceinline__ uint32_t pack2(float a, float b);
 template <>
@@ -332,8 +339,9 @@ enum PagedMode { kOwn = 0, kPrefix = 1, kOwnAfterPrefix = 2 };
 // An attention kernel's part of a handle's workspace.
 struct PagedSplit {
   PagedParts parts;
-  void* list = nullptr;    // items whose parts a second kernel joins
+  void* list = nullptr;    // items for a joining kernel
   int* counter = nullptr;  // words that are zero between calls
+  int* tickets = nullptr;  // one such word per (sequence, KV head)
   int grid = 0;            // resident blocks
 };
 

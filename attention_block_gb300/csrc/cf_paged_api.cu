@@ -254,7 +254,8 @@ int cf_paged_create(const cf_paged_config* cfg, cf_paged_handle** out) {
   // The words that start at zero, then the lists, then two sets of states:
   // of the sequences' own keys and of the prefix.  A call uses one attention
   // kernel for each, so the kernels share them.
-  const size_t counters = take(16 * 4);
+  const size_t counters = take(2 * 4);
+  const size_t tickets = take(c.dtype != CF_F32 ? (size_t)c.max_batch * c.n_kv_heads * 4 : 4);
   const size_t zero = bytes;
   const int64_t all_rows = (int64_t)c.max_tokens * c.n_q_heads;
   size_t few_list = 0, tc_list = 0, at_o[2] = {0, 0}, at_ml[2] = {0, 0};
@@ -294,14 +295,13 @@ int cf_paged_create(const cf_paged_config* cfg, cf_paged_handle** out) {
                           all_rows <= few_rows};
   const PagedParts prefix = {reinterpret_cast<float*>(ws + at_o[1]),
                              reinterpret_cast<float2*>(ws + at_ml[1]), slot_rows, 1};
-  int* words = reinterpret_cast<int*>(ws + counters);
   h->few.parts = h->tc.parts = own;
   h->few.list = ws + few_list;
-  h->few.counter = words;
+  h->few.counter = reinterpret_cast<int*>(ws + counters);
+  h->few.tickets = reinterpret_cast<int*>(ws + tickets);
   h->tc.list = ws + tc_list;
   h->few_prefix.parts = h->tc_prefix.parts = prefix;
   h->few_prefix.grid = h->few.grid;
-  h->few_prefix.counter = words + 4;
   h->tc_prefix.grid = h->tc.grid;
   *out = h;
   return CF_OK;

@@ -6,15 +6,15 @@
 // 16-row tile leaves tcgen05's 128 rows empty) have far more than the 16
 // flops a byte needs.
 //
-// The key tiles of all (sequence, KV head) items are one line of units, cut
-// into pieces (PagedParts).  A worker is one warp: it takes whole tiles
-// through a cp.async ring of its own, which runs ahead across items and
-// pieces, keeps its own softmax state and never waits for another warp.
-// Ragged lengths and small batches thereby fill the GPU.  A second kernel
-// joins the parts of split items, in a fixed order: which warp computed a
-// part does not matter.  A position that no row sees is not read: its slot
-// is filled with zeros by the copy (source size 0), so what lies there cannot
-// reach a product.
+// The key tiles of all (sequence, KV head) items are one line of units that
+// the warps share evenly (PagedParts), so ragged lengths and small batches
+// fill the GPU.  A warp takes its whole run of tiles through a cp.async ring
+// of its own that runs ahead across items, keeps its own softmax state, and
+// waits for nobody until its run is done.  Then the block joins the parts of
+// items that several of its warps share, and the last block to finish a part
+// of an item that lies in several blocks joins those, in a fixed order.
+// A position that no row sees is not read: its slot is filled with zeros by
+// the copy (source size 0), so what lies there cannot reach a product.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -27,44 +27,28 @@ using namespace cf;
 
 namespace {
 
-constexpr int kFewWarps = 4;
+constexpr int kFewWarps = 8;  // one block per SM
 constexpr int kFewThreads = kFewWarps * 32;
-constexpr int kFewStages = 3;
-constexpr int kBlocksPerSm = 2;
-constexpr int kPieces = 3;      // pieces per warp where there is work for them ...
-constexpr int kFineUnits = 12;  // ... which is from this many units per warp on
 constexpr int kJoinThreads = 256;
 
 template <int D>
 struct Shape {
-  static constexpr int KS = 2048 / D;           // positions of a unit: 8 KB of K and V
-  static constexpr int STAGE = 2 * KS * D * 2;  // bytes
-  static constexpr int SMEM = kFewWarps * kFewStages * STAGE;
-  // 1 KB of static shared memory and 1 KB that the system takes for a block
-  static_assert(kBlocksPerSm * (SMEM + 2048) <= 228 * 1024, "two blocks on an SM");
+  static constexpr int KS = 2048 / D;   // positions of a unit
+  static constexpr int SLOT = KS * D * 2;  // bytes of its K or V: 4 KB
+  // K and V of two units: a slot is refilled as soon as it is read, so three
+  // are on their way while one is worked on
+  static constexpr int RING = 4 * SLOT;
+  static constexpr int ROWS = kFewRows * D * 4;  // o of a part
+  static constexpr int WARP = RING + ROWS;
+  static constexpr int SMEM = kFewWarps * WARP;
+  static_assert(ROWS <= RING && SMEM <= 224 * 1024, "shared memory");
 };
 
-// Units of a piece.  Memory serves some SMs faster than others: with one piece
-// per warp the fast ones idle at the end, so a long line is cut finer and the
-// later pieces go to whoever is free.
-__host__ __device__ inline long long few_upc(long long total, int warps) {
-  const long long n = total >= (long long)kFineUnits * warps ? (long long)kPieces * warps : warps;
-#ifdef __CUDA_ARCH__
-  return div_units(total + n - 1, n);
-#else
-  return (total + n - 1) / n;
-#endif
-}
-
-// An item for the joining kernel.
+// What is left of an item at a warp's end, in shared memory; and an item for
+// the kernel that joins the prefix.
 struct alignas(16) FewItem {
   long long i0;
   int tiles, t0, p0, n, b, h;
-};
-// Head of the list of such items.
-struct alignas(16) FewList {
-  long long upc;
-  int pad[2];
 };
 
 // A sequence's tokens and its key tiles; at least one tile where there are
@@ -122,15 +106,25 @@ struct FewArgs {
   PagedAttnParams p;
   PagedPrefixParts pre;
   PagedParts ws;
-  FewList* head;
   FewItem* list;
-  int* counter;  // pieces handed out, warps done, items listed, joining blocks done
+  int* counter;   // items listed, joining blocks done
+  int* tickets;   // per item: parts written so far
   int row_limit;  // rows per item, at most
-  int split;      // the joining kernel's lane groups per row
 };
 
+// Row of out (and of the prefix's states) of an item's row.
+__device__ __forceinline__ long long out_row(const PagedAttnParams& p, const FewItem& it, int row) {
+  const int i = row / p.g.G;
+  return (long long)(it.t0 + i) * p.g.nq + it.h * p.g.G + row - i * p.g.G;
+}
+// Row of an item's own state.
+__device__ __forceinline__ long long state_row(const FewArgs& a, const FewItem& it, int row) {
+  return a.ws.state_base + (a.ws.by_token ? out_row(a.p, it, row)
+                                          : ((long long)it.b * a.p.g.nkv + it.h) * kFewRows + row);
+}
+
 template <typename T, int D, int MODE>
-__global__ void __launch_bounds__(kFewThreads, kBlocksPerSm)
+__global__ void __launch_bounds__(kFewThreads, 1)
     paged_few_kernel(const __grid_constant__ FewArgs a) {
   using S = Shape<D>;
   constexpr bool PRE = MODE == kPrefix;
@@ -141,10 +135,15 @@ __global__ void __launch_bounds__(kFewThreads, kBlocksPerSm)
   using M = MmaKind<T>;
   const PagedAttnParams& p = a.p;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ long long s_first[32];  // first unit of every fourth thread's sequences
+  __shared__ long long s_first[32];  // first unit of every eighth thread's sequences
   __shared__ long long s_scan[kFewWarps];
-  __shared__ uint32_t s_valid[kFewWarps][kFewStages];
-  __shared__ int s_piece[kFewWarps][4];
+  __shared__ uint32_t s_valid[kFewWarps][2];
+  // per warp: the part of an item that began before its run (F), and of one
+  // that goes on behind it (L; if it also began before, there is no F)
+  __shared__ FewItem s_item[2][kFewWarps];
+  __shared__ float2 s_ml[2][kFewWarps][kFewRows];
+  __shared__ int s_has[2][kFewWarps];
+  __shared__ int s_last[2];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int gq = lane >> 2, tq = lane & 3;
 
@@ -174,51 +173,40 @@ __global__ void __launch_bounds__(kFewThreads, kBlocksPerSm)
   }
   if (tid % kFewWarps == 0) s_first[tid / kFewWarps] = before;
   const int workers = gridDim.x * kFewWarps, me = blockIdx.x * kFewWarps + warp;
-  const long long upc = PRE ? a.pre.upc : few_upc(total, workers);
-  // pieces 0 .. workers - 1 are dealt out, the others fetched from a counter
-  const bool fine = upc > 0 && total > upc * workers;
-  if (!PRE && blockIdx.x == 0 && tid == 0) a.head->upc = upc;
+  const long long upc = PRE ? a.pre.upc / kFewWarps : div_units(total + workers - 1, workers);
+  const long long block_upc = upc * kFewWarps;
+  if (blockIdx.x * block_upc >= total) return;
+  if (lane == 0) s_has[0][warp] = s_has[1][warp] = 0;
   __syncthreads();
 
-  // The walk's start in a piece; past the last one it has no units.
-  auto locate = [&](Cursor<KS, PRE>& c, int piece) {
-    c.u = (long long)piece * upc;
-    c.end = min(total, c.u + upc);
-    if (c.u >= total) {
-      c.end = c.u = total;
-      return;
-    }
+  // The start of this warp's run.
+  Cursor<KS, PRE> cur;
+  cur.u = me * upc;
+  cur.end = min(total, cur.u + upc);
+  if (cur.u < cur.end) {
     // the last run of sequences that begins at or before unit u
-    const int n = __popc(__ballot_sync(~0u, s_first[lane] <= c.u));
+    const int n = __popc(__ballot_sync(~0u, s_first[lane] <= cur.u));
     long long at = s_first[n - 1];
     int b = (n - 1) * kFewWarps * per;
     while (true) {
-      c.w = work_of<KS, PRE>(p, b);
-      const long long len = (long long)c.w.tiles * p.g.nkv;
-      if (c.u < at + len) break;
+      cur.w = work_of<KS, PRE>(p, b);
+      const long long len = (long long)cur.w.tiles * p.g.nkv;
+      if (cur.u < at + len) break;
       at += len;
       ++b;
     }
-    c.b = b;
-    const long long off = c.u - at;
-    c.h = (int)div_units(off, c.w.tiles);
-    c.tile = (int)(off - (long long)c.h * c.w.tiles);
-    c.i0 = c.u - c.tile;
-  };
+    cur.b = b;
+    const long long off = cur.u - at;
+    cur.h = (int)div_units(off, cur.w.tiles);
+    cur.tile = (int)(off - (long long)cur.h * cur.w.tiles);
+    cur.i0 = cur.u - cur.tile;
+  }
 
   const char* kbase = static_cast<const char*>(p.k_pages);
   const char* vbase = static_cast<const char*>(p.v_pages);
-  const uint32_t ring_s = smem_u32(smem + warp * kFewStages * S::STAGE);
+  uint8_t* mem = smem + warp * S::WARP;
+  const uint32_t ring_s = smem_u32(mem);
 
-  int seq = 0, ld_seq = 0;  // pieces begun so far, less one; the copies run ahead
-  int upcoming = 0;         // lane 0: the piece after the one the copies are in
-  auto fetch_piece = [&]() {
-    if (lane == 0) upcoming = fine ? workers + atomicAdd(a.counter, 1) : 1 << 30;
-  };
-  Cursor<KS, PRE> cur;
-  locate(cur, me);
-  if (lane == 0) s_piece[warp][0] = me;
-  if (cur.u < cur.end) fetch_piece();
   Cursor<KS, PRE> ld = cur;  // runs ahead of cur
 
   // The page of this lane's position in the tile that ld stands on, fetched
@@ -233,42 +221,56 @@ __global__ void __launch_bounds__(kFewThreads, kBlocksPerSm)
     const int* table = PRE ? p.prefix_table : p.page_table + (int64_t)ld.b * p.g.max_pages;
     ld_page = __ldg(table + (j >> p.g.page_shift));
   };
-  auto issue = [&](int stage) {
+  // Copies a unit's K or V into a slot; lane i holds position i's byte offset,
+  // or -1 (zeros).
+  constexpr int RP = 32 / C;  // rows of one copy instruction
+  const int r0 = lane / C, c0 = lane % C;
+  const uint32_t d0 = ring_s + r0 * (D * 2) + ((c0 ^ r0) << 4);
+  const int64_t ss = p.g.slot_stride * 2;
+  const bool octets = p.g.page_shift >= 3;
+  auto copy = [&](int slot, const char* src, int64_t off) {
+    const uint32_t d = d0 + slot * S::SLOT;
+    if (octets && __all_sync(~0u, off >= 0 || lane >= KS)) {
+      // eight consecutive positions lie in one page: one lookup serves them
+#pragma unroll
+      for (int y = 0; y < KS / 8; ++y) {
+        const char* at = src + __shfl_sync(~0u, off, 8 * y) + r0 * ss + c0 * 16;
+#pragma unroll
+        for (int z = 0; z < 8 / RP; ++z) {
+          cp16((d + (8 * y + z * RP) * (D * 2)) ^ ((z * RP) << 4), at);
+          at += RP * ss;
+        }
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < KS / RP; ++i) {
+        const int64_t o = __shfl_sync(~0u, off, i * RP + r0);
+        cp16((d + i * RP * (D * 2)) ^ (((i * RP) & 7) << 4), src + (o >= 0 ? o + c0 * 16 : 0),
+             o >= 0);
+      }
+    }
+  };
+  int64_t v_off = -1;  // of the unit whose V is still to be copied
+  bool v_some = false;
+  auto issue_k = [&](int pair) {
+    v_some = false;
     if (ld.u < ld.end) {
-      int64_t off = -1;  // no copy: zeros
+      v_off = -1;  // no copy: zeros
       if (ld_pos >= 0) {
         if ((unsigned)ld_page >= (unsigned)p.g.num_pages)
           atomicOr(p.errflag, kDevErrPosRange);
         else
-          off = ((int64_t)ld_page * p.g.page_stride +
-                 (int64_t)(ld_pos & p.g.page_mask) * p.g.slot_stride +
-                 (int64_t)ld.h * p.g.head_stride) * 2;
+          v_off = ((int64_t)ld_page * p.g.page_stride +
+                   (int64_t)(ld_pos & p.g.page_mask) * p.g.slot_stride +
+                   (int64_t)ld.h * p.g.head_stride) * 2;
       }
       const uint32_t valid = __ballot_sync(~0u, ld_pos >= 0);
-      if (lane == 0) s_valid[warp][stage] = valid;
-      const uint32_t dst = ring_s + stage * S::STAGE;
+      if (lane == 0) s_valid[warp][pair] = valid;
+      v_some = valid != 0;
       const int ob = ld.b, oh = ld.h;
       ld.next(p);
-      if (ld.u >= ld.end && ld.end < total) {  // later pieces lie further on
-        ++ld_seq;
-        const int piece = __shfl_sync(~0u, upcoming, 0);
-        if (lane == 0) s_piece[warp][ld_seq & 3] = piece;
-        locate(ld, piece);
-        if (ld.u < ld.end) fetch_piece();
-      }
       fetch_page();
-      if (valid) {
-#pragma unroll
-        for (int i = 0; i < KS * C / 32; ++i) {
-          const int row = i * (32 / C) + lane / C, c = lane % C;
-          const int64_t o = __shfl_sync(~0u, off, row);
-          const bool there = o >= 0;
-          const int64_t at = there ? o + c * 16 : 0;
-          const uint32_t d = dst + row * (D * 2) + ((c ^ (row & 7)) << 4);
-          cp16(d, kbase + at, there);
-          cp16(d + KS * D * 2, vbase + at, there);
-        }
-      }
+      if (v_some) copy(2 * pair, kbase, v_off);
       if (ld.u < ld.end && (ld.b != ob || ld.h != oh)) {  // the next item's queries
         const int row = lane * 64 / D, i = row / p.g.G;
         if (row < ld.w.n * p.g.G)
@@ -278,12 +280,19 @@ __global__ void __launch_bounds__(kFewThreads, kBlocksPerSm)
     }
     cp_commit();
   };
+  auto issue_v = [&](int pair) {
+    if (v_some) copy(2 * pair + 1, vbase, v_off);
+    cp_commit();
+  };
 
   fetch_page();
 #pragma unroll
-  for (int s = 0; s < kFewStages - 1; ++s) issue(s);
+  for (int s = 0; s < 2; ++s) {
+    issue_k(s);
+    issue_v(s);
+  }
 
-  int stage = 0;
+  int pair = 0;
   uint32_t qf[D / 16][4];
   float o[NO][4], m[2], l[2];
   int pos[2];  // positions of this thread's two rows
@@ -314,13 +323,12 @@ __global__ void __launch_bounds__(kFewThreads, kBlocksPerSm)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[k][e] = 0.f;
     }
-    issue(stage == 0 ? kFewStages - 1 : stage - 1);
-    cp_wait<kFewStages - 1>();
+    cp_wait<3>();  // K has landed
     __syncwarp();
-    const uint32_t valid = s_valid[warp][stage];
+    const uint32_t valid = s_valid[warp][pair];
+    const uint32_t ks = ring_s + 2 * pair * S::SLOT, vs = ks + S::SLOT;
+    float c[NT][4];
     if (valid) {
-      const uint32_t ks = ring_s + stage * S::STAGE, vs = ks + KS * D * 2;
-      float c[NT][4];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -334,6 +342,10 @@ __global__ void __launch_bounds__(kFewThreads, kBlocksPerSm)
           M::mma(c[nt], qf[2 * k2 + 1], r2, r3);
         }
       }
+    }
+    __syncwarp();  // K is read before its next copies are issued
+    issue_k(pair);
+    if (valid) {
       // mask, running maximum
       const int j0 = cur.w.base(cur.tile);
       float mx[2] = {m[0], m[1]};
@@ -354,7 +366,7 @@ __global__ void __launch_bounds__(kFewThreads, kBlocksPerSm)
         mx[r] = fmaxf(mx[r], __shfl_xor_sync(~0u, mx[r], 1));
         mx[r] = fmaxf(mx[r], __shfl_xor_sync(~0u, mx[r], 2));
         const float ref = mx[r] == -INFINITY ? 0.f : mx[r];
-        corr[r] = exp2f(m[r] - ref);
+        corr[r] = ex2(m[r] - ref);
         m[r] = mx[r];
         mx[r] = ref;
         l[r] *= corr[r];
@@ -369,9 +381,13 @@ __global__ void __launch_bounds__(kFewThreads, kBlocksPerSm)
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          c[nt][e] = exp2f(c[nt][e] - mx[e >> 1]);
+          c[nt][e] = ex2(c[nt][e] - mx[e >> 1]);
           l[e >> 1] += c[nt][e];
         }
+    }
+    cp_wait<3>();  // V has landed
+    __syncwarp();
+    if (valid) {
       // o += P V; bf16 probabilities enter as hi + lo pairs (the tensor cores
       // have the time), fp16 ones with their 11 bits
 #pragma unroll
@@ -395,8 +411,9 @@ __global__ void __launch_bounds__(kFewThreads, kBlocksPerSm)
         }
       }
     }
-    __syncwarp();  // the stage is read before its next copies are issued
-    stage = stage + 1 == kFewStages ? 0 : stage + 1;
+    __syncwarp();
+    issue_v(pair);
+    pair ^= 1;
 
     const bool item_done = cur.tile + 1 == cur.w.tiles;
     if (!item_done && cur.u + 1 < cur.end) {
@@ -405,48 +422,60 @@ __global__ void __launch_bounds__(kFewThreads, kBlocksPerSm)
     }
 
     // ---- the warp's part of the item is complete
-    const bool whole = item_done && first_tile == 0;
+    const bool begins = first_tile == 0;
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       l[r] += __shfl_xor_sync(~0u, l[r], 1);
       l[r] += __shfl_xor_sync(~0u, l[r], 2);
     }
-    // (a sequence with more tokens than the call allows has no keys: all rows zero)
-    if ((MODE != kOwn || !whole) && (PRE || cur.w.n <= p.max_q)) {
-      const long long piece = s_piece[warp][seq & 3];
-      const long long slot = 2 * piece + (piece * upc >= cur.i0 ? 0 : 1);
+    FewItem it;
+    it.i0 = cur.i0;
+    it.tiles = cur.w.tiles;
+    it.t0 = cur.w.t0;
+    it.p0 = cur.w.p0;
+    it.n = cur.w.n;
+    it.b = cur.b;
+    it.h = cur.h;
+    if (!begins || !item_done) {
+      // kept in shared memory until the block's warps are done; the ring is
+      // free at the run's end, where an L is left
+      const int kind = item_done ? 0 : 1;
+      if (kind) {
+        cp_wait<0>();
+        __syncwarp();
+      }
+      float* dst = reinterpret_cast<float*>(kind ? mem : mem + S::RING);
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const int row = gq + 8 * r, i = row / p.g.G;
-        if (row >= nrows) continue;
-        long long at = slot * kFewRows + row;
-        if (whole)
-          at = a.ws.state_base +
-               (a.ws.by_token
-                    ? (long long)(cur.w.t0 + i) * p.g.nq + cur.h * p.g.G + row - i * p.g.G
-                    : ((long long)cur.b * p.g.nkv + cur.h) * kFewRows + row);
-        if (tq == 0) __stcg(a.ws.ml + at, make_float2(m[r], l[r]));
-        float* dst = a.ws.o + at * D + 2 * tq;
+        if (gq + 8 * r >= nrows) continue;
+        if (tq == 0) s_ml[kind][warp][gq + 8 * r] = make_float2(m[r], l[r]);
 #pragma unroll
         for (int k = 0; k < NO; ++k)
-          __stcg(reinterpret_cast<float2*>(dst + 8 * k), make_float2(o[k][2 * r], o[k][2 * r + 1]));
+          *reinterpret_cast<float2*>(dst + (gq + 8 * r) * D + 8 * k + 2 * tq) =
+              make_float2(o[k][2 * r], o[k][2 * r + 1]);
       }
-      if (!PRE && first_tile == 0 && lane == 0) {
-        FewItem x;
-        x.i0 = cur.i0;
-        x.tiles = cur.w.tiles;
-        x.t0 = cur.w.t0;
-        x.p0 = cur.w.p0;
-        x.n = cur.w.n;
-        x.b = cur.b;
-        x.h = cur.h;
-        a.list[atomicAdd(a.counter + 2, 1)] = x;
+      if (lane == 0) {
+        s_item[kind][warp] = it;
+        s_has[kind][warp] = 1;
       }
+    } else if (MODE != kOwn && (PRE || it.n <= p.max_q)) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        const int row = gq + 8 * r;
+        if (row >= nrows) continue;
+        const long long at = state_row(a, it, row);
+        if (tq == 0) __stcg(a.ws.ml + at, make_float2(m[r], l[r]));
+#pragma unroll
+        for (int k = 0; k < NO; ++k)
+          __stcg(reinterpret_cast<float2*>(a.ws.o + at * D + 8 * k + 2 * tq),
+                 make_float2(o[k][2 * r], o[k][2 * r + 1]));
+      }
+      if (!PRE && lane == 0) a.list[atomicAdd(a.counter, 1)] = it;
     } else {
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const int row = gq + 8 * r, i = row / p.g.G;
-        const long long at = (long long)(cur.w.t0 + i) * p.g.nq + cur.h * p.g.G + row - i * p.g.G;
+        const int row = gq + 8 * r;
+        const long long at = out_row(p, it, row);
         const float inv = l[r] == 0.f ? 0.f : 1.f / l[r];
         T* dst = static_cast<T*>(p.out) + at * D + 8 * tq;
 #pragma unroll
@@ -462,103 +491,135 @@ __global__ void __launch_bounds__(kFewThreads, kBlocksPerSm)
         if (p.lse && row < nrows && tq == 0)
           p.lse[at] = m[r] == -INFINITY ? -INFINITY : (m[r] + log2f(l[r])) * 0.69314718055994531f;
       }
+      // a sequence with more tokens than the call allows has no keys: its
+      // other rows are zero too
+      for (int x = kFewRows * (D / 4) + lane; !PRE && x < nrows * (D / 4); x += 32) {
+        const PagedState4 none{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+        paged_store4<T, D>(none, p.out, p.lse, out_row(p, it, x / (D / 4)), x % (D / 4) * 4);
+      }
     }
-    for (int x = kFewRows * (D / 4) + lane; !PRE && x < nrows * (D / 4); x += 32) {
-      const int row = x / (D / 4), col = (x - row * (D / 4)) * 4, i = row / p.g.G;
-      const PagedState4 none{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-      paged_store4<T, D>(none, p.out, p.lse,
-                         (long long)(cur.w.t0 + i) * p.g.nq + cur.h * p.g.G + row - i * p.g.G, col);
-    }
-    const bool piece_done = cur.u + 1 == cur.end;
     cur.next(p);
-    if (piece_done && cur.end < total) {
-      ++seq;
-      locate(cur, s_piece[warp][seq & 3]);
-    }
     fresh = true;
     first_tile = cur.tile;
   }
   cp_wait<0>();
-  // the last warp out leaves the counters at zero for the next call
-  if (fine && lane == 0 && atomicAdd(a.counter + 1, 1) == workers - 1) {
-    a.counter[0] = 0;
-    a.counter[1] = 0;
+  __syncthreads();
+
+  // ---- items that several warps share.  The parts of one lie side by side:
+  // L of the warp that begins it, L of those it runs through, F of the last.
+  constexpr int C4 = D / 4;
+  auto finish = [&](PagedState4& s, const FewItem& it, int row, int col) {
+    if (MODE == kOwn) {
+      paged_store4<T, D>(s, p.out, p.lse, out_row(p, it, row), col);
+    } else {
+      const long long at = state_row(a, it, row);
+      __stcg(reinterpret_cast<float4*>(a.ws.o + at * D + col), s.o);
+      if (col == 0) __stcg(a.ws.ml + at, make_float2(s.m, s.l));
+    }
+  };
+  if (tid < 2) s_last[tid] = 0;
+  FewItem cut[2];                 // items that go on in other blocks: the first's, the last's
+  bool has_cut[2] = {false, false};
+  for (int w0 = 0, k0 = 0; w0 < kFewWarps;) {
+    if (!s_has[k0][w0]) {
+      w0 += k0;
+      k0 ^= 1;
+      continue;
+    }
+    const FewItem it = s_item[k0][w0];
+    int last = w0, kind = k0;  // of the item's last part in this block
+    while (kind == 1 && last + 1 < kFewWarps) {
+      ++last;
+      kind = s_has[0][last] ? 0 : 1;
+    }
+    const bool here = it.i0 >= blockIdx.x * block_upc;  // begins in this block
+    const long long slot = 2 * (long long)blockIdx.x + (blockIdx.x * block_upc >= it.i0 ? 0 : 1);
+    for (int x = tid; x < it.n * p.g.G * C4; x += kFewThreads) {
+      const int row = x / C4, col = (x - row * C4) * 4;
+      PagedState4 s{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+      for (int w = w0; w <= last; ++w) {
+        const int k = w == last ? kind : 1;
+        const float* src =
+            reinterpret_cast<const float*>(smem + w * S::WARP + (k ? 0 : S::RING)) + row * D + col;
+        s.join(s_ml[k][w][row].x, s_ml[k][w][row].y, *reinterpret_cast<const float4*>(src));
+      }
+      if (here && kind == 0) {
+        finish(s, it, row, col);
+      } else {
+        const long long at = slot * kFewRows + row;
+        __stcg(reinterpret_cast<float4*>(a.ws.o + at * D + col), s.o);
+        if (col == 0) __stcg(a.ws.ml + at, make_float2(s.m, s.l));
+      }
+    }
+    if (!here || kind != 0) {
+      cut[here ? 1 : 0] = it;
+      has_cut[here ? 1 : 0] = true;
+    } else if (MODE == kOwnAfterPrefix && tid == 0) {
+      a.list[atomicAdd(a.counter, 1)] = it;
+    }
+    // on to what follows that part: after an F its warp's L, if any
+    w0 = kind == 0 ? last : kFewWarps;
+    k0 = 1;
+  }
+  if (PRE || !(has_cut[0] || has_cut[1])) return;
+  __syncthreads();
+  if (tid == 0) {
+    __threadfence();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (!has_cut[i]) continue;
+      const PagedItemParts parts(cut[i].i0, cut[i].tiles, block_upc);
+      int* ticket = a.tickets + (long long)cut[i].b * p.g.nkv + cut[i].h;
+      if (atomicAdd(ticket, 1) != parts.n - 1) continue;
+      *ticket = 0;
+      s_last[i] = 1;
+      if (MODE == kOwnAfterPrefix) a.list[atomicAdd(a.counter, 1)] = cut[i];
+    }
+    __threadfence();
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    if (!s_last[i]) continue;
+    const PagedItemParts parts(cut[i].i0, cut[i].tiles, block_upc);
+    for (int x = tid; x < cut[i].n * p.g.G * C4; x += kFewThreads) {
+      const int row = x / C4, col = (x - row * C4) * 4;
+      PagedState4 s{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+      paged_join_row<D>(s, a.ws.o, a.ws.ml, PagedRowParts(parts, kFewRows, row, -1), col);
+      finish(s, cut[i], row, col);
+    }
   }
 }
 
-// Joins the states of the listed items, and the prefix's: one row per group of
-// D / 4 lanes, or per block, whose groups then share the row's parts.
+// Joins the listed items' states and the prefix's, a row per D / 4 lanes.
 template <typename T, int D>
-__global__ void __launch_bounds__(kJoinThreads) paged_few_join_kernel(const __grid_constant__ FewArgs a) {
+__global__ void __launch_bounds__(kJoinThreads)
+    paged_few_join_kernel(const __grid_constant__ FewArgs a) {
   constexpr int W = D / 4, NG = kJoinThreads / W;
-  __shared__ float4 s_o[NG][W];
-  __shared__ float2 s_ml[NG];
   const PagedAttnParams& p = a.p;
-  const int tid = threadIdx.x, grp = tid / W, col = (tid % W) * 4;
+  const int tid = threadIdx.x, col = (tid % W) * 4;
   pdl_wait();
   pdl_trigger();
-  const long long rows = (long long)a.counter[2] * a.row_limit;
-  const long long upc = a.head->upc;
-  const int split = a.split;  // groups per row: 1 or NG
-  const long long step = (long long)gridDim.x * NG / split;
-  for (long long x0 = (long long)blockIdx.x * NG / split; x0 < rows; x0 += step) {
-    const long long x = split == 1 ? x0 + grp : x0;
-    PagedState4 s{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-    long long at = -1;
-    if (x < rows) {
-      const long long item = div_units(x, a.row_limit);
-      const int row = (int)(x - item * a.row_limit);
-      const FewItem it = a.list[item];
-      const int i = row / p.g.G, gi = row - i * p.g.G;
-      if (i < it.n) {
-        const long long t = it.t0 + i;
-        at = t * p.g.nq + it.h * p.g.G + gi;
-        const PagedRowParts own(PagedItemParts(it.i0, it.tiles, upc), kFewRows, row,
-                                a.ws.state_base +
-                                    (a.ws.by_token
-                                         ? at
-                                         : ((long long)it.b * p.g.nkv + it.h) * kFewRows + row));
-        const bool with_pre = a.pre.rows && it.p0 + i >= 0;
-        if (split == 1) {
-          paged_join_row<D>(s, a.ws.o, a.ws.ml, own, col);
-          if (with_pre)
-            paged_join_row<D>(s, a.pre.o, a.pre.ml, paged_prefix_row(a.pre, p.g, t, it.h, gi), col);
-        } else {
-#pragma unroll 4
-          for (int k = grp; k < own.n; k += NG) {
-            const long long r = own.row(k);
-            const float2 ml = __ldcg(a.ws.ml + r);
-            s.join(ml.x, ml.y, __ldcg(reinterpret_cast<const float4*>(a.ws.o + r * D + col)));
-          }
-          if (with_pre) {
-            const PagedRowParts pr = paged_prefix_row(a.pre, p.g, t, it.h, gi);
-#pragma unroll 4
-            for (int k = grp; k < pr.n; k += NG) {
-              const long long r = pr.row(k);
-              const float2 ml = __ldcg(a.pre.ml + r);
-              s.join(ml.x, ml.y, __ldcg(reinterpret_cast<const float4*>(a.pre.o + r * D + col)));
-            }
-          }
-        }
-      }
-    }
-    if (split != 1) {
-      s_o[grp][tid % W] = s.o;
-      if (col == 0) s_ml[grp] = make_float2(s.m, s.l);
-      __syncthreads();
-      if (grp == 0) {
-#pragma unroll
-        for (int g = 1; g < NG; ++g) s.join(s_ml[g].x, s_ml[g].y, s_o[g][tid % W]);
-      }
-      __syncthreads();
-    }
-    if (at >= 0 && (split == 1 || grp == 0)) paged_store4<T, D>(s, p.out, p.lse, at, col);
+  const long long rows = (long long)a.counter[0] * a.row_limit;
+  for (long long x = (long long)blockIdx.x * NG + tid / W; x < rows; x += (long long)gridDim.x * NG) {
+    const long long item = div_units(x, a.row_limit);
+    const int row = (int)(x - item * a.row_limit);
+    const FewItem it = a.list[item];
+    if (row >= it.n * p.g.G) continue;
+    const long long at = state_row(a, it, row);
+    const float2 ml = __ldcg(a.ws.ml + at);
+    PagedState4 s{ml.x, ml.y, __ldcg(reinterpret_cast<const float4*>(a.ws.o + at * D + col))};
+    const int i = row / p.g.G;
+    if (it.p0 + i >= 0)
+      paged_join_row<D>(s, a.pre.o, a.pre.ml,
+                        paged_prefix_row(a.pre, p.g, it.t0 + i, it.h, row - i * p.g.G), col);
+    paged_store4<T, D>(s, p.out, p.lse, out_row(p, it, row), col);
   }
   // the last block out empties the list for the next call
   __syncthreads();
-  if (tid == 0 && atomicAdd(a.counter + 3, 1) == (int)gridDim.x - 1) {
-    a.counter[2] = 0;
-    a.counter[3] = 0;
+  if (tid == 0 && atomicAdd(a.counter + 1, 1) == (int)gridDim.x - 1) {
+    a.counter[0] = 0;
+    a.counter[1] = 0;
   }
 }
 
@@ -603,19 +664,16 @@ int cf::paged_few_grid(int dtype, int head_dim, int sm_count) {
       return 0;
     }
   }
-  return kBlocksPerSm * sm_count;  // __launch_bounds__ and Shape see to it that they fit
+  return sm_count;
 }
 
-long long cf::paged_few_part_rows(int grid) {
-  return 2LL * kPieces * grid * kFewWarps * kFewRows;
-}
+long long cf::paged_few_part_rows(int grid) { return 2LL * grid * kFewRows; }
 
-size_t cf::paged_few_list_bytes(long long items) {
-  return sizeof(FewList) + (size_t)items * sizeof(FewItem);
-}
+size_t cf::paged_few_list_bytes(long long items) { return (size_t)items * sizeof(FewItem); }
 
 PagedPrefixParts cf::paged_few_prefix(const PagedAttnParams& p, const PagedSplit& ws) {
   const int KS = p.g.D == 64 ? Shape<64>::KS : Shape<128>::KS;
+  const long long warps = (long long)ws.grid * kFewWarps;
   PagedPrefixParts x;
   x.o = ws.parts.o;
   x.ml = ws.parts.ml;
@@ -623,7 +681,7 @@ PagedPrefixParts cf::paged_few_prefix(const PagedAttnParams& p, const PagedSplit
   x.rows = kFewRows;
   x.tiles = (p.prefix_len + KS - 1) / KS;
   x.item_cost = 0;
-  x.upc = few_upc((long long)x.tiles * p.g.nkv, ws.grid * kFewWarps);
+  x.upc = ((long long)x.tiles * p.g.nkv + warps - 1) / warps * kFewWarps;  // a block's
   return x;
 }
 
@@ -634,17 +692,15 @@ bool cf::paged_few_launch(int dtype, const PagedAttnParams& p, const PagedSplit&
   a.p = p;
   a.pre = pre;
   a.ws = ws.parts;
-  a.head = static_cast<FewList*>(ws.list);
-  a.list = reinterpret_cast<FewItem*>(a.head + 1);
+  a.list = static_cast<FewItem*>(ws.list);
   a.counter = ws.counter;
+  a.tickets = ws.tickets;
   a.row_limit = std::min(kFewRows, p.max_q * p.g.G);
-  // a block per row while the rows may not fill the GPU's lane groups anyway
-  const int ng = kJoinThreads / (p.g.D / 4), blocks = ws.grid * 4;
-  const long long rows = (long long)p.batch * p.g.nkv * a.row_limit;
-  a.split = rows <= 2LL * blocks ? ng : 1;
   void* args[] = {&a};
   if (!launch_pdl(f.main, ws.grid, kFewThreads, f.smem, st, args)) return false;
-  if (mode == kPrefix) return true;
-  const long long want = a.split == 1 ? (rows + ng - 1) / ng : rows;
-  return launch_pdl(f.join, (int)std::min<long long>(blocks, want), kJoinThreads, 0, st, args);
+  if (mode != kOwnAfterPrefix) return true;
+  const int ng = kJoinThreads / (p.g.D / 4);
+  const long long rows = (long long)p.batch * p.g.nkv * a.row_limit;
+  return launch_pdl(f.join, (int)std::min<long long>(8LL * ws.grid, (rows + ng - 1) / ng),
+                    kJoinThreads, 0, st, args);
 }
