@@ -550,6 +550,13 @@ class PagedKv:
         self._int = torch.int32
         self._f32 = torch.float32
         self._dev = torch.cuda.current_device()
+        inner = (c.n_kv_heads, c.page_size) if c.layout else (c.page_size, c.n_kv_heads)
+        self._pool_shape = (c.num_pages, *inner, c.head_dim)
+        self._pool_stride = (c.page_stride or c.page_size * self._kvrow, inner[1] * c.head_dim,
+                             c.head_dim, 1)
+        # (torch.cuda.current_stream() builds a Stream object: 2.8 us a call)
+        self._raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda d: torch.cuda.current_stream(d).cuda_stream)
         self._append = lib().cf_paged_append
         self._attention = lib().cf_paged_attention
         self._prefix = lib().cf_paged_prefix_attention
@@ -558,40 +565,38 @@ class PagedKv:
     def _at(self, x, dtype, numel, what):
         if x is None or isinstance(x, int):
             return x
-        if x.dtype is not dtype or x.get_device() != self._dev or not x.is_contiguous() or \
-                x.numel() < numel:
-            raise CfError(CF_ERR_INVALID_ARG, f"{what}: {x.dtype} {tuple(x.shape)} on {x.device}")
-        return x.data_ptr()
+        if x.dtype is dtype and x.get_device() == self._dev and x.is_contiguous() and \
+                x.numel() >= numel:
+            return x.data_ptr()
+        raise CfError(CF_ERR_INVALID_ARG, f"{what}: {x.dtype} {tuple(x.shape)} on {x.device}")
 
     # Address and row stride of [n, heads, d] rows (or [n, heads * d]).
     def _rows(self, x, n, row, stride, what):
         if x is None or isinstance(x, int):
             return x, int(stride) if stride else row
         shape, st = x.shape, x.stride()
-        if x.dtype is not self._dtype or x.get_device() != self._dev or len(shape) < 2 or \
-                shape[0] < n or x.numel() != shape[0] * row or st[-1] != 1 or \
-                (len(shape) == 3 and st[1] != shape[2]) or len(shape) > 3:
-            raise CfError(CF_ERR_INVALID_ARG,
-                          f"{what}: {x.dtype} {tuple(shape)} strides {st} on {x.device}")
-        # the stride of a single row says nothing
-        return x.data_ptr(), int(stride) if stride else (st[0] if shape[0] > 1 else row)
+        if x.dtype is self._dtype and x.get_device() == self._dev and shape[0] >= n and \
+                st[-1] == 1 and (shape[1] == row if len(shape) == 2 else len(shape) == 3 and
+                                 shape[1] * shape[2] == row and st[1] == shape[2]):
+            # the stride of a single row says nothing
+            return x.data_ptr(), int(stride) if stride else (st[0] if shape[0] > 1 else row)
+        raise CfError(CF_ERR_INVALID_ARG,
+                      f"{what}: {x.dtype} {tuple(shape)} strides {st} on {x.device}")
 
     # Address of a pool of num_pages pages.
     def _pool(self, x, what):
         if isinstance(x, int):
             return x
-        c = self.cfg
-        page = c.page_size * self._kvrow
-        st = x.stride()
-        want = st[0] if x.dim() == 4 and x.shape[0] > 1 else (c.page_stride or page)
-        if x.dtype is not self._dtype or x.get_device() != self._dev or x.dim() != 4 or \
-                x.shape[0] != c.num_pages or x.numel() != c.num_pages * page or \
-                x.shape[3] != c.head_dim or st[3] != 1 or st[2] != c.head_dim or \
-                st[1] != x.shape[2] * c.head_dim or want != (c.page_stride or page) or \
-                x.shape[1] != (c.n_kv_heads if c.layout else c.page_size):
-            raise CfError(CF_ERR_INVALID_ARG,
-                          f"{what}: {x.dtype} {tuple(x.shape)} strides {st} on {x.device}")
-        return x.data_ptr()
+        if x.dtype is self._dtype and x.get_device() == self._dev and x.shape == self._pool_shape \
+                and (x.stride() == self._pool_stride or
+                     (self.cfg.num_pages == 1 and x.stride()[1:] == self._pool_stride[1:])):
+            return x.data_ptr()
+        raise CfError(CF_ERR_INVALID_ARG,
+                      f"{what}: {x.dtype} {tuple(x.shape)} strides {x.stride()} on {x.device}")
+
+    # The stream given, or torch's current one on the handle's device.
+    def _on(self, stream):
+        return self._raw_stream(self._dev) if stream is None else _stream(stream)
 
     def append(self, batch, n_tokens, q, k, v, q_start, kv_len, page_table, k_pages, v_pages,
                q_out, rope_pos=None, q_stride=None, kv_stride=None, q_out_stride=None,
@@ -611,7 +616,7 @@ class PagedKv:
             self._at(rope_pos, i32, axes * n_tokens, "rope_pos"),
             self._at(page_table, i32, batch * c.max_pages, "page_table"),
             self._pool(k_pages, "k_pages"), self._pool(v_pages, "v_pages"), op, os_,
-            _stream(stream))
+            self._on(stream))
         if rc != CF_OK:
             raise CfError(rc, "cf_paged_append")
         return q_out
@@ -627,7 +632,7 @@ class PagedKv:
             self._at(page_table, i32, batch * c.max_pages, "page_table"),
             self._pool(k_pages, "k_pages"), self._pool(v_pages, "v_pages"), window, n_sinks,
             self._at(out, self._dtype, n_tokens * self._qrow, "out"),
-            self._at(lse, self._f32, n_tokens * c.n_q_heads, "lse"), _stream(stream))
+            self._at(lse, self._f32, n_tokens * c.n_q_heads, "lse"), self._on(stream))
         if rc != CF_OK:
             raise CfError(rc, "cf_paged_attention")
         return out
@@ -646,7 +651,7 @@ class PagedKv:
             self._at(prefix_table, i32, -(-prefix_len // c.page_size), "prefix_table"),
             prefix_len, self._pool(k_pages, "k_pages"), self._pool(v_pages, "v_pages"),
             self._at(out, self._dtype, n_tokens * self._qrow, "out"),
-            self._at(lse, self._f32, n_tokens * c.n_q_heads, "lse"), _stream(stream))
+            self._at(lse, self._f32, n_tokens * c.n_q_heads, "lse"), self._on(stream))
         if rc != CF_OK:
             raise CfError(rc, "cf_paged_prefix_attention")
         return out

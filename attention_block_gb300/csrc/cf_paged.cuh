@@ -179,18 +179,16 @@ __device__ __forceinline__ long long div_units(long long a, long long b) {
   return a / b;
 }
 
-// Partial states of one item: the pieces first .. first + n - 1.
+// Slots of one item's partial states, in the order of its n pieces.
 struct PagedItemParts {
-  long long i0, upc, first;
-  int n;
-  __device__ __forceinline__ PagedItemParts(long long i0_, long long tiles, long long upc_)
-      : i0(i0_), upc(upc_), first(div_units(i0_, upc_)) {
-    n = (int)(div_units(i0_ + tiles - 1, upc_) - first) + 1;
+  int first, odd, n;
+  __device__ __forceinline__ PagedItemParts(long long i0, long long tiles, long long upc) {
+    const long long c = div_units(i0, upc);
+    first = (int)(2 * c);
+    odd = c * upc >= i0 ? 0 : 1;  // later pieces all begin behind i0
+    n = (int)(div_units(i0 + tiles - 1, upc) - c) + 1;
   }
-  __device__ __forceinline__ long long slot(int k) const {
-    const long long c = first + k;
-    return 2 * c + (c * upc >= i0 ? 0 : 1);
-  }
+  __device__ __forceinline__ int slot(int k) const { return first + 2 * k + (k == 0 ? odd : 0); }
 };
 
 // The shared prefix's states, as the kernels that join them to the sequences'
@@ -215,7 +213,7 @@ struct PagedRowParts {
                                            long long state_)
       : parts(p), rows(rows_), r(r_), n(p.n), state(state_) {}
   __device__ __forceinline__ long long row(int k) const {
-    return n == 1 ? state : parts.slot(k) * rows + r;
+    return n == 1 ? state : (long long)parts.slot(k) * rows + r;
   }
 };
 __device__ __forceinline__ PagedRowParts paged_prefix_row(const PagedPrefixParts& x,
@@ -246,16 +244,26 @@ struct PagedState4 {
 
 // Joins a row's states into s: the D / 4 lanes that share the row call it
 // together, each for its 4 columns at `col`.  Each lane fetches one part's
-// maximum and sum, so all parts' values are on their way at once.
+// maximum and sum, and the parts' values come eight at a time, the first
+// eight together with the maxima.
 template <int D>
 __device__ __forceinline__ void paged_join_row(PagedState4& s, const float* o, const float2* ml,
                                                const PagedRowParts& x, int col) {
-  constexpr int W = D / 4;
+  constexpr int W = D / 4, B = 8;
   const int lane = threadIdx.x & 31, gl = lane % W;
   const uint32_t mask = W == 32 ? ~0u : 0xffffu << (lane & 16);
   for (int k0 = 0; k0 < x.n; k0 += W) {
+    const int n = min(W, x.n - k0);
     float2 v = make_float2(-INFINITY, 0.f);
-    if (k0 + gl < x.n) v = __ldcg(ml + x.row(k0 + gl));
+    if (gl < n) v = __ldcg(ml + x.row(k0 + gl));
+    float4 y[B];
+    auto fetch = [&](int k) {
+#pragma unroll
+      for (int i = 0; i < B; ++i)
+        y[i] = k + i < n ? __ldcg(reinterpret_cast<const float4*>(o + x.row(k0 + k + i) * D + col))
+                         : make_float4(0.f, 0.f, 0.f, 0.f);
+    };
+    fetch(0);
     float mx = v.x;
 #pragma unroll
     for (int d = W / 2; d >= 1; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(mask, mx, d));
@@ -267,15 +275,16 @@ __device__ __forceinline__ void paged_join_row(PagedState4& s, const float* o, c
     s.m = mn;
     s.l = s.l * a + l;
     s.o = make_float4(s.o.x * a, s.o.y * a, s.o.z * a, s.o.w * a);
-    const int n = min(W, x.n - k0);
-#pragma unroll 8
-    for (int k = 0; k < n; ++k) {
-      const float wk = __shfl_sync(mask, w, k, W);
-      const float4 y = __ldcg(reinterpret_cast<const float4*>(o + x.row(k0 + k) * D + col));
-      s.o.x = fmaf(y.x, wk, s.o.x);
-      s.o.y = fmaf(y.y, wk, s.o.y);
-      s.o.z = fmaf(y.z, wk, s.o.z);
-      s.o.w = fmaf(y.w, wk, s.o.w);
+    for (int k = 0; k < n; k += B) {
+      if (k) fetch(k);
+#pragma unroll
+      for (int i = 0; i < B; ++i) {
+        const float wk = __shfl_sync(mask, w, (k + i) % W, W);
+        s.o.x = fmaf(y[i].x, wk, s.o.x);
+        s.o.y = fmaf(y[i].y, wk, s.o.y);
+        s.o.z = fmaf(y[i].z, wk, s.o.z);
+        s.o.w = fmaf(y[i].w, wk, s.o.w);
+      }
     }
   }
 }
@@ -340,8 +349,7 @@ enum PagedMode { kOwn = 0, kPrefix = 1, kOwnAfterPrefix = 2 };
 struct PagedSplit {
   PagedParts parts;
   void* list = nullptr;    // items for a joining kernel
-  int* counter = nullptr;  // words that are zero between calls
-  int* tickets = nullptr;  // one such word per (sequence, KV head)
+  int* tickets = nullptr;  // a word per (sequence, KV head), zero between calls
   int grid = 0;            // resident blocks
 };
 
@@ -351,12 +359,12 @@ bool paged_attn_simple_launch(int dtype, const PagedAttnParams& p, cudaStream_t 
 
 // The kernel for few rows (tokens x grouped heads), and the one on the fifth
 // generation's tensor cores for many.  grid: resident blocks, 0 on failure;
-// part_rows and list_bytes: workspace; launch with kPrefix: the call's tokens
+// part_rows and
+// list_bytes: workspace; launch with kPrefix: the call's tokens
 // against the prefix alone; prefix: how such a launch cuts it.
 constexpr int kFewRows = 16;
 int paged_few_grid(int dtype, int head_dim, int sm_count);
 long long paged_few_part_rows(int grid);
-size_t paged_few_list_bytes(long long items);
 PagedPrefixParts paged_few_prefix(const PagedAttnParams& p, const PagedSplit& ws);
 bool paged_few_launch(int dtype, const PagedAttnParams& p, const PagedSplit& ws, PagedMode mode,
                       const PagedPrefixParts& pre, cudaStream_t st);

@@ -254,17 +254,15 @@ int cf_paged_create(const cf_paged_config* cfg, cf_paged_handle** out) {
   // The words that start at zero, then the lists, then two sets of states:
   // of the sequences' own keys and of the prefix.  A call uses one attention
   // kernel for each, so the kernels share them.
-  const size_t counters = take(2 * 4);
   const size_t tickets = take(c.dtype != CF_F32 ? (size_t)c.max_batch * c.n_kv_heads * 4 : 4);
   const size_t zero = bytes;
   const int64_t all_rows = (int64_t)c.max_tokens * c.n_q_heads;
-  size_t few_list = 0, tc_list = 0, at_o[2] = {0, 0}, at_ml[2] = {0, 0};
+  size_t tc_list = 0, at_o[2] = {0, 0}, at_ml[2] = {0, 0};
   const int64_t few_rows = (int64_t)c.max_batch * c.n_kv_heads * kFewRows;
   int64_t slot_rows = 0;
   if (c.dtype != CF_F32) {
     h->few.grid = paged_few_grid(c.dtype, c.head_dim, h->sm_count);
     if (h->few.grid == 0) return fail(CF_ERR_CUDA);
-    few_list = take(paged_few_list_bytes((long long)c.max_batch * c.n_kv_heads));
     slot_rows = paged_few_part_rows(h->few.grid);
     if ((int64_t)c.max_tokens * h->geom.G > kFewRows) {
       h->tc.grid = paged_tc_grid(c.dtype, c.head_dim, h->sm_count);
@@ -296,8 +294,6 @@ int cf_paged_create(const cf_paged_config* cfg, cf_paged_handle** out) {
   const PagedParts prefix = {reinterpret_cast<float*>(ws + at_o[1]),
                              reinterpret_cast<float2*>(ws + at_ml[1]), slot_rows, 1};
   h->few.parts = h->tc.parts = own;
-  h->few.list = ws + few_list;
-  h->few.counter = reinterpret_cast<int*>(ws + counters);
   h->few.tickets = reinterpret_cast<int*>(ws + tickets);
   h->tc.list = ws + tc_list;
   h->few_prefix.parts = h->tc_prefix.parts = prefix;

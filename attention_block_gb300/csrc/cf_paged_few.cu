@@ -44,8 +44,7 @@ struct Shape {
   static_assert(ROWS <= RING && SMEM <= 224 * 1024, "shared memory");
 };
 
-// What is left of an item at a warp's end, in shared memory; and an item for
-// the kernel that joins the prefix.
+// An item, as far as those need it that join its parts.
 struct alignas(16) FewItem {
   long long i0;
   int tiles, t0, p0, n, b, h;
@@ -106,8 +105,6 @@ struct FewArgs {
   PagedAttnParams p;
   PagedPrefixParts pre;
   PagedParts ws;
-  FewItem* list;
-  int* counter;   // items listed, joining blocks done
   int* tickets;   // per item: parts written so far
   int row_limit;  // rows per item, at most
 };
@@ -135,8 +132,9 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   using M = MmaKind<T>;
   const PagedAttnParams& p = a.p;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ long long s_first[32];  // first unit of every eighth thread's sequences
+  __shared__ long long s_first[kFewThreads];  // first unit of each thread's sequences
   __shared__ long long s_scan[kFewWarps];
+  __shared__ int s_top[kFewWarps];
   __shared__ uint32_t s_valid[kFewWarps][2];
   // per warp: the part of an item that began before its run (F), and of one
   // that goes on behind it (L; if it also began before, there is no F)
@@ -147,7 +145,9 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int gq = lane >> 2, tq = lane & 3;
 
-  pdl_wait();
+  // After a prefix launch this one reads only what that launch has waited for
+  // already, so it starts beside its last blocks and waits for it at the end.
+  if constexpr (MODE != kOwnAfterPrefix) pdl_wait();
   pdl_trigger();
 
   // Units of every sequence, summed up over the batch: each thread has a run
@@ -155,52 +155,86 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   const int nseq = PRE ? 1 : p.batch;
   const int per = (nseq + kFewThreads - 1) / kFewThreads;
   long long mine = 0;
-  for (int b = tid * per; b < min(nseq, (tid + 1) * per); ++b)
-    mine += (long long)work_of<KS, PRE>(p, b).tiles * p.g.nkv;
+  int top = 0;  // units of the longest item
+  for (int b = tid * per; b < min(nseq, (tid + 1) * per); ++b) {
+    const int t = work_of<KS, PRE>(p, b).tiles;
+    mine += (long long)t * p.g.nkv;
+    top = max(top, t);
+  }
+  top = __reduce_max_sync(~0u, top);
   long long incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const long long v = __shfl_up_sync(~0u, incl, o);
     if (lane >= o) incl += v;
   }
-  if (lane == 31) s_scan[warp] = incl;
+  if (lane == 31) {
+    s_scan[warp] = incl;
+    s_top[warp] = top;
+  }
   __syncthreads();
   long long before = incl - mine, total = 0;
 #pragma unroll
   for (int w = 0; w < kFewWarps; ++w) {
     if (w < warp) before += s_scan[w];
     total += s_scan[w];
+    top = max(top, s_top[w]);
   }
-  if (tid % kFewWarps == 0) s_first[tid / kFewWarps] = before;
-  const int workers = gridDim.x * kFewWarps, me = blockIdx.x * kFewWarps + warp;
-  const long long upc = PRE ? a.pre.upc / kFewWarps : div_units(total + workers - 1, workers);
-  const long long block_upc = upc * kFewWarps;
-  if (blockIdx.x * block_upc >= total) return;
+  s_first[tid] = before;
+  const long long block_upc =
+      PRE ? a.pre.upc : div_units(total + gridDim.x * kFewWarps - 1, gridDim.x * kFewWarps) * kFewWarps;
   if (lane == 0) s_has[0][warp] = s_has[1][warp] = 0;
   __syncthreads();
 
-  // The start of this warp's run.
-  Cursor<KS, PRE> cur;
-  cur.u = me * upc;
-  cur.end = min(total, cur.u + upc);
-  if (cur.u < cur.end) {
+  // A cursor at unit u of the line.
+  auto locate = [&](Cursor<KS, PRE>& c, long long u) {
     // the last run of sequences that begins at or before unit u
-    const int n = __popc(__ballot_sync(~0u, s_first[lane] <= cur.u));
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < kFewThreads / 32; ++i)
+      n += __popc(__ballot_sync(~0u, s_first[i * 32 + lane] <= u));
     long long at = s_first[n - 1];
-    int b = (n - 1) * kFewWarps * per;
+    int b = (n - 1) * per;
     while (true) {
-      cur.w = work_of<KS, PRE>(p, b);
-      const long long len = (long long)cur.w.tiles * p.g.nkv;
-      if (cur.u < at + len) break;
+      c.w = work_of<KS, PRE>(p, b);
+      const long long len = (long long)c.w.tiles * p.g.nkv;
+      if (u < at + len) break;
       at += len;
       ++b;
     }
-    cur.b = b;
-    const long long off = cur.u - at;
-    cur.h = (int)div_units(off, cur.w.tiles);
-    cur.tile = (int)(off - (long long)cur.h * cur.w.tiles);
-    cur.i0 = cur.u - cur.tile;
+    c.b = b;
+    const long long off = u - at;
+    c.h = (int)div_units(off, c.w.tiles);
+    c.tile = (int)(off - (long long)c.h * c.w.tiles);
+    c.i0 = u - c.tile;
+    c.u = u;
+  };
+  // This block's units.  Where items are short, by themselves or beside a
+  // block's share, a block takes the items that begin in its share, whole:
+  // one item more at most, and nothing to join across blocks.  That takes about
+  // 4 us for 4 rows and 10 us for 16, the time of 24 and 60 units.
+  Cursor<KS, PRE> cur;
+  long long lo = min(total, blockIdx.x * block_upc), hi = min(total, lo + block_upc);
+  const bool snap = !PRE && block_upc >= 3LL * top && (top <= 16 + 2 * a.row_limit || block_upc >= 8LL * top);
+  if (snap) {
+    if (lo < total) {
+      locate(cur, lo);
+      if (cur.tile) lo = cur.i0 + cur.w.tiles;
+    }
+    if (hi < total) {
+      locate(cur, hi);
+      if (cur.tile) hi = cur.i0 + cur.w.tiles;
+    }
   }
+  if (lo >= hi) {
+    if constexpr (MODE == kOwnAfterPrefix) pdl_wait();
+    return;
+  }
+  // and this warp's run of them
+  const int run = (int)((hi - lo + kFewWarps - 1) / kFewWarps);
+  cur.u = lo + (long long)warp * run;
+  cur.end = min(hi, cur.u + run);
+  if (cur.u < cur.end) locate(cur, cur.u);
 
   const char* kbase = static_cast<const char*>(p.k_pages);
   const char* vbase = static_cast<const char*>(p.v_pages);
@@ -348,6 +382,10 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     if (valid) {
       // mask, running maximum
       const int j0 = cur.w.base(cur.tile);
+      // do the rows see different parts of this tile?
+      const bool edge = !PRE && cur.w.n > 1 &&
+                        (j0 + KS - 1 > cur.w.p0 ||
+                         (p.window != 0 && cur.w.p0 + cur.w.n - 1 - j0 >= p.window));
       float mx[2] = {m[0], m[1]};
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -355,8 +393,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         for (int e = 0; e < 4; ++e) {
           const int jj = nt * 8 + 2 * tq + (e & 1);
           bool see = (valid >> jj) & 1;
-          if (!PRE && cur.w.n > 1)
-            see = see && paged_visible(pos[e >> 1], j0 + jj, p.window, p.n_sinks);
+          if (edge) see = see && paged_visible(pos[e >> 1], j0 + jj, p.window, p.n_sinks);
           c[nt][e] = see ? c[nt][e] * p.scale_log2 : -INFINITY;
           mx[e >> 1] = fmaxf(mx[e >> 1], c[nt][e]);
         }
@@ -470,7 +507,6 @@ __global__ void __launch_bounds__(kFewThreads, 1)
           __stcg(reinterpret_cast<float2*>(a.ws.o + at * D + 8 * k + 2 * tq),
                  make_float2(o[k][2 * r], o[k][2 * r + 1]));
       }
-      if (!PRE && lane == 0) a.list[atomicAdd(a.counter, 1)] = it;
     } else {
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
@@ -520,6 +556,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   if (tid < 2) s_last[tid] = 0;
   FewItem cut[2];                 // items that go on in other blocks: the first's, the last's
   bool has_cut[2] = {false, false};
+  int task = 0;
   for (int w0 = 0, k0 = 0; w0 < kFewWarps;) {
     if (!s_has[k0][w0]) {
       w0 += k0;
@@ -532,10 +569,13 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       ++last;
       kind = s_has[0][last] ? 0 : 1;
     }
-    const bool here = it.i0 >= blockIdx.x * block_upc;  // begins in this block
-    const long long slot = 2 * (long long)blockIdx.x + (blockIdx.x * block_upc >= it.i0 ? 0 : 1);
-    for (int x = tid; x < it.n * p.g.G * C4; x += kFewThreads) {
-      const int row = x / C4, col = (x - row * C4) * 4;
+    const bool here = it.i0 >= lo;  // begins in this block
+    const long long slot = 2 * (long long)blockIdx.x + (lo >= it.i0 ? 0 : 1);
+    // rows are dealt out to the warps across items
+    const int nrows = it.n * p.g.G, col = (lane % C4) * 4;
+    for (int row0 = 0; row0 < nrows; row0 += 32 / C4, ++task) {
+      const int row = row0 + lane / C4;
+      if (task % kFewWarps != warp || row >= nrows) continue;
       PagedState4 s{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
       for (int w = w0; w <= last; ++w) {
         const int k = w == last ? kind : 1;
@@ -554,28 +594,24 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     if (!here || kind != 0) {
       cut[here ? 1 : 0] = it;
       has_cut[here ? 1 : 0] = true;
-    } else if (MODE == kOwnAfterPrefix && tid == 0) {
-      a.list[atomicAdd(a.counter, 1)] = it;
     }
     // on to what follows that part: after an F its warp's L, if any
     w0 = kind == 0 ? last : kFewWarps;
     k0 = 1;
   }
+  if constexpr (MODE == kOwnAfterPrefix) pdl_wait();
   if (PRE || !(has_cut[0] || has_cut[1])) return;
   __syncthreads();
-  if (tid == 0) {
+  if (tid < 2 && has_cut[tid]) {
     __threadfence();
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      if (!has_cut[i]) continue;
-      const PagedItemParts parts(cut[i].i0, cut[i].tiles, block_upc);
-      int* ticket = a.tickets + (long long)cut[i].b * p.g.nkv + cut[i].h;
-      if (atomicAdd(ticket, 1) != parts.n - 1) continue;
+    const FewItem it = cut[tid];
+    const PagedItemParts parts(it.i0, it.tiles, block_upc);
+    int* ticket = a.tickets + (long long)it.b * p.g.nkv + it.h;
+    if (atomicAdd(ticket, 1) == parts.n - 1) {
       *ticket = 0;
-      s_last[i] = 1;
-      if (MODE == kOwnAfterPrefix) a.list[atomicAdd(a.counter, 1)] = cut[i];
+      s_last[tid] = 1;
+      __threadfence();
     }
-    __threadfence();
   }
   __syncthreads();
 #pragma unroll
@@ -591,35 +627,34 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   }
 }
 
-// Joins the listed items' states and the prefix's, a row per D / 4 lanes.
+// Joins the own states of every row and the prefix's: a row per D / 4 lanes.
 template <typename T, int D>
-__global__ void __launch_bounds__(kJoinThreads)
+__global__ void __launch_bounds__(kJoinThreads, 2)
     paged_few_join_kernel(const __grid_constant__ FewArgs a) {
   constexpr int W = D / 4, NG = kJoinThreads / W;
   const PagedAttnParams& p = a.p;
   const int tid = threadIdx.x, col = (tid % W) * 4;
   pdl_wait();
   pdl_trigger();
-  const long long rows = (long long)a.counter[0] * a.row_limit;
+  const long long rows = (long long)p.batch * p.g.nkv * a.row_limit;
   for (long long x = (long long)blockIdx.x * NG + tid / W; x < rows; x += (long long)gridDim.x * NG) {
-    const long long item = div_units(x, a.row_limit);
-    const int row = (int)(x - item * a.row_limit);
-    const FewItem it = a.list[item];
-    if (row >= it.n * p.g.G) continue;
+    const long long pair = div_units(x, a.row_limit);
+    const int row = (int)(x - pair * a.row_limit);
+    FewItem it;
+    it.b = (int)div_units(pair, p.g.nkv);
+    it.h = (int)(pair - (long long)it.b * p.g.nkv);
+    const PagedSeq q = paged_seq(p.q_start, p.kv_len, it.b, p.n_tokens, p.max_q, p.g, p.errflag);
+    // (a sequence with more tokens than the call allows is written already)
+    if (row >= q.n * p.g.G || q.n > p.max_q) continue;
+    it.t0 = q.t0;
     const long long at = state_row(a, it, row);
     const float2 ml = __ldcg(a.ws.ml + at);
     PagedState4 s{ml.x, ml.y, __ldcg(reinterpret_cast<const float4*>(a.ws.o + at * D + col))};
     const int i = row / p.g.G;
-    if (it.p0 + i >= 0)
+    if (q.len - q.n + i >= 0)
       paged_join_row<D>(s, a.pre.o, a.pre.ml,
                         paged_prefix_row(a.pre, p.g, it.t0 + i, it.h, row - i * p.g.G), col);
     paged_store4<T, D>(s, p.out, p.lse, out_row(p, it, row), col);
-  }
-  // the last block out empties the list for the next call
-  __syncthreads();
-  if (tid == 0 && atomicAdd(a.counter + 1, 1) == (int)gridDim.x - 1) {
-    a.counter[0] = 0;
-    a.counter[1] = 0;
   }
 }
 
@@ -669,8 +704,6 @@ int cf::paged_few_grid(int dtype, int head_dim, int sm_count) {
 
 long long cf::paged_few_part_rows(int grid) { return 2LL * grid * kFewRows; }
 
-size_t cf::paged_few_list_bytes(long long items) { return (size_t)items * sizeof(FewItem); }
-
 PagedPrefixParts cf::paged_few_prefix(const PagedAttnParams& p, const PagedSplit& ws) {
   const int KS = p.g.D == 64 ? Shape<64>::KS : Shape<128>::KS;
   const long long warps = (long long)ws.grid * kFewWarps;
@@ -692,8 +725,6 @@ bool cf::paged_few_launch(int dtype, const PagedAttnParams& p, const PagedSplit&
   a.p = p;
   a.pre = pre;
   a.ws = ws.parts;
-  a.list = static_cast<FewItem*>(ws.list);
-  a.counter = ws.counter;
   a.tickets = ws.tickets;
   a.row_limit = std::min(kFewRows, p.max_q * p.g.G);
   void* args[] = {&a};
