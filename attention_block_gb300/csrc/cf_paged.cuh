@@ -321,6 +321,24 @@ __device__ __forceinline__ void quad_transpose(uint32_t (&w)[4], int q) {
   }
 }
 
+template <typename T>
+struct MmaExp;  // exponent bits of a 16-bit type
+template <>
+struct MmaExp<__half> {
+  static constexpr uint32_t mask = 0x7c00u;
+};
+template <>
+struct MmaExp<__nv_bfloat16> {
+  static constexpr uint32_t mask = 0x7f80u;
+};
+
+// Whether one of the two 16-bit values in w is an infinity or NaN.
+template <typename T>
+__device__ __forceinline__ bool nonfinite2(uint32_t w) {
+  const uint32_t e = MmaExp<T>::mask;
+  return (w & e) == e || ((w >> 16) & e) == e;
+}
+
 // 2^x, off by 2 ulp; results below 2^-126 are 0.
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -341,6 +359,79 @@ __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// One row of attention by one warp on the CUDA cores: the row at position pos
+// of sequence b sees, in one list, the prefix, its sinks and its window.  A
+// lane forms the whole dot product of one key; then every lane sums its
+// columns of 32 weighted values.  Masked positions are never loaded.  The
+// warp takes the chunks of 32 keys w, w + step, ..; q: the row's query in
+// fp32, shared memory.
+template <typename T, int D>
+struct PagedRow {
+  static constexpr int E = D / 32;  // columns of a lane
+  float m, l, o[E];                 // running maximum (base 2), the lane's share of the sum, o
+  __device__ __forceinline__ void run(const PagedAttnParams& p, const float* q, int b, int pos,
+                                      int len, int kvh, int w, int step) {
+    constexpr int W = 16 / sizeof(T);
+    const int lane = threadIdx.x & 31;
+    const PagedRange r = paged_range(pos, pos, len, p.window, p.n_sinks);
+    const int pre = pos < 0 ? 0 : p.prefix_len;
+    const int total = pos < 0 ? 0 : pre + r.sink + (r.hi - r.lo);
+    const int* table = p.page_table + (int64_t)b * p.g.max_pages;
+    m = -INFINITY;
+    l = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = 0.f;
+    for (int base = w * 32; base < total; base += step * 32) {
+      int idx = base + lane;
+      int64_t off = -1;  // no page: zeros stand for the key and the value
+      float sc = -INFINITY;
+      if (idx < total) {
+        sc = 0.f;
+        if (idx < pre) {
+          off = paged_offset(p.prefix_table, idx, p.g, p.errflag);
+        } else {
+          idx -= pre;
+          off = paged_offset(table, idx < r.sink ? idx : r.lo + idx - r.sink, p.g, p.errflag);
+        }
+      }
+      if (off >= 0) {
+        off += (int64_t)kvh * p.g.head_stride;
+        const T* k = static_cast<const T*>(p.k_pages) + off;
+        float acc = 0.f;
+#pragma unroll 4
+        for (int i = 0; i < D; i += W) {
+          float f[W];
+          load_cvt<T, W>(k + i, f);
+#pragma unroll
+          for (int e = 0; e < W; ++e) acc = fmaf(f[e], q[i + e], acc);
+        }
+        sc = acc * p.scale_log2;
+      }
+      float mx = sc;
+#pragma unroll
+      for (int d = 16; d >= 1; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, d));
+      const float m_new = fmaxf(m, mx);
+      const float ref = m_new == -INFINITY ? 0.f : m_new;
+      const float pr = exp2f(sc - ref), corr = exp2f(m - ref);
+      m = m_new;
+      l = l * corr + pr;
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] *= corr;
+      const int n = min(32, total - base);
+      for (int k = 0; k < n; ++k) {
+        const int64_t vo = __shfl_sync(~0u, off, k);
+        const float wk = __shfl_sync(~0u, pr, k);
+        if (vo < 0) continue;
+        float f[E];
+        load_cvt<T, E>(static_cast<const T*>(p.v_pages) + vo + lane * E, f);
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = fmaf(wk, f[e], o[e]);
+      }
+    }
+    l = warp_sum(l);
+  }
+};
+
 // What a launch attends to: the sequences' own keys; the shared prefix (it
 // leaves states only); own keys, joined with the prefix's states.
 enum PagedMode { kOwn = 0, kPrefix = 1, kOwnAfterPrefix = 2 };
@@ -349,7 +440,8 @@ enum PagedMode { kOwn = 0, kPrefix = 1, kOwnAfterPrefix = 2 };
 struct PagedSplit {
   PagedParts parts;
   void* list = nullptr;    // items for a joining kernel
-  int* tickets = nullptr;  // a word per (sequence, KV head), zero between calls
+  int* tickets = nullptr;  // words that are zero between calls: few rows, one per (sequence,
+                           // KV head); many, two
   int grid = 0;            // resident blocks
 };
 
@@ -372,7 +464,7 @@ bool paged_few_launch(int dtype, const PagedAttnParams& p, const PagedSplit& ws,
 constexpr int kTcRows = 256;
 int paged_tc_grid(int dtype, int head_dim, int sm_count);
 long long paged_tc_part_rows(int grid);
-size_t paged_tc_list_bytes(int grid);
+size_t paged_tc_list_bytes(int grid, long long row_tiles);
 PagedPrefixParts paged_tc_prefix(const PagedAttnParams& p, const PagedSplit& ws);
 bool paged_tc_launch(int dtype, const PagedAttnParams& p, const PagedSplit& ws, PagedMode mode,
                      const PagedPrefixParts& pre, cudaStream_t st);

@@ -362,6 +362,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     const uint32_t valid = s_valid[warp][pair];
     const uint32_t ks = ring_s + 2 * pair * S::SLOT, vs = ks + S::SLOT;
     float c[NT][4];
+    bool edge = false;  // do the rows see different parts of this tile?
     if (valid) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
@@ -382,8 +383,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     if (valid) {
       // mask, running maximum
       const int j0 = cur.w.base(cur.tile);
-      // do the rows see different parts of this tile?
-      const bool edge = !PRE && cur.w.n > 1 &&
+      edge = !PRE && cur.w.n > 1 &&
                         (j0 + KS - 1 > cur.w.p0 ||
                          (p.window != 0 && cur.w.p0 + cur.w.n - 1 - j0 >= p.window));
       float mx[2] = {m[0], m[1]};
@@ -425,6 +425,55 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     cp_wait<3>();  // V has landed
     __syncwarp();
     if (valid) {
+      // Where rows see different parts of a tile, an infinity or NaN in V that
+      // one row sees would reach the others as 0 * inf: such a tile is summed
+      // without the tensor cores, by the rows that see it.
+      bool apart = false;
+      if (edge) {
+        bool bad = false;
+#pragma unroll
+        for (int i = 0; i < S::SLOT / 512; ++i) {
+          uint32_t w[4];
+          asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                       : "r"(vs + (i * 32 + lane) * 16));
+#pragma unroll
+          for (int e = 0; e < 4; ++e) bad |= nonfinite2<T>(w[e]);
+        }
+        apart = __any_sync(~0u, bad);
+      }
+      if (apart) {
+        const int j0 = cur.w.base(cur.tile);
+#pragma unroll
+        for (int x = 0; x < NT * 2; ++x) {
+#pragma unroll 1
+          for (int q = 0; q < 4; ++q) {
+            const int jj = (x >> 1) * 8 + 2 * q + (x & 1);
+            const float w0 = __shfl_sync(~0u, c[x >> 1][x & 1], gq * 4 + q);
+            const float w1 = __shfl_sync(~0u, c[x >> 1][2 + (x & 1)], gq * 4 + q);
+            const bool there = (valid >> jj) & 1;
+            const bool s0 = there && paged_visible(pos[0], j0 + jj, p.window, p.n_sinks);
+            const bool s1 = there && paged_visible(pos[1], j0 + jj, p.window, p.n_sinks);
+#pragma unroll
+            for (int k = 0; k < NO; ++k) {
+              uint32_t v;
+              asm volatile("ld.shared.u32 %0, [%1];"
+                           : "=r"(v)
+                           : "r"(vs + jj * (D * 2) + ((k ^ (jj & 7)) << 4) + tq * 4));
+              float f[2];
+              Elem<T>::words(&v, 1, f);
+              if (s0) {
+                o[k][0] = fmaf(w0, f[0], o[k][0]);
+                o[k][1] = fmaf(w0, f[1], o[k][1]);
+              }
+              if (s1) {
+                o[k][2] = fmaf(w1, f[0], o[k][2]);
+                o[k][3] = fmaf(w1, f[1], o[k][3]);
+              }
+            }
+          }
+        }
+      } else {
       // o += P V; bf16 probabilities enter as hi + lo pairs (the tensor cores
       // have the time), fp16 ones with their 11 bits
 #pragma unroll
@@ -446,6 +495,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             M::mma(o[2 * n2 + 1], lo, r2, r3);
           }
         }
+      }
       }
     }
     __syncwarp();

@@ -1,11 +1,10 @@
 // cf_paged_simple.cu -- attention over the paged cache on the CUDA cores.
 //
-// One block of four warps per (token, query head).  The keys the row sees
-// form one list (prefix, sinks, window); the warps take chunks of 32 of it in
-// turn.  A lane forms the whole dot product of one key; then every lane sums
-// its columns of the 32 weighted values.  Each warp keeps a running maximum
-// and sum (online softmax, base 2) and the four states are joined at the end.
-// Masked positions are never loaded.
+// One block of four warps per (token, query head); the warps take chunks of 32
+// of the keys that the row sees in turn (PagedRow), keep a running maximum and
+// sum each (online softmax, base 2), and the four states are joined at the
+// end.  fp32 storage has no tensor-core form that keeps its precision; this
+// one is for checking models, and bound by the CUDA cores and latency.
 #include <cuda_runtime.h>
 
 #include <cfloat>
@@ -21,8 +20,7 @@ constexpr int kSimpleWarps = 4;
 template <typename T, int D>
 __global__ void __launch_bounds__(kSimpleWarps * 32)
     paged_attn_simple_kernel(const __grid_constant__ PagedAttnParams p) {
-  constexpr int E = D / 32;       // columns of a lane
-  constexpr int W = 16 / sizeof(T);
+  constexpr int E = D / 32;  // columns of a lane
   __shared__ float s_q[D];
   __shared__ float s_o[kSimpleWarps][D];
   __shared__ float s_m[kSimpleWarps], s_l[kSimpleWarps];
@@ -49,70 +47,14 @@ __global__ void __launch_bounds__(kSimpleWarps * 32)
       paged_seq(p.q_start, p.kv_len, b, p.n_tokens, p.max_q, p.g, p.errflag);
   if (s.n <= 0) return;
   const int pos = s.len - s.n + (int)(t - s.t0);
-  const bool bad = s.n > p.max_q || s.len == 0;
-  const PagedRange r = paged_range(pos, pos, s.len, p.window, p.n_sinks);
-  const int own = pos < 0 || bad ? 0 : r.sink + (r.hi - r.lo);
-  const int pre = pos < 0 ? 0 : p.prefix_len;
-  const int total = pre + own;
-  const int* table = p.page_table + (int64_t)b * p.g.max_pages;
-
-  float m = -INFINITY, l = 0.f, o[E];
+  // (a sequence with more tokens than the call allows has length 0: pos < 0)
+  PagedRow<T, D> x;
+  x.run(p, s_q, b, pos, s.len, kvh, warp, kSimpleWarps);
 #pragma unroll
-  for (int e = 0; e < E; ++e) o[e] = 0.f;
-  for (int base = warp * 32; base < total; base += kSimpleWarps * 32) {
-    int idx = base + lane;
-    int64_t off = -1;  // no page: zeros stand for the key and the value
-    float sc = -INFINITY;
-    if (idx < total) {
-      sc = 0.f;
-      if (idx < pre) {
-        off = paged_offset(p.prefix_table, idx, p.g, p.errflag);
-      } else {
-        idx -= pre;
-        off = paged_offset(table, idx < r.sink ? idx : r.lo + idx - r.sink, p.g, p.errflag);
-      }
-    }
-    if (off >= 0) {
-      off += (int64_t)kvh * p.g.head_stride;
-      const T* k = static_cast<const T*>(p.k_pages) + off;
-      float acc = 0.f;
-#pragma unroll 4
-      for (int i = 0; i < D; i += W) {
-        float f[W];
-        load_cvt<T, W>(k + i, f);
-#pragma unroll
-        for (int e = 0; e < W; ++e) acc = fmaf(f[e], s_q[i + e], acc);
-      }
-      sc = acc * p.scale_log2;
-    }
-    float mx = sc;
-#pragma unroll
-    for (int d = 16; d >= 1; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(~0u, mx, d));
-    const float m_new = fmaxf(m, mx);
-    const float ref = m_new == -INFINITY ? 0.f : m_new;
-    const float pr = exp2f(sc - ref), corr = exp2f(m - ref);
-    m = m_new;
-    l = l * corr + pr;
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] *= corr;
-    const int n = min(32, total - base);
-    for (int k = 0; k < n; ++k) {
-      const int64_t vo = __shfl_sync(~0u, off, k);
-      const float w = __shfl_sync(~0u, pr, k);
-      if (vo < 0) continue;
-      float f[E];
-      const T* v = static_cast<const T*>(p.v_pages) + vo + lane * E;
-      if constexpr (E * sizeof(T) >= 4) load_cvt<T, E>(v, f);
-#pragma unroll
-      for (int e = 0; e < E; ++e) o[e] = fmaf(w, f[e], o[e]);
-    }
-  }
-  l = warp_sum(l);
-#pragma unroll
-  for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = o[e];
+  for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = x.o[e];
   if (lane == 0) {
-    s_m[warp] = m;
-    s_l[warp] = l;
+    s_m[warp] = x.m;
+    s_l[warp] = x.l;
   }
   __syncthreads();
   float mt = -INFINITY;

@@ -19,7 +19,11 @@
 //             lies there reaches no product): tiles of 64-column slabs, rows
 //             of 128 bytes, the 16-byte chunks of a row swizzled
 //   12        one thread issues S = Q K^T (operands in shared memory) and
-//             O += P V (P from TMEM, V as an N-major operand)
+//             O += P V (P from TMEM, V as an N-major operand).  Where the rows
+//             of a tile see different parts of it, the warp looks for
+//             infinities and NaN in its V, which would reach the rows that do
+//             not see them as 0 * inf: such an item is listed and computed
+//             again, row by row, by the joining kernel
 // The halves alternate: while one is in its softmax the tensor core works on
 // the other.  TMEM: S (or P) and O of both halves, 512 columns.
 //
@@ -42,14 +46,14 @@ constexpr int kTcThreads = 512;
 constexpr int kCopyThreads = 128;
 constexpr int kHalf = 128;     // rows of a half
 constexpr int kBN = 128;       // positions of a tile
-constexpr int kItemCost = 3;   // what an item costs beside its tiles, in tiles
+constexpr int kItemCost = 5;   // what an item costs beside its tiles, in tiles
 constexpr float kGrow = 8.0f;  // log2 of the growth that forces a rescale
 
 template <int D>
 struct TcShape {
   static constexpr int TILE = kBN * D * 2;                   // bytes of a K, V or Q tile
   static constexpr int SLOTS = D == 128 ? 5 : 10;            // K and V tiles in flight
-  static constexpr int SMEM = (2 + SLOTS) * TILE + 1024;     // + alignment
+  static constexpr int SMEM = (2 + SLOTS) * TILE;  // 1024-aligned; 3 KB are left for the rest
   static constexpr uint32_t S_COL = 0, O_COL = 2 * kBN;      // TMEM columns
 };
 
@@ -236,6 +240,56 @@ __device__ __forceinline__ bool tile_active(const PagedRange& r, int base) {
   return r.hi > r.lo && ((base < r.hi && base + kBN > r.lo) || base < r.sink);
 }
 
+// Whether all rows of half h see the whole tile at `base`.
+template <bool PRE>
+__device__ __forceinline__ bool half_full(const PagedAttnParams& p, int plo, int phi, int base) {
+  if constexpr (PRE) return base + kBN <= p.prefix_len;
+  return base + kBN - 1 <= plo &&
+         (p.window == 0 || phi - base < p.window || base + kBN <= p.n_sinks);
+}
+// What a launch asks about a row tile's key tiles, one by one.  V is looked
+// through where an active half does not see the tile whole.  (All rows see the
+// prefix alike.)
+template <bool PRE>
+struct TileCheck {
+  PagedRange h[2];
+  int plo[2], phi[2];
+  __device__ __forceinline__ explicit TileCheck(const RowTile& t)
+      : h{t.half[0], t.half[1]}, plo{t.plo[0], t.plo[1]}, phi{t.phi[0], t.phi[1]} {}
+  __device__ __forceinline__ bool active(int i, int base) const { return tile_active(h[i], base); }
+  // Of the tiles [lo, hi): the longest run behind the sink tiles that both
+  // halves see whole.
+  __device__ __forceinline__ void middle(const PagedAttnParams& p, int lo, int hi, int ns, int skip,
+                                         int& mid_lo, int& mid_hi) const {
+    mid_lo = max(lo, ns);
+    mid_hi = mid_lo;
+    if (h[0].hi <= h[0].lo || h[1].hi <= h[1].lo) return;
+    if constexpr (PRE) {
+      mid_hi = max(mid_lo, min(hi, p.prefix_len / kBN));
+    } else {
+      // half_full: base + kBN - 1 <= plo, and behind the window's start
+      mid_hi = (min(plo[0], plo[1]) + 1) / kBN - skip;
+      if (p.window != 0)
+        mid_lo = max(mid_lo, (max(0, max(phi[0], phi[1]) - p.window + 1) + kBN - 1) / kBN - skip);
+      mid_hi = max(mid_lo, min(hi, mid_hi));
+    }
+  }
+  // The row of the tile from which on V is looked through (a multiple of 4:
+  // the warp reads four at a time), or -1.
+  __device__ __forceinline__ int look(const PagedAttnParams& p, int base) const {
+    if constexpr (PRE) return -1;
+    const bool a0 = active(0, base), a1 = active(1, base);
+    const bool f0 = !a0 || half_full<PRE>(p, plo[0], phi[0], base);
+    const bool f1 = !a1 || half_full<PRE>(p, plo[1], phi[1], base);
+    if (f0 && f1) return -1;
+    // without a window's start in the tile, all rows see up to the first one's
+    // position
+    const int lo = a0 ? plo[0] : plo[1], hi = a1 ? phi[1] : phi[0];
+    if (p.window != 0 && hi - base >= p.window) return 0;
+    return min(kBN - 4, max(0, lo + 1 - base)) & ~3;
+  }
+};
+
 // A walk over a block's units: row tiles, KV heads, key tiles.  On the line of
 // units an item has kItemCost empty ones before its tiles, so that blocks with
 // many small items get fewer of them.
@@ -276,11 +330,18 @@ struct alignas(16) TcMeta {
   int t0, p0, rows, j, h;
 };
 
+// Items to be computed again.
+struct TcRedo {
+  int b, t0, p0, rows, j, h;
+};
+
 struct TcArgs {
   PagedAttnParams p;
   PagedPrefixParts pre;
   PagedParts ws;
   TcMeta* meta;
+  TcRedo* redo;
+  int* n_redo;  // and, next to it, blocks that are done with the list; both 0 between calls
   int slots;  // upper bound on the row tiles' numbers
 };
 
@@ -290,7 +351,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const __grid_co
   using S = TcShape<D>;
   constexpr int C = D / 8;  // 16-byte chunks of a row
   const PagedAttnParams& p = a.p;
-  extern __shared__ uint8_t smem_raw[];
+  extern __shared__ __align__(1024) uint8_t sm[];
   __shared__ long long s_scan[kTcThreads / 32];
   __shared__ TcCursor<PRE> s_cur;
   __shared__ TcCursor<PRE> s_wcur[13];  // each working warp's place: too much for registers
@@ -299,12 +360,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const __grid_co
   __shared__ __align__(8) uint64_t s_sfull[2], s_pfull[2], s_ofull[2];
   __shared__ uint32_t s_tmem;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                           ~uintptr_t(1023));
   const uint32_t sq = smem_u32(sm);                   // Q, two tiles
   const uint32_t skv = sq + 2 * S::TILE;              // K and V slots
   int* err = p.errflag;
 
+  if (sq & 1023u) {  // the swizzle goes by the address
+    if (tid == 0) atomicOr(err, kDevErrTimeout);
+    return;
+  }
   if (tid == 0) {
     for (int i = 0; i < S::SLOTS; ++i) {
       mbar_init(&s_full[i], kCopyThreads);
@@ -451,13 +514,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const __grid_co
 #pragma unroll
           for (int k = 0; k < kBN / 32; ++k) tmem_ld32(ts + 32 * k, s + 32 * k);
           tmem_wait_ld();
-          // all rows of the half see the whole tile?
-          bool full;
-          if constexpr (PRE)
-            full = base + kBN <= p.prefix_len;
-          else
-            full = base + kBN - 1 <= plo &&
-                   (p.window == 0 || phi - base < p.window || base + kBN <= p.n_sinks);
+          const bool full = half_full<PRE>(p, plo, phi, base);
           if (!full) {
 #pragma unroll
             for (int c = 0; c < kBN / 32; ++c) {
@@ -814,20 +871,21 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const __grid_co
         ++n_tiles[h];
       };
       while (cur.u < u1) {
-        const PagedRange h0 = cur.t.half[0], h1 = cur.t.half[1];
+        const TileCheck<PRE> tc(cur.t);
         const int ns = cur.t.ns, skip = cur.t.skip, first = cur.tile;
         const int count = (int)min((long long)(cur.t.tiles - first), u1 - cur.u);
         wait_bar(&s_qfull, items & 1, err);
         ++items;
         fence_proxy_async_smem();  // the copies wrote as ordinary stores
+        bool bad = false;  // an infinity or NaN in a tile that was looked through
         bool acc0 = false, acc1 = false;
         bool pend = false;  // half 1's O += P V of the last tile is still to come
         int pend_slot = 0;
-#pragma unroll 1
-        for (int tile = first; tile < first + count; ++tile) {
-          const int base = (tile < ns ? tile : tile + skip) * kBN;
-          const bool act0 = tile_active(h0, base), act1 = tile_active(h1, base);
-          const bool last = tile + 1 == first + count;
+        // One tile: the scores of half 0, O of half 1 for the tile before, the
+        // scores of half 1, O of half 0.  This warp's own instructions are on
+        // the critical path, so the usual tile has its own copy of the code,
+        // without any question.
+        auto step = [&](bool act0, bool act1, int look, bool last) {
           const int kslot = ring.slot;
           wait_bar(&s_full[kslot], ring.phase, err);
           ring.next(S::SLOTS);
@@ -848,6 +906,26 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const __grid_co
           const int vslot = ring.slot;
           wait_bar(&s_full[vslot], ring.phase, err);
           ring.next(S::SLOTS);
+          if (look >= 0) {  // the softmax of these scores is under way
+            // rows from the first that not all see; those behind the last
+            // position are zeros
+            const uint32_t v0 = skv + vslot * S::TILE + look * 128 + lane * 16;
+            uint32_t top[4] = {0u, 0u, 0u, 0u};  // largest magnitudes, 16 bits each
+#pragma unroll
+            for (int slab = 0; slab < D / 64; ++slab) {
+#pragma unroll 4
+              for (int i = 0; i < (kBN - look) * 128; i += 512) {
+                uint32_t w[4];
+                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                             : "r"(v0 + slab * (kBN * 128) + i));
+#pragma unroll
+                for (int e = 0; e < 4; ++e) top[e] = __vmaxu2(top[e], w[e] & 0x7fff7fffu);
+              }
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) bad |= nonfinite2<T>(top[e]);
+          }
           fence_proxy_async_smem();
           tc05_fence_after();
           if (act0) {
@@ -863,6 +941,29 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const __grid_co
             if (leader) tc05_commit(&s_empty[vslot]);
             __syncwarp();
           }
+        };
+        // the tiles that both halves see whole, but for the run's last
+        int mid_lo, mid_hi;
+        tc.middle(p, first, first + count - 1, ns, skip, mid_lo, mid_hi);
+#pragma unroll 1
+        for (int tile = first; tile < first + count; ++tile) {
+          if (tile == mid_lo && mid_lo < mid_hi) {
+#pragma unroll 1
+            for (; tile < mid_hi; ++tile) step(true, true, -1, false);
+          }
+          const int base = (tile < ns ? tile : tile + skip) * kBN;
+          step(tc.active(0, base), tc.active(1, base), tc.look(p, base),
+               tile + 1 == first + count);
+        }
+        if (!PRE && __any_sync(~0u, bad) && lane == 0) {
+          TcRedo x;
+          x.b = cur.t.b;
+          x.t0 = cur.t.t0;
+          x.p0 = cur.t.p0;
+          x.rows = cur.t.rows;
+          x.j = cur.t.j;
+          x.h = cur.h;
+          a.redo[atomicAdd(a.n_redo, 1)] = x;
         }
         if (lane == 0) {
           cur.u += count - 1;
@@ -881,26 +982,63 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const __grid_co
 }
 
 // Joins the parts of the item that block x of the main kernel began, if that
-// was split: a thread per row and 4 columns.
+// was split: a row per D / 4 lanes.  Then computes listed items again.
 template <typename T, int D>
 __global__ void __launch_bounds__(256) paged_tc_join_kernel(const __grid_constant__ TcArgs a) {
+  __shared__ float s_q[8][D];
+  const PagedAttnParams& p = a.p;
+  const int tid = threadIdx.x, lane = tid & 31;
   pdl_wait();
   pdl_trigger();
   const TcMeta x = a.meta[blockIdx.x];
-  if (x.tiles == 0) return;
-  const PagedAttnParams& p = a.p;
+  const int n_redo = a.n_redo[0];
   constexpr int C4 = D / 4;
-  const int rows = min(2 * kHalf, x.rows - x.j * 2 * kHalf);
-  const PagedItemParts parts(x.i0, x.tiles, x.upc);
-  for (int e = blockIdx.y * 256 + threadIdx.x; e < rows * C4; e += gridDim.y * 256) {
-    const int r = e / C4, col = (e - r * C4) * 4;
-    PagedState4 s{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-    const int gr = x.j * 2 * kHalf + r, i = gr / p.g.G, g = gr - i * p.g.G;
-    const long long t = x.t0 + i;
-    paged_join_row<D>(s, a.ws.o, a.ws.ml, PagedRowParts(parts, 2 * kHalf, r, 0), col);
-    if (a.pre.rows && x.p0 + i >= 0)
-      paged_join_row<D>(s, a.pre.o, a.pre.ml, paged_prefix_row(a.pre, p.g, t, x.h, g), col);
-    paged_store4<T, D>(s, p.out, p.lse, t * p.g.nq + x.h * p.g.G + g, col);
+  bool join = x.tiles != 0;
+  for (int i = 0; i < n_redo && join; ++i)
+    join = a.redo[i].t0 != x.t0 || a.redo[i].j != x.j || a.redo[i].h != x.h;
+  if (join) {
+    const int rows = min(2 * kHalf, x.rows - x.j * 2 * kHalf);
+    const PagedItemParts parts(x.i0, x.tiles, x.upc);
+    for (int e = blockIdx.y * 256 + tid; e < rows * C4; e += gridDim.y * 256) {
+      const int r = e / C4, col = (e - r * C4) * 4;
+      PagedState4 s{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+      const int gr = x.j * 2 * kHalf + r, i = gr / p.g.G, g = gr - i * p.g.G;
+      const long long t = x.t0 + i;
+      paged_join_row<D>(s, a.ws.o, a.ws.ml, PagedRowParts(parts, 2 * kHalf, r, 0), col);
+      if (a.pre.rows && x.p0 + i >= 0)
+        paged_join_row<D>(s, a.pre.o, a.pre.ml, paged_prefix_row(a.pre, p.g, t, x.h, g), col);
+      paged_store4<T, D>(s, p.out, p.lse, t * p.g.nq + x.h * p.g.G + g, col);
+    }
+  }
+  if (n_redo == 0) return;
+  const int warps = gridDim.x * gridDim.y * 8;
+  float* q = s_q[tid >> 5];
+  for (int e = (blockIdx.y * gridDim.x + blockIdx.x) * 8 + (tid >> 5); e < n_redo * 2 * kHalf;
+       e += warps) {
+    const TcRedo it = a.redo[e / (2 * kHalf)];
+    const int gr = it.j * 2 * kHalf + e % (2 * kHalf);
+    if (gr >= it.rows) continue;
+    const int i = gr / p.g.G;
+    const long long t = it.t0 + i, h = it.h * p.g.G + gr - i * p.g.G;
+    __syncwarp();
+    for (int c = lane; c < D; c += 32)
+      q[c] = Elem<T>::to_f(static_cast<const T*>(p.q)[t * p.q_stride + h * D + c]);
+    __syncwarp();
+    PagedRow<T, D> r;
+    r.run(p, q, it.b, it.p0 + i, it.p0 + it.rows / p.g.G, it.h, 0, 1);
+    const float inv = r.l == 0.f ? 0.f : 1.f / r.l;
+    T* out = static_cast<T*>(p.out) + (t * p.g.nq + h) * D + lane * (D / 32);
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) out[c] = Elem<T>::from_f(r.o[c] * inv);
+    if (p.lse && lane == 0)
+      p.lse[t * p.g.nq + h] =
+          r.m == -INFINITY ? -INFINITY : (r.m + log2f(r.l)) * 0.69314718055994531f;
+  }
+  // the last block out empties the list
+  __syncthreads();
+  if (tid == 0 && atomicAdd(a.n_redo + 1, 1) == (int)(gridDim.x * gridDim.y) - 1) {
+    a.n_redo[0] = 0;
+    a.n_redo[1] = 0;
   }
 }
 
@@ -950,7 +1088,10 @@ int cf::paged_tc_grid(int dtype, int head_dim, int sm_count) {
 
 long long cf::paged_tc_part_rows(int grid) { return 2LL * grid * kTcRows; }
 
-size_t cf::paged_tc_list_bytes(int grid) { return (size_t)grid * sizeof(TcMeta); }
+size_t cf::paged_tc_list_bytes(int grid, long long row_tiles) {
+  // every part of an item can be listed
+  return (size_t)grid * sizeof(TcMeta) + (size_t)(row_tiles + grid) * sizeof(TcRedo);
+}
 
 PagedPrefixParts cf::paged_tc_prefix(const PagedAttnParams& p, const PagedSplit& ws) {
   PagedPrefixParts x;
@@ -974,6 +1115,8 @@ bool cf::paged_tc_launch(int dtype, const PagedAttnParams& p, const PagedSplit& 
   a.pre = pre;
   a.ws = ws.parts;
   a.meta = static_cast<TcMeta*>(ws.list);
+  a.redo = reinterpret_cast<TcRedo*>(a.meta + ws.grid);
+  a.n_redo = ws.tickets;
   a.slots = (int)((long long)p.n_tokens * p.g.G / kTcRows) + p.batch;
   void* args[] = {&a};
   if (!launch_pdl(f.main, dim3(ws.grid), kTcThreads, f.smem, st, args)) return false;

@@ -162,6 +162,54 @@ def test_unseen_slots_and_table_entries_do_not_matter(dtype, q_len):
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("heads,q_len,kv_len,window,sinks", [
+    ((4, 4), [3], [40], 0, 0), ((8, 2), [2, 4], [70, 4], 20, 1),        # few rows
+    ((2, 2), [300], [300], 0, 0), ((4, 2), [150, 60], [400, 60], 0, 0),  # many
+    ((2, 1), [200], [500], 70, 9)], ids=str)
+def test_infinities_that_some_rows_see_reach_no_others(dtype, d, heads, q_len, kv_len, window, sinks):
+    """Keys and values of infinity or NaN at positions that later (or, behind
+    the window, earlier) tokens see: the other rows stay exact, and the rows
+    that see them get them."""
+    pr = Problem(q_len, kv_len, *heads, d=d, dtype=dtype, seed=12)
+    kp, vp = pr.split(pr.pools)
+    hit = {}
+    for b in range(pr.batch):
+        p0 = kv_len[b] - q_len[b]
+        hit[b] = sorted({kv_len[b] - 1, p0 + q_len[b] // 2, p0 + 1, max(p0 - 5, 0)})
+        for n, j in enumerate(hit[b]):
+            v = pr.slot(vp, pr.table[b], j)
+            v[:, n::7] = [math.inf, -math.inf, math.nan, math.inf][n]
+    clean = [p.clone() for p in pr.pools]
+    want = ref_attention(pr, window, sinks)
+    r = Run(pr)
+    r.attend(window, sinks)
+    assert r.kv.status() == OK
+    got = r.out.double().cpu()
+    finite = want[0].isfinite()
+    assert torch.equal(got.isfinite(), finite)
+    assert torch.equal(got.isnan(), want[0].isnan())
+    close(torch.where(finite, got, 0.0), torch.where(finite, want[0], 0.0),
+          torch.where(finite, want[1], 0.0), "finite values")
+    assert (got[want[0].isinf()] == want[0][want[0].isinf()]).all()
+    close(r.lse, want[2], want[3], "lse")
+    # a key of NaN at the last position: only the last token's row knows of it
+    pr.pools = clean
+    kp, vp = pr.split(pr.pools)
+    for b in range(pr.batch):
+        for j in hit[b]:
+            pr.slot(vp, pr.table[b], j)[...] = 1.0
+        pr.slot(kp, pr.table[b], kv_len[b] - 1)[...] = math.nan
+    want = ref_attention(pr, window, sinks)
+    r = Run(pr)
+    r.attend(window, sinks)
+    last = [pr.starts[b + 1] - 1 for b in range(pr.batch)]
+    keep = [t for t in range(pr.tokens) if t not in last]
+    close(r.out[keep], want[0][keep], want[1][keep], "rows before the last")
+    assert r.out[last].isnan().all()
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 def test_infinite_keys_and_extreme_scores(dtype):
     """Scores of +-6e4 and values near the type's limits: no overflow on the
     way, and -inf scores (a key of -inf) weigh nothing."""
