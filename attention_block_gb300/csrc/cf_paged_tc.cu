@@ -431,8 +431,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const __grid_co
     }
   };
   long long mine = 0;
+  RowTile mine_t;  // the last of this thread's row tiles: with one each, the one
   walk([&](const RowTile& t) {
     mine += (long long)(t.tiles + kItemCost) * p.g.nkv;
+    mine_t = t;
     return false;
   });
   long long incl = mine;
@@ -455,7 +457,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const __grid_co
   if (u0 >= u1) return;
   if (before <= u0 && u0 < before + mine) {
     long long at = before;
-    walk([&](const RowTile& t) {
+    auto start = [&](const RowTile& t) {
       const int len = t.tiles + kItemCost;
       const long long n = (long long)len * p.g.nkv;
       if (u0 < at + n) {
@@ -470,7 +472,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const __grid_co
       }
       at += n;
       return false;
-    });
+    };
+    if (per == 1)
+      start(mine_t);
+    else
+      walk(start);
   }
   if (warp == 12) {
     tmem_alloc(&s_tmem, 512);
@@ -594,48 +600,45 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const __grid_co
       const long long prow0 =
           (2 * (long long)blockIdx.x + (u0 >= cur.i0 ? 0 : 1)) * (2 * kHalf) + hf * kHalf;
       const int q4 = lane & 3;
-#pragma unroll 1
-      for (int hh = 0; hh < 2; ++hh) {  // 16 rows of the warp at a time
-        float own[2], inv[2], mt[2];
-        int row[2], np[2];
-        long long orow[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int src = hh * 16 + e * 8 + (lane >> 2);  // lane that has this row's state
-          const float rm = __shfl_sync(~0u, m2, src);
-          float rl = __shfl_sync(~0u, l, src);
-          row[e] = (warp & 3) * 32 + src;
-          const int rg = t.j * 2 * kHalf + hf * kHalf + row[e];
-          const bool there = rg < t.rows;
-          if (!there) row[e] = -1;
-          own[e] = 1.f;
-          mt[e] = rm;
-          np[e] = 0;
-          const int i = rg / p.g.G;
-          orow[e] = ((long long)t.t0 + i) * p.g.nq + cur.h * p.g.G + rg - i * p.g.G;
-          if (part) {
-            orow[e] = whole ? a.ws.state_base + orow[e] : prow0 + row[e];
-            if (there && q4 == 0) __stcg(a.ws.ml + orow[e], make_float2(rm, rl));
-          }
-          if (JOIN && !part && there && t.p0 + i >= 0) {
+      // this lane's own row: where it goes, and what its values are scaled by
+      long long my_row = -1;
+      float my_inv = 1.f, my_own = 1.f, my_ref = 0.f;
+      if (gr < t.rows) {
+        const int i = gr / p.g.G;
+        my_row = ((long long)t.t0 + i) * p.g.nq + cur.h * p.g.G + gr - i * p.g.G;
+        if (part) {
+          my_row = whole ? a.ws.state_base + my_row : prow0 + r;
+          __stcg(a.ws.ml + my_row, make_float2(m2, l));
+        } else {
+          float mt = m2, lt = l;
+          if (JOIN && t.p0 + i >= 0) {
             const PagedRowParts pp =
-                paged_prefix_row(a.pre, p.g, (long long)t.t0 + i, cur.h, rg - i * p.g.G);
-            np[e] = pp.n;
+                paged_prefix_row(a.pre, p.g, (long long)t.t0 + i, cur.h, gr - i * p.g.G);
 #pragma unroll 4
-            for (int k = 0; k < pp.n; ++k) mt[e] = fmaxf(mt[e], __ldcg(a.pre.ml + pp.row(k)).x);
-            const float ref = mt[e] == -INFINITY ? 0.f : mt[e];
-            own[e] = ex2(rm - ref);
-            rl *= own[e];
+            for (int k = 0; k < pp.n; ++k) mt = fmaxf(mt, __ldcg(a.pre.ml + pp.row(k)).x);
+            my_ref = mt == -INFINITY ? 0.f : mt;
+            my_own = ex2(m2 - my_ref);
+            lt *= my_own;
 #pragma unroll 4
             for (int k = 0; k < pp.n; ++k) {
               const float2 ml = __ldcg(a.pre.ml + pp.row(k));
-              rl += ml.y * ex2(ml.x - ref);
+              lt += ml.y * ex2(ml.x - my_ref);
             }
           }
-          inv[e] = part ? 1.f : (rl == 0.f ? 0.f : 1.f / rl);
-          if (!part && p.lse && there && q4 == 0)
-            p.lse[orow[e]] =
-                mt[e] == -INFINITY ? -INFINITY : (mt[e] + log2f(rl)) * 0.69314718055994531f;
+          my_inv = lt == 0.f ? 0.f : 1.f / lt;
+          if (p.lse)
+            p.lse[my_row] = mt == -INFINITY ? -INFINITY : (mt + log2f(lt)) * 0.69314718055994531f;
+        }
+      }
+#pragma unroll 1
+      for (int hh = 0; hh < 2; ++hh) {  // 16 rows of the warp at a time
+        float inv[2];
+        long long orow[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int src = hh * 16 + e * 8 + (lane >> 2);  // lane that has this row
+          orow[e] = __shfl_sync(~0u, my_row, src);
+          inv[e] = __shfl_sync(~0u, my_inv, src);
         }
 #pragma unroll 1
         for (int c64 = 0; c64 < D; c64 += 64) {
@@ -664,32 +667,36 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const __grid_co
                 const bool odd = q4 & 1;
                 const float g0 = __shfl_xor_sync(~0u, odd ? A0 : B0, 1);
                 const float g1 = __shfl_xor_sync(~0u, odd ? A1 : B1, 1);
-                if (row[e] >= 0)
+                if (orow[e] >= 0)
                   __stcg(reinterpret_cast<float4*>(a.ws.o + orow[e] * D + c + 16 * b2 + 8 * (q4 & 1) +
                                                    4 * (q4 >> 1)),
                          odd ? make_float4(g0, g1, B0, B1) : make_float4(A0, A1, g0, g1));
               }
             } else {
-              if (JOIN && np[e]) {
-                const int rg = t.j * 2 * kHalf + hf * kHalf + row[e], i = rg / p.g.G;
-                const PagedRowParts pp =
-                    paged_prefix_row(a.pre, p.g, (long long)t.t0 + i, cur.h, rg - i * p.g.G);
-                const float ref = mt[e] == -INFINITY ? 0.f : mt[e];
-#pragma unroll
-                for (int b = 0; b < 4; ++b) {
-                  o[4 * b + 2 * e] *= own[e];
-                  o[4 * b + 2 * e + 1] *= own[e];
-                }
-#pragma unroll 2
-                for (int k = 0; k < np[e]; ++k) {
-                  const long long at = pp.row(k);
-                  const float f = ex2(__ldcg(a.pre.ml + at).x - ref);
+              if constexpr (JOIN) {
+                const int src = hh * 16 + e * 8 + (lane >> 2);
+                const float own = __shfl_sync(~0u, my_own, src), ref = __shfl_sync(~0u, my_ref, src);
+                const int rg = t.j * 2 * kHalf + hf * kHalf + (warp & 3) * 32 + src;
+                const int i = rg / p.g.G;
+                if (rg < t.rows && t.p0 + i >= 0) {
+                  const PagedRowParts pp =
+                      paged_prefix_row(a.pre, p.g, (long long)t.t0 + i, cur.h, rg - i * p.g.G);
 #pragma unroll
                   for (int b = 0; b < 4; ++b) {
-                    const float2 v =
-                        __ldcg(reinterpret_cast<const float2*>(a.pre.o + at * D + c + 8 * b + 2 * q4));
-                    o[4 * b + 2 * e] = fmaf(v.x, f, o[4 * b + 2 * e]);
-                    o[4 * b + 2 * e + 1] = fmaf(v.y, f, o[4 * b + 2 * e + 1]);
+                    o[4 * b + 2 * e] *= own;
+                    o[4 * b + 2 * e + 1] *= own;
+                  }
+#pragma unroll 2
+                  for (int k = 0; k < pp.n; ++k) {
+                    const long long at = pp.row(k);
+                    const float f = ex2(__ldcg(a.pre.ml + at).x - ref);
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) {
+                      const float2 v = __ldcg(
+                          reinterpret_cast<const float2*>(a.pre.o + at * D + c + 8 * b + 2 * q4));
+                      o[4 * b + 2 * e] = fmaf(v.x, f, o[4 * b + 2 * e]);
+                      o[4 * b + 2 * e + 1] = fmaf(v.y, f, o[4 * b + 2 * e + 1]);
+                    }
                   }
                 }
               }
@@ -698,7 +705,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const __grid_co
               for (int b = 0; b < 4; ++b)
                 w[b] = pack2<T>(o[4 * b + 2 * e] * inv[e], o[4 * b + 2 * e + 1] * inv[e]);
               quad_transpose(w, q4);  // lane q: the 8 columns of octet q
-              if (row[e] >= 0)
+              if (orow[e] >= 0)
                 *reinterpret_cast<uint4*>(static_cast<T*>(p.out) + orow[e] * D + c + 8 * q4) =
                     make_uint4(w[0], w[1], w[2], w[3]);
             }
