@@ -274,19 +274,25 @@ struct TileCheck {
       mid_hi = max(mid_lo, min(hi, mid_hi));
     }
   }
-  // The row of the tile from which on V is looked through (a multiple of 4:
-  // the warp reads four at a time), or -1.
-  __device__ __forceinline__ int look(const PagedAttnParams& p, int base) const {
-    if constexpr (PRE) return -1;
+  // Rows [lo, hi) of the tile's V to look through, none if lo >= hi: of the
+  // positions that some row sees and some does not, behind the first row's
+  // position or where the windows start.
+  __device__ __forceinline__ void look(const PagedAttnParams& p, int base, int& lo, int& hi) const {
+    lo = kBN;
+    hi = 0;
+    if constexpr (PRE) return;
     const bool a0 = active(0, base), a1 = active(1, base);
-    const bool f0 = !a0 || half_full<PRE>(p, plo[0], phi[0], base);
-    const bool f1 = !a1 || half_full<PRE>(p, plo[1], phi[1], base);
-    if (f0 && f1) return -1;
-    // without a window's start in the tile, all rows see up to the first one's
-    // position
-    const int lo = a0 ? plo[0] : plo[1], hi = a1 ? phi[1] : phi[0];
-    if (p.window != 0 && hi - base >= p.window) return 0;
-    return min(kBN - 4, max(0, lo + 1 - base)) & ~3;
+    if (!a0 && !a1) return;
+    const int first = a0 ? plo[0] : plo[1], last = a1 ? phi[1] : phi[0];
+    if (last > first && last >= base && first + 1 < base + kBN) {
+      lo = max(0, first + 1 - base);
+      hi = min(kBN, last + 1 - base);
+    }
+    const int w0 = max(first - p.window + 1, p.n_sinks), w1 = last - p.window + 1;
+    if (p.window != 0 && w0 < w1 && w1 > base && w0 < base + kBN) {
+      lo = min(lo, max(0, w0 - base));
+      hi = max(hi, min(kBN, w1 - base));
+    }
   }
 };
 
@@ -892,7 +898,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const __grid_co
         // scores of half 1, O of half 0.  This warp's own instructions are on
         // the critical path, so the usual tile has its own copy of the code,
         // without any question.
-        auto step = [&](bool act0, bool act1, int look, bool last) {
+        auto step = [&](bool act0, bool act1, int look_lo, int look_hi, bool last) {
           const int kslot = ring.slot;
           wait_bar(&s_full[kslot], ring.phase, err);
           ring.next(S::SLOTS);
@@ -913,15 +919,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const __grid_co
           const int vslot = ring.slot;
           wait_bar(&s_full[vslot], ring.phase, err);
           ring.next(S::SLOTS);
-          if (look >= 0) {  // the softmax of these scores is under way
-            // rows from the first that not all see; those behind the last
-            // position are zeros
-            const uint32_t v0 = skv + vslot * S::TILE + look * 128 + lane * 16;
+          if (look_lo < look_hi) {  // the softmax of these scores is under way
+            const uint32_t v0 = skv + vslot * S::TILE + lane * 16;
             uint32_t top[4] = {0u, 0u, 0u, 0u};  // largest magnitudes, 16 bits each
 #pragma unroll
             for (int slab = 0; slab < D / 64; ++slab) {
 #pragma unroll 4
-              for (int i = 0; i < (kBN - look) * 128; i += 512) {
+              for (int i = (look_lo & ~3) * 128; i < look_hi * 128; i += 512) {  // four rows
                 uint32_t w[4];
                 asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                              : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
@@ -956,11 +960,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const __grid_co
         for (int tile = first; tile < first + count; ++tile) {
           if (tile == mid_lo && mid_lo < mid_hi) {
 #pragma unroll 1
-            for (; tile < mid_hi; ++tile) step(true, true, -1, false);
+            for (; tile < mid_hi; ++tile) step(true, true, kBN, 0, false);
           }
           const int base = (tile < ns ? tile : tile + skip) * kBN;
-          step(tc.active(0, base), tc.active(1, base), tc.look(p, base),
-               tile + 1 == first + count);
+          int look_lo, look_hi;
+          tc.look(p, base, look_lo, look_hi);
+          step(tc.active(0, base), tc.active(1, base), look_lo, look_hi, tile + 1 == first + count);
         }
         if (!PRE && __any_sync(~0u, bad) && lane == 0) {
           TcRedo x;
