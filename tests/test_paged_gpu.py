@@ -628,3 +628,126 @@ def test_offsets_past_32_bits():
             want = torch.einsum("hns,shd->nhd", s.softmax(-1), V)
             err = (o[int(st[b]):int(st[b + 1])].double() - want).norm() / want.norm()
             assert err <= 2 * 2.0 ** -8, err
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("case", [
+    dict(q_len=[1] * 700, kv=lambda b: b % 41, heads=(4, 1), d=64),          # runs of sequences per thread
+    dict(q_len=[2] * 600, kv=lambda b: 2 + b % 37, heads=(16, 1), d=64),     # more row tiles than threads
+    dict(q_len=[1] * 40 + [0] * 300 + [3], kv=lambda b: 5 + b, heads=(2, 2), d=128),
+    dict(q_len=[1, 0, 1100, 1], kv=lambda b: [900, 3, 1200, 31][b], heads=(2, 1), d=64, window=33, sinks=2),
+], ids=["700x1", "600x2", "idle", "long"])
+def test_many_sequences(dtype, case):
+    n = len(case["q_len"])
+    pr = Problem(case["q_len"], [max(case["kv"](b), 0) for b in range(n)], *case["heads"],
+                 d=case["d"], dtype=dtype, seed=70)
+    attend_and_check(pr, case.get("window", 0), case.get("sinks", 0))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("q_len,heads,prefix", [
+    ([1] * 300, (8, 4), 40),      # short prefix, more items than blocks
+    ([4] * 150, (8, 2), 700),     # drafts: states of whole items and of cut ones
+    ([200] * 3, (4, 2), 300),     # prompts behind a prefix
+    ([1], (4, 4), 5000),          # few rows, one long prefix
+], ids=str)
+def test_prefix_of_large_batches(dtype, q_len, heads, prefix):
+    pr = Problem(q_len, [n + 3 * (b % 9) for b, n in enumerate(q_len)], *heads, d=64,
+                 dtype=dtype, prefix=prefix, seed=71)
+    attend_and_check(pr)
+
+
+def test_calls_of_every_kind_on_one_handle_repeat_their_bits():
+    """Few rows, many rows, windows and prefixes in turn, twice: nothing of a
+    call stays behind in the workspace, and no order of arrival shows."""
+    pr = Problem([1] * 9 + [70, 130], [40 * (b + 1) for b in range(11)], 8, 2, seed=72, prefix=90)
+    r = Run(pr)
+    one = torch.arange(10, dtype=torch.int32, device="cuda")
+
+    def all_calls():
+        got = []
+        for call in range(4):
+            out, lse = torch.empty_like(r.out), torch.empty_like(r.lse)
+            a = (r.k_pages, r.v_pages, out)
+            if call == 0:    # the first nine sequences, single tokens
+                r.kv.attention(9, 9, 1, r.q, one, r.kv_len, r.table, *a, lse=lse)
+                out, lse = out[:9], lse[:9]
+            elif call == 1:
+                r.kv.attention(11, pr.tokens, 130, r.q, r.q_start, r.kv_len, r.table, *a, lse=lse,
+                               window=50, n_sinks=3)
+            elif call == 2:
+                r.kv.prefix_attention(11, pr.tokens, 130, r.q, r.q_start, r.kv_len, r.table,
+                                      r.ptable, 90, *a, lse=lse)
+            else:
+                r.kv.prefix_attention(9, 9, 1, r.q, None, r.kv_len, r.table, r.ptable, 90, *a,
+                                      lse=lse)
+                out, lse = out[:9], lse[:9]
+            got += [out.clone(), lse.clone()]
+        return got
+
+    first = all_calls()
+    for _ in range(3):
+        for x, y in zip(first, all_calls()):
+            assert torch.equal(x, y)
+    want = ref_attention(pr)
+    close(first[4], want[0], want[1], "prefix")
+    assert r.kv.status() == OK
+
+
+@pytest.mark.parametrize("prefix", [0, 60])
+def test_captured_prompts_replay_with_other_lengths(prefix):
+    pr = Problem([100, 3, 40], [150, 3, 90], 8, 2, seed=73, prefix=prefix, max_pages=16, spare=60)
+    spare = sorted(set(range(pr.num_pages)) - set(pr.table.flatten().tolist()) -
+                   set(pr.prefix_table.tolist()))
+    for b in range(3):
+        for i in range(16):
+            if pr.table[b, i] < 0:
+                pr.table[b, i] = spare.pop() if spare else 0
+    r = Run(pr, poison=False)
+    r.attend()  # kernels are loaded before the capture
+    st, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g, stream=st):
+        r.attend()
+        r.attend()
+    for lens, starts in (([150, 3, 90], [0, 100, 103, 143]), ([100, 77, 41], [0, 100, 103, 143]),
+                         ([230, 1, 70], [0, 70, 71, 120])):
+        r.kv_len.copy_(torch.tensor(lens, dtype=torch.int32))
+        r.q_start.copy_(torch.tensor(starts, dtype=torch.int32))
+        r.out.fill_(float("nan")), r.lse.fill_(float("nan"))
+        torch.cuda.synchronize()
+        g.replay()
+        pr.kv_len, pr.starts = lens, starts
+        pr.q_len = [starts[b + 1] - starts[b] for b in range(3)]
+        r.check()
+
+
+def test_another_device_or_stream():
+    """The call goes to torch's current stream, or to the one given."""
+    pr = Problem([1, 1], [300, 17], 4, 2, seed=74)
+    r = Run(pr)
+    want = ref_attention(pr)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    for how in ("current", "given", "raw"):
+        r.out.fill_(float("nan"))
+        s.wait_stream(torch.cuda.current_stream())
+        if how == "current":
+            with torch.cuda.stream(s):
+                r.attend()
+        else:
+            r.attend(stream=s if how == "given" else s.cuda_stream)
+        s.synchronize()
+        close(r.out, want[0], want[1], how)
+
+
+def test_workspace_follows_the_largest_call():
+    """Handles of the smallest size, and outputs next to their neighbours."""
+    pr = Problem([1], [33], 8, 2, seed=75)
+    r = Run(pr)
+    big = torch.full((3, 8, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    r.out = big[1:2]
+    r.attend()
+    want = ref_attention(pr)
+    close(big[1:2], want[0], want[1], "out")
+    assert (big[0] == 7).all() and (big[2] == 7).all()
