@@ -126,6 +126,45 @@ def test_window_and_sinks(dtype, window, sinks, q_len, kv_len):
     attend_and_check(Problem(q_len, kv_len, 8, 2, dtype=dtype, seed=4), window, sinks)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("heads,n,window,sinks", [((8, 8), 3000, 500, 4), ((8, 2), 2500, 0, 0),
+                                                  ((4, 4), 2049, 128, 130)], ids=str)
+def test_long_prompts_against_plain_torch(dtype, d, heads, n, window, sinks):
+    """Many items per block, twenty times over: every run gives the same bits,
+    and they are within the roundings of the 64-bit result."""
+    nq, nkv = heads
+    g = torch.Generator(device="cuda").manual_seed(n)
+    page, pages = 64, -(-n // 64)
+    kp, vp = (torch.randn(pages, page, nkv, d, generator=g, device="cuda").to(DT[dtype])
+              for _ in range(2))
+    q = (2 * torch.randn(n, nq, d, generator=g, device="cuda")).to(DT[dtype])
+    kv = binding.PagedKv(n_q_heads=nq, n_kv_heads=nkv, head_dim=d, page_size=page,
+                         num_pages=pages, max_pages=pages, max_batch=1, max_tokens=n, dtype=dtype)
+    st = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    table = torch.arange(pages, dtype=torch.int32, device="cuda").view(1, -1)
+    outs = []
+    for _ in range(20):
+        outs.append(torch.full_like(q, float("nan")))
+        kv.attention(1, n, n, q, st, st[1:], table, kp, vp, outs[-1], window=window, n_sinks=sinks)
+    assert kv.status() == OK
+    K, V = (x.reshape(-1, nkv, d)[:n].double().repeat_interleave(nq // nkv, 1) for x in (kp, vp))
+    i = torch.arange(n, device="cuda")
+    hide = i[None] > i[:, None]
+    if window:
+        hide |= (i[:, None] - i[None] >= window) & (i[None] >= sinks)
+    u = half_step(dtype)
+    for h in range(nq):
+        w = (q[:, h].double() @ K[:, h].T / math.sqrt(d)).masked_fill_(hide, -math.inf).softmax(-1)
+        want, mag = w @ V[:, h], w @ V[:, h].abs()
+        # both roundings, and the fp32 scores: |q k| / sqrt(d) <= 64 d 2^-23 stays below u / 2
+        tol = u * want.abs() + (u + 2.0 ** -12) * mag + 2.0 ** -24
+        err = (outs[0][:, h].double() - want).abs()
+        assert (err <= tol).all(), (h, (err - tol).max())
+    for o in outs[1:]:
+        assert torch.equal(o, outs[0])
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 def test_rows_that_see_nothing(dtype):
     """No keys at all, more tokens than keys, an idle sequence, and tokens
