@@ -53,11 +53,8 @@ template <int D>
 struct TcShape {
   static constexpr int TILE = kBN * D * 2;                   // bytes of a K, V or Q tile
   static constexpr int SLOTS = D == 128 ? 5 : 10;            // K and V tiles in flight
-  // With 64 columns there is room for two items' Q, and in TMEM for a third
-  // buffer of scores.
-  static constexpr int QB = D == 128 ? 1 : 2, SB = D == 128 ? 2 : 3;
-  static constexpr int SMEM = (2 * QB + SLOTS) * TILE;  // 1024-aligned; 3 KB are left for the rest
-  static constexpr uint32_t S_COL = 0, O_COL = SB * kBN;     // TMEM columns
+  static constexpr int SMEM = (2 + SLOTS) * TILE;  // 1024-aligned; 3 KB are left for the rest
+  static constexpr uint32_t S_COL = 0, O_COL = 2 * kBN;      // TMEM columns
 };
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -365,12 +362,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const __grid_co
   __shared__ TcCursor<PRE> s_cur;
   __shared__ TcCursor<PRE> s_wcur[13];  // each working warp's place: too much for registers
   __shared__ __align__(8) uint64_t s_full[S::SLOTS], s_empty[S::SLOTS];
-  __shared__ __align__(8) uint64_t s_qfull[S::QB], s_qempty[S::QB], s_done;
-  __shared__ __align__(8) uint64_t s_sfull[S::SB], s_pfull[S::SB], s_ofull[2];
+  __shared__ __align__(8) uint64_t s_qfull, s_qempty, s_done;
+  __shared__ __align__(8) uint64_t s_sfull[2], s_pfull[2], s_ofull[2];
   __shared__ uint32_t s_tmem;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const uint32_t sq = smem_u32(sm);                   // Q, two tiles each
-  const uint32_t skv = sq + 2 * S::QB * S::TILE;              // K and V slots
+  const uint32_t sq = smem_u32(sm);                   // Q, two tiles
+  const uint32_t skv = sq + 2 * S::TILE;              // K and V slots
   int* err = p.errflag;
 
   if (sq & 1023u) {  // the swizzle goes by the address
@@ -382,17 +379,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const __grid_co
       mbar_init(&s_full[i], kCopyThreads);
       mbar_init(&s_empty[i], 1);
     }
-    for (int i = 0; i < S::QB; ++i) {
-      mbar_init(&s_qfull[i], kCopyThreads);
-      mbar_init(&s_qempty[i], 1);
-    }
+    mbar_init(&s_qfull, kCopyThreads);
+    mbar_init(&s_qempty, 1);
     mbar_init(&s_done, 1);
     for (int h = 0; h < 2; ++h) {
+      mbar_init(&s_sfull[h], 1);
+      mbar_init(&s_pfull[h], 4);
       mbar_init(&s_ofull[h], 1);
-    }
-    for (int i = 0; i < S::SB; ++i) {
-      mbar_init(&s_sfull[i], 1);
-      mbar_init(&s_pfull[i], 4);
     }
     fence_mbar_init_cluster();
   }
@@ -506,20 +499,18 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const __grid_co
     const int hf = warp >> 2;                   // half
     const int r = (warp & 3) * 32 + lane;       // row of the half = TMEM lane
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + lanes + S::S_COL + hf * kBN;
     const uint32_t to = tmem + lanes + S::O_COL + hf * D;
     const float sc = p.scale_log2;
     TcCursor<PRE>& cur = s_wcur[warp];
     if (lane == 0) cur = s_cur;
     __syncwarp();
     uint32_t n_tiles = 0;  // active tiles so far: parity of the barriers
-    // The buffer of scores: the half's own, or, of three, in the order in which
-    // both halves' scores are formed.
-    RingPos buf(S::SB == 3 ? 0 : hf, S::SB);
     while (cur.u < u1) {
       const RowTile& t = cur.t;
       const int gr = t.j * 2 * kHalf + hf * kHalf + r;  // row of the sequence
       const int pos = PRE ? 0 : t.p0 + gr / p.g.G;
-      const PagedRange rng = t.half[hf], other = t.half[hf ^ 1];
+      const PagedRange rng = t.half[hf];
       const int plo = t.plo[hf], phi = t.phi[hf];
       const int first = cur.tile, count = (int)min((long long)(t.tiles - first), u1 - cur.u);
       const int ns = t.ns, skip = t.skip;
@@ -528,11 +519,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const __grid_co
 #pragma unroll 1
       for (int tile = first; tile < first + count; ++tile) {
         const int base = (tile < ns ? tile : tile + skip) * kBN;
-        if (S::SB == 3 && hf == 1 && tile_active(other, base)) buf.next(S::SB);
         if (tile_active(rng, base)) {
-          const int sb = buf.slot;
-          const uint32_t ts = tmem + lanes + S::S_COL + sb * kBN;
-          wait_bar(&s_sfull[sb], S::SB == 3 ? buf.phase : n_tiles & 1, err);
+          wait_bar(&s_sfull[hf], n_tiles & 1, err);
           tc05_fence_after();
           float s[kBN];
 #pragma unroll
@@ -600,13 +588,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const __grid_co
           tmem_wait_st();
           tc05_fence_before();
           __syncwarp();
-          if (lane == 0) mbar_arrive(&s_pfull[sb]);
+          if (lane == 0) mbar_arrive(&s_pfull[hf]);
           l = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
           some = true;
           ++n_tiles;
-          if (S::SB == 3) buf.next(S::SB);
         }
-        if (S::SB == 3 && hf == 0 && tile_active(other, base)) buf.next(S::SB);
       }
       // ---- the block's part of the item
       const bool whole = first == 0 && count == t.tiles;
@@ -845,11 +831,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const __grid_co
       }
       // Q last: its buffer is free only when the previous item's scores are done
       if (new_q) {
-        const uint32_t qb = items % S::QB, q0 = sq + qb * 2 * S::TILE;
-        if (items >= S::QB) wait_bar(&s_qempty[qb], (items / S::QB - 1) & 1, err);
-        copy(q0, qbase, qoff[0], false);
-        copy(q0 + S::TILE, qbase, qoff[1], false);
-        cp_arrive(&s_qfull[qb]);
+        if (items) wait_bar(&s_qempty, (items - 1) & 1, err);
+        copy(sq, qbase, qoff[0], false);
+        copy(sq + S::TILE, qbase, qoff[1], false);
+        cp_arrive(&s_qfull);
         ++items;
       }
     }
@@ -869,196 +854,118 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const __grid_co
       const uint64_t dk0 = smem_desc_k_sw128(skv, 1024), dq0 = smem_desc_k_sw128(sq, 1024);
       const uint64_t dv0 = smem_desc_mn_sw128(skv, kBN * 128, 1024);
       RingPos ring(0, S::SLOTS);
-      RingPos sbuf(0, S::SB), pbuf(0, S::SB);  // of three buffers, those of the next S and P
       uint32_t items = 0, n_tiles[2] = {0, 0};
-      // S of half h of the item whose Q lies in buffer qb
-      auto scores = [&](int h, int slot, int qb) {
-        const int sb = S::SB == 3 ? sbuf.slot : h;
+      auto scores = [&](int h, int slot) {
         if (leader) {
-          const uint64_t dk = dk0 + slot * (S::TILE / 16), dq = dq0 + (2 * qb + h) * (S::TILE / 16);
+          const uint64_t dk = dk0 + slot * (S::TILE / 16), dq = dq0 + h * (S::TILE / 16);
 #pragma unroll
           for (int x = 0; x < D / 16; ++x) {
             const uint32_t off = ((x >> 2) * (kBN * 128) + (x & 3) * 32) / 16;
-            tc05_mma_f16(tmem + S::S_COL + sb * kBN, dq + off, dk + off, id_s, x > 0);
+            tc05_mma_f16(tmem + S::S_COL + h * kBN, dq + off, dk + off, id_s, x > 0);
           }
-          tc05_commit(&s_sfull[sb]);
+          tc05_commit(&s_sfull[h]);
         }
         __syncwarp();
-        if (S::SB == 3) sbuf.next(S::SB);
       };
       // O of half h (+)= P V; frees the slot where it is V's last reader
       auto values = [&](int h, int slot, bool acc, bool free_slot) {
-        const int sb = S::SB == 3 ? pbuf.slot : h;
-        wait_bar(&s_pfull[sb], S::SB == 3 ? pbuf.phase : n_tiles[h] & 1, err);
+        wait_bar(&s_pfull[h], n_tiles[h] & 1, err);
         tc05_fence_after();
         if (leader) {
           const uint64_t dv = dv0 + slot * (S::TILE / 16);
 #pragma unroll
           for (int x = 0; x < kBN / 16; ++x)
-            tc05_mma_f16_ts(tmem + S::O_COL + h * D, tmem + S::S_COL + sb * kBN + x * 8,
+            tc05_mma_f16_ts(tmem + S::O_COL + h * D, tmem + S::S_COL + h * kBN + x * 8,
                             dv + x * (16 * 128 / 16), id_o, acc || x > 0);
           tc05_commit(&s_ofull[h]);
           if (free_slot) tc05_commit(&s_empty[slot]);
         }
         __syncwarp();
         ++n_tiles[h];
-        if (S::SB == 3) pbuf.next(S::SB);
-      };
-      // Looks for infinities and NaN in rows [lo, hi) of V (while the softmax
-      // of the tile's scores is under way).
-      auto look = [&](int vslot, int lo, int hi) {
-        const uint32_t v0 = skv + vslot * S::TILE + lane * 16;
-        uint32_t top[4] = {0u, 0u, 0u, 0u};  // largest magnitudes, 16 bits each
-#pragma unroll
-        for (int slab = 0; slab < D / 64; ++slab) {
-#pragma unroll 4
-          for (int i = (lo & ~3) * 128; i < hi * 128; i += 512) {  // four rows
-            uint32_t w[4];
-            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                         : "r"(v0 + slab * (kBN * 128) + i));
-#pragma unroll
-            for (int e = 0; e < 4; ++e) top[e] = __vmaxu2(top[e], w[e] & 0x7fff7fffu);
-          }
-        }
-        bool found = false;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) found |= nonfinite2<T>(top[e]);
-        return found;
-      };
-      auto landed = [&](const RingPos& r) {  // a tile of K or V
-        wait_bar(&s_full[r.slot], r.phase, err);
-        fence_proxy_async_smem();  // the copies wrote as ordinary stores
-        tc05_fence_after();
       };
       while (cur.u < u1) {
         const TileCheck<PRE> tc(cur.t);
         const int ns = cur.t.ns, skip = cur.t.skip, first = cur.tile;
         const int count = (int)min((long long)(cur.t.tiles - first), u1 - cur.u);
-        const int qb = items % S::QB;
-        wait_bar(&s_qfull[qb], (items / S::QB) & 1, err);
+        wait_bar(&s_qfull, items & 1, err);
         ++items;
-        fence_proxy_async_smem();
+        fence_proxy_async_smem();  // the copies wrote as ordinary stores
         bool bad = false;  // an infinity or NaN in a tile that was looked through
         bool acc0 = false, acc1 = false;
-        // the tiles that both halves see whole, but for the run's last.  This
-        // warp's own instructions are on the critical path, so those have their
-        // own copy of the code, without any question.
-        int mid_lo, mid_hi;
-        tc.middle(p, first, first + count - 1, ns, skip, mid_lo, mid_hi);
-        const int end = first + count;
-        if constexpr (S::SB == 3) {
-          // Three buffers: the next tile's scores are formed while the softmax
-          // of this tile's is under way.
-          auto base_of = [&](int tile) { return (tile < ns ? tile : tile + skip) * kBN; };
-          bool act0 = tc.active(0, base_of(first)), act1 = tc.active(1, base_of(first));
-          landed(ring);
-          if (act0) scores(0, ring.slot, qb);
-          if (act1) scores(1, ring.slot, qb);
+        bool pend = false;  // half 1's O += P V of the last tile is still to come
+        int pend_slot = 0;
+        // One tile: the scores of half 0, O of half 1 for the tile before, the
+        // scores of half 1, O of half 0.  This warp's own instructions are on
+        // the critical path, so the usual tile has its own copy of the code,
+        // without any question.
+        auto step = [&](bool act0, bool act1, int look_lo, int look_hi, bool last) {
+          const int kslot = ring.slot;
+          wait_bar(&s_full[kslot], ring.phase, err);
+          ring.next(S::SLOTS);
+          fence_proxy_async_smem();
+          tc05_fence_after();
+          if (act0) scores(0, kslot);
+          if (pend) {
+            values(1, pend_slot, acc1, true);
+            acc1 = true;
+            pend = false;
+          }
+          if (act1) scores(1, kslot);
           if (leader) {
-            tc05_commit(&s_empty[ring.slot]);
-            if (count == 1) tc05_commit(&s_qempty[qb]);
+            tc05_commit(&s_empty[kslot]);
+            if (last) tc05_commit(&s_qempty);
           }
           __syncwarp();
+          const int vslot = ring.slot;
+          wait_bar(&s_full[vslot], ring.phase, err);
           ring.next(S::SLOTS);
-          // This tile's O and the next one's scores; ring stands on this V.
-          auto step = [&](bool act0, bool act1, int look_lo, int look_hi, bool more, bool next0,
-                          bool next1, bool next_last) {
-            const RingPos v = ring;
-            ring.next(S::SLOTS);
-            const int kslot = ring.slot;
-            if (more) {
-              landed(ring);
-              if (next0) scores(0, kslot, qb);
-            }
-            landed(v);
-            if (look_lo < look_hi) bad |= look(v.slot, look_lo, look_hi);
-            if (act0) {
-              values(0, v.slot, acc0, !act1);
-              acc0 = true;
-            }
-            if (more) {
-              if (next1) scores(1, kslot, qb);
-              if (leader) {
-                tc05_commit(&s_empty[kslot]);
-                if (next_last) tc05_commit(&s_qempty[qb]);
+          if (look_lo < look_hi) {  // the softmax of these scores is under way
+            const uint32_t v0 = skv + vslot * S::TILE + lane * 16;
+            uint32_t top[4] = {0u, 0u, 0u, 0u};  // largest magnitudes, 16 bits each
+#pragma unroll
+            for (int slab = 0; slab < D / 64; ++slab) {
+#pragma unroll 4
+              for (int i = (look_lo & ~3) * 128; i < look_hi * 128; i += 512) {  // four rows
+                uint32_t w[4];
+                asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                             : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                             : "r"(v0 + slab * (kBN * 128) + i));
+#pragma unroll
+                for (int e = 0; e < 4; ++e) top[e] = __vmaxu2(top[e], w[e] & 0x7fff7fffu);
               }
-              __syncwarp();
-              ring.next(S::SLOTS);
             }
-            if (act1) {
-              values(1, v.slot, acc1, true);
-              acc1 = true;
-            } else if (!act0) {
-              if (leader) tc05_commit(&s_empty[v.slot]);
-              __syncwarp();
-            }
-          };
-#pragma unroll 1
-          for (int tile = first; tile < end; ++tile) {
-            if (tile >= mid_lo && tile + 1 < mid_hi) {  // the next tile is seen whole, too
-#pragma unroll 1
-              for (; tile + 1 < mid_hi; ++tile) step(true, true, kBN, 0, true, true, true, false);
-            }
-            int look_lo, look_hi;
-            tc.look(p, base_of(tile), look_lo, look_hi);
-            const bool more = tile + 1 < end;
-            const int nb = more ? base_of(tile + 1) : 0;
-            const bool n0 = more && tc.active(0, nb), n1 = more && tc.active(1, nb);
-            step(act0, act1, look_lo, look_hi, more, n0, n1, tile + 2 == end);
-            act0 = n0;
-            act1 = n1;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) bad |= nonfinite2<T>(top[e]);
           }
-        } else {
-          // Two: the scores of half 0, O of half 1 for the tile before, the
-          // scores of half 1, O of half 0.
-          bool pend = false;  // half 1's O += P V of the last tile is still to come
-          int pend_slot = 0;
-          auto step = [&](bool act0, bool act1, int look_lo, int look_hi, bool last) {
-            const int kslot = ring.slot;
-            landed(ring);
-            ring.next(S::SLOTS);
-            if (act0) scores(0, kslot, qb);
-            if (pend) {
-              values(1, pend_slot, acc1, true);
-              acc1 = true;
-              pend = false;
-            }
-            if (act1) scores(1, kslot, qb);
-            if (leader) {
-              tc05_commit(&s_empty[kslot]);
-              if (last) tc05_commit(&s_qempty[qb]);
-            }
+          fence_proxy_async_smem();
+          tc05_fence_after();
+          if (act0) {
+            values(0, vslot, acc0, !act1);
+            acc0 = true;
+          }
+          if (act1 && !last) {
+            pend = true;
+            pend_slot = vslot;
+          } else if (act1) {
+            values(1, vslot, acc1, true);
+          } else if (!act0) {
+            if (leader) tc05_commit(&s_empty[vslot]);
             __syncwarp();
-            const int vslot = ring.slot;
-            landed(ring);
-            ring.next(S::SLOTS);
-            if (look_lo < look_hi) bad |= look(vslot, look_lo, look_hi);
-            if (act0) {
-              values(0, vslot, acc0, !act1);
-              acc0 = true;
-            }
-            if (act1 && !last) {
-              pend = true;
-              pend_slot = vslot;
-            } else if (act1) {
-              values(1, vslot, acc1, true);
-            } else if (!act0) {
-              if (leader) tc05_commit(&s_empty[vslot]);
-              __syncwarp();
-            }
-          };
-#pragma unroll 1
-          for (int tile = first; tile < end; ++tile) {
-            if (tile == mid_lo && mid_lo < mid_hi) {
-#pragma unroll 1
-              for (; tile < mid_hi; ++tile) step(true, true, kBN, 0, false);
-            }
-            const int base = (tile < ns ? tile : tile + skip) * kBN;
-            int look_lo, look_hi;
-            tc.look(p, base, look_lo, look_hi);
-            step(tc.active(0, base), tc.active(1, base), look_lo, look_hi, tile + 1 == end);
           }
+        };
+        // the tiles that both halves see whole, but for the run's last
+        int mid_lo, mid_hi;
+        tc.middle(p, first, first + count - 1, ns, skip, mid_lo, mid_hi);
+#pragma unroll 1
+        for (int tile = first; tile < first + count; ++tile) {
+          if (tile == mid_lo && mid_lo < mid_hi) {
+#pragma unroll 1
+            for (; tile < mid_hi; ++tile) step(true, true, kBN, 0, false);
+          }
+          const int base = (tile < ns ? tile : tile + skip) * kBN;
+          int look_lo, look_hi;
+          tc.look(p, base, look_lo, look_hi);
+          step(tc.active(0, base), tc.active(1, base), look_lo, look_hi, tile + 1 == first + count);
         }
         if (!PRE && __any_sync(~0u, bad) && lane == 0) {
           TcRedo x;
