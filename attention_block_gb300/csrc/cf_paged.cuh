@@ -244,12 +244,12 @@ struct PagedState4 {
 
 // Joins a row's states into s: the D / 4 lanes that share the row call it
 // together, each for its 4 columns at `col`.  Each lane fetches one part's
-// maximum and sum, and the parts' values come eight at a time, the first
-// eight together with the maxima.
-template <int D>
+// maximum and sum, and the parts' values come B at a time, the first ones
+// together with the maxima.
+template <int D, int B = 8>
 __device__ __forceinline__ void paged_join_row(PagedState4& s, const float* o, const float2* ml,
                                                const PagedRowParts& x, int col) {
-  constexpr int W = D / 4, B = 8;
+  constexpr int W = D / 4;
   const int lane = threadIdx.x & 31, gl = lane % W;
   const uint32_t mask = W == 32 ? ~0u : 0xffffu << (lane & 16);
   for (int k0 = 0; k0 < x.n; k0 += W) {

@@ -994,9 +994,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const __grid_co
 }
 
 // Joins the parts of the item that block x of the main kernel began, if that
-// was split: a row per D / 4 lanes.  Then computes listed items again.
+// was split: a row per D / 4 lanes.  Then computes listed items again.  Bound
+// by the launch and by reads of the parts that are in L2; four blocks on an SM
+// with four parts in flight per lane and 16 blocks to an item take 2-10 us
+// less than eight in flight at two or three blocks with 32 to an item (8191
+// tokens, window 1024: 197.5 -> 185.6 us with the main kernel; 4 prompts of
+// 517-2048 behind 0-2049: 150.3 -> 144.6).
+constexpr int kTcJoinY = 16;
 template <typename T, int D>
-__global__ void __launch_bounds__(256) paged_tc_join_kernel(const __grid_constant__ TcArgs a) {
+__global__ void __launch_bounds__(256, 4) paged_tc_join_kernel(const __grid_constant__ TcArgs a) {
   __shared__ float s_q[8][D];
   const PagedAttnParams& p = a.p;
   const int tid = threadIdx.x, lane = tid & 31;
@@ -1016,9 +1022,9 @@ __global__ void __launch_bounds__(256) paged_tc_join_kernel(const __grid_constan
       PagedState4 s{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
       const int gr = x.j * 2 * kHalf + r, i = gr / p.g.G, g = gr - i * p.g.G;
       const long long t = x.t0 + i;
-      paged_join_row<D>(s, a.ws.o, a.ws.ml, PagedRowParts(parts, 2 * kHalf, r, 0), col);
+      paged_join_row<D, 4>(s, a.ws.o, a.ws.ml, PagedRowParts(parts, 2 * kHalf, r, 0), col);
       if (a.pre.rows && x.p0 + i >= 0)
-        paged_join_row<D>(s, a.pre.o, a.pre.ml, paged_prefix_row(a.pre, p.g, t, x.h, g), col);
+        paged_join_row<D, 4>(s, a.pre.o, a.pre.ml, paged_prefix_row(a.pre, p.g, t, x.h, g), col);
       paged_store4<T, D>(s, p.out, p.lse, t * p.g.nq + x.h * p.g.G + g, col);
     }
   }
@@ -1132,5 +1138,5 @@ bool cf::paged_tc_launch(int dtype, const PagedAttnParams& p, const PagedSplit& 
   a.slots = (int)((long long)p.n_tokens * p.g.G / kTcRows) + p.batch;
   void* args[] = {&a};
   if (!launch_pdl(f.main, dim3(ws.grid), kTcThreads, f.smem, st, args)) return false;
-  return mode == kPrefix || launch_pdl(f.join, dim3(ws.grid, 32), 256, 0, st, args);
+  return mode == kPrefix || launch_pdl(f.join, dim3(ws.grid, kTcJoinY), 256, 0, st, args);
 }
