@@ -441,8 +441,9 @@ struct PagedSplit {
   PagedParts parts;
   void* list = nullptr;    // items for a joining kernel
   int* tickets = nullptr;  // words that are zero between calls: few rows, one per (sequence,
-                           // KV head); many, two
+                           // KV head); many, three
   int grid = 0;            // resident blocks
+  long long items = 0;     // that the lists have room for
 };
 
 // Host launchers (one translation unit each); false: the launch failed.
@@ -464,7 +465,7 @@ bool paged_few_launch(int dtype, const PagedAttnParams& p, const PagedSplit& ws,
 constexpr int kTcRows = 256;
 int paged_tc_grid(int dtype, int head_dim, int sm_count);
 long long paged_tc_part_rows(int grid);
-size_t paged_tc_list_bytes(int grid, long long row_tiles);
+size_t paged_tc_list_bytes(int grid, long long items);
 PagedPrefixParts paged_tc_prefix(const PagedAttnParams& p, const PagedSplit& ws);
 bool paged_tc_launch(int dtype, const PagedAttnParams& p, const PagedSplit& ws, PagedMode mode,
                      const PagedPrefixParts& pre, cudaStream_t st);

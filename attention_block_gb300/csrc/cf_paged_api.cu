@@ -255,7 +255,7 @@ int cf_paged_create(const cf_paged_config* cfg, cf_paged_handle** out) {
   // of the sequences' own keys and of the prefix.  A call uses one attention
   // kernel for each, so the kernels share them.
   const size_t tickets = take(c.dtype != CF_F32 ? (size_t)c.max_batch * c.n_kv_heads * 4 : 4);
-  const size_t redo = take(2 * 4);
+  const size_t redo = take(3 * 4);
   const size_t zero = bytes;
   const int64_t all_rows = (int64_t)c.max_tokens * c.n_q_heads;
   size_t tc_list = 0, at_o[2] = {0, 0}, at_ml[2] = {0, 0};
@@ -268,12 +268,13 @@ int cf_paged_create(const cf_paged_config* cfg, cf_paged_handle** out) {
     if ((int64_t)c.max_tokens * h->geom.G > kFewRows) {
       h->tc.grid = paged_tc_grid(c.dtype, c.head_dim, h->sm_count);
       if (h->tc.grid == 0) return fail(CF_ERR_CUDA);
-      tc_list = take(paged_tc_list_bytes(
-          h->tc.grid, ((int64_t)c.max_tokens * h->geom.G / kTcRows + c.max_batch) * c.n_kv_heads));
+      h->tc.items = ((int64_t)c.max_tokens * h->geom.G / kTcRows + c.max_batch) * c.n_kv_heads;
+      tc_list = take(paged_tc_list_bytes(h->tc.grid, h->tc.items));
       slot_rows = std::max<int64_t>(slot_rows, paged_tc_part_rows(h->tc.grid));
     }
-    // single rows: a prefix call's, and the few-row kernel's own
-    const int64_t rows[2] = {slot_rows + std::min(all_rows, few_rows), slot_rows + all_rows};
+    // single rows: the sequences' own before a prefix's are joined, and a prefix's
+    const int64_t rows[2] = {slot_rows + (h->tc.grid ? all_rows : std::min(all_rows, few_rows)),
+                             slot_rows + all_rows};
     for (int i = 0; i < 2; ++i) {
       at_o[i] = take((size_t)rows[i] * c.head_dim * 4);
       at_ml[i] = take((size_t)rows[i] * 8);

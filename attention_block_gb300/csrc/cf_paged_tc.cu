@@ -328,8 +328,9 @@ struct TcCursor {
   }
 };
 
-// A split item, for the kernel that joins its parts: written by the block
-// that begins it.
+// An item whose states the joining kernel takes up, written by the block that
+// begins it: a split one (one per block at most, at the block's place), and
+// after a prefix every one (in a list, in no order).
 struct alignas(16) TcMeta {
   long long i0, upc;
   int tiles;  // 0: this block begins no split item
@@ -346,8 +347,11 @@ struct TcArgs {
   PagedPrefixParts pre;
   PagedParts ws;
   TcMeta* meta;
+  int n_meta, max_redo;  // places of the lists: short only where starts contradict themselves
   TcRedo* redo;
-  int* n_redo;  // and, next to it, blocks that are done with the list; both 0 between calls
+  // Items to be computed again, blocks that are done with them, items listed
+  // in meta; all 0 between calls.
+  int* n_redo;
   int slots;  // upper bound on the row tiles' numbers
 };
 
@@ -389,7 +393,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const __grid_co
     }
     fence_mbar_init_cluster();
   }
-  pdl_wait();
+  // After a prefix launch this one reads only what that launch has waited for
+  // already, so it starts on the SMs that it leaves and waits for it at the end.
+  if constexpr (!JOIN) pdl_wait();
   pdl_trigger();
 
   // ---- this block's units
@@ -459,8 +465,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const __grid_co
   }
   const long long upc = PRE ? a.pre.upc : div_units(total + gridDim.x - 1, gridDim.x);
   const long long u0 = blockIdx.x * upc, u1 = min(total, u0 + upc);
-  if (!PRE && tid == 0) a.meta[blockIdx.x].tiles = 0;
-  if (u0 >= u1) return;
+  if (MODE == kOwn && tid == 0) a.meta[blockIdx.x].tiles = 0;
+  if (u0 >= u1) {
+    if constexpr (JOIN) pdl_wait();
+    return;
+  }
   if (before <= u0 && u0 < before + mine) {
     long long at = before;
     auto start = [&](const RowTile& t) {
@@ -601,14 +610,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const __grid_co
         tc05_fence_after();
       }
       const float m2 = m * sc;  // base 2
-      const bool part = PRE || !whole;  // leaves a state, not a result
+      const bool part = MODE != kOwn || !whole;  // leaves a state, not a result
       // this block's slot for the item (PagedParts)
       const long long prow0 =
           (2 * (long long)blockIdx.x + (u0 >= cur.i0 ? 0 : 1)) * (2 * kHalf) + hf * kHalf;
       const int q4 = lane & 3;
       // this lane's own row: where it goes, and what its values are scaled by
       long long my_row = -1;
-      float my_inv = 1.f, my_own = 1.f, my_ref = 0.f;
+      float my_inv = 1.f;
       if (gr < t.rows) {
         const int i = gr / p.g.G;
         my_row = ((long long)t.t0 + i) * p.g.nq + cur.h * p.g.G + gr - i * p.g.G;
@@ -616,24 +625,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const __grid_co
           my_row = whole ? a.ws.state_base + my_row : prow0 + r;
           __stcg(a.ws.ml + my_row, make_float2(m2, l));
         } else {
-          float mt = m2, lt = l;
-          if (JOIN && t.p0 + i >= 0) {
-            const PagedRowParts pp =
-                paged_prefix_row(a.pre, p.g, (long long)t.t0 + i, cur.h, gr - i * p.g.G);
-#pragma unroll 4
-            for (int k = 0; k < pp.n; ++k) mt = fmaxf(mt, __ldcg(a.pre.ml + pp.row(k)).x);
-            my_ref = mt == -INFINITY ? 0.f : mt;
-            my_own = ex2(m2 - my_ref);
-            lt *= my_own;
-#pragma unroll 4
-            for (int k = 0; k < pp.n; ++k) {
-              const float2 ml = __ldcg(a.pre.ml + pp.row(k));
-              lt += ml.y * ex2(ml.x - my_ref);
-            }
-          }
-          my_inv = lt == 0.f ? 0.f : 1.f / lt;
+          my_inv = l == 0.f ? 0.f : 1.f / l;
           if (p.lse)
-            p.lse[my_row] = mt == -INFINITY ? -INFINITY : (mt + log2f(lt)) * 0.69314718055994531f;
+            p.lse[my_row] = m2 == -INFINITY ? -INFINITY : (m2 + log2f(l)) * 0.69314718055994531f;
         }
       }
 #pragma unroll 1
@@ -648,78 +642,51 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const __grid_co
         }
 #pragma unroll 1
         for (int c64 = 0; c64 < D; c64 += 64) {
-        float o2[2][16];
-        if (some) {
-          tmem_ld_frag(to + ((uint32_t)(16 * hh) << 16) + c64, o2[0]);
-          tmem_ld_frag(to + ((uint32_t)(16 * hh) << 16) + c64 + 32, o2[1]);
-          tmem_wait_ld();
-        } else {
+          float o2[2][16];
+          if (some) {
+            tmem_ld_frag(to + ((uint32_t)(16 * hh) << 16) + c64, o2[0]);
+            tmem_ld_frag(to + ((uint32_t)(16 * hh) << 16) + c64 + 32, o2[1]);
+            tmem_wait_ld();
+          } else {
 #pragma unroll
-          for (int x = 0; x < 32; ++x) o2[x >> 4][x & 15] = 0.f;
-        }
+            for (int x = 0; x < 32; ++x) o2[x >> 4][x & 15] = 0.f;
+          }
 #pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          const int c = c64 + 32 * y;
-          float(&o)[16] = o2[y];
+          for (int y = 0; y < 2; ++y) {
+            const int c = c64 + 32 * y;
+            const float(&o)[16] = o2[y];
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            if (part) {
-              // of two octets A, B the even lanes of a quad store A's words, the
-              // odd ones B's, 16 bytes each
+            for (int e = 0; e < 2; ++e) {
+              if (part) {
+                // of two octets A, B the even lanes of a quad store A's words,
+                // the odd ones B's, 16 bytes each
 #pragma unroll
-              for (int b2 = 0; b2 < 2; ++b2) {
-                const float A0 = o[8 * b2 + 2 * e], A1 = o[8 * b2 + 2 * e + 1];
-                const float B0 = o[8 * b2 + 4 + 2 * e], B1 = o[8 * b2 + 5 + 2 * e];
-                const bool odd = q4 & 1;
-                const float g0 = __shfl_xor_sync(~0u, odd ? A0 : B0, 1);
-                const float g1 = __shfl_xor_sync(~0u, odd ? A1 : B1, 1);
-                if (orow[e] >= 0)
-                  __stcg(reinterpret_cast<float4*>(a.ws.o + orow[e] * D + c + 16 * b2 + 8 * (q4 & 1) +
-                                                   4 * (q4 >> 1)),
-                         odd ? make_float4(g0, g1, B0, B1) : make_float4(A0, A1, g0, g1));
-              }
-            } else {
-              if constexpr (JOIN) {
-                const int src = hh * 16 + e * 8 + (lane >> 2);
-                const float own = __shfl_sync(~0u, my_own, src), ref = __shfl_sync(~0u, my_ref, src);
-                const int rg = t.j * 2 * kHalf + hf * kHalf + (warp & 3) * 32 + src;
-                const int i = rg / p.g.G;
-                if (rg < t.rows && t.p0 + i >= 0) {
-                  const PagedRowParts pp =
-                      paged_prefix_row(a.pre, p.g, (long long)t.t0 + i, cur.h, rg - i * p.g.G);
-#pragma unroll
-                  for (int b = 0; b < 4; ++b) {
-                    o[4 * b + 2 * e] *= own;
-                    o[4 * b + 2 * e + 1] *= own;
-                  }
-#pragma unroll 2
-                  for (int k = 0; k < pp.n; ++k) {
-                    const long long at = pp.row(k);
-                    const float f = ex2(__ldcg(a.pre.ml + at).x - ref);
-#pragma unroll
-                    for (int b = 0; b < 4; ++b) {
-                      const float2 v = __ldcg(
-                          reinterpret_cast<const float2*>(a.pre.o + at * D + c + 8 * b + 2 * q4));
-                      o[4 * b + 2 * e] = fmaf(v.x, f, o[4 * b + 2 * e]);
-                      o[4 * b + 2 * e + 1] = fmaf(v.y, f, o[4 * b + 2 * e + 1]);
-                    }
-                  }
+                for (int b2 = 0; b2 < 2; ++b2) {
+                  const float A0 = o[8 * b2 + 2 * e], A1 = o[8 * b2 + 2 * e + 1];
+                  const float B0 = o[8 * b2 + 4 + 2 * e], B1 = o[8 * b2 + 5 + 2 * e];
+                  const bool odd = q4 & 1;
+                  const float g0 = __shfl_xor_sync(~0u, odd ? A0 : B0, 1);
+                  const float g1 = __shfl_xor_sync(~0u, odd ? A1 : B1, 1);
+                  if (orow[e] >= 0)
+                    __stcg(reinterpret_cast<float4*>(a.ws.o + orow[e] * D + c + 16 * b2 +
+                                                     8 * (q4 & 1) + 4 * (q4 >> 1)),
+                           odd ? make_float4(g0, g1, B0, B1) : make_float4(A0, A1, g0, g1));
                 }
-              }
-              uint32_t w[4];
+              } else {
+                uint32_t w[4];
 #pragma unroll
-              for (int b = 0; b < 4; ++b)
-                w[b] = pack2<T>(o[4 * b + 2 * e] * inv[e], o[4 * b + 2 * e + 1] * inv[e]);
-              quad_transpose(w, q4);  // lane q: the 8 columns of octet q
-              if (orow[e] >= 0)
-                *reinterpret_cast<uint4*>(static_cast<T*>(p.out) + orow[e] * D + c + 8 * q4) =
-                    make_uint4(w[0], w[1], w[2], w[3]);
+                for (int b = 0; b < 4; ++b)
+                  w[b] = pack2<T>(o[4 * b + 2 * e] * inv[e], o[4 * b + 2 * e + 1] * inv[e]);
+                quad_transpose(w, q4);  // lane q: the 8 columns of octet q
+                if (orow[e] >= 0)
+                  *reinterpret_cast<uint4*>(static_cast<T*>(p.out) + orow[e] * D + c + 8 * q4) =
+                      make_uint4(w[0], w[1], w[2], w[3]);
+              }
             }
           }
         }
-        }
       }
-      if (!PRE && !whole && first == 0 && tid == 0) {
+      if (!PRE && part && first == 0 && tid == 0) {
         TcMeta x;
         x.i0 = cur.i0;
         x.upc = upc;
@@ -729,7 +696,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const __grid_co
         x.rows = t.rows;
         x.j = t.j;
         x.h = cur.h;
-        a.meta[blockIdx.x] = x;
+        const int at = JOIN ? atomicAdd(a.n_redo + 2, 1) : blockIdx.x;
+        if (at < a.n_meta) a.meta[at] = x;
       }
       tc05_fence_before();  // O is read before the next item's first product
       __syncwarp();
@@ -975,7 +943,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const __grid_co
           x.rows = cur.t.rows;
           x.j = cur.t.j;
           x.h = cur.h;
-          a.redo[atomicAdd(a.n_redo, 1)] = x;
+          const int at = atomicAdd(a.n_redo, 1);
+          if (at < a.max_redo) a.redo[at] = x;
         }
         if (lane == 0) {
           cur.u += count - 1;
@@ -991,15 +960,19 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const __grid_co
   }
   __syncthreads();
   if (warp == 12) tmem_dealloc(tmem, 512);
+  if constexpr (JOIN) pdl_wait();
 }
 
-// Joins the parts of the item that block x of the main kernel began, if that
-// was split: a row per D / 4 lanes.  Then computes listed items again.  Bound
-// by the launch and by reads of the parts that are in L2; four blocks on an SM
-// with four parts in flight per lane and 16 blocks to an item take 2-10 us
-// less than eight in flight at two or three blocks with 32 to an item (8191
-// tokens, window 1024: 197.5 -> 185.6 us with the main kernel; 4 prompts of
-// 517-2048 behind 0-2049: 150.3 -> 144.6).
+// Joins the states of the listed items, and the prefix's to them: a row per
+// D / 4 lanes, gridDim.y blocks to an item.  Then computes again the items
+// where that was asked for.  Bound by the launch and by reads of the states
+// that are in L2; four blocks on an SM with four parts in flight per lane and
+// up to 16 blocks to an item take 2-15 us less than eight in flight at two or
+// three blocks with 32 to an item (with the main kernel, 8191 tokens, window
+// 1024: 202 -> 185 us; 4 prompts of 517-2048 behind 0-2049: 150 -> 143).  That
+// all items after a prefix are joined here, and none by the main kernel with a
+// thread to a row, is 312 -> 167 us for 128 sequences of 8 tokens behind 8192
+// shared positions (32 / 8 heads of 128).
 constexpr int kTcJoinY = 16;
 template <typename T, int D>
 __global__ void __launch_bounds__(256, 4) paged_tc_join_kernel(const __grid_constant__ TcArgs a) {
@@ -1008,13 +981,16 @@ __global__ void __launch_bounds__(256, 4) paged_tc_join_kernel(const __grid_cons
   const int tid = threadIdx.x, lane = tid & 31;
   pdl_wait();
   pdl_trigger();
-  const TcMeta x = a.meta[blockIdx.x];
-  const int n_redo = a.n_redo[0];
+  const bool prefix = a.pre.rows != 0;
+  const int n_redo = min(a.n_redo[0], a.max_redo);
+  const int n_items = prefix ? min(a.n_redo[2], a.n_meta) : a.n_meta;
   constexpr int C4 = D / 4;
-  bool join = x.tiles != 0;
-  for (int i = 0; i < n_redo && join; ++i)
-    join = a.redo[i].t0 != x.t0 || a.redo[i].j != x.j || a.redo[i].h != x.h;
-  if (join) {
+  for (int item = blockIdx.x; item < n_items; item += gridDim.x) {
+    const TcMeta x = a.meta[item];
+    bool join = x.tiles != 0;
+    for (int i = 0; i < n_redo && join; ++i)
+      join = a.redo[i].t0 != x.t0 || a.redo[i].j != x.j || a.redo[i].h != x.h;
+    if (!join) continue;
     const int rows = min(2 * kHalf, x.rows - x.j * 2 * kHalf);
     const PagedItemParts parts(x.i0, x.tiles, x.upc);
     for (int e = blockIdx.y * 256 + tid; e < rows * C4; e += gridDim.y * 256) {
@@ -1022,13 +998,15 @@ __global__ void __launch_bounds__(256, 4) paged_tc_join_kernel(const __grid_cons
       PagedState4 s{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
       const int gr = x.j * 2 * kHalf + r, i = gr / p.g.G, g = gr - i * p.g.G;
       const long long t = x.t0 + i;
-      paged_join_row<D, 4>(s, a.ws.o, a.ws.ml, PagedRowParts(parts, 2 * kHalf, r, 0), col);
-      if (a.pre.rows && x.p0 + i >= 0)
+      const long long row = t * p.g.nq + x.h * p.g.G + g;
+      paged_join_row<D, 4>(s, a.ws.o, a.ws.ml,
+                           PagedRowParts(parts, 2 * kHalf, r, a.ws.state_base + row), col);
+      if (prefix && x.p0 + i >= 0)
         paged_join_row<D, 4>(s, a.pre.o, a.pre.ml, paged_prefix_row(a.pre, p.g, t, x.h, g), col);
-      paged_store4<T, D>(s, p.out, p.lse, t * p.g.nq + x.h * p.g.G + g, col);
+      paged_store4<T, D>(s, p.out, p.lse, row, col);
     }
   }
-  if (n_redo == 0) return;
+  if (n_redo == 0 && !prefix) return;
   const int warps = gridDim.x * gridDim.y * 8;
   float* q = s_q[tid >> 5];
   for (int e = (blockIdx.y * gridDim.x + blockIdx.x) * 8 + (tid >> 5); e < n_redo * 2 * kHalf;
@@ -1052,11 +1030,12 @@ __global__ void __launch_bounds__(256, 4) paged_tc_join_kernel(const __grid_cons
       p.lse[t * p.g.nq + h] =
           r.m == -INFINITY ? -INFINITY : (r.m + log2f(r.l)) * 0.69314718055994531f;
   }
-  // the last block out empties the list
+  // the last block out empties the lists
   __syncthreads();
   if (tid == 0 && atomicAdd(a.n_redo + 1, 1) == (int)(gridDim.x * gridDim.y) - 1) {
     a.n_redo[0] = 0;
     a.n_redo[1] = 0;
+    a.n_redo[2] = 0;
   }
 }
 
@@ -1106,9 +1085,10 @@ int cf::paged_tc_grid(int dtype, int head_dim, int sm_count) {
 
 long long cf::paged_tc_part_rows(int grid) { return 2LL * grid * kTcRows; }
 
-size_t cf::paged_tc_list_bytes(int grid, long long row_tiles) {
-  // every part of an item can be listed
-  return (size_t)grid * sizeof(TcMeta) + (size_t)(row_tiles + grid) * sizeof(TcRedo);
+size_t cf::paged_tc_list_bytes(int grid, long long items) {
+  // every part of an item can be listed for another pass
+  return (size_t)std::max<long long>(grid, items) * sizeof(TcMeta) +
+         (size_t)(items + grid) * sizeof(TcRedo);
 }
 
 PagedPrefixParts cf::paged_tc_prefix(const PagedAttnParams& p, const PagedSplit& ws) {
@@ -1133,10 +1113,17 @@ bool cf::paged_tc_launch(int dtype, const PagedAttnParams& p, const PagedSplit& 
   a.pre = pre;
   a.ws = ws.parts;
   a.meta = static_cast<TcMeta*>(ws.list);
-  a.redo = reinterpret_cast<TcRedo*>(a.meta + ws.grid);
+  const long long n_list = std::max<long long>(ws.grid, ws.items);
+  a.n_meta = (int)(mode == kOwn ? ws.grid : n_list);
+  a.max_redo = (int)(ws.items + ws.grid);
+  a.redo = reinterpret_cast<TcRedo*>(a.meta + n_list);
   a.n_redo = ws.tickets;
   a.slots = (int)((long long)p.n_tokens * p.g.G / kTcRows) + p.batch;
   void* args[] = {&a};
   if (!launch_pdl(f.main, dim3(ws.grid), kTcThreads, f.smem, st, args)) return false;
-  return mode == kPrefix || launch_pdl(f.join, dim3(ws.grid, kTcJoinY), 256, 0, st, args);
+  if (mode == kPrefix) return true;
+  // fewer blocks to an item where its rows are fewer
+  const long long rows = std::min<long long>(kTcRows, (long long)p.max_q * p.g.G);
+  const int y = (int)std::min<long long>(kTcJoinY, (rows * (p.g.D / 4) + 255) / 256);
+  return launch_pdl(f.join, dim3(ws.grid * (kTcJoinY / y), y), 256, 0, st, args);
 }

@@ -733,6 +733,22 @@ def test_calls_of_every_kind_on_one_handle_repeat_their_bits():
     assert r.kv.status() == OK
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("head_dim", [64, 128])
+def test_prefix_with_many_short_prompts(dtype, head_dim):
+    # more than 16 rows a head, several items to a block, rows that see nothing, sequences without
+    # tokens; then twice more on the handle: every call finds the lists empty again
+    pr = Problem([8, 5, 0, 9] * 60, [8, 130, 0, 4] * 60, 8, 2, d=head_dim, dtype=dtype, prefix=300,
+                 seed=31)
+    r = attend_and_check(pr)
+    first = r.out.clone()
+    for _ in range(2):
+        r.out.fill_(float("nan"))
+        r.attend()
+        assert torch.equal(r.out, first)
+    assert r.kv.status() == OK
+
+
 @pytest.mark.parametrize("prefix", [0, 60])
 def test_captured_prompts_replay_with_other_lengths(prefix):
     pr = Problem([100, 3, 40], [150, 3, 90], 8, 2, seed=73, prefix=prefix, max_pages=16, spare=60)
