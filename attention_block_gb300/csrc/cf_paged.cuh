@@ -452,8 +452,7 @@ bool paged_attn_simple_launch(int dtype, const PagedAttnParams& p, cudaStream_t 
 
 // The kernel for few rows (tokens x grouped heads), and the one on the fifth
 // generation's tensor cores for many.  grid: resident blocks, 0 on failure;
-// part_rows and
-// list_bytes: workspace; launch with kPrefix: the call's tokens
+// part_rows and list_bytes: workspace; launch with kPrefix: the call's tokens
 // against the prefix alone; prefix: how such a launch cuts it.
 constexpr int kFewRows = 16;
 int paged_few_grid(int dtype, int head_dim, int sm_count);

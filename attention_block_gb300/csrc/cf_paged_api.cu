@@ -141,7 +141,9 @@ int attention(cf_paged_handle* h, int32_t batch, int32_t n_tokens, int32_t max_q
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   // fp32 has no tensor-core form.  Up to 16 rows per KV head (tokens of one
   // sequence x grouped heads) share a tile of the few-row kernel; more go to
-  // the tensor-core kernel.  For the prefix the rows are the whole call's.
+  // the tensor-core kernel, which takes 76 us for 54 with 4 rows (16 sequences
+  // of 4097 positions) and 129 for 100 with 16 (32 of 4004).  For the prefix
+  // the rows are the whole call's.
   bool ok;
   if (c.dtype == CF_F32) {
     ok = paged_attn_simple_launch(c.dtype, p, st);

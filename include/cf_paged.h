@@ -33,16 +33,17 @@
  *   s_j = scale * q_h . k_j,   o_h = sum_j exp(s_j) v_j / sum_j exp(s_j)   over visible j
  *   lse_h = ln sum_j exp(s_j)
  * A row that sees no key (p < 0, also where there is a prefix) gets o = 0 and
- * lse = -infinity.  What lies
- * in slots that no row of the sequence sees (past kv_len, behind the window,
- * in pages that only such positions map to) never reaches a result, and the
- * table's entries for them are not read as pages.
+ * lse = -infinity.  What lies in a slot, be it an infinity or a NaN, reaches
+ * the rows that see its position and no other.  Table entries of positions
+ * that no row of the sequence sees (past kv_len, behind the window) are not
+ * read as pages.
  *
  * Arithmetic: products and sums in fp32 (fp32 storage: plain fp32 FMAs; fp16
  * and bf16: tensor-core products of the stored values).  Probabilities enter
- * the product with V rounded to the storage type; their sum is taken before
- * that rounding.  Outputs are rounded once.  Angles are exact to 2^-32 of a
- * turn for every int32 position.
+ * the product with V rounded to the storage type (in bf16, with max_q * nq/nkv
+ * of 16 at most, as a sum of two such values); their sum is taken before that
+ * rounding.  Outputs are rounded once.  Angles are exact to 2^-32 of a turn for
+ * every int32 position.  The same call on the same data gives the same bits.
  *
  * Conventions for every function:
  *   - CF_OK (0) or a negative CF_ERR_* code of cf.h; nothing is printed and no
@@ -105,9 +106,10 @@ typedef struct cf_paged_config {
 
 typedef struct cf_paged_handle cf_paged_handle; /* opaque */
 
-/* Validate cfg and allocate the handle's workspace (partial results of split
- * sequences, and an error word: about 130 MB
- * plus, per token of max_tokens, up to 2 * nq * (d + 2) fp32 values) on the current device.
+/* Validate cfg and allocate the handle's workspace on the current device: an
+ * error word and, but for fp32, partial results of split sequences (up to
+ * 160,000 * (d + 2) fp32 values, 81 MB for d = 128) and of whole ones beside a
+ * prefix (per token of max_tokens up to 2 * nq * (d + 2) fp32 values).
  * On failure nothing stays allocated and *out is NULL.  Errors: INVALID_ARG
  * (NULL, sizes, strides, sections that do not add up), UNSUPPORTED
  * (head_dim, page_size), CUDA. */
