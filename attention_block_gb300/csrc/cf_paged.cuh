@@ -448,7 +448,12 @@ struct PagedSplit {
 
 // Host launchers (one translation unit each); false: the launch failed.
 bool paged_append_launch(int dtype, const PagedAppendParams& p, int sm_count, cudaStream_t st);
-bool paged_attn_simple_launch(int dtype, const PagedAttnParams& p, cudaStream_t st);
+
+// The fp32 kernel.  grid: resident blocks, 0 on failure; part_rows: workspace;
+// a ticket per resident block.
+int paged_f32_grid(int head_dim, int sm_count);
+long long paged_f32_part_rows(int grid);
+bool paged_f32_launch(const PagedAttnParams& p, const PagedSplit& ws, cudaStream_t st);
 
 // The kernel for few rows (tokens x grouped heads), and the one on the fifth
 // generation's tensor cores for many.  grid: resident blocks, 0 on failure;

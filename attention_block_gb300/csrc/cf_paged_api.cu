@@ -146,7 +146,7 @@ int attention(cf_paged_handle* h, int32_t batch, int32_t n_tokens, int32_t max_q
   // the rows are the whole call's.
   bool ok;
   if (c.dtype == CF_F32) {
-    ok = paged_attn_simple_launch(c.dtype, p, st);
+    ok = paged_f32_launch(p, h->few, st);
   } else {
     PagedPrefixParts pre;
     std::memset(&pre, 0, sizeof(pre));
@@ -256,7 +256,11 @@ int cf_paged_create(const cf_paged_config* cfg, cf_paged_handle** out) {
   // The words that start at zero, then the lists, then two sets of states:
   // of the sequences' own keys and of the prefix.  A call uses one attention
   // kernel for each, so the kernels share them.
-  const size_t tickets = take(c.dtype != CF_F32 ? (size_t)c.max_batch * c.n_kv_heads * 4 : 4);
+  h->few.grid = c.dtype == CF_F32 ? paged_f32_grid(c.head_dim, h->sm_count)
+                                  : paged_few_grid(c.dtype, c.head_dim, h->sm_count);
+  if (h->few.grid == 0) return fail(CF_ERR_CUDA);
+  const size_t tickets =
+      take(4 * (c.dtype == CF_F32 ? (size_t)h->few.grid : (size_t)c.max_batch * c.n_kv_heads));
   const size_t redo = take(3 * 4);
   const size_t zero = bytes;
   const int64_t all_rows = (int64_t)c.max_tokens * c.n_q_heads;
@@ -264,8 +268,6 @@ int cf_paged_create(const cf_paged_config* cfg, cf_paged_handle** out) {
   const int64_t few_rows = (int64_t)c.max_batch * c.n_kv_heads * kFewRows;
   int64_t slot_rows = 0;
   if (c.dtype != CF_F32) {
-    h->few.grid = paged_few_grid(c.dtype, c.head_dim, h->sm_count);
-    if (h->few.grid == 0) return fail(CF_ERR_CUDA);
     slot_rows = paged_few_part_rows(h->few.grid);
     if ((int64_t)c.max_tokens * h->geom.G > kFewRows) {
       h->tc.grid = paged_tc_grid(c.dtype, c.head_dim, h->sm_count);
@@ -281,6 +283,10 @@ int cf_paged_create(const cf_paged_config* cfg, cf_paged_handle** out) {
       at_o[i] = take((size_t)rows[i] * c.head_dim * 4);
       at_ml[i] = take((size_t)rows[i] * 8);
     }
+  } else {
+    slot_rows = paged_f32_part_rows(h->few.grid);
+    at_o[0] = take((size_t)slot_rows * c.head_dim * 4);
+    at_ml[0] = take((size_t)slot_rows * 8);
   }
   if (cudaMalloc(&h->ws, bytes) != cudaSuccess) {
     cudaGetLastError();

@@ -14,7 +14,8 @@
  *                              a few first positions that stay visible
  *   cf_paged_prefix_attention  the same without a window, for a batch whose
  *                              sequences all continue one shared prefix; the
- *                              prefix is read once for the whole batch
+ *                              prefix is read once for the whole batch (fp32:
+ *                              once per sequence)
  *
  * A call holds `n_tokens` new tokens of `batch` sequences.  Sequence b has
  * the tokens q_start[b] .. q_start[b+1]-1 (n_b of them, none allowed) and,

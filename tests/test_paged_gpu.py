@@ -749,6 +749,23 @@ def test_prefix_with_many_short_prompts(dtype, head_dim):
     assert r.kv.status() == OK
 
 
+@pytest.mark.parametrize("head_dim", [64, 128])
+@pytest.mark.parametrize("q_len,kv_len,heads,prefix,window", [
+    ([1], [5000], (4, 1), 0, 0),              # 4 rows, the positions over many blocks
+    ([1, 1], [3001, 5], (16, 1), 0, 700),     # 16 rows, one block has nothing to see
+    ([3, 0, 2], [900, 4, 2], (6, 2), 333, 0),  # a prefix, an idle sequence
+    ([130], [700], (3, 1), 0, 90),            # several row tiles, rows of two tokens in one
+], ids=str)
+def test_fp32_over_many_blocks(head_dim, q_len, kv_len, heads, prefix, window):
+    pr = Problem(q_len, kv_len, *heads, d=head_dim, dtype="f32", prefix=prefix, seed=32)
+    r = attend_and_check(pr, window, 2 if window else 0)
+    first = r.out.clone()
+    for _ in range(2):  # the tickets are back at zero, the order of arrival does not show
+        r.out.fill_(float("nan"))
+        r.attend(window, 2 if window else 0)
+        assert torch.equal(r.out, first)
+
+
 @pytest.mark.parametrize("prefix", [0, 60])
 def test_captured_prompts_replay_with_other_lengths(prefix):
     pr = Problem([100, 3, 40], [150, 3, 90], 8, 2, seed=73, prefix=prefix, max_pages=16, spare=60)
