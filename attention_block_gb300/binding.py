@@ -658,7 +658,7 @@ class PagedKv:
 
     def status(self) -> int:
         import torch
-        torch.cuda.synchronize()
+        torch.cuda.synchronize(self._dev)
         return lib().cf_paged_get_status(self.handle)
 
     def close(self) -> None:

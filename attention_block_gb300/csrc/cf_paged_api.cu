@@ -99,7 +99,8 @@ int attention(cf_paged_handle* h, int32_t batch, int32_t n_tokens, int32_t max_q
   for (const void* p : ints)
     if (p == nullptr || !aligned(p, 4)) return CF_ERR_INVALID_ARG;
   if (!aligned(q_start, 4) || !aligned(lse, 4)) return CF_ERR_INVALID_ARG;
-  if (q_stride < qrow || (q_stride * (int64_t)es) % 16 != 0) return CF_ERR_INVALID_ARG;
+  if (q_stride < qrow || q_stride > (int64_t)1 << 40 || (q_stride * (int64_t)es) % 16 != 0)
+    return CF_ERR_INVALID_ARG;
   const size_t ob = (size_t)n_tokens * qrow * es, lb = (size_t)n_tokens * c.n_q_heads * 4;
   const size_t pool = (size_t)h->pool_elems * es;
   struct {

@@ -75,7 +75,10 @@ __global__ void __launch_bounds__(kF32Threads, D == 64 ? 2 : 1)
   auto first_no = [&](int b, int t0) { return (int)((long long)t0 * G / R) + b; };
   for (int b = tid; b < p.batch; b += kF32Threads) {
     const int t0 = p.q_start ? p.q_start[b] : b, t1 = p.q_start ? p.q_start[b + 1] : b + 1;
-    if (t0 < 0 || t1 > p.n_tokens || t1 <= t0) continue;
+    if (t0 < 0 || t1 > p.n_tokens || t1 < t0) {
+      atomicOr(p.errflag, kDevErrPosRange);
+      continue;
+    }
     const int j = (int)blockIdx.x - first_no(b, t0);
     if (j >= 0 && j < ((t1 - t0) * G + R - 1) / R) atomicMax(&s_seq, b);
   }
@@ -371,6 +374,7 @@ bool cf::paged_f32_launch(const PagedAttnParams& p, const PagedSplit& ws, cudaSt
   a.p = p;
   a.ws = ws.parts;
   a.tickets = ws.tickets;
-  f.fn<<<dim3((unsigned)tiles, p.g.nkv, (unsigned)splits), kF32Threads, f.smem, st>>>(a);
-  return cudaGetLastError() == cudaSuccess;
+  void* args[] = {&a};
+  return cudaLaunchKernel((const void*)f.fn, dim3((unsigned)tiles, p.g.nkv, (unsigned)splits),
+                          dim3(kF32Threads), args, f.smem, st) == cudaSuccess;
 }

@@ -385,6 +385,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const __grid_co
 
   if (sq & 1023u) {  // the swizzle goes by the address
     if (tid == 0) atomicOr(err, kDevErrTimeout);
+    if constexpr (JOIN) pdl_wait();
     return;
   }
   if (tid == 0) {

@@ -456,6 +456,37 @@ def test_more_tokens_than_max_q_and_bad_starts_are_reported():
     assert r.out[2:].isnan().all()
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("prefix", [0, 40])
+def test_bad_starts_and_lengths_of_prompts_are_reported(dtype, prefix):
+    pr = Problem([70, 3, 40], [90, 30, 40], 4, 2, dtype=dtype, prefix=prefix, seed=33)
+    r = Run(pr)
+    good = ref_attention(pr)
+    r.attend(max_q=69)
+    assert r.kv.status() == RANGE
+    assert (r.out[:70] == 0).all() and torch.isinf(r.lse[:70]).all()
+    close(r.out[70:], good[0][70:], good[1][70:], "good sequences")
+    r.out.fill_(float("nan"))
+    r.q_start.copy_(torch.tensor([0, 70, 60, 999], dtype=torch.int32))
+    r.attend()
+    assert r.kv.status() == RANGE
+    close(r.out[:70], good[0][:70], good[1][:70], "the good sequence")
+    assert r.out[70:].isnan().all()
+    r.q_start.copy_(torch.tensor(pr.starts, dtype=torch.int32))
+    r.attend()
+    r.check()
+
+
+def test_strides_that_overflow_are_refused():
+    pr = Problem([1, 2], [20, 30], 4, 2, seed=34)
+    r = Run(pr)
+    for stride in (2 ** 62, (1 << 40) + 8):
+        with pytest.raises(binding.CfError) as e:
+            r.kv.attention(2, 3, 2, r.q, r.q_start, r.kv_len, r.table, r.k_pages, r.v_pages, r.out,
+                           q_stride=stride)
+        assert e.value.code == binding.CF_ERR_INVALID_ARG
+
+
 # -------------------------------------------------------------- refusals --
 def test_refusals():
     pr = Problem([1, 2], [20, 30], 4, 2, seed=32)
