@@ -69,19 +69,34 @@ __global__ void __launch_bounds__(kF32Threads, D == 64 ? 2 : 1)
   float* sq = reinterpret_cast<float*>(sm + kF32Warps * S::WARP);
 
   // Row tile j of sequence b has the number t0 * G / R + b + j: unique, below
-  // T * G / R + batch.
+  // T * G / R + batch, and the first ones increase.  So this block's sequence is
+  // the last whose first number is not above its own; a round of the search
+  // leaves a 192nd of the batch.
+  auto start = [&](int b) { return p.q_start ? p.q_start[b] : b; };
+  auto first_no = [&](int b, int t0) { return (int)((long long)t0 * G / R) + b; };
+  int lo = 0, hi = p.batch;
+  while (hi - lo > kF32Threads) {
+    const int w = (hi - lo + kF32Threads - 1) / kF32Threads, b = lo + tid * w;
+    if (tid == 0) s_seq = lo;
+    __syncthreads();
+    if (b < hi && first_no(b, start(b)) <= (int)blockIdx.x) atomicMax(&s_seq, b);
+    __syncthreads();
+    lo = s_seq;
+    hi = min(hi, lo + w);
+    __syncthreads();
+  }
   if (tid == 0) s_seq = -1;
   __syncthreads();
-  auto first_no = [&](int b, int t0) { return (int)((long long)t0 * G / R) + b; };
-  for (int b = tid; b < p.batch; b += kF32Threads) {
-    const int t0 = p.q_start ? p.q_start[b] : b, t1 = p.q_start ? p.q_start[b + 1] : b + 1;
-    if (t0 < 0 || t1 > p.n_tokens || t1 < t0) {
-      atomicOr(p.errflag, kDevErrPosRange);
-      continue;
-    }
+  if (lo + tid < hi) {
+    const int b = lo + tid, t0 = start(b), t1 = p.q_start ? p.q_start[b + 1] : b + 1;
     const int j = (int)blockIdx.x - first_no(b, t0);
-    if (j >= 0 && j < ((t1 - t0) * G + R - 1) / R) atomicMax(&s_seq, b);
+    if (t0 >= 0 && t1 <= p.n_tokens && t1 > t0 && j >= 0 && j < ((t1 - t0) * G + R - 1) / R)
+      atomicMax(&s_seq, b);
   }
+  if (p.q_start && blockIdx.x + blockIdx.y + blockIdx.z == 0)  // one block reports bad starts
+    for (int b = tid; b < p.batch; b += kF32Threads)
+      if (p.q_start[b] < 0 || p.q_start[b + 1] > p.n_tokens || p.q_start[b + 1] < p.q_start[b])
+        atomicOr(p.errflag, kDevErrPosRange);
   __syncthreads();
   const int b = s_seq;
   if (b < 0) return;  // no row tile has this number

@@ -797,6 +797,15 @@ def test_fp32_over_many_blocks(head_dim, q_len, kv_len, heads, prefix, window):
         assert torch.equal(r.out, first)
 
 
+@pytest.mark.parametrize("q_len,heads", [
+    ([1] * 193, (4, 2)), ([0, 1, 2, 0] * 150, (4, 2)), ([1] * 700, (5, 1)),
+    ([0] * 400 + [40] + [0] * 300, (6, 1)), ([1] * 3 + [0] * 37000 + [2] * 40, (3, 1))], ids=lambda x: str(len(x)))
+def test_fp32_finds_its_sequences(q_len, heads):
+    pr = Problem(q_len, [n + b % 5 for b, n in enumerate(q_len)], *heads, d=64, page=8,
+                 dtype="f32", seed=35)
+    attend_and_check(pr)
+
+
 @pytest.mark.parametrize("prefix", [0, 60])
 def test_captured_prompts_replay_with_other_lengths(prefix):
     pr = Problem([100, 3, 40], [150, 3, 90], 8, 2, seed=73, prefix=prefix, max_pages=16, spare=60)
