@@ -97,8 +97,11 @@ struct Cursor {
     h = 0;
     if (u >= end) return;
     do {
-      ++b;
-      w = work_of<TK, PRE>(p, b);
+      if (PRE || b + 1 >= p.batch) {  // only where lengths change under the call: stop
+        u = end;
+        return;
+      }
+      w = work_of<TK, PRE>(p, ++b);
     } while (w.tiles == 0);
   }
 };
@@ -200,13 +203,13 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     while (true) {
       c.w = work_of<KS, PRE>(p, b);
       const long long len = (long long)c.w.tiles * p.g.nkv;
-      if (u < at + len) break;
+      if (u < at + len || b + 1 >= nseq) break;
       at += len;
       ++b;
     }
     c.b = b;
     const long long off = u - at;
-    c.h = (int)div_units(off, c.w.tiles);
+    c.h = (int)div_units(off, max(c.w.tiles, 1));
     c.tile = (int)(off - (long long)c.h * c.w.tiles);
     c.i0 = u - c.tile;
     c.u = u;
