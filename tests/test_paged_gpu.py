@@ -249,6 +249,38 @@ def test_infinities_that_some_rows_see_reach_no_others(dtype, d, heads, q_len, k
 
 
 @pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("q_len,kv_len", [([3, 2], [40, 9]), ([150, 20, 300], [170, 20, 300])], ids=str)
+def test_infinities_behind_a_prefix(dtype, q_len, kv_len):
+    """The same beside a shared prefix: own values that some rows see, twice on
+    one handle, with a call without any between."""
+    pr = Problem(q_len, kv_len, 8, 2, dtype=dtype, prefix=200, seed=36)
+    plain = ref_attention(pr)
+    r0 = Run(pr)
+    kp, vp = pr.split(pr.pools)
+    for b in range(pr.batch):
+        p0 = kv_len[b] - q_len[b]
+        pr.slot(vp, pr.table[b], p0 + 1)[:, ::5] = math.inf
+        pr.slot(vp, pr.table[b], kv_len[b] - 1)[:, 1::5] = math.nan
+    want = ref_attention(pr)
+    r = Run(pr)
+    finite = want[0].isfinite()
+    for call in range(2):
+        r.out.fill_(0.0)
+        r.attend()
+        assert r.kv.status() == OK
+        got = r.out.double().cpu()
+        assert torch.equal(got.isfinite(), finite) and torch.equal(got.isnan(), want[0].isnan())
+        close(torch.where(finite, got, 0.0), torch.where(finite, want[0], 0.0),
+              torch.where(finite, want[1], 0.0), "finite values")
+        if call == 0:
+            r.k_pages, r0.k_pages = r0.k_pages, r.k_pages
+            r.v_pages, r0.v_pages = r0.v_pages, r.v_pages
+            r.attend()
+            close(r.out, plain[0], plain[1], "the call between")
+            r.k_pages, r.v_pages = r0.k_pages, r0.v_pages
+
+
+@pytest.mark.parametrize("dtype", TYPES)
 def test_infinite_keys_and_extreme_scores(dtype):
     """Scores of +-6e4 and values near the type's limits: no overflow on the
     way, and -inf scores (a key of -inf) weigh nothing."""
