@@ -90,6 +90,8 @@ SIGNATURES = {
                                                       _vp, _vp]),
     "cf_test_cluster_gather": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, _vp, _vp, _vp, _vp]),
     "cf_test_tc05_gemm": (ctypes.c_int, [ctypes.c_int] * 4 + [_vp] * 5),
+    "cf_test_paged_line": (ctypes.c_int, [ctypes.c_int32] * 8 + [_vp] * 2 + [ctypes.c_int32]
+                           + [_vp] * 2),
     "cf_test_lost_transfer": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, ctypes.c_longlong,
                                              _vp, _vp, _vp, _vp]),
     "cf_bench_cluster_collective": (ctypes.c_int, [ctypes.c_int, ctypes.c_int, ctypes.c_int,

@@ -12,6 +12,17 @@ namespace cf {
 
 constexpr int kMaxPairs = 64;  // rotated pairs of a head (head_dim 128)
 
+// How a call's work is cut is computed by functions that also run on the host,
+// where a test walks them over any starts and lengths.
+#define CF_HOST_DEVICE __host__ __device__ __forceinline__
+CF_HOST_DEVICE void record_error(int* errflag, int bits) {
+#ifdef __CUDA_ARCH__
+  atomicOr(errflag, bits);
+#else
+  *errflag |= bits;
+#endif
+}
+
 // Addressing of the pages, common to every call of a handle.
 struct PagedGeom {
   int nq, nkv, G, D;
@@ -45,30 +56,31 @@ struct PagedAttnParams {
   float scale_log2;  // score scale * log2(e): softmax in base 2
 };
 
+// Whether a sequence's starts are in order and within the call's tokens.
+CF_HOST_DEVICE bool starts_ordered(int t0, int t1, int n_tokens) {
+  return t0 >= 0 && t1 >= t0 && t1 <= n_tokens;
+}
+
 // The tokens of sequence b: first, count and its length; a malformed entry is
 // recorded and leaves the sequence without tokens or without keys.
 struct PagedSeq {
   int t0, n, len;
 };
-__device__ __forceinline__ PagedSeq paged_seq(const int* q_start, const int* kv_len, int b,
-                                              int n_tokens, int max_q, const PagedGeom& g,
-                                              int* errflag) {
+CF_HOST_DEVICE PagedSeq paged_seq(const int* q_start, const int* kv_len, int b, int n_tokens,
+                                  int max_q, const PagedGeom& g, int* errflag) {
   PagedSeq s;
   s.t0 = q_start ? q_start[b] : b;
   const int t1 = q_start ? q_start[b + 1] : b + 1;
   s.len = kv_len[b];
-  s.n = t1 - s.t0;
-  bool bad = false;
-  if (s.t0 < 0 || t1 > n_tokens || t1 < s.t0) {
-    s.n = s.t0 = 0;
-    bad = true;
-  }
+  bool bad = !starts_ordered(s.t0, t1, n_tokens);
+  s.n = bad ? 0 : t1 - s.t0;
+  if (bad) s.t0 = 0;
   const long long cap = (long long)g.max_pages << g.page_shift;
   if (s.len < 0 || s.len > cap || s.n > max_q) {
     s.len = 0;
     bad = true;
   }
-  if (bad) atomicOr(errflag, kDevErrPosRange);
+  if (bad) record_error(errflag, kDevErrPosRange);
   return s;
 }
 
@@ -76,8 +88,7 @@ __device__ __forceinline__ PagedSeq paged_seq(const int* q_start, const int* kv_
 struct PagedRange {
   int sink, lo, hi;
 };
-__device__ __forceinline__ PagedRange paged_range(int p_lo, int p_hi, int len, int window,
-                                                  int n_sinks) {
+CF_HOST_DEVICE PagedRange paged_range(int p_lo, int p_hi, int len, int window, int n_sinks) {
   PagedRange r;
   r.hi = min(p_hi + 1, len);
   if (r.hi < 0) r.hi = 0;
@@ -110,7 +121,7 @@ struct PagedTiles {
   int sink, lo, hi;
   int ns, skip;  // sink tiles, and tiles between them and the window's first
   int tiles;
-  __device__ __forceinline__ void set(const PagedRange& r) {
+  CF_HOST_DEVICE void set(const PagedRange& r) {
     sink = r.sink;
     lo = r.lo;
     hi = r.hi;
@@ -174,7 +185,7 @@ __device__ __forceinline__ void pdl_trigger() {
 }
 
 // a / b, in 32 bits where both fit (a 64-bit division is a long chain).
-__device__ __forceinline__ long long div_units(long long a, long long b) {
+CF_HOST_DEVICE long long div_units(long long a, long long b) {
   if (((a | b) >> 32) == 0) return (long long)((uint32_t)a / (uint32_t)b);
   return a / b;
 }
@@ -182,13 +193,13 @@ __device__ __forceinline__ long long div_units(long long a, long long b) {
 // Slots of one item's partial states, in the order of its n pieces.
 struct PagedItemParts {
   int first, odd, n;
-  __device__ __forceinline__ PagedItemParts(long long i0, long long tiles, long long upc) {
+  CF_HOST_DEVICE PagedItemParts(long long i0, long long tiles, long long upc) {
     const long long c = div_units(i0, upc);
     first = (int)(2 * c);
     odd = c * upc >= i0 ? 0 : 1;  // later pieces all begin behind i0
     n = (int)(div_units(i0 + tiles - 1, upc) - c) + 1;
   }
-  __device__ __forceinline__ int slot(int k) const { return first + 2 * k + (k == 0 ? odd : 0); }
+  CF_HOST_DEVICE int slot(int k) const { return first + 2 * k + (k == 0 ? odd : 0); }
 };
 
 // The shared prefix's states, as the kernels that join them to the sequences'

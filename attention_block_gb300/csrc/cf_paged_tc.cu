@@ -44,6 +44,7 @@
 
 #include "cf_paged.cuh"
 #include "cf_tc05.cuh"
+#include "cf_test.h"
 
 using namespace cf;
 
@@ -56,6 +57,7 @@ constexpr int kBN = 128;       // positions of a tile
 // What an item costs beside its tiles, in tiles.  4 prompts of 517-2048 tokens
 // (32 / 8 heads of 128): 241 us with 0, 155 with 2, 145 with 5, 150 with 8.
 constexpr int kItemCost = 5;
+constexpr int kPagedRunInts = 9;  // of a run that cf_test_paged_line reports
 constexpr float kGrow = 8.0f;  // log2 of the growth that forces a rescale
 
 template <int D>
@@ -189,8 +191,9 @@ __device__ __forceinline__ void set_regs_down() {
 }
 
 // A row tile (256 rows of a sequence, or of the whole call for the prefix)
-// and its key tiles.  Row tile j of sequence b has the number
-// t0 * G / 256 + b + j: unique, increasing, below T * G / 256 + batch.
+// and its key tiles.  Where the starts are in order, row tile j of sequence b
+// has the number t0 * G / 256 + b + j: unique, increasing, below
+// T * G / 256 + batch.
 struct RowTile : PagedTiles<kBN> {
   int b, j, jn;        // sequence, row tile, row tiles of the sequence
   int t0, p0, rows;    // first token, its position, rows of the sequence
@@ -199,7 +202,7 @@ struct RowTile : PagedTiles<kBN> {
 };
 
 template <bool PRE>
-__device__ __forceinline__ void seq_of(const PagedAttnParams& p, int b, RowTile& t) {
+CF_HOST_DEVICE void seq_of(const PagedAttnParams& p, int b, RowTile& t) {
   t.b = b;
   if constexpr (PRE) {
     t.t0 = t.p0 = 0;
@@ -215,7 +218,7 @@ __device__ __forceinline__ void seq_of(const PagedAttnParams& p, int b, RowTile&
 
 // Fills in row tile j of the sequence that seq_of() set.
 template <bool PRE>
-__device__ __forceinline__ void tile_of(const PagedAttnParams& p, int j, RowTile& t) {
+CF_HOST_DEVICE void tile_of(const PagedAttnParams& p, int j, RowTile& t) {
   t.j = j;
   PagedRange u{0, 0, 0};
 #pragma unroll
@@ -314,7 +317,7 @@ struct TcCursor {
   int h, tile;
   long long u, i0;  // this unit, the item's first
   // true when the unit left was the last of its item in this walk
-  __device__ __forceinline__ bool next(const PagedAttnParams& p, long long end) {
+  CF_HOST_DEVICE bool next(const PagedAttnParams& p, long long end) {
     ++u;
     if (++tile < t.tiles) return u >= end;
     tile = 0;
@@ -325,7 +328,7 @@ struct TcCursor {
     if (u >= end) return true;
     int j = t.j + 1;
     while (j >= t.jn) {
-      if (PRE || t.b + 1 >= p.batch) {  // starts that contradict themselves: stop
+      if (PRE || t.b + 1 >= p.batch) {  // only where starts or lengths change under the call: stop
         u = end;
         return true;
       }
@@ -336,6 +339,84 @@ struct TcCursor {
     return true;
   }
 };
+
+// A thread's share of the row tiles while the block finds its units: those of
+// some numbers or, where starts are out of order (numbers then mean nothing),
+// of some sequences.  All threads' shares, one after another, are all row tiles
+// in the order of TcCursor, whatever the starts are.
+template <bool PRE>
+struct TcShare {
+  bool ordered;
+  int lo, hi, per;  // numbers, or sequences, lo .. hi - 1
+  CF_HOST_DEVICE TcShare(const PagedAttnParams& p, int slots, bool ordered_, int thread)
+      : ordered(ordered_) {
+    const int n = ordered ? slots : p.batch;
+    per = (n + kTcThreads - 1) / kTcThreads;
+    lo = min(n, thread * per);
+    hi = min(n, lo + per);
+  }
+  static CF_HOST_DEVICE int first_no(const PagedAttnParams& p, int b) {
+    const int t0 = p.q_start ? min(max(p.q_start[b], 0), p.n_tokens) : b;
+    return (int)((long long)t0 * p.g.G / (2 * kHalf)) + b;
+  }
+  // Calls f(tile) for the share's row tiles, in order, until it says stop.
+#pragma nv_exec_check_disable  // f runs where walk does
+  template <typename F>
+  CF_HOST_DEVICE void walk(const PagedAttnParams& p, F&& f) const {
+    if (lo >= hi) return;
+    RowTile t;
+    if constexpr (PRE) {
+      seq_of<PRE>(p, 0, t);
+      for (int j = lo; j < hi; ++j) {
+        tile_of<PRE>(p, j, t);
+        if (f(t)) return;
+      }
+    } else {
+      int b = lo, end = hi;
+      if (ordered) {  // the last sequence whose first number is <= lo
+        int e = p.batch - 1;
+        b = 0;
+        end = p.batch;
+        while (b < e) {
+          const int mid = (b + e + 1) >> 1;
+          if (first_no(p, mid) <= lo)
+            b = mid;
+          else
+            e = mid - 1;
+        }
+      }
+      for (; b < end; ++b) {
+        const int no = ordered ? first_no(p, b) : 0;
+        if (ordered && no >= hi) return;
+        seq_of<PRE>(p, b, t);
+        const int j1 = ordered ? min(t.jn, hi - no) : t.jn;
+        for (int j = ordered ? max(0, lo - no) : 0; j < j1; ++j) {
+          tile_of<PRE>(p, j, t);
+          if (f(t)) return;
+        }
+      }
+    }
+  }
+};
+
+// Sets c to unit u of the line if that lies in the row tile t, whose units
+// begin at `at`; else at moves on behind the row tile.
+template <bool PRE>
+CF_HOST_DEVICE bool start_in(const PagedAttnParams& p, const RowTile& t, long long u, long long& at,
+                             TcCursor<PRE>& c) {
+  const int len = t.tiles + kItemCost;
+  const long long n = (long long)len * p.g.nkv;
+  if (u >= at + n) {
+    at += n;
+    return false;
+  }
+  c.t = t;
+  c.h = (int)div_units(u - at, len);
+  c.i0 = at + (long long)c.h * len + kItemCost;
+  c.tile = u > c.i0 ? (int)(u - c.i0) : 0;
+  c.u = c.i0 + c.tile;
+  return true;
+}
 
 // An item whose states the joining kernel takes up, written by the block that
 // begins it: a split one (one per block at most, at the block's place), and
@@ -362,6 +443,7 @@ struct TcArgs {
   // in meta; all 0 between calls.
   int* n_redo;
   int slots;  // upper bound on the row tiles' numbers
+  int grid;   // blocks of the main kernel
 };
 
 template <typename T, int D, int MODE>
@@ -409,64 +491,37 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const __grid_co
   pdl_trigger();
 
   // ---- this block's units
+  bool ordered = true;
   if constexpr (!PRE)  // the lookups below depend on one another: have their lines on the way
     for (int b = tid; b < p.batch; b += kTcThreads) {
-      if (p.q_start) prefetch_line(p.q_start + b + 1);
       prefetch_line(p.kv_len + b);
+      if (p.q_start) ordered &= starts_ordered(p.q_start[b], p.q_start[b + 1], p.n_tokens);
     }
   const int nslots = PRE ? (p.n_tokens * p.g.G + 255) / 256 : a.slots;
-  const int per = (nslots + kTcThreads - 1) / kTcThreads;
-  const int s_lo = min(nslots, tid * per), s_hi = min(nslots, s_lo + per);
-  // Calls f(tile) for the row tiles numbered s_lo .. s_hi - 1, in order, until it says stop.
-  auto walk = [&](auto&& f) {
-    if (s_lo >= s_hi) return;
-    RowTile t;
-    if constexpr (PRE) {
-      seq_of<PRE>(p, 0, t);
-      for (int j = s_lo; j < s_hi; ++j) {
-        tile_of<PRE>(p, j, t);
-        if (f(t)) return;
-      }
-    } else {
-      // the last sequence whose first number is <= s_lo
-      int lo = 0, hi = p.batch - 1;
-      auto first_no = [&](int b) {
-        const int t0 = p.q_start ? min(max(p.q_start[b], 0), p.n_tokens) : b;
-        return (int)((long long)t0 * p.g.G / (2 * kHalf)) + b;
-      };
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (first_no(mid) <= s_lo)
-          lo = mid;
-        else
-          hi = mid - 1;
-      }
-      for (int b = lo; b < p.batch; ++b) {
-        const int no = first_no(b);
-        if (no >= s_hi) return;
-        seq_of<PRE>(p, b, t);
-        for (int j = max(0, s_lo - no); j < t.jn && no + j < s_hi; ++j) {
-          tile_of<PRE>(p, j, t);
-          if (f(t)) return;
-        }
-      }
-    }
-  };
-  long long mine = 0;
+  TcShare<PRE> share(p, nslots, true, tid);
+  long long mine, incl;
   RowTile mine_t;  // the last of this thread's row tiles: with one each, the one
-  walk([&](const RowTile& t) {
-    mine += (long long)(t.tiles + kItemCost) * p.g.nkv;
-    mine_t = t;
-    return false;
-  });
-  long long incl = mine;
+  auto sum = [&]() {
+    mine = 0;
+    share.walk(p, [&](const RowTile& t) {
+      mine += (long long)(t.tiles + kItemCost) * p.g.nkv;
+      mine_t = t;
+      return false;
+    });
+    incl = mine;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long v = __shfl_up_sync(~0u, incl, o);
-    if (lane >= o) incl += v;
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(~0u, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) s_scan[warp] = incl;
+  };
+  sum();
+  if (!__syncthreads_and(ordered)) {  // the sum was over numbers that mean nothing
+    share = TcShare<PRE>(p, nslots, false, tid);
+    sum();
+    __syncthreads();
   }
-  if (lane == 31) s_scan[warp] = incl;
-  __syncthreads();
   long long before = incl - mine, total = 0;
 #pragma unroll
   for (int w = 0; w < kTcThreads / 32; ++w) {
@@ -482,26 +537,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const __grid_co
   }
   if (before <= u0 && u0 < before + mine) {
     long long at = before;
-    auto start = [&](const RowTile& t) {
-      const int len = t.tiles + kItemCost;
-      const long long n = (long long)len * p.g.nkv;
-      if (u0 < at + n) {
-        TcCursor<PRE> c;
-        c.t = t;
-        c.h = (int)div_units(u0 - at, len);
-        c.i0 = at + (long long)c.h * len + kItemCost;
-        c.tile = (int)max(0LL, u0 - c.i0);
-        c.u = c.i0 + c.tile;
-        s_cur = c;
-        return true;
-      }
-      at += n;
-      return false;
-    };
-    if (per == 1)
-      start(mine_t);
+    if (share.ordered && share.per == 1)
+      start_in(p, mine_t, u0, at, s_cur);
     else
-      walk(start);
+      share.walk(p, [&](const RowTile& t) { return start_in(p, t, u0, at, s_cur); });
   }
   if (warp == 12) {
     tmem_alloc(&s_tmem, 512);
@@ -997,7 +1036,8 @@ __global__ void __launch_bounds__(256, 4) paged_tc_join_kernel(const __grid_cons
   constexpr int C4 = D / 4;
   for (int item = blockIdx.x; item < n_items; item += gridDim.x) {
     const TcMeta x = a.meta[item];
-    bool join = x.tiles != 0;
+    // (an item that ends behind the line: lengths changed under the call)
+    bool join = x.tiles != 0 && x.i0 + x.tiles <= x.upc * a.grid;
     for (int i = 0; i < n_redo && join; ++i)
       join = a.redo[i].t0 != x.t0 || a.redo[i].j != x.j || a.redo[i].h != x.h;
     if (!join) continue;
@@ -1129,6 +1169,7 @@ bool cf::paged_tc_launch(int dtype, const PagedAttnParams& p, const PagedSplit& 
   a.redo = reinterpret_cast<TcRedo*>(a.meta + n_list);
   a.n_redo = ws.tickets;
   a.slots = (int)((long long)p.n_tokens * p.g.G / kTcRows) + p.batch;
+  a.grid = ws.grid;
   void* args[] = {&a};
   if (!launch_pdl(f.main, dim3(ws.grid), kTcThreads, f.smem, st, args)) return false;
   if (mode == kPrefix) return true;
@@ -1136,4 +1177,73 @@ bool cf::paged_tc_launch(int dtype, const PagedAttnParams& p, const PagedSplit& 
   const long long rows = std::min<long long>(kTcRows, (long long)p.max_q * p.g.G);
   const int y = (int)std::min<long long>(kTcJoinY, (rows * (p.g.D / 4) + 255) / 256);
   return launch_pdl(f.join, dim3(ws.grid * (kTcJoinY / y), y), 256, 0, st, args);
+}
+
+extern "C" int cf_test_paged_line(int32_t batch, int32_t n_tokens, int32_t max_q, int32_t group,
+                                  int32_t n_kv_heads, int32_t window, int32_t n_sinks, int32_t grid,
+                                  const int32_t* q_start, const int32_t* kv_len, int32_t max_runs,
+                                  int32_t* runs, int64_t* line) {
+  if (batch < 1 || n_tokens < 1 || max_q < 1 || group < 1 || n_kv_heads < 1 || grid < 1 ||
+      window < 0 || n_sinks < 0 || kv_len == nullptr || runs == nullptr || line == nullptr)
+    return CF_ERR_INVALID_ARG;
+  int err = 0;
+  PagedAttnParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.g.nkv = n_kv_heads;
+  p.g.G = group;
+  p.g.max_pages = 1 << 20;
+  p.g.page_shift = 10;
+  p.q_start = q_start;
+  p.kv_len = kv_len;
+  p.errflag = &err;
+  p.batch = batch;
+  p.n_tokens = n_tokens;
+  p.max_q = max_q;
+  p.window = window;
+  p.n_sinks = n_sinks;
+  bool ordered = true;
+  for (int b = 0; q_start && b < batch; ++b)
+    ordered &= starts_ordered(q_start[b], q_start[b + 1], n_tokens);
+  const int slots = (int)((long long)n_tokens * group / kTcRows) + batch;
+  long long first[kTcThreads + 1] = {0};
+  for (int t = 0; t < kTcThreads; ++t) {
+    long long mine = 0;
+    TcShare<false>(p, slots, ordered, t).walk(p, [&](const RowTile& r) {
+      mine += (long long)(r.tiles + kItemCost) * n_kv_heads;
+      return false;
+    });
+    first[t + 1] = first[t] + mine;
+  }
+  const long long total = first[kTcThreads], upc = div_units(total + grid - 1, grid);
+  line[0] = total;
+  line[1] = upc;
+  int n = 0;
+  for (int block = 0; block < grid; ++block) {
+    const long long u0 = block * upc, u1 = min(total, u0 + upc);
+    if (u0 >= u1) break;
+    TcCursor<false> c;
+    bool found = false;
+    for (int t = 0; t < kTcThreads && !found; ++t)
+      if (first[t] <= u0 && u0 < first[t + 1]) {
+        long long at = first[t];
+        TcShare<false>(p, slots, ordered, t).walk(p, [&](const RowTile& r) {
+          return found = start_in(p, r, u0, at, c);
+        });
+      }
+    if (!found) return CF_ERR_DEVICE_POS_RANGE;
+    while (c.u < u1) {
+      const int count = (int)min((long long)(c.t.tiles - c.tile), u1 - c.u);
+      const PagedItemParts parts(c.i0, c.t.tiles, upc);
+      if (n < max_runs) {
+        const int32_t run[kPagedRunInts] = {block, c.t.b, c.t.j, c.h, c.t.tiles, c.tile, count,
+                                            parts.slot(0), parts.slot(parts.n - 1)};
+        std::memcpy(runs + (size_t)n * kPagedRunInts, run, sizeof(run));
+      }
+      ++n;
+      c.u += count - 1;
+      c.tile += count - 1;
+      c.next(p, u1);
+    }
+  }
+  return n;
 }

@@ -66,7 +66,8 @@
  *     stand for its positions, and nothing is appended to it;
  *   - an appended token with p < 0 is skipped (its q_out row too);
  *   - q_start values that decrease or leave [0, n_tokens]: such a sequence
- *     has no tokens.
+ *     has no tokens, the others have theirs.  Where two sequences then claim a
+ *     token, what the call writes is unspecified, though within its outputs.
  */
 #ifndef CF_PAGED_H
 #define CF_PAGED_H

@@ -97,6 +97,20 @@ int cf_ffn_debug_a(const struct cf_ffn_handle* h, int32_t batch, float* a_out);
 int cf_test_tc05_gemm(int dtype, int a_mn, int n, int k, const void* a, const void* b, float* d,
                       int* errflag, void* stream);
 
+/* How the many-row kernel of cf_paged_attention shares a call's key tiles out
+ * over `grid` blocks, computed on the host by the kernel's own functions:
+ * q_start (or NULL) and kv_len are host arrays.  Each run of tiles of one item
+ * (a row tile of a sequence and a KV head) in one block is nine int32 of
+ * runs [max_runs, 9]: block, sequence, row tile, KV head, tiles of the item,
+ * first tile, tiles of the run, first and last slot of the item's states (a
+ * workspace has 2 * grid).  line[0..1]: units of the whole call and of a
+ * block.  Returns the number of runs, or CF_ERR_INVALID_ARG, or
+ * CF_ERR_DEVICE_POS_RANGE where a block does not find its first unit. */
+int cf_test_paged_line(int32_t batch, int32_t n_tokens, int32_t max_q, int32_t group,
+                       int32_t n_kv_heads, int32_t window, int32_t n_sinks, int32_t grid,
+                       const int32_t* q_start, const int32_t* kv_len, int32_t max_runs,
+                       int32_t* runs, int64_t* line);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,49 @@
+"""The paged cache's operators at the edges of what include/cf_paged.h allows:
+malformed starts, values that are no numbers, overlaps, shapes."""
+import pytest
+import torch
+
+from paged_util import Problem, ref_attention
+from test_paged_gpu import RANGE, Run, close
+
+pytestmark = pytest.mark.gpu
+
+
+# ---------------------------------------------------------- malformed starts --
+def with_starts(starts, kv_len, tokens, heads, **kw):
+    """A problem whose starts are given: a sequence has none of the tokens
+    where its start decreases or leaves them."""
+    q_len = [b - a if 0 <= a <= b <= tokens else 0 for a, b in zip(starts, starts[1:])]
+    pr = Problem(q_len, kv_len, *heads, extra_tokens=tokens - sum(q_len), **kw)
+    pr.starts = list(starts)
+    return pr
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("prefix", [0, 60])
+@pytest.mark.parametrize("starts,kv_len,tokens,heads", [
+    # a start far too large in front of a long sequence, which all the work lies in
+    ([0, 64, 2000, 128, 192, 256, 320, 384, 448], [1000, 5, 5, 3000, 100, 64, 80, 90], 512, (8, 2)),
+    ([0, 64, 2000, 128, 192, 256, 320, 384, 448], [3000, 5, 5, 70, 100, 64, 80, 90], 512, (8, 2)),
+    # the sequences in falling order, the bad ones between them
+    ([300, 400, 200, 300, 100, 200, 0, 100], [400, 1, 300, 1, 250, 1, 700], 400, (4, 2)),
+    ([8, 12, 0, 4], [20, 9, 30], 12, (1, 1)),
+    # single tokens of many sequences, two entries lost
+    ([t if t not in (100, 170) else (-3, 10 ** 9)[t > 100] for t in range(251)],
+     [1 + 3 * (b % 50) for b in range(250)], 250, (8, 2)),
+    ([3 * t if t != 31 else 2 ** 31 - 1 for t in range(61)], [9 + b for b in range(60)], 180, (16, 1)),
+    ([5, 4, 3, 2, 1, 0], [5, 4, 3, 2, 1], 5, (8, 2)),
+    ([-2 ** 31, 2 ** 31 - 1, -2 ** 31, 2 ** 31 - 1], [50, 40, 30], 70, (8, 2)),
+], ids=["far", "near", "falling", "swapped", "singles", "drafts", "none", "limits"])
+def test_sequences_beside_malformed_starts(dtype, prefix, starts, kv_len, tokens, heads):
+    """Malformed entries are reported, their sequences have no tokens, and
+    every other sequence gets its rows; twice, so that nothing stays behind."""
+    pr = with_starts(starts, kv_len, tokens, heads, dtype=dtype, prefix=prefix, seed=81, d=64)
+    r = Run(pr)
+    want = ref_attention(pr)
+    for _ in range(2):
+        r.out.fill_(float("nan")), r.lse.fill_(float("nan"))
+        r.attend()
+        assert r.kv.status() == RANGE
+        close(r.out, want[0], want[1], "out")
+        close(r.lse, want[2], want[3], "lse")
