@@ -461,7 +461,7 @@ struct PagedSplit {
 bool paged_append_launch(int dtype, const PagedAppendParams& p, int sm_count, cudaStream_t st);
 
 // The fp32 kernel.  grid: resident blocks, 0 on failure; part_rows: workspace;
-// a ticket per resident block.
+// a ticket per resident block and a word more.
 int paged_f32_grid(int head_dim, int sm_count);
 long long paged_f32_part_rows(int grid);
 bool paged_f32_launch(const PagedAttnParams& p, const PagedSplit& ws, cudaStream_t st);

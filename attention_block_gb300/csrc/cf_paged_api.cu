@@ -261,7 +261,7 @@ int cf_paged_create(const cf_paged_config* cfg, cf_paged_handle** out) {
                                   : paged_few_grid(c.dtype, c.head_dim, h->sm_count);
   if (h->few.grid == 0) return fail(CF_ERR_CUDA);
   const size_t tickets =
-      take(4 * (c.dtype == CF_F32 ? (size_t)h->few.grid : (size_t)c.max_batch * c.n_kv_heads));
+      take(4 * (c.dtype == CF_F32 ? (size_t)h->few.grid + 1 : (size_t)c.max_batch * c.n_kv_heads));
   const size_t redo = take(3 * 4);
   const size_t zero = bytes;
   const int64_t all_rows = (int64_t)c.max_tokens * c.n_q_heads;

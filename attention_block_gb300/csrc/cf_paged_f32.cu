@@ -11,6 +11,8 @@
 // several products (16 rows to a lane's one position: 331 us for 2 prompts of
 // 512, 32 / 8 heads of 128; 4 x 4: 260 us).  For the sum a lane has D / 32
 // columns and all R rows.  The warps' states are joined in a fixed order.
+// A block finds its row tile by the tile's number, from the starts where those
+// are in order.  Where they are not the row tiles are counted up over the batch.
 // Where the row tiles do not fill the GPU, several blocks share each one's
 // positions, and the last of them to finish joins their states in order.
 // 16 sequences of 4097 positions: 99 us, 5.4 TB/s; one of 32769: 52 us.
@@ -41,6 +43,7 @@ struct F32Args {
   PagedAttnParams p;
   PagedParts ws;  // R rows per (row tile, KV head, split)
   int* tickets;   // one per (row tile, KV head); zero between calls
+  const int* disorder;  // batches of more than kF32Threads: whether starts are out of order
 };
 
 __device__ __forceinline__ float4 lds4(uint32_t at) {
@@ -62,46 +65,87 @@ __global__ void __launch_bounds__(kF32Threads, D == 64 ? 2 : 1)
   const PagedAttnParams& p = a.p;
   extern __shared__ __align__(1024) uint8_t sm[];
   __shared__ float2 s_ml[kF32Warps][R];
-  __shared__ int s_seq, s_last;
+  __shared__ long long s_sum[kF32Warps];
+  __shared__ int s_seq, s_no, s_last;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int kvh = blockIdx.y, G = p.g.G;
   const int rg = lane / KG, kg = lane % KG;  // rows 4 rg .. + 3, positions kg + n KG
   float* sq = reinterpret_cast<float*>(sm + kF32Warps * S::WARP);
 
-  // Row tile j of sequence b has the number t0 * G / R + b + j: unique, below
-  // T * G / R + batch, and the first ones increase.  So this block's sequence is
-  // the last whose first number is not above its own; a round of the search
-  // leaves a 192nd of the batch.
   auto start = [&](int b) { return p.q_start ? p.q_start[b] : b; };
   auto first_no = [&](int b, int t0) { return (int)((long long)t0 * G / R) + b; };
-  int lo = 0, hi = p.batch;
-  while (hi - lo > kF32Threads) {
-    const int w = (hi - lo + kF32Threads - 1) / kF32Threads, b = lo + tid * w;
-    if (tid == 0) s_seq = lo;
-    __syncthreads();
-    if (b < hi && first_no(b, start(b)) <= (int)blockIdx.x) atomicMax(&s_seq, b);
-    __syncthreads();
-    lo = s_seq;
-    hi = min(hi, lo + w);
-    __syncthreads();
-  }
+  // Row tiles of sequence b.
+  auto row_tiles = [&](int b) {
+    const int t0 = start(b), t1 = p.q_start ? p.q_start[b + 1] : b + 1;
+    return starts_ordered(t0, t1, p.n_tokens) ? ((t1 - t0) * G + R - 1) / R : 0;
+  };
+  bool disorder = false;
+  if (p.q_start)
+    disorder = p.batch > kF32Threads
+                   ? *a.disorder != 0
+                   : __syncthreads_or(tid < p.batch && !starts_ordered(start(tid), start(tid + 1),
+                                                                       p.n_tokens)) != 0;
   if (tid == 0) s_seq = -1;
   __syncthreads();
-  if (lo + tid < hi) {
-    const int b = lo + tid, t0 = start(b), t1 = p.q_start ? p.q_start[b + 1] : b + 1;
-    const int j = (int)blockIdx.x - first_no(b, t0);
-    if (t0 >= 0 && t1 <= p.n_tokens && t1 > t0 && j >= 0 && j < ((t1 - t0) * G + R - 1) / R)
-      atomicMax(&s_seq, b);
+  if (!disorder) {
+    // Row tile j of sequence b has the number t0 * G / R + b + j: unique, below
+    // T * G / R + batch, and the first ones increase.  So this block's sequence
+    // is the last whose first number is not above its own; a round of the search
+    // leaves a 192nd of the batch.
+    int lo = 0, hi = p.batch;
+    while (hi - lo > kF32Threads) {
+      const int w = (hi - lo + kF32Threads - 1) / kF32Threads, b = lo + tid * w;
+      if (tid == 0) s_seq = lo;
+      __syncthreads();
+      if (b < hi && first_no(b, start(b)) <= (int)blockIdx.x) atomicMax(&s_seq, b);
+      __syncthreads();
+      lo = s_seq;
+      hi = min(hi, lo + w);
+      __syncthreads();
+      if (tid == 0) s_seq = -1;
+      __syncthreads();
+    }
+    if (lo + tid < hi) {
+      const int b = lo + tid, no = first_no(b, start(b)), j = (int)blockIdx.x - no;
+      if (j >= 0 && j < row_tiles(b)) {
+        s_seq = b;
+        s_no = no;
+      }
+    }
+  } else {
+    // The tile with this number when all are counted up.  They are as few as
+    // above unless sequences claim a token twice.
+    long long no = 0;
+    for (int b0 = 0; b0 < p.batch; b0 += kF32Threads) {
+      const int n = b0 + tid < p.batch ? row_tiles(b0 + tid) : 0;
+      long long incl = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long v = __shfl_up_sync(~0u, incl, o);
+        if (lane >= o) incl += v;
+      }
+      if (lane == 31) s_sum[warp] = incl;
+      __syncthreads();
+      long long before = no + incl - n;
+#pragma unroll
+      for (int w = 0; w < kF32Warps; ++w) {
+        if (w < warp) before += s_sum[w];
+        no += s_sum[w];
+      }
+      if (before <= blockIdx.x && blockIdx.x < before + n) {
+        s_seq = b0 + tid;
+        s_no = (int)before;
+      }
+      __syncthreads();
+    }
+    if (blockIdx.x + blockIdx.y + blockIdx.z == 0 && tid == 0)
+      atomicOr(p.errflag, kDevErrPosRange);
   }
-  if (p.q_start && blockIdx.x + blockIdx.y + blockIdx.z == 0)  // one block reports bad starts
-    for (int b = tid; b < p.batch; b += kF32Threads)
-      if (p.q_start[b] < 0 || p.q_start[b + 1] > p.n_tokens || p.q_start[b + 1] < p.q_start[b])
-        atomicOr(p.errflag, kDevErrPosRange);
   __syncthreads();
   const int b = s_seq;
   if (b < 0) return;  // no row tile has this number
   const PagedSeq s = paged_seq(p.q_start, p.kv_len, b, p.n_tokens, p.max_q, p.g, p.errflag);
-  const int r0 = ((int)blockIdx.x - first_no(b, s.t0)) * R;
+  const int r0 = ((int)blockIdx.x - s_no) * R;
   const int nr = min(R, s.n * G - r0);
   const int p0 = s.len - s.n;
   const int plo = p0 + r0 / G, phi = p0 + (r0 + nr - 1) / G;
@@ -343,6 +387,17 @@ __global__ void __launch_bounds__(kF32Threads, D == 64 ? 2 : 1)
   }
 }
 
+// Whether starts are out of order, for the blocks of a large batch: 3 to 8 us of
+// 33 for 700 single tokens, of 208 for 300 x 4, of 409 for 700 x 2.
+__global__ void __launch_bounds__(1024)
+    paged_f32_order_kernel(const int* q_start, int batch, int n_tokens, int* disorder) {
+  bool bad = false;
+  for (int b = threadIdx.x; b < batch; b += 1024)
+    bad |= !starts_ordered(q_start[b], q_start[b + 1], n_tokens);
+  const int any = __syncthreads_or(bad);
+  if (threadIdx.x == 0) *disorder = any;
+}
+
 struct F32Fn {
   void (*fn)(F32Args);
   int smem;
@@ -389,6 +444,14 @@ bool cf::paged_f32_launch(const PagedAttnParams& p, const PagedSplit& ws, cudaSt
   a.p = p;
   a.ws = ws.parts;
   a.tickets = ws.tickets;
+  a.disorder = ws.tickets + ws.grid;
+  if (p.q_start && p.batch > kF32Threads) {
+    int* disorder = ws.tickets + ws.grid;
+    void* order[] = {&a.p.q_start, &a.p.batch, &a.p.n_tokens, &disorder};
+    if (cudaLaunchKernel((const void*)&paged_f32_order_kernel, dim3(1), dim3(1024), order, 0, st) !=
+        cudaSuccess)
+      return false;
+  }
   void* args[] = {&a};
   return cudaLaunchKernel((const void*)f.fn, dim3((unsigned)tiles, p.g.nkv, (unsigned)splits),
                           dim3(kF32Threads), args, f.smem, st) == cudaSuccess;

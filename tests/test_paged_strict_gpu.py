@@ -4,7 +4,7 @@ import pytest
 import torch
 
 from paged_util import Problem, ref_attention
-from test_paged_gpu import RANGE, Run, close
+from test_paged_gpu import RANGE, TYPES, Run, close
 
 pytestmark = pytest.mark.gpu
 
@@ -19,7 +19,7 @@ def with_starts(starts, kv_len, tokens, heads, **kw):
     return pr
 
 
-@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("prefix", [0, 60])
 @pytest.mark.parametrize("starts,kv_len,tokens,heads", [
     # a start far too large in front of a long sequence, which all the work lies in
