@@ -98,8 +98,13 @@ __global__ void __launch_bounds__(kAppendThreads, TPB == 1 ? 4 : 8)
   if (p.q_start) {
     __syncthreads();
     for (int b = tid; b < p.batch; b += kAppendThreads) {
-      const int a = max(p.q_start[b], t_lo), e = min(p.q_start[b + 1], t_lo + nt);
-      for (int t = a; t < e; ++t) s_seq[t - t_lo] = b;
+      const int t0 = p.q_start[b], t1 = p.q_start[b + 1];
+      if (!starts_ordered(t0, t1, p.n_tokens)) {  // claims no token; one block reports it
+        if (blockIdx.x + blockIdx.y == 0) atomicOr(p.errflag, kDevErrPosRange);
+        continue;
+      }
+      const int a = max(t0, t_lo), e = min(t1, t_lo + nt);
+      for (int t = a; t < e; ++t) atomicMax(&s_seq[t - t_lo], b);
     }
   }
   __syncthreads();

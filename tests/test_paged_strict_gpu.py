@@ -4,7 +4,7 @@ import pytest
 import torch
 
 from paged_util import Problem, ref_attention
-from test_paged_gpu import RANGE, TYPES, Run, close
+from test_paged_gpu import RANGE, TYPES, Run, check_append, close, run_append
 
 pytestmark = pytest.mark.gpu
 
@@ -47,3 +47,21 @@ def test_sequences_beside_malformed_starts(dtype, prefix, starts, kv_len, tokens
         assert r.kv.status() == RANGE
         close(r.out, want[0], want[1], "out")
         close(r.lse, want[2], want[3], "lse")
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("starts,kv_len,tokens", [
+    ([0, 4, -5, 4, 6], [9, 3, 20, 30], 6),      # one from -5 to 4: claims nothing
+    ([0, 3, 1], [9, 30], 3),                     # decreases, and owns no token
+    ([0, 3, 99, 3, 5], [9, 3, 8, 30], 5),
+    ([20, 40, 0, 20], [30, 7, 45], 40),
+], ids=str)
+def test_append_reports_malformed_starts(dtype, starts, kv_len, tokens):
+    pr = with_starts(starts, kv_len, tokens, (4, 2), dtype=dtype, seed=82)
+    for _ in range(5):
+        r, q = run_append(pr)
+        check_append(pr, r, q, status=RANGE)
+        owned = torch.zeros(tokens, dtype=torch.bool)
+        for b, n in enumerate(pr.q_len):
+            owned[starts[b]:starts[b] + n] = True
+        assert q[~owned].isnan().all()
