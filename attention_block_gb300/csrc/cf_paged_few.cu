@@ -125,6 +125,22 @@ __device__ __forceinline__ long long state_row(const FewArgs& a, const FewItem& 
                                           : ((long long)it.b * a.p.g.nkv + it.h) * kFewRows + row);
 }
 
+// Two probabilities in 16 bits: fp16 rounds them.  bf16 takes hi + lo, hi cut off
+// and lo the rest, at least 2^-18 of the whole: both are positive where the
+// probability is (from 2^-115 on), so an infinity in V keeps its sign in both
+// products, where a lo of 0 or below would make it NaN.  The sum is off by 2^-16.
+template <typename T>
+__device__ __forceinline__ void split_weights(float a, float b, uint32_t& hi, uint32_t& lo) {
+  if constexpr (MmaKind<T>::kAttnHiLo) {
+    const uint32_t x = __float_as_uint(a), y = __float_as_uint(b);
+    hi = __byte_perm(x, y, 0x7632);
+    lo = pack2<T>(fmaxf(a - __uint_as_float(x & 0xffff0000u), a * 0x1p-18f),
+                  fmaxf(b - __uint_as_float(y & 0xffff0000u), b * 0x1p-18f));
+  } else {
+    hi = pack2<T>(a, b);
+  }
+}
+
 template <typename T, int D, int MODE>
 __global__ void __launch_bounds__(kFewThreads, 1)
     paged_few_kernel(const __grid_constant__ FewArgs a) {
@@ -486,8 +502,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         uint32_t hi[4], lo[4];
 #pragma unroll
         for (int x = 0; x < 4; ++x)
-          M::split2(c[2 * kk + (x >> 1)][2 * (x & 1)], c[2 * kk + (x >> 1)][2 * (x & 1) + 1],
-                    hi[x], lo[x]);
+          split_weights<T>(c[2 * kk + (x >> 1)][2 * (x & 1)],
+                           c[2 * kk + (x >> 1)][2 * (x & 1) + 1], hi[x], lo[x]);
 #pragma unroll
         for (int n2 = 0; n2 < NO / 2; ++n2) {
           const int row = kk * 16 + (lane & 15), ch = n2 * 2 + (lane >> 4);

@@ -35,9 +35,11 @@
  *   lse_h = ln sum_j exp(s_j)
  * A row that sees no key (p < 0, also where there is a prefix) gets o = 0 and
  * lse = -infinity.  What lies in a slot, be it an infinity or a NaN, reaches
- * the rows that see its position and no other.  Table entries of positions
- * that no row of the sequence sees (past kv_len, behind the window) are not
- * read as pages.
+ * the rows that see its position and no other.  An infinity in V gives them an
+ * infinity; NaN where one of the other sign is seen too, and where its
+ * probability may count as 0 in the product (fp16: below 2^-24 of the row's
+ * largest, bf16 2^-115, fp32 2^-126).  Table entries of positions that no row
+ * of the sequence sees (past kv_len, behind the window) are not read as pages.
  *
  * Arithmetic: products and sums in fp32 (fp32 storage: plain fp32 FMAs; fp16
  * and bf16: tensor-core products of the stored values).  Probabilities enter

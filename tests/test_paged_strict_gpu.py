@@ -1,10 +1,12 @@
 """The paged cache's operators at the edges of what include/cf_paged.h allows:
 malformed starts, values that are no numbers, overlaps, shapes."""
+import math
+
 import pytest
 import torch
 
 from paged_util import Problem, ref_attention
-from test_paged_gpu import RANGE, TYPES, Run, check_append, close, run_append
+from test_paged_gpu import OK, RANGE, TYPES, Run, check_append, close, run_append
 
 pytestmark = pytest.mark.gpu
 
@@ -65,3 +67,39 @@ def test_append_reports_malformed_starts(dtype, starts, kv_len, tokens):
         for b, n in enumerate(pr.q_len):
             owned[starts[b]:starts[b] + n] = True
         assert q[~owned].isnan().all()
+
+
+# ----------------------------------------------------- infinities and NaN --
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("heads,q_len,kv_len,prefix", [
+    ((4, 4), [1, 1, 1], [40, 300, 517], 0),
+    ((8, 2), [1], [2000], 0),             # one sequence over many warps and blocks
+    ((16, 1), [1, 1], [33, 120], 0),
+    ((4, 2), [3, 2], [200, 90], 0),       # short drafts: early tiles that all rows see
+    ((4, 2), [1, 1], [20, 9], 150),       # a prefix, few rows in all
+    ((8, 2), [1] * 20, [5] * 20, 150),    # a prefix, many
+    ((4, 2), [150], [400], 0), ((4, 2), [100, 40], [130, 60], 200)], ids=str)
+def test_infinities_that_every_row_sees(dtype, d, heads, q_len, kv_len, prefix):
+    """Values of +-infinity, with probabilities above 2^-24 of the largest, stay
+    infinities of their sign (NaN where both meet); other columns stay exact."""
+    pr = Problem(q_len, kv_len, *heads, d=d, dtype=dtype, prefix=prefix, seed=80, q_scale=0.5)
+    vp = pr.split(pr.pools)[1]
+    at = [(pr.table[b], j) for b in range(pr.batch) for j in (0, kv_len[b] // 2)]
+    at += [(pr.prefix_table, j) for j in (3, prefix - 2) if prefix]
+    for n, (row, j) in enumerate(at):
+        v = pr.slot(vp, row, j)
+        v[:, n % 2::7] = (math.inf, -math.inf)[n % 2]
+        v[:, 5::14] = -(math.inf, -math.inf)[n % 2]
+        v[:, 12] = math.nan
+    want = ref_attention(pr)
+    r = Run(pr)
+    r.attend()
+    assert r.kv.status() == OK
+    got, finite = r.out.double().cpu(), want[0].isfinite()
+    assert want[0].isinf().any() and want[0].isnan().any()
+    assert torch.equal(got.isnan(), want[0].isnan())
+    assert (got[want[0].isinf()] == want[0][want[0].isinf()]).all()
+    close(torch.where(finite, got, 0.0), torch.where(finite, want[0], 0.0),
+          torch.where(finite, want[1], 0.0), "finite values")
+    close(r.lse, want[2], want[3], "lse")
