@@ -300,6 +300,12 @@ __device__ __forceinline__ void paged_join_row(PagedState4& s, const float* o, c
   }
 }
 
+// A row's lse from its maximum in base 2 and its sum.  The sum decides: where
+// every score is NaN the maximum is still -infinity.
+__device__ __forceinline__ float paged_lse(float m, float l) {
+  return l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+}
+
 // Normalises and stores 4 columns of a row, and its lse.
 template <typename T, int D>
 __device__ __forceinline__ void paged_store4(const PagedState4& s, void* out, float* lse,
@@ -307,8 +313,7 @@ __device__ __forceinline__ void paged_store4(const PagedState4& s, void* out, fl
   const float inv = s.l == 0.f ? 0.f : 1.f / s.l;
   const float f[4] = {s.o.x * inv, s.o.y * inv, s.o.z * inv, s.o.w * inv};
   store4<T>(static_cast<T*>(out) + row * D + col, f);
-  if (lse && col == 0)
-    lse[row] = s.m == -INFINITY ? -INFINITY : (s.m + log2f(s.l)) * 0.69314718055994531f;
+  if (lse && col == 0) lse[row] = paged_lse(s.m, s.l);
 }
 
 // Transposes w over a quad of lanes: lane q ends with word q of lanes 0..3.

@@ -595,8 +595,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
           if (row < nrows)
             *reinterpret_cast<uint4*>(dst + 8 * k) = make_uint4(w[0], w[1], w[2], w[3]);
         }
-        if (p.lse && row < nrows && tq == 0)
-          p.lse[at] = m[r] == -INFINITY ? -INFINITY : (m[r] + log2f(l[r])) * 0.69314718055994531f;
+        if (p.lse && row < nrows && tq == 0) p.lse[at] = paged_lse(m[r], l[r]);
       }
       // a sequence with more tokens than the call allows has no keys: its
       // other rows are zero too

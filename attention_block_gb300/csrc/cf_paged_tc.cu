@@ -675,8 +675,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const __grid_co
           __stcg(a.ws.ml + my_row, make_float2(m2, l));
         } else {
           my_inv = l == 0.f ? 0.f : 1.f / l;
-          if (p.lse)
-            p.lse[my_row] = m2 == -INFINITY ? -INFINITY : (m2 + log2f(l)) * 0.69314718055994531f;
+          if (p.lse) p.lse[my_row] = paged_lse(m2, l);
         }
       }
 #pragma unroll 1
@@ -1076,9 +1075,7 @@ __global__ void __launch_bounds__(256, 4) paged_tc_join_kernel(const __grid_cons
     T* out = static_cast<T*>(p.out) + (t * p.g.nq + h) * D + lane * (D / 32);
 #pragma unroll
     for (int c = 0; c < D / 32; ++c) out[c] = Elem<T>::from_f(r.o[c] * inv);
-    if (p.lse && lane == 0)
-      p.lse[t * p.g.nq + h] =
-          r.m == -INFINITY ? -INFINITY : (r.m + log2f(r.l)) * 0.69314718055994531f;
+    if (p.lse && lane == 0) p.lse[t * p.g.nq + h] = paged_lse(r.m, r.l);
   }
   // the last block out empties the lists
   __syncthreads();

@@ -33,8 +33,9 @@
  *   visible(p, j) = 0 <= j <= p  and  (window == 0 or p - j < window or j < n_sinks)
  *   s_j = scale * q_h . k_j,   o_h = sum_j exp(s_j) v_j / sum_j exp(s_j)   over visible j
  *   lse_h = ln sum_j exp(s_j)
- * A row that sees no key (p < 0, also where there is a prefix) gets o = 0 and
- * lse = -infinity.  What lies in a slot, be it an infinity or a NaN, reaches
+ * A row that sees no key (p < 0, also where there is a prefix), or only keys
+ * with scores of -infinity, gets o = 0 and lse = -infinity; a score of NaN
+ * makes both NaN.  What lies in a slot, be it an infinity or a NaN, reaches
  * the rows that see its position and no other.  An infinity in V gives them an
  * infinity; NaN where one of the other sign is seen too, and where its
  * probability may count as 0 in the product (fp16: below 2^-24 of the row's

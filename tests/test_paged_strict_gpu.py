@@ -103,3 +103,29 @@ def test_infinities_that_every_row_sees(dtype, d, heads, q_len, kv_len, prefix):
     close(torch.where(finite, got, 0.0), torch.where(finite, want[0], 0.0),
           torch.where(finite, want[1], 0.0), "finite values")
     close(r.lse, want[2], want[3], "lse")
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("q_len,kv_len,prefix,window", [
+    ([1, 1, 1], [1, 200, 900], 0, 0), ([3, 2], [3, 90], 0, 0), ([3, 2], [3, 90], 0, 1),
+    ([150, 1], [300, 1], 0, 0), ([150, 1], [300, 1], 0, 1), ([1, 2], [1, 40], 70, 0),
+    ([60, 1], [90, 1], 70, 0)], ids=str)
+def test_rows_of_nan_say_so_in_lse(dtype, q_len, kv_len, prefix, window):
+    """-infinity stands for rows without a key; a NaN in a query, or in every
+    key that a row sees, is NaN in o and in lse."""
+    pr = Problem(q_len, kv_len, 4, 2, dtype=dtype, prefix=prefix, seed=83)
+    kp = pr.split(pr.pools)[0]
+    pr.q[0, 1, 5] = math.nan            # one head of the first token
+    pr.q[-1, :, 0] = math.nan           # every head of the last one
+    for j in range(kv_len[0] - q_len[0], kv_len[0]):  # with a window of 1: all that a row sees
+        pr.slot(kp, pr.table[0], j)[0] = math.nan
+    want = ref_attention(pr, window)
+    r = Run(pr)
+    r.attend(window)
+    assert r.kv.status() == OK
+    assert want[2].isnan().any() and want[2].isfinite().any()
+    assert torch.equal(r.out.isnan().cpu(), want[0].isnan())
+    close(r.lse, want[2], want[3], "lse")
+    finite = want[0].isfinite()
+    close(torch.where(finite, r.out.double().cpu(), 0.0), torch.where(finite, want[0], 0.0),
+          torch.where(finite, want[1], 0.0), "finite values")
