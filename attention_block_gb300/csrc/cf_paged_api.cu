@@ -77,6 +77,18 @@ size_t rows_bytes(int64_t n, int64_t stride, int64_t row, size_t es) {
   return n > 0 ? (size_t)((n - 1) * stride + row) * es : 0;
 }
 
+// Whether one of n rows of na bytes from a meets one of n rows of nb bytes from
+// b, both `stride` bytes apart.
+bool rows_meet(const void* a, int64_t na, const void* b, int64_t nb, int64_t n, int64_t stride) {
+  const int64_t d = (int64_t)(reinterpret_cast<uintptr_t>(b) - reinterpret_cast<uintptr_t>(a));
+  // row i of a and row i + t of b do where -nb < d + t * stride < na: the least
+  // t with the left side, in -(n - 1) .. n - 1, decides
+  const int64_t x = -nb - d;
+  const int64_t floor = x / stride - (x % stride < 0 ? 1 : 0);
+  const int64_t t = std::max(floor + 1, 1 - n);
+  return t <= n - 1 && d + t * stride < na;
+}
+
 int attention(cf_paged_handle* h, int32_t batch, int32_t n_tokens, int32_t max_q, const void* q,
               int64_t q_stride, const int32_t* q_start, const int32_t* kv_len,
               const int32_t* page_table, const int32_t* prefix_table, int32_t prefix_len,
@@ -357,10 +369,14 @@ int cf_paged_append(cf_paged_handle* h, int32_t batch, int32_t n_tokens, const v
             {rope_pos, (size_t)n_tokens * (axes3 ? 3 : 1) * 4, false},
             {page_table, (size_t)batch * c.max_pages * 4, false}};
   const bool in_place = q != nullptr && q == q_out && q_stride == q_out_stride;
+  // in place the rotated rows may lie between the rows of k and v
+  const bool between = in_place && (n_tokens == 1 || q_stride == kv_stride);
   for (const auto& x : in) {
     if (overlap(k_pages, pool, x.p, x.n) || overlap(v_pages, pool, x.p, x.n)) return CF_ERR_ALIAS;
-    // in place the rotated rows may lie between the rows of k and v
-    if (!(in_place && x.rows) && overlap(q_out, qo, x.p, x.n)) return CF_ERR_ALIAS;
+    if (in_place && &x == in) continue;  // q itself
+    if (between && x.rows ? rows_meet(q, qrow * es, x.p, kvrow * es, n_tokens, q_stride * es)
+                          : overlap(q_out, qo, x.p, x.n))
+      return CF_ERR_ALIAS;
   }
   if (overlap(q_out, qo, k_pages, pool) || overlap(q_out, qo, v_pages, pool)) return CF_ERR_ALIAS;
   // pools that interleave keys and values overlap as ranges, not as pages

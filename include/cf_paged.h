@@ -130,9 +130,9 @@ int cf_paged_create(const cf_paged_config* cfg, cf_paged_handle** out);
  *   page_table [batch, max_pages] int32
  *   k_pages, v_pages              the slots of the new tokens are written
  *   q_out    [n_tokens, nq, d]    rows q_out_stride elements apart; the
- *            rotated queries.  May be q itself (same address and stride),
- *            must otherwise not overlap an input, nor its rows' gaps
- *            (CF_ERR_ALIAS)
+ *            rotated queries.  May be q itself (same address and stride; rows
+ *            of k and v of that stride may then lie between its own), must
+ *            otherwise not overlap an input, nor its rows' gaps (CF_ERR_ALIAS)
  * q and q_out may both be NULL: then only k and v are taken.  Two tokens of
  * one call must not map to the same slot.  Strides are multiples of 16 bytes,
  * pointers to storage 16-byte aligned, int32 arrays 4-byte aligned.

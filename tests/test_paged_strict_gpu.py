@@ -5,6 +5,7 @@ import math
 import pytest
 import torch
 
+from attention_block_gb300 import binding
 from paged_util import Problem, ref_attention
 from test_paged_gpu import OK, RANGE, TYPES, Run, check_append, close, run_append
 
@@ -129,3 +130,38 @@ def test_rows_of_nan_say_so_in_lse(dtype, q_len, kv_len, prefix, window):
     finite = want[0].isfinite()
     close(torch.where(finite, r.out.double().cpu(), 0.0), torch.where(finite, want[0], 0.0),
           torch.where(finite, want[1], 0.0), "finite values")
+
+
+# ---------------------------------------------------------------- overlaps --
+def test_in_place_append_refuses_keys_that_share_the_queries_elements():
+    """q_out == q lets k and v lie between the rows of q, not on them."""
+    pr = Problem([2, 3], [9, 30], 4, 2, seed=84)
+    r = Run(pr)
+    L, s = binding.lib(), torch.cuda.current_stream().cuda_stream
+    row = (4 + 2 * 2) * 128
+    x = torch.zeros(8 * row, dtype=torch.bfloat16, device="cuda")
+    at = x.data_ptr()
+
+    def append(n, k, v, ks=row, qs=row, q=at + 2 * row):
+        return L.cf_paged_append(r.kv.handle, 2 if n > 1 else 1, n, q, k, v, qs, ks,
+                                 r.q_start.data_ptr() if n > 1 else None, r.kv_len.data_ptr(), None,
+                                 r.table.data_ptr(), r.k_pages.data_ptr(), r.v_pages.data_ptr(), q,
+                                 qs, s)
+
+    q, w = at + 2 * row, 2 * 512  # w: bytes of a row's queries
+    other = torch.zeros(8 * row, dtype=torch.bfloat16, device="cuda")
+    free = other.data_ptr()
+    for n in (5, 1):
+        assert append(n, q + w, q + w + 512) == OK               # the merged projection
+        assert append(n, q + w + 512, q + w) == OK
+        assert append(n, free, free + 512) == OK
+        for bad in (q, q + 16, q + w - 16, q + 512, q - 512 + 16):
+            assert append(n, bad, q + w) == binding.CF_ERR_ALIAS, bad - q
+            assert append(n, q + w, bad) == binding.CF_ERR_ALIAS, bad - q
+    assert append(5, q - 512, q + w) == OK                       # the row before, behind its queries
+    assert append(5, q + 2 * row, q + w) == binding.CF_ERR_ALIAS     # the next row's queries
+    assert append(5, q + 8 * row, q + w) == binding.CF_ERR_ALIAS     # the last row's
+    assert append(1, q + 2 * row, q + w) == OK                   # there is no next row
+    assert append(5, free, free + 512, ks=256) == OK
+    assert append(5, q + w, free, ks=256) == binding.CF_ERR_ALIAS    # rows of another stride among q's
+    assert r.kv.status() == OK
