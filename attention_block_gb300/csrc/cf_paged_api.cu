@@ -381,7 +381,8 @@ int cf_paged_append(cf_paged_handle* h, int32_t batch, int32_t n_tokens, const v
   if (overlap(q_out, qo, k_pages, pool) || overlap(q_out, qo, v_pages, pool)) return CF_ERR_ALIAS;
   // pools that interleave keys and values overlap as ranges, not as pages
   const int64_t page = (int64_t)c.page_size * kvrow;
-  if (c.page_stride < 2 * page && overlap(k_pages, pool, v_pages, pool)) return CF_ERR_ALIAS;
+  if (rows_meet(k_pages, page * es, v_pages, page * es, c.num_pages, c.page_stride * es))
+    return CF_ERR_ALIAS;
 
   PagedAppendParams p;
   std::memset(&p, 0, sizeof(p));

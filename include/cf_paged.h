@@ -128,7 +128,8 @@ int cf_paged_create(const cf_paged_config* cfg, cf_paged_handle** out);
  *   rope_pos [axes, n_tokens] int32 (axes: 3 with rope_sections, else 1), or
  *            NULL: every axis takes p
  *   page_table [batch, max_pages] int32
- *   k_pages, v_pages              the slots of the new tokens are written
+ *   k_pages, v_pages              the slots of the new tokens are written; the
+ *            pools may alternate by pages, but share none (CF_ERR_ALIAS)
  *   q_out    [n_tokens, nq, d]    rows q_out_stride elements apart; the
  *            rotated queries.  May be q itself (same address and stride; rows
  *            of k and v of that stride may then lie between its own), must

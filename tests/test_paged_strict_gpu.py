@@ -165,3 +165,27 @@ def test_in_place_append_refuses_keys_that_share_the_queries_elements():
     assert append(5, free, free + 512, ks=256) == OK
     assert append(5, q + w, free, ks=256) == binding.CF_ERR_ALIAS    # rows of another stride among q's
     assert r.kv.status() == OK
+
+
+@pytest.mark.parametrize("layout", [0, 1])
+def test_pools_that_share_pages_are_refused(layout):
+    """With a page stride of two pages keys and values may alternate; they may
+    not share a page."""
+    pr = Problem([2, 3], [9, 30], 4, 2, seed=85, interleaved=True, layout=layout)
+    r = Run(pr)
+    L, s = binding.lib(), torch.cuda.current_stream().cuda_stream
+    x = [t.cuda() for t in (pr.q, pr.k, pr.v)]
+    page = 2 * pr.page * pr.nkv * pr.d  # bytes
+
+    def append(k, v):
+        return L.cf_paged_append(r.kv.handle, 2, 5, x[0].data_ptr(), x[1].data_ptr(),
+                                 x[2].data_ptr(), 512, 256, r.q_start.data_ptr(),
+                                 r.kv_len.data_ptr(), None, r.table.data_ptr(), k, v,
+                                 r.out.data_ptr(), 512, s)
+
+    k = r.k_pages.data_ptr()
+    assert append(k, k + page) == OK and append(k + page, k) == OK
+    for off in (0, 16, page // 2, page - 16, page + 16, 2 * page, 3 * page + 16):
+        assert append(k, k + off) == binding.CF_ERR_ALIAS, off
+        assert append(k + off, k) == binding.CF_ERR_ALIAS, off
+    assert r.kv.status() == OK
