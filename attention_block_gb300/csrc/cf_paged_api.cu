@@ -77,6 +77,16 @@ size_t rows_bytes(int64_t n, int64_t stride, int64_t row, size_t es) {
   return n > 0 ? (size_t)((n - 1) * stride + row) * es : 0;
 }
 
+// Zeros n bytes and waits for that: cudaMemset of device memory may return
+// before it is done, and calls on streams that do not wait for the default one
+// may follow at once.
+bool clear(void* p, size_t n) {
+  if (cudaMemset(p, 0, n) == cudaSuccess && cudaStreamSynchronize(nullptr) == cudaSuccess)
+    return true;
+  cudaGetLastError();
+  return false;
+}
+
 // Whether one of n rows of na bytes from a meets one of n rows of nb bytes from
 // b, both `stride` bytes apart.
 bool rows_meet(const void* a, int64_t na, const void* b, int64_t nb, int64_t n, int64_t stride) {
@@ -306,10 +316,7 @@ int cf_paged_create(const cf_paged_config* cfg, cf_paged_handle** out) {
     h->ws = nullptr;
     return fail(CF_ERR_CUDA);
   }
-  if (cudaMemset(h->ws, 0, zero) != cudaSuccess) {
-    cudaGetLastError();
-    return fail(CF_ERR_CUDA);
-  }
+  if (!clear(h->ws, zero)) return fail(CF_ERR_CUDA);
   uint8_t* ws = static_cast<uint8_t*>(h->ws);
   h->errflag = reinterpret_cast<int*>(ws);
   const PagedParts own = {reinterpret_cast<float*>(ws + at_o[0]),
@@ -437,7 +444,7 @@ int cf_paged_get_status(cf_paged_handle* h) {
   int flag = 0;
   if (cudaMemcpy(&flag, h->errflag, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess)
     return CF_ERR_CUDA;
-  if (flag != 0 && cudaMemset(h->errflag, 0, sizeof(int)) != cudaSuccess) return CF_ERR_CUDA;
+  if (flag != 0 && !clear(h->errflag, sizeof(int))) return CF_ERR_CUDA;
   if (flag & kDevErrTimeout) return CF_ERR_DEVICE_TIMEOUT;
   if (flag & kDevErrPosRange) return CF_ERR_DEVICE_POS_RANGE;
   return CF_OK;

@@ -189,3 +189,25 @@ def test_pools_that_share_pages_are_refused(layout):
         assert append(k, k + off) == binding.CF_ERR_ALIAS, off
         assert append(k + off, k) == binding.CF_ERR_ALIAS, off
     assert r.kv.status() == OK
+
+
+# ------------------------------------------------------- handles and shapes --
+def test_a_new_handle_serves_every_stream():
+    """Its workspace is ready when create returns, also for streams that do not
+    wait for the default one, and however much that still has to do."""
+    a = torch.randn(8192, 8192, device="cuda")
+    side = torch.cuda.Stream()
+    pr = Problem([1], [900], 4, 2, seed=86)
+    r = Run(pr)
+    want = ref_attention(pr)
+    torch.cuda.synchronize()
+    done = torch.cuda.Event()
+    with torch.cuda.stream(torch.cuda.default_stream()):
+        for _ in range(20):
+            a @ a
+        done.record()
+    r.kv = binding.PagedKv(**pr.config())
+    assert done.query()
+    r.attend(stream=side)
+    side.synchronize()
+    r.check()
