@@ -836,6 +836,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const __grid_co
       __syncwarp();
       if (lane == 0) fresh = cur.next(p, u1);
       fresh = __shfl_sync(~0u, fresh, 0);
+      __syncwarp();  // the cursor lies in shared memory; a shuffle orders nothing there
       look_up();
 #pragma unroll 1
       for (int kv = 0; kv < 2; ++kv) {
