@@ -491,17 +491,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const __grid_co
   pdl_trigger();
 
   // ---- this block's units
-  bool ordered = true;
   if constexpr (!PRE)  // the lookups below depend on one another: have their lines on the way
     for (int b = tid; b < p.batch; b += kTcThreads) {
+      if (p.q_start) prefetch_line(p.q_start + b + 1);
       prefetch_line(p.kv_len + b);
-      if (p.q_start) ordered &= starts_ordered(p.q_start[b], p.q_start[b + 1], p.n_tokens);
     }
   const int nslots = PRE ? (p.n_tokens * p.g.G + 255) / 256 : a.slots;
   TcShare<PRE> share(p, nslots, true, tid);
   long long mine, incl;
   RowTile mine_t;  // the last of this thread's row tiles: with one each, the one
-  auto sum = [&]() {
+#pragma unroll 1
+  while (true) {
     mine = 0;
     share.walk(p, [&](const RowTile& t) {
       mine += (long long)(t.tiles + kItemCost) * p.g.nkv;
@@ -515,12 +515,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const __grid_co
       if (lane >= o) incl += v;
     }
     if (lane == 31) s_scan[warp] = incl;
-  };
-  sum();
-  if (!__syncthreads_and(ordered)) {  // the sum was over numbers that mean nothing
-    share = TcShare<PRE>(p, nslots, false, tid);
-    sum();
-    __syncthreads();
+    bool done = true;
+    if (!PRE && p.q_start && share.ordered)
+      for (int b = tid; b < p.batch; b += kTcThreads)
+        done &= starts_ordered(p.q_start[b], p.q_start[b + 1], p.n_tokens);
+    if (__syncthreads_and(done)) break;
+    share = TcShare<PRE>(p, nslots, false, tid);  // the sum was over numbers that mean nothing
   }
   long long before = incl - mine, total = 0;
 #pragma unroll
