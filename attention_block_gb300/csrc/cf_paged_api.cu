@@ -30,6 +30,10 @@ namespace {
 
 size_t elem_size(int dtype) { return dtype == CF_F32 ? 4 : 2; }
 
+// The largest stride of n rows or pages: what they span, in bytes too, stays
+// far below 2^63.
+int64_t max_stride(int64_t n) { return std::min((int64_t)1 << 40, ((int64_t)1 << 56) / n); }
+
 bool overlap(const void* a, size_t na, const void* b, size_t nb) {
   if (a == nullptr || b == nullptr || na == 0 || nb == 0) return false;
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
@@ -121,7 +125,7 @@ int attention(cf_paged_handle* h, int32_t batch, int32_t n_tokens, int32_t max_q
   for (const void* p : ints)
     if (p == nullptr || !aligned(p, 4)) return CF_ERR_INVALID_ARG;
   if (!aligned(q_start, 4) || !aligned(lse, 4)) return CF_ERR_INVALID_ARG;
-  if (q_stride < qrow || q_stride > (int64_t)1 << 40 || (q_stride * (int64_t)es) % 16 != 0)
+  if (q_stride < qrow || q_stride > max_stride(n_tokens) || (q_stride * (int64_t)es) % 16 != 0)
     return CF_ERR_INVALID_ARG;
   const size_t ob = (size_t)n_tokens * qrow * es, lb = (size_t)n_tokens * c.n_q_heads * 4;
   const size_t pool = (size_t)h->pool_elems * es;
@@ -227,7 +231,7 @@ int cf_paged_create(const cf_paged_config* cfg, cf_paged_handle** out) {
   const size_t es = elem_size(c.dtype);
   const int64_t page = (int64_t)c.page_size * c.n_kv_heads * c.head_dim;
   if (c.page_stride == 0) c.page_stride = page;
-  if (c.page_stride < page || c.page_stride > (int64_t)1 << 40 ||
+  if (c.page_stride < page || c.page_stride > max_stride(c.num_pages) ||
       (c.page_stride * (int64_t)es) % 16 != 0)
     return CF_ERR_INVALID_ARG;
 
@@ -356,7 +360,7 @@ int cf_paged_append(cf_paged_handle* h, int32_t batch, int32_t n_tokens, const v
       !aligned(page_table, 4) || !aligned(q_start, 4) || !aligned(rope_pos, 4))
     return CF_ERR_INVALID_ARG;
   auto bad_stride = [&](int64_t s, int64_t row) {
-    return s < row || s > (int64_t)1 << 40 || (s * (int64_t)es) % 16 != 0;
+    return s < row || s > max_stride(n_tokens) || (s * (int64_t)es) % 16 != 0;
   };
   if (bad_stride(kv_stride, kvrow)) return CF_ERR_INVALID_ARG;
   if (q != nullptr && (bad_stride(q_stride, qrow) || bad_stride(q_out_stride, qrow)))

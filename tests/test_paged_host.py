@@ -61,6 +61,14 @@ def test_create_rejects_bad_config_before_cuda(kw, code):
     assert rc == code and not h
 
 
+@pytest.mark.parametrize("kw", [
+    dict(num_pages=2 ** 31 - 1, page_size=1024, n_q_heads=65535, n_kv_heads=65535),
+    dict(num_pages=1 << 25, page_stride=1 << 40)], ids=str)
+def test_pools_whose_bytes_pass_63_bits_are_refused(kw):
+    rc, h = binding.cf_paged_create_rc(binding.make_paged_config(**dict(BASE, **kw)))
+    assert rc == binding.CF_ERR_INVALID_ARG and not h
+
+
 def test_null_arguments():
     assert binding.cf_paged_create_rc(None)[0] == binding.CF_ERR_INVALID_ARG
     lib = binding.lib()

@@ -211,3 +211,24 @@ def test_a_new_handle_serves_every_stream():
     r.attend(stream=side)
     side.synchronize()
     r.check()
+
+
+def test_strides_whose_span_overflows_are_refused():
+    """Rows so far apart that the tensor's bytes pass 63 bits: nothing runs."""
+    n = 1 << 20
+    kv = binding.PagedKv(n_q_heads=1, n_kv_heads=1, head_dim=64, page_size=16, num_pages=1,
+                         max_pages=1, max_batch=1, max_tokens=n, dtype="bf16")
+    x = torch.zeros(64 * 64, dtype=torch.bfloat16, device="cuda")
+    i32 = torch.zeros(64, dtype=torch.int32, device="cuda")
+    L, s = binding.lib(), torch.cuda.current_stream().cuda_stream
+    a = [x[i:].data_ptr() for i in range(0, 1024, 64)]
+    far = 1 << 40
+    assert L.cf_paged_attention(kv.handle, 1, n, 1, a[0], far, i32.data_ptr(), i32.data_ptr(),
+                                i32.data_ptr(), a[1], a[2], 0, 0, a[3], None, s) == \
+        binding.CF_ERR_INVALID_ARG
+    for strides in ((far, 64, 64), (64, far, 64), (64, 64, far)):
+        q, kv_, out = strides
+        assert L.cf_paged_append(kv.handle, 1, n, a[0], a[1], a[2], q, kv_, i32.data_ptr(),
+                                 i32.data_ptr(), None, i32.data_ptr(), a[3], a[4], a[5], out, s) == \
+            binding.CF_ERR_INVALID_ARG
+    assert kv.status() == OK and (x == 0).all()
