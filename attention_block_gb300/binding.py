@@ -535,8 +535,9 @@ class PagedKv:
 
     Rows of q, k, v and q_out may be strided: a tensor's stride along dim 0 is
     used, a raw address counts as dense unless the stride is given.  Tensors
-    are checked for dtype, device and dense inner dimensions; raw addresses
-    are taken as they are."""
+    are checked for dtype, device, dense inner dimensions and, page tables and
+    positions of three axes, for the width they are read by; raw addresses are
+    taken as they are."""
 
     def __init__(self, **cfg):
         self.cfg = c = make_paged_config(**cfg)
@@ -563,12 +564,13 @@ class PagedKv:
         self._attention = lib().cf_paged_attention
         self._prefix = lib().cf_paged_prefix_attention
 
-    # Address of a tensor after checking it, or the address given.
-    def _at(self, x, dtype, numel, what):
+    # Address of a tensor after checking it, or the address given.  cols: the
+    # width that an array of two axes is read by (one of one axis lies flat).
+    def _at(self, x, dtype, numel, what, cols=0):
         if x is None or isinstance(x, int):
             return x
         if x.dtype is dtype and x.get_device() == self._dev and x.is_contiguous() and \
-                x.numel() >= numel:
+                x.numel() >= numel and (not cols or x.dim() < 2 or x.shape[-1] == cols):
             return x.data_ptr()
         raise CfError(CF_ERR_INVALID_ARG, f"{what}: {x.dtype} {tuple(x.shape)} on {x.device}")
 
@@ -615,8 +617,8 @@ class PagedKv:
         rc = self._append(
             self.handle, batch, n_tokens, qp, kp, vp, qs, ks,
             self._at(q_start, i32, batch + 1, "q_start"), self._at(kv_len, i32, batch, "kv_len"),
-            self._at(rope_pos, i32, axes * n_tokens, "rope_pos"),
-            self._at(page_table, i32, batch * c.max_pages, "page_table"),
+            self._at(rope_pos, i32, axes * n_tokens, "rope_pos", n_tokens if axes > 1 else 0),
+            self._at(page_table, i32, batch * c.max_pages, "page_table", c.max_pages),
             self._pool(k_pages, "k_pages"), self._pool(v_pages, "v_pages"), op, os_,
             self._on(stream))
         if rc != CF_OK:
@@ -631,7 +633,7 @@ class PagedKv:
         rc = self._attention(
             self.handle, batch, n_tokens, max_q, qp, qs,
             self._at(q_start, i32, batch + 1, "q_start"), self._at(kv_len, i32, batch, "kv_len"),
-            self._at(page_table, i32, batch * c.max_pages, "page_table"),
+            self._at(page_table, i32, batch * c.max_pages, "page_table", c.max_pages),
             self._pool(k_pages, "k_pages"), self._pool(v_pages, "v_pages"), window, n_sinks,
             self._at(out, self._dtype, n_tokens * self._qrow, "out"),
             self._at(lse, self._f32, n_tokens * c.n_q_heads, "lse"), self._on(stream))
@@ -649,7 +651,7 @@ class PagedKv:
         rc = self._prefix(
             self.handle, batch, n_tokens, max_q, qp, qs,
             self._at(q_start, i32, batch + 1, "q_start"), self._at(kv_len, i32, batch, "kv_len"),
-            self._at(page_table, i32, batch * c.max_pages, "page_table"),
+            self._at(page_table, i32, batch * c.max_pages, "page_table", c.max_pages),
             self._at(prefix_table, i32, -(-prefix_len // c.page_size), "prefix_table"),
             prefix_len, self._pool(k_pages, "k_pages"), self._pool(v_pages, "v_pages"),
             self._at(out, self._dtype, n_tokens * self._qrow, "out"),

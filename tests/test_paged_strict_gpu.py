@@ -7,7 +7,7 @@ import torch
 
 from attention_block_gb300 import binding
 from paged_util import Problem, ref_attention
-from test_paged_gpu import OK, RANGE, TYPES, Run, check_append, close, run_append
+from test_paged_gpu import OK, RANGE, TYPES, Run, check_append, close, dev, run_append
 
 pytestmark = pytest.mark.gpu
 
@@ -232,3 +232,34 @@ def test_strides_whose_span_overflows_are_refused():
                                  i32.data_ptr(), None, i32.data_ptr(), a[3], a[4], a[5], out, s) == \
             binding.CF_ERR_INVALID_ARG
     assert kv.status() == OK and (x == 0).all()
+
+
+def test_tables_of_another_width_are_refused():
+    """[batch, max_pages] and [axes, n_tokens] arrays are read by those widths:
+    a tensor of two axes has to have them."""
+    pr = Problem([2, 3], [9, 30], 4, 2, max_pages=4, seed=87)
+    r = Run(pr, rope_sections=(16, 24, 24))
+    rest = (r.k_pages, r.v_pages)
+    wide = torch.zeros(2, pr.max_pages + 1, dtype=torch.int32, device="cuda")
+    q, k, v = dev(pr.q), dev(pr.k), dev(pr.v)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    for table in (wide, wide.T.contiguous()):
+        with pytest.raises(binding.CfError) as e:
+            r.kv.attention(2, 5, 3, q, r.q_start, r.kv_len, table, *rest, r.out)
+        assert e.value.code == binding.CF_ERR_INVALID_ARG
+        with pytest.raises(binding.CfError):
+            r.kv.prefix_attention(2, 5, 3, q, r.q_start, r.kv_len, table, r.ptable, 0, *rest, r.out)
+        with pytest.raises(binding.CfError):
+            r.kv.append(2, 5, q, k, v, r.q_start, r.kv_len, table, *rest, r.out)
+    for shape in ((3, 6), (5, 3), (4, 6)):
+        with pytest.raises(binding.CfError):
+            r.kv.append(2, 5, q, k, v, r.q_start, r.kv_len, r.table, *rest, r.out,
+                        rope_pos=torch.zeros(*shape, **i32))
+    assert r.out.isnan().all()
+    # rows beyond the call's, and arrays of one axis, are fine
+    more = torch.cat([r.table, r.table])
+    for table in (r.table, more, r.table.flatten()):
+        for pos in (torch.zeros(3, 5, **i32), torch.zeros(15, **i32), None):
+            r.kv.append(2, 5, q, k, v, r.q_start, r.kv_len, table, *rest, r.out, rope_pos=pos)
+        r.kv.attention(2, 5, 3, q, r.q_start, r.kv_len, table, *rest, r.out)
+    assert r.kv.status() == OK
