@@ -3,6 +3,7 @@
 // address of a position, and launch entry points (include/cf_paged.h).
 #pragma once
 
+#include <cuda_runtime.h>
 #include <stdint.h>
 
 #include "cf.h"
@@ -38,7 +39,7 @@ struct PagedAppendParams {
   int64_t q_stride, kv_stride, q_out_stride;
   const int *q_start, *kv_len, *rope_pos, *page_table;
   int* errflag;
-  int batch, n_tokens, rope_dim, axes;
+  int batch, n_tokens, rope_dim;
   uint64_t turn[kMaxPairs];  // theta^(-2i/r) / (2 pi) in 2^-64 of a turn
   uint8_t axis[kMaxPairs];   // which row of rope_pos pair i follows
 };
@@ -177,6 +178,13 @@ struct PagedParts {
 __device__ __forceinline__ void prefetch_line(const void* at) {
   asm volatile("{\n\t.reg .u32 v;\n\tld.global.ca.u32 v, [%0];\n\t}" ::"l"(at));
 }
+// Waits until the launch in front has ended and what it wrote can be seen.
+// Every kernel here calls it before it triggers the next (pdl_trigger), so one
+// that has begun knows that everything before the launch in front has ended
+// too.  The one exception is the launch behind a prefix's (kOwnAfterPrefix): it
+// triggers first and waits at its end, and until then reads nothing that the
+// prefix's launch writes, and writes nothing that it uses.  That needs the
+// prefix's launch to wait before it triggers.
 __device__ __forceinline__ void pdl_wait() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
@@ -461,6 +469,23 @@ struct PagedSplit {
   int grid = 0;            // resident blocks
   long long items = 0;     // that the lists have room for
 };
+
+// Launches a kernel that may begin before the one in front of it in the stream
+// has ended (and waits for that one itself, pdl_wait); false: it failed.
+inline bool launch_pdl(const void* fn, dim3 grid, int threads, int smem, cudaStream_t st,
+                       void** args) {
+  cudaLaunchConfig_t lc = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  lc.gridDim = grid;
+  lc.blockDim = dim3(threads, 1, 1);
+  lc.dynamicSmemBytes = smem;
+  lc.stream = st;
+  lc.attrs = attr;
+  lc.numAttrs = 1;
+  return cudaLaunchKernelExC(&lc, fn, args) == cudaSuccess;
+}
 
 // Host launchers (one translation unit each); false: the launch failed.
 bool paged_append_launch(int dtype, const PagedAppendParams& p, int sm_count, cudaStream_t st);

@@ -3,17 +3,18 @@
 //
 // The rotation angle is kept as a fraction of a turn in 64-bit fixed point:
 // pos * turn_i mod 2^64 is the exact fraction of pos times the host's
-// float64 rate, so far positions lose nothing; its top 32 bits go to
-// sincospif.  The cosines and sines of a token are formed once per block in
+// float64 rate, so far positions lose no more than that rate's rounding (2^-24
+// of a turn near 2^31); its top 32 bits go to sincospif as a float (2^-26).  The cosines and sines of a token are formed once per block in
 // shared memory and serve all of its heads.
 //
 // Bound by memory: each element is read once and written once as 16-byte
 // vectors (9600 tokens, 32 + 2 x 8 heads of 128: 36 us, 5.5 TB/s, 0.81 of a
-// copy's rate; a single token: 3 us, the launch).  A unit of work is two vectors of a head: the halves of W rotated
-// pairs (i and i + r/2), or two vectors that are copied.  A thread keeps to
-// one unit of a head and walks over the heads of the block's tokens; the
-// first loads are under way before the block knows where its
-// tokens go (sequence, length, page: loads that depend on one another).
+// copy's rate; a single token: 3 us, the launch).  A unit of work is two
+// vectors of a head: the halves of W rotated pairs (i and i + r/2), or two
+// vectors that are copied.  A thread keeps to one unit of a head and walks over
+// the heads of the block's tokens; the first loads are under way before the
+// block knows where its tokens go (sequence, length, page: loads that depend on
+// one another).
 #include <cuda_runtime.h>
 
 #include "cf_paged.cuh"
@@ -181,17 +182,8 @@ template <typename T, int D, int TPB>
 bool launch_n(const PagedAppendParams& p, int gy, cudaStream_t st) {
   PagedAppendParams pp = p;
   void* args[] = {&pp};
-  cudaLaunchConfig_t lc = {};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  lc.gridDim = dim3((p.n_tokens + TPB - 1) / TPB, gy, 1);
-  lc.blockDim = dim3(kAppendThreads, 1, 1);
-  lc.stream = st;
-  lc.attrs = attr;
-  lc.numAttrs = 1;
-  return cudaLaunchKernelExC(&lc, (const void*)&paged_append_kernel<T, D, TPB>, args) ==
-         cudaSuccess;
+  return launch_pdl((const void*)&paged_append_kernel<T, D, TPB>,
+                    dim3((p.n_tokens + TPB - 1) / TPB, gy, 1), kAppendThreads, 0, st, args);
 }
 
 template <typename T, int D>

@@ -167,7 +167,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   const int gq = lane >> 2, tq = lane & 3;
 
   // After a prefix launch this one reads only what that launch has waited for
-  // already, so it starts beside its last blocks and waits for it at the end.
+  // already (pdl_wait), so it starts beside its last blocks and waits for it at
+  // the end.
   if constexpr (MODE != kOwnAfterPrefix) pdl_wait();
   pdl_trigger();
 
@@ -747,20 +748,6 @@ FewFns few_fns(int dtype, int d, int mode) {
   return d == 64 ? few_fns_td<__nv_bfloat16, 64>(mode) : few_fns_td<__nv_bfloat16, 128>(mode);
 }
 
-bool launch_pdl(const void* fn, int grid, int threads, int smem, cudaStream_t st, void** args) {
-  cudaLaunchConfig_t lc = {};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  lc.gridDim = dim3(grid, 1, 1);
-  lc.blockDim = dim3(threads, 1, 1);
-  lc.dynamicSmemBytes = smem;
-  lc.stream = st;
-  lc.attrs = attr;
-  lc.numAttrs = 1;
-  return cudaLaunchKernelExC(&lc, fn, args) == cudaSuccess;
-}
-
 }  // namespace
 
 int cf::paged_few_grid(int dtype, int head_dim, int sm_count) {
@@ -801,10 +788,10 @@ bool cf::paged_few_launch(int dtype, const PagedAttnParams& p, const PagedSplit&
   a.tickets = ws.tickets;
   a.row_limit = std::min(kFewRows, p.max_q * p.g.G);
   void* args[] = {&a};
-  if (!launch_pdl(f.main, ws.grid, kFewThreads, f.smem, st, args)) return false;
+  if (!launch_pdl(f.main, dim3(ws.grid), kFewThreads, f.smem, st, args)) return false;
   if (mode != kOwnAfterPrefix) return true;
   const int ng = kJoinThreads / (p.g.D / 4);
   const long long rows = (long long)p.batch * p.g.nkv * a.row_limit;
-  return launch_pdl(f.join, (int)std::min<long long>(8LL * ws.grid, (rows + ng - 1) / ng),
+  return launch_pdl(f.join, dim3((unsigned)std::min<long long>(8LL * ws.grid, (rows + ng - 1) / ng)),
                     kJoinThreads, 0, st, args);
 }

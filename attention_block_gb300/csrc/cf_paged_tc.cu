@@ -486,7 +486,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const __grid_co
     fence_mbar_init_cluster();
   }
   // After a prefix launch this one reads only what that launch has waited for
-  // already, so it starts on the SMs that it leaves and waits for it at the end.
+  // already (pdl_wait), so it starts on the SMs that it leaves and waits for it
+  // at the end.
   if constexpr (!JOIN) pdl_wait();
   pdl_trigger();
 
@@ -1101,20 +1102,6 @@ TcFns fns_td(int mode) {
 TcFns tc_fns(int dtype, int d, int mode) {
   if (dtype == CF_F16) return d == 64 ? fns_td<__half, 64>(mode) : fns_td<__half, 128>(mode);
   return d == 64 ? fns_td<__nv_bfloat16, 64>(mode) : fns_td<__nv_bfloat16, 128>(mode);
-}
-
-bool launch_pdl(const void* fn, dim3 grid, int threads, int smem, cudaStream_t st, void** args) {
-  cudaLaunchConfig_t lc = {};
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  lc.gridDim = grid;
-  lc.blockDim = dim3(threads, 1, 1);
-  lc.dynamicSmemBytes = smem;
-  lc.stream = st;
-  lc.attrs = attr;
-  lc.numAttrs = 1;
-  return cudaLaunchKernelExC(&lc, fn, args) == cudaSuccess;
 }
 
 }  // namespace
