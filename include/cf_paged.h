@@ -46,8 +46,10 @@
  * and bf16: tensor-core products of the stored values).  Probabilities enter
  * the product with V rounded to the storage type (in bf16, with max_q * nq/nkv
  * of 16 at most, as a sum of two such values); their sum is taken before that
- * rounding.  Outputs are rounded once.  Angles are exact to 2^-32 of a turn for
- * every int32 position.  The same call on the same data gives the same bits.
+ * rounding, so that in fp16 a probability below 2^-25 counts there and not in
+ * the product.  Outputs are rounded once.  Angles are off by 2^-25 of a turn at
+ * most for positions up to 2^28, by 2^-23 for every int32 position (rope_theta
+ * of 1 or more).  The same call on the same data gives the same bits.
  *
  * Conventions for every function:
  *   - CF_OK (0) or a negative CF_ERR_* code of cf.h; nothing is printed and no
@@ -67,7 +69,8 @@
  *     is appended for it;
  *   - a needed page number outside [0, num_pages): keys and values of zero
  *     stand for its positions, and nothing is appended to it;
- *   - an appended token with p < 0 is skipped (its q_out row too);
+ *   - an appended token with p < 0 is skipped; its q_out row, like that of every
+ *     token that is not appended, stays as it was;
  *   - q_start values that decrease or leave [0, n_tokens]: such a sequence
  *     has no tokens, the others have theirs.  Where two sequences then claim a
  *     token, what the call writes is unspecified, though within its outputs.
@@ -114,7 +117,8 @@ typedef struct cf_paged_handle cf_paged_handle; /* opaque */
 /* Validate cfg and allocate the handle's workspace on the current device: an
  * error word and, but for fp32, partial results of split sequences (up to
  * 160,000 * (d + 2) fp32 values, 81 MB for d = 128) and of whole ones beside a
- * prefix (per token of max_tokens up to 2 * nq * (d + 2) fp32 values).
+ * prefix (per token of max_tokens up to 2 * nq * (d + 2) fp32 values; calls
+ * without a prefix use none of these, but the handle has them all the same).
  * On failure nothing stays allocated and *out is NULL.  Errors: INVALID_ARG
  * (NULL, sizes, strides, sections that do not add up), UNSUPPORTED
  * (head_dim, page_size), CUDA. */

@@ -1,6 +1,7 @@
 """The paged cache's operators at the edges of what include/cf_paged.h allows:
 malformed starts, values that are no numbers, overlaps, shapes."""
 import math
+from decimal import Decimal, getcontext
 
 import pytest
 import torch
@@ -50,6 +51,77 @@ def test_sequences_beside_malformed_starts(dtype, prefix, starts, kv_len, tokens
         assert r.kv.status() == RANGE
         close(r.out, want[0], want[1], "out")
         close(r.lse, want[2], want[3], "lse")
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("prefix", [0, 90])
+@pytest.mark.parametrize("n", [3, 70])
+def test_tokens_claimed_twice_leave_the_rest_alone(dtype, prefix, n):
+    """Many sequences that claim the same tokens: the call ends, reports them,
+    writes nothing beside its outputs, and the next call finds all as it was."""
+    batch = 41
+    pr = Problem([n] + [0] * (batch - 1), [n + 40 + 3 * b for b in range(batch)], 8, 2, d=64,
+                 dtype=dtype, prefix=prefix, extra_tokens=2, seed=88)
+    r = Run(pr)
+    good = r.q_start.clone()
+    big = torch.full((3 * pr.tokens, pr.nq, pr.d), 7.0, dtype=r.out.dtype, device="cuda")
+    big_lse = torch.full((3 * pr.tokens, pr.nq), 7.0, device="cuda")
+    r.out, r.lse = big[pr.tokens:2 * pr.tokens], big_lse[pr.tokens:2 * pr.tokens]
+    for _ in range(3):
+        r.q_start.copy_(torch.tensor([n * (b % 2) for b in range(batch + 1)], dtype=torch.int32))
+        r.attend()
+        assert r.kv.status() == RANGE
+        r.q_start.copy_(good)
+        r.out.fill_(float("nan")), r.lse.fill_(float("nan"))
+        r.attend()
+        r.check()
+    for x in (big, big_lse):
+        assert (x[:pr.tokens] == 7).all() and (x[2 * pr.tokens:] == 7).all()
+
+
+def test_a_token_whose_page_is_lost_keeps_its_query_row():
+    pr = Problem([3, 2], [20, 30], 4, 2, seed=89)
+    r = Run(pr)
+    q, k, v = dev(pr.q), dev(pr.k), dev(pr.v)
+    r.table[0, 1] = pr.num_pages  # positions 16..31 of the first sequence: all three tokens
+    before = r.k_pages.clone().nan_to_num(7.0), r.v_pages.clone().nan_to_num(7.0)
+    r.kv.append(2, 5, q, k, v, r.q_start, r.kv_len, r.table, r.k_pages, r.v_pages, r.out)
+    assert r.kv.status() == RANGE
+    assert r.out[:3].isnan().all() and r.out[3:].isfinite().all()
+    for got, old in zip((r.k_pages, r.v_pages), before):
+        assert int((got.nan_to_num(7.0) != old).flatten(2).any(-1).sum()) == 2  # two slots, of the second
+
+
+def test_angles_are_as_exact_as_stated():
+    """cos and sin of every angle, read off rotated unit vectors in fp32, against
+    angles in 60 digits.  The header's 2^-25 and 2^-23 of a turn, and 2^-24 for
+    sincospif (2 ulp of 1 and the fp32 results' rounding: (2 + 1) 2^-24 / 2 pi)."""
+    d, n = 128, 64
+    g = torch.Generator().manual_seed(90)
+    near = torch.cat([torch.arange(16), torch.randint(0, 2 ** 28, (n - 16,), generator=g)])
+    far = torch.randint(-2 ** 31, 2 ** 31, (n,), generator=g)
+    far[:3] = torch.tensor([2 ** 31 - 1, -2 ** 31, 2 ** 30 + 1])
+    kv = binding.PagedKv(n_q_heads=1, n_kv_heads=1, head_dim=d, page_size=16, num_pages=4,
+                         max_pages=4, max_batch=1, max_tokens=n, dtype="f32", rope_theta=5e5)
+    x = torch.zeros(n, 1, d, device="cuda")
+    x[..., :d // 2] = 1.0  # a = 1, b = 0: the pair becomes (cos, sin)
+    pools = torch.zeros(2, 4, 16, 1, d, device="cuda")
+    i32 = dict(dtype=torch.int32, device="cuda")
+    st, table = torch.tensor([0, n], **i32), torch.arange(4, **i32).view(1, 4)
+    getcontext().prec = 60
+    pi = Decimal("3.14159265358979323846264338327950288419716939937510582097494")
+    rate = [Decimal(500000) ** (Decimal(-2 * i) / d) / (2 * pi) for i in range(d // 2)]
+    for pos, bound in ((near, 2.0 ** -25), (far, 2.0 ** -23)):
+        out = torch.empty_like(x)
+        kv.append(1, n, x, x, x, st, st[1:], table, pools[0], pools[1], out,
+                  rope_pos=pos.to(**i32).view(1, n))
+        assert kv.status() == OK
+        c, s = out[:, 0, :d // 2].double().cpu(), out[:, 0, d // 2:].double().cpu()
+        turns = torch.atan2(s, c) / (2 * math.pi)
+        want = torch.tensor([[float(int(p) * r - (int(p) * r).to_integral_value()) for r in rate]
+                             for p in pos], dtype=torch.float64)
+        off = (turns - want + 0.5) % 1 - 0.5
+        assert off.abs().max() <= bound + 2.0 ** -24, off.abs().max()
 
 
 @pytest.mark.parametrize("dtype", TYPES)
