@@ -34,9 +34,9 @@
 // Bound by the tensor core where items are long (one prompt of 8192 tokens, 32
 // / 8 heads of 128: 399 us, 1380 TFLOP/s, 0.72 of a library product's rate),
 // by the softmax's chain otherwise: 1.65 us a unit, 1.07 of them products, and
-// about 8 us an item for masked tiles, the wait for O and the result.  With 64
-// columns exp2 and masks take longer than the products (8191 tokens, window
-// 1024, 32 heads: 187 us).
+// an item's masked tiles, wait for O and result, which weigh about 5 units
+// (kItemCost).  With 64 columns exp2 and masks take longer than the products
+// (8191 tokens, window 1024, 32 heads: 187 us).
 #include <cuda_runtime.h>
 
 #include <algorithm>
