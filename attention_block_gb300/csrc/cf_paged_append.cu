@@ -4,8 +4,9 @@
 // The rotation angle is kept as a fraction of a turn in 64-bit fixed point:
 // pos * turn_i mod 2^64 is the exact fraction of pos times the host's
 // float64 rate, so far positions lose no more than that rate's rounding (2^-24
-// of a turn near 2^31); its top 32 bits go to sincospif as a float (2^-26).  The cosines and sines of a token are formed once per block in
-// shared memory and serve all of its heads.
+// of a turn near 2^31); its top 32 bits go to sincospif as a float (2^-26).
+// The cosines and sines of a token are formed once per block in shared memory
+// and serve all of its heads.
 //
 // Bound by memory: each element is read once and written once as 16-byte
 // vectors (9600 tokens, 32 + 2 x 8 heads of 128: 36 us, 5.5 TB/s, 0.81 of a
