@@ -456,6 +456,15 @@ struct PagedRow {
   }
 };
 
+// log2 of what weights are multiplied by before they become 16-bit operands,
+// where none is above 2^largest: fp16 has few exponents, and weights below
+// 2^-25 would count in their sum and not in the product.  Times 2^(15 - largest)
+// it holds them down to 2^(largest - 40).  A part's states are scaled back.
+template <typename T>
+CF_HOST_DEVICE constexpr int weight_lift(int largest) {
+  return MmaExp<T>::mask == 0x7c00u ? 15 - largest : 0;
+}
+
 // What a launch attends to: the sequences' own keys; the shared prefix (it
 // leaves states only); own keys, joined with the prefix's states.
 enum PagedMode { kOwn = 0, kPrefix = 1, kOwnAfterPrefix = 2 };

@@ -151,6 +151,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   constexpr int NT = KS / 8;  // key octets of a stage
   constexpr int NO = D / 8;   // column octets of o
   using M = MmaKind<T>;
+  constexpr int LIFT = weight_lift<T>(0);
   const PagedAttnParams& p = a.p;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ long long s_first[kFewThreads];  // first unit of each thread's sequences
@@ -427,7 +428,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         const float ref = mx[r] == -INFINITY ? 0.f : mx[r];
         corr[r] = ex2(m[r] - ref);
         m[r] = mx[r];
-        mx[r] = ref;
+        mx[r] = ref - LIFT;
         l[r] *= corr[r];
       }
       if (__any_sync(~0u, corr[0] != 1.f || corr[1] != 1.f)) {
@@ -497,7 +498,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         }
       } else {
       // o += P V; bf16 probabilities enter as hi + lo pairs (the tensor cores
-      // have the time), fp16 ones with their 11 bits
+      // have the time), fp16 ones with their 11 bits, times 2^LIFT
 #pragma unroll
       for (int kk = 0; kk < KS / 16; ++kk) {
         uint32_t hi[4], lo[4];
@@ -536,6 +537,15 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     for (int r = 0; r < 2; ++r) {
       l[r] += __shfl_xor_sync(~0u, l[r], 1);
       l[r] += __shfl_xor_sync(~0u, l[r], 2);
+    }
+    if constexpr (LIFT != 0) {
+      constexpr float back = 1.f / (1 << LIFT);
+      l[0] *= back;
+      l[1] *= back;
+#pragma unroll
+      for (int k = 0; k < NO; ++k)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[k][e] *= back;
     }
     FewItem it;
     it.i0 = cur.i0;

@@ -28,15 +28,16 @@
 // the other.  TMEM: S (or P) and O of both halves, 512 columns.
 //
 // O is rescaled only where a row's maximum grew by more than 2^8 since its
-// last rescale: P then stays below 2^8 and keeps its relative precision in
-// 16-bit floating point, and most tiles pass without touching O.
+// last rescale: P then stays below 2^8 (fp16 holds it times 2^7) and keeps its
+// relative precision in 16-bit floating point, and most tiles pass without
+// touching O.
 //
 // Bound by the tensor core where items are long (one prompt of 8192 tokens, 32
 // / 8 heads of 128: 399 us, 1380 TFLOP/s, 0.72 of a library product's rate),
 // by the softmax's chain otherwise: 1.65 us a unit, 1.07 of them products, and
 // an item's masked tiles, wait for O and result, which weigh about 5 units
 // (kItemCost).  With 64 columns exp2 and masks take longer than the products
-// (8191 tokens, window 1024, 32 heads: 187 us).
+// (8191 tokens, window 1024, 32 heads: 189 us).
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -58,7 +59,7 @@ constexpr int kBN = 128;       // positions of a tile
 // (32 / 8 heads of 128): 241 us with 0, 155 with 2, 145 with 5, 150 with 8.
 constexpr int kItemCost = 5;
 constexpr int kPagedRunInts = 9;  // of a run that cf_test_paged_line reports
-constexpr float kGrow = 8.0f;  // log2 of the growth that forces a rescale
+constexpr int kGrow = 8;       // log2 of the growth that forces a rescale
 
 template <int D>
 struct TcShape {
@@ -451,6 +452,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const __grid_co
   constexpr bool PRE = MODE == kPrefix, JOIN = MODE == kOwnAfterPrefix;
   using S = TcShape<D>;
   constexpr int C = D / 8;  // 16-byte chunks of a row
+  constexpr int LIFT = weight_lift<T>(kGrow);
+  constexpr float BACK = 1.f / (1 << LIFT);
   const PagedAttnParams& p = a.p;
   extern __shared__ __align__(1024) uint8_t sm[];
   __shared__ long long s_scan[kTcThreads / 32];
@@ -609,7 +612,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const __grid_co
           for (int e = 0; e < 4; ++e) mx4[e] = fmaxf(mx4[e], s[kBN - 4 + e]);
           const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
           const float m_new = fmaxf(m, mx);
-          const bool grow = (m_new - m) * sc > kGrow;  // also from -inf
+          const bool grow = (m_new - m) * sc > (float)kGrow;  // also from -inf
           if (__any_sync(~0u, grow)) {
             const float corr = m_new == -INFINITY ? 1.f : ex2((m - m_new) * sc);
             if (some) {
@@ -628,7 +631,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const __grid_co
             l *= corr;
             m = m_new;
           }
-          const float ref = m == -INFINITY ? 0.f : m * sc;
+          const float ref = (m == -INFINITY ? 0.f : m * sc) - LIFT;
           const float2 sc2 = make_float2(sc, sc), ref2 = make_float2(-ref, -ref);
           float2 sum[2] = {make_float2(l, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
@@ -660,6 +663,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const __grid_co
         tc05_fence_after();
       }
       const float m2 = m * sc;  // base 2
+      l *= BACK;
       const bool part = MODE != kOwn || !whole;  // leaves a state, not a result
       // this block's slot for the item (PagedParts)
       const long long prow0 =
@@ -675,7 +679,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const __grid_co
           my_row = whole ? a.ws.state_base + my_row : prow0 + r;
           __stcg(a.ws.ml + my_row, make_float2(m2, l));
         } else {
-          my_inv = l == 0.f ? 0.f : 1.f / l;
+          my_inv = l == 0.f ? 0.f : BACK / l;
           if (p.lse) p.lse[my_row] = paged_lse(m2, l);
         }
       }
@@ -711,8 +715,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) paged_tc_kernel(const __grid_co
                 // the odd ones B's, 16 bytes each
 #pragma unroll
                 for (int b2 = 0; b2 < 2; ++b2) {
-                  const float A0 = o[8 * b2 + 2 * e], A1 = o[8 * b2 + 2 * e + 1];
-                  const float B0 = o[8 * b2 + 4 + 2 * e], B1 = o[8 * b2 + 5 + 2 * e];
+                  const float A0 = o[8 * b2 + 2 * e] * BACK, A1 = o[8 * b2 + 2 * e + 1] * BACK;
+                  const float B0 = o[8 * b2 + 4 + 2 * e] * BACK, B1 = o[8 * b2 + 5 + 2 * e] * BACK;
                   const bool odd = q4 & 1;
                   const float g0 = __shfl_xor_sync(~0u, odd ? A0 : B0, 1);
                   const float g1 = __shfl_xor_sync(~0u, odd ? A1 : B1, 1);

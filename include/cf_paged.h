@@ -38,16 +38,16 @@
  * makes both NaN.  What lies in a slot, be it an infinity or a NaN, reaches
  * the rows that see its position and no other.  An infinity in V gives them an
  * infinity; NaN where one of the other sign is seen too, and where its
- * probability may count as 0 in the product (fp16: below 2^-24 of the row's
+ * probability may count as 0 in the product (fp16: below 2^-31 of the row's
  * largest, bf16 2^-115, fp32 2^-126).  Table entries of positions that no row
  * of the sequence sees (past kv_len, behind the window) are not read as pages.
  *
  * Arithmetic: products and sums in fp32 (fp32 storage: plain fp32 FMAs; fp16
  * and bf16: tensor-core products of the stored values).  Probabilities enter
  * the product with V rounded to the storage type (in bf16, with max_q * nq/nkv
- * of 16 at most, as a sum of two such values); their sum is taken before that
- * rounding, so that in fp16 a probability below 2^-25 counts there and not in
- * the product.  Outputs are rounded once.  Angles are off by 2^-25 of a turn at
+ * of 16 at most, as a sum of two such values; in fp16 times 2^15 or, with
+ * more, 2^7, which holds them down to 2^-40 or 2^-32); their sum is taken
+ * before that rounding.  Outputs are rounded once.  Angles are off by 2^-25 of a turn at
  * most for positions up to 2^28, by 2^-23 for every int32 position (rope_theta
  * of 1 or more).  The same call on the same data gives the same bits.
  *

@@ -7,7 +7,7 @@ import pytest
 import torch
 
 from attention_block_gb300 import binding
-from paged_util import Problem, ref_attention
+from paged_util import Problem, half_step, ref_attention
 from test_paged_gpu import OK, RANGE, TYPES, Run, check_append, close, dev, run_append
 
 pytestmark = pytest.mark.gpu
@@ -202,6 +202,37 @@ def test_rows_of_nan_say_so_in_lse(dtype, q_len, kv_len, prefix, window):
     finite = want[0].isfinite()
     close(torch.where(finite, r.out.double().cpu(), 0.0), torch.where(finite, want[0], 0.0),
           torch.where(finite, want[1], 0.0), "finite values")
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("q_len,prefix", [([1], 0), ([2], 0), ([40], 0), ([1], 20000), ([40], 20000)],
+                         ids=str)
+def test_flat_tails_far_below_the_largest_weight_count(dtype, q_len, prefix):
+    """One key of weight 1 and a value of 0, 20000 of 2^-26 and values of 1: the
+    product has the tail as the sum has it.  Scores of 0 and 2 ln 2^13 = 18.02
+    are off by (64 + 2) 2^-23 18.02 at most, their weights relatively by twice
+    that; the weights' rounding and the result's are half a step each, and a
+    fp16 result below 2^-14 is off by 2^-25."""
+    n, d, own = q_len[0], 64, 20000 - prefix
+    own = own or 64
+    pr = Problem(q_len, [own], 8, 2, d=d, page=64, dtype=dtype, prefix=prefix, seed=91)
+    kp, vp = pr.split(pr.pools)
+    kp.zero_(), vp.fill_(1.0)
+    pr.q.zero_()
+    pr.q[..., 0] = 16.0
+    top = torch.tensor(26 * math.log(2) * 8 / 16).to(pr.q.dtype)  # times 16 / sqrt(64)
+    row = pr.prefix_table if prefix else pr.table[0]
+    pr.slot(kp, row, 7)[:, 0] = top
+    pr.slot(vp, row, 7)[...] = 0.0
+    r = Run(pr, poison=False)
+    r.attend()
+    assert r.kv.status() == OK
+    w = math.exp(-2 * float(top))
+    seen = torch.arange(own - n, own, dtype=torch.float64) + prefix  # keys but for the one
+    want = (seen * w / (1 + seen * w))[:, None, None].expand(r.out.shape)
+    u, ds = half_step(dtype), 66 * 2.0 ** -23 * 2 * float(top)
+    tol = want * (2 * u + 2 * ds + (20064 + 8) * 2.0 ** -23) + 2.0 ** -25
+    close(r.out, want, tol, "out")
 
 
 # ---------------------------------------------------------------- overlaps --
