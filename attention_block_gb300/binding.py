@@ -23,6 +23,7 @@ CF_ERR_DEVICE_POS_RANGE = -6
 CF_ERR_DEVICE_TIMEOUT = -7
 
 CF_F32, CF_F16, CF_BF16 = 0, 1, 2
+CF_CODE_INT8, CF_CODE_E4M3 = 0, 1
 
 
 class CfConfig(ctypes.Structure):
@@ -53,6 +54,10 @@ class CfPagedConfig(ctypes.Structure):
         ("page_stride", ctypes.c_int64), ("rope_theta", ctypes.c_float),
         ("rope_dim", ctypes.c_int32), ("rope_sections", ctypes.c_int32 * 3),
         ("rope_interleaved", ctypes.c_int32), ("scale", ctypes.c_float)]
+
+
+class CfPaged8Config(ctypes.Structure):
+    _fields_ = [("cache", CfPagedConfig), ("code", ctypes.c_int32)]
 
 
 class CfLaunchInfo(ctypes.Structure):
@@ -124,6 +129,15 @@ SIGNATURES = {
                                   + [_vp] * 5),
     "cf_paged_get_status": (ctypes.c_int, [_vp]),
     "cf_paged_destroy": (None, [_vp]),
+    "cf_paged8_create": (ctypes.c_int, [ctypes.POINTER(CfPaged8Config), ctypes.POINTER(_vp)]),
+    "cf_paged8_append": (ctypes.c_int, [_vp, ctypes.c_int32, ctypes.c_int32] + [_vp] * 3
+                         + [ctypes.c_int64] * 2 + [_vp] * 8 + [ctypes.c_int64, _vp]),
+    "cf_paged8_attention": (ctypes.c_int, [_vp] + [ctypes.c_int32] * 3 + [_vp, ctypes.c_int64]
+                            + [_vp] * 6 + [ctypes.c_int32] * 2 + [_vp] * 3),
+    "cf_paged8_read": (ctypes.c_int, [_vp] + [ctypes.c_int32] * 2 + [_vp] * 8
+                       + [ctypes.c_int64, _vp]),
+    "cf_paged8_get_status": (ctypes.c_int, [_vp]),
+    "cf_paged8_destroy": (None, [_vp]),
 }
 
 TIMELINE_SLOTS = 32
@@ -545,6 +559,14 @@ class PagedKv:
         if rc != CF_OK:
             raise CfError(rc, "cf_paged_create")
         self.handle = h
+        self._layout(c)
+        self._pool_dtypes = (self._dtype,)
+        self._append = lib().cf_paged_append
+        self._attention = lib().cf_paged_attention
+        self._prefix = lib().cf_paged_prefix_attention
+
+    # What the checks of tensors go by.
+    def _layout(self, c):
         self._qrow = c.n_q_heads * c.head_dim
         self._kvrow = c.n_kv_heads * c.head_dim
         import torch
@@ -560,9 +582,6 @@ class PagedKv:
         # (torch.cuda.current_stream() builds a Stream object: 2.8 us a call)
         self._raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
             lambda d: torch.cuda.current_stream(d).cuda_stream)
-        self._append = lib().cf_paged_append
-        self._attention = lib().cf_paged_attention
-        self._prefix = lib().cf_paged_prefix_attention
 
     # Address of a tensor after checking it, or the address given.  cols: the
     # width that an array of two axes is read by (one of one axis lies flat).
@@ -591,9 +610,10 @@ class PagedKv:
     def _pool(self, x, what):
         if isinstance(x, int):
             return x
-        if x.dtype is self._dtype and x.get_device() == self._dev and x.shape == self._pool_shape \
-                and (x.stride() == self._pool_stride or
-                     (self.cfg.num_pages == 1 and x.stride()[1:] == self._pool_stride[1:])):
+        if x.dtype in self._pool_dtypes and x.get_device() == self._dev and \
+                x.shape == self._pool_shape and (
+                    x.stride() == self._pool_stride or
+                    (self.cfg.num_pages == 1 and x.stride()[1:] == self._pool_stride[1:])):
             return x.data_ptr()
         raise CfError(CF_ERR_INVALID_ARG,
                       f"{what}: {x.dtype} {tuple(x.shape)} strides {x.stride()} on {x.device}")
@@ -675,3 +695,124 @@ class PagedKv:
             self.close()
         except Exception:
             pass
+
+
+# ------------------------------------------------ paged KV cache in 8 bits --
+def cf_paged8_create_rc(cfg: CfPaged8Config | None) -> tuple[int, int | None]:
+    """Return code and handle without raising (boundary tests)."""
+    h = _vp()
+    rc = lib().cf_paged8_create(ctypes.byref(cfg) if cfg is not None else None, ctypes.byref(h))
+    return rc, h.value
+
+
+def make_paged8_config(code=CF_CODE_E4M3, **cache) -> CfPaged8Config:
+    if isinstance(code, str):
+        code = {"int8": CF_CODE_INT8, "e4m3": CF_CODE_E4M3}[code]
+    return CfPaged8Config(make_paged_config(**cache), int(code))
+
+
+class Paged8Kv(PagedKv):
+    """Owns one cf_paged8_handle (include/cf_paged8.h): a paged KV cache whose
+    pages hold 8-bit codes (code="int8" or "e4m3") with a scale per position
+    and head.  Raises CfError on any non-zero return code.
+
+    Pools are tensors of the code's type or torch.uint8; scales is a dense
+    float32 tensor [num_pages, n_kv_heads, page_size, 2].  Tensors are checked
+    as by PagedKv."""
+
+    def __init__(self, code="e4m3", **cache):
+        cfg = make_paged8_config(code, **cache)
+        rc, h = cf_paged8_create_rc(cfg)
+        if rc != CF_OK:
+            raise CfError(rc, "cf_paged8_create")
+        self.handle = h
+        self.cfg = c = cfg.cache
+        self._layout(c)
+        import torch
+        self._pool_dtypes = (torch.uint8, torch.int8 if cfg.code == CF_CODE_INT8
+                             else torch.float8_e4m3fn)
+        self._scale_shape = (c.num_pages, c.n_kv_heads, c.page_size, 2)
+        self._append = lib().cf_paged8_append
+        self._attention = lib().cf_paged8_attention
+        self._read = lib().cf_paged8_read
+
+    # Address of the scales.
+    def _scales(self, x):
+        if isinstance(x, int):
+            return x
+        if x.dtype is self._f32 and x.get_device() == self._dev and \
+                x.shape == self._scale_shape and x.is_contiguous():
+            return x.data_ptr()
+        raise CfError(CF_ERR_INVALID_ARG, f"scales: {x.dtype} {tuple(x.shape)} on {x.device}")
+
+    def append(self, batch, n_tokens, q, k, v, q_start, kv_len, page_table, k_pages, v_pages,
+               scales, q_out, rope_pos=None, q_stride=None, kv_stride=None, q_out_stride=None,
+               stream=None):
+        """Rotates q into q_out, and appends the codes of the rotated k and of v
+        with their scales (cf_paged8_append)."""
+        c, i32 = self.cfg, self._int
+        qp, qs = self._rows(q, n_tokens, self._qrow, q_stride, "q")
+        kp, ks = self._rows(k, n_tokens, self._kvrow, kv_stride, "k")
+        vp, vs = self._rows(v, n_tokens, self._kvrow, kv_stride, "v")
+        op, os_ = self._rows(q_out, n_tokens, self._qrow, q_out_stride, "q_out")
+        if ks != vs and n_tokens > 1:
+            raise CfError(CF_ERR_INVALID_ARG, "k and v have different row strides")
+        axes = 3 if any(c.rope_sections) else 1
+        rc = self._append(
+            self.handle, batch, n_tokens, qp, kp, vp, qs, ks,
+            self._at(q_start, i32, batch + 1, "q_start"), self._at(kv_len, i32, batch, "kv_len"),
+            self._at(rope_pos, i32, axes * n_tokens, "rope_pos", n_tokens if axes > 1 else 0),
+            self._at(page_table, i32, batch * c.max_pages, "page_table", c.max_pages),
+            self._pool(k_pages, "k_pages"), self._pool(v_pages, "v_pages"), self._scales(scales),
+            op, os_, self._on(stream))
+        if rc != CF_OK:
+            raise CfError(rc, "cf_paged8_append")
+        return q_out
+
+    def attention(self, batch, n_tokens, max_q, q, q_start, kv_len, page_table, k_pages, v_pages,
+                  scales, out, lse=None, window=0, n_sinks=0, q_stride=None, stream=None):
+        """Causal attention over the sequences' pages (cf_paged8_attention)."""
+        c, i32 = self.cfg, self._int
+        qp, qs = self._rows(q, n_tokens, self._qrow, q_stride, "q")
+        rc = self._attention(
+            self.handle, batch, n_tokens, max_q, qp, qs,
+            self._at(q_start, i32, batch + 1, "q_start"), self._at(kv_len, i32, batch, "kv_len"),
+            self._at(page_table, i32, batch * c.max_pages, "page_table", c.max_pages),
+            self._pool(k_pages, "k_pages"), self._pool(v_pages, "v_pages"), self._scales(scales),
+            window, n_sinks, self._at(out, self._dtype, n_tokens * self._qrow, "out"),
+            self._at(lse, self._f32, n_tokens * c.n_q_heads, "lse"), self._on(stream))
+        if rc != CF_OK:
+            raise CfError(rc, "cf_paged8_attention")
+        return out
+
+    def prefix_attention(self, *args, **kw):
+        raise CfError(CF_ERR_UNSUPPORTED, "a shared prefix over a cache of 8-bit codes")
+
+    def read(self, batch, n_rows, row_start, first, page_table, k_pages, v_pages, scales, k_out,
+             v_out, out_stride=None, stream=None):
+        """Positions of the sequences as rows of the storage type
+        (cf_paged8_read); k_out or v_out may be None."""
+        c, i32 = self.cfg, self._int
+        kp, ks = self._rows(k_out, n_rows, self._kvrow, out_stride, "k_out")
+        vp, vs = self._rows(v_out, n_rows, self._kvrow, out_stride, "v_out")
+        if kp is not None and vp is not None and ks != vs and n_rows > 1:
+            raise CfError(CF_ERR_INVALID_ARG, "k_out and v_out have different row strides")
+        rc = self._read(
+            self.handle, batch, n_rows, self._at(row_start, i32, batch + 1, "row_start"),
+            self._at(first, i32, batch, "first"),
+            self._at(page_table, i32, batch * c.max_pages, "page_table", c.max_pages),
+            self._pool(k_pages, "k_pages"), self._pool(v_pages, "v_pages"), self._scales(scales),
+            kp, vp, vs if kp is None else ks, self._on(stream))
+        if rc != CF_OK:
+            raise CfError(rc, "cf_paged8_read")
+        return k_out, v_out
+
+    def status(self) -> int:
+        import torch
+        torch.cuda.synchronize(self._dev)
+        return lib().cf_paged8_get_status(self.handle)
+
+    def close(self) -> None:
+        if getattr(self, "handle", None):
+            lib().cf_paged8_destroy(self.handle)
+            self.handle = None

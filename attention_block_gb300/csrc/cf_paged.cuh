@@ -36,6 +36,7 @@ struct PagedAppendParams {
   PagedGeom g;
   const void *q, *k, *v;
   void *q_out, *k_pages, *v_pages;
+  float2* scales;  // of a cache of 8-bit codes
   int64_t q_stride, kv_stride, q_out_stride;
   const int *q_start, *kv_len, *rope_pos, *page_table;
   int* errflag;
@@ -47,6 +48,7 @@ struct PagedAppendParams {
 struct PagedAttnParams {
   PagedGeom g;
   const void *q, *k_pages, *v_pages;
+  const float2* scales;  // of a cache of 8-bit codes
   void* out;
   float* lse;
   int64_t q_stride;
@@ -497,7 +499,10 @@ inline bool launch_pdl(const void* fn, dim3 grid, int threads, int smem, cudaStr
 }
 
 // Host launchers (one translation unit each); false: the launch failed.
-bool paged_append_launch(int dtype, const PagedAppendParams& p, int sm_count, cudaStream_t st);
+// code: what the pages hold, kCodeNone (values) or a cf_code of cf_paged8.h.
+constexpr int kCodeNone = -1;
+bool paged_append_launch(int dtype, int code, const PagedAppendParams& p, int sm_count,
+                         cudaStream_t st);
 
 // The fp32 kernel.  grid: resident blocks, 0 on failure; part_rows: workspace;
 // a ticket per resident block and a word more.

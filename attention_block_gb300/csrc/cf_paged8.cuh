@@ -1,0 +1,96 @@
+// cf_paged8.cuh -- what the kernels of the paged cache of 8-bit codes share:
+// where scales lie, codes from values and back, and launch entry points
+// (include/cf_paged8.h).
+#pragma once
+
+#include "cf_paged.cuh"
+#include "cf_paged8.h"
+
+namespace cf {
+
+// Index of the scales of position j, KV head 0: a KV head's are page_size
+// apart.  The page must lie in the pool (paged_offset).
+__device__ __forceinline__ int64_t paged8_scale(const int* table, int j, const PagedGeom& g) {
+  return (((int64_t)table[j >> g.page_shift] * g.nkv) << g.page_shift) + (j & g.page_mask);
+}
+
+// Largest magnitude of a code.
+template <int CODE>
+constexpr float kCodeTop = CODE == CF_CODE_INT8 ? 127.f : 448.f;
+
+// Four codes of values that are within the codes' range.
+template <int CODE>
+__device__ __forceinline__ uint32_t code4(const float* f) {
+  if constexpr (CODE == CF_CODE_INT8) {
+    uint32_t w = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w |= (uint32_t)(__float2int_rn(f[e]) & 0xff) << (8 * e);
+    return w;
+  } else {
+    uint16_t lo, hi;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(f[1]), "f"(f[0]));
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(f[3]), "f"(f[2]));
+    return (uint32_t)lo | (uint32_t)hi << 16;
+  }
+}
+
+// Codes and scale of a head that LANES neighbouring lanes hold, 16 values each:
+// w[0] the codes of the first eight, w[1] of the others.
+template <int CODE, int LANES>
+__device__ __forceinline__ void quantise_head(const float (&f)[16], float& scale, uint2 (&w)[2]) {
+  const uint32_t group = (uint32_t)((1ull << LANES) - 1) << (threadIdx.x & 31 & ~(LANES - 1));
+  uint32_t top = 0;  // as whole numbers magnitudes are in order, NaN last
+#pragma unroll
+  for (int e = 0; e < 16; ++e) top = max(top, __float_as_uint(f[e]) & 0x7fffffffu);
+#pragma unroll
+  for (int d = LANES / 2; d >= 1; d >>= 1) top = max(top, __shfl_xor_sync(group, top, d));
+  const float amax = __uint_as_float(top);
+  const bool finite = top < 0x7f800000u, zero = amax < 0x1p-100f;
+  scale = finite ? (zero ? 0.f : amax / kCodeTop<CODE>) : __uint_as_float(0x7fc00000u);
+  const float inv = finite && !zero ? kCodeTop<CODE> / amax : 0.f;
+  float y[16];
+#pragma unroll
+  for (int e = 0; e < 16; ++e) y[e] = finite ? f[e] * inv : 0.f;
+  w[0] = make_uint2(code4<CODE>(y), code4<CODE>(y + 4));
+  w[1] = make_uint2(code4<CODE>(y + 8), code4<CODE>(y + 12));
+}
+
+// Four codes as two words of fp16 values: of codes 0 and 2, and of 1 and 3.
+// int8: whole.  e4m3: 2^-8 of the value (kCodeUnit), by moving the bits: the
+// subnormal codes become subnormal fp16 values, and none a NaN or infinity.
+template <int CODE>
+constexpr float kCodeUnit = CODE == CF_CODE_INT8 ? 1.f : 256.f;
+template <int CODE>
+__device__ __forceinline__ void code_halves(uint32_t w, uint32_t& even, uint32_t& odd) {
+  if constexpr (CODE == CF_CODE_INT8) {
+    // 1024 + (code + 128) is the fp16 with those low bits
+    const uint32_t u = w ^ 0x80808080u;
+    const __half2 bias = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
+    const uint32_t e = __byte_perm(u, 0x64646464u, 0x4240), o = __byte_perm(u, 0x64646464u, 0x4341);
+    const __half2 a = __hsub2(*reinterpret_cast<const __half2*>(&e), bias);
+    const __half2 b = __hsub2(*reinterpret_cast<const __half2*>(&o), bias);
+    even = *reinterpret_cast<const uint32_t*>(&a);
+    odd = *reinterpret_cast<const uint32_t*>(&b);
+  } else {
+    // seeeemmm -> s0eeeemm m0000000
+    even = ((w << 8) & 0x80008000u) | ((w << 7) & 0x3f803f80u);
+    odd = (w & 0x80008000u) | ((w >> 1) & 0x3f803f80u);
+  }
+}
+
+// Host launchers; false: the launch failed.
+struct Paged8ReadParams {
+  PagedGeom g;
+  const void *k_pages, *v_pages;
+  const float2* scales;
+  const int *row_start, *first, *page_table;
+  void *k_out, *v_out;
+  int64_t out_stride;
+  int* errflag;
+  int batch, n_rows;
+};
+bool paged8_read_launch(int dtype, int code, const Paged8ReadParams& p, int sm_count,
+                        cudaStream_t st);
+bool paged8_rows_launch(int dtype, int code, const PagedAttnParams& p, cudaStream_t st);
+
+}  // namespace cf

@@ -1,0 +1,116 @@
+// cf_paged8_read.cu -- positions of a cache of 8-bit codes back as rows of
+// fp16 or bf16 (cf_paged8_read).
+//
+// Bound by memory: per head d codes and a scale read, 2 d bytes written.  A
+// block takes a run of rows: a thread per row looks up where it lies (sequence
+// by bisection of the starts, page), then 16 codes at a time are expanded by
+// neighbouring threads.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+
+#include "cf_paged8.cuh"
+
+using namespace cf;
+
+namespace {
+
+constexpr int kReadThreads = 256;
+constexpr int kReadRows = 16;  // of a block
+
+template <typename T, int D, int CODE>
+__global__ void __launch_bounds__(kReadThreads)
+    paged8_read_kernel(const __grid_constant__ Paged8ReadParams p) {
+  constexpr int C = D / 16;  // 16-byte pieces of a head's codes
+  __shared__ int64_t s_code[kReadRows], s_scale[kReadRows];  // -1: zeros, -2: not a row
+  const int tid = threadIdx.x, r0 = blockIdx.x * kReadRows;
+  pdl_wait();
+  pdl_trigger();
+  if (blockIdx.x == 0)  // one block reports starts that are out of order
+    for (int b = tid; b < p.batch; b += kReadThreads)
+      if (!starts_ordered(p.row_start[b], p.row_start[b + 1], p.n_rows))
+        atomicOr(p.errflag, kDevErrPosRange);
+  if (tid < kReadRows) {
+    const int r = r0 + tid;
+    int64_t code = -2, scale = -2;
+    if (r < p.n_rows) {
+      // the last sequence whose start is at or before the row: those behind it
+      // begin later
+      int lo = 0, hi = p.batch;
+      while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (p.row_start[mid] <= r)
+          lo = mid + 1;
+        else
+          hi = mid;
+      }
+      const int b = lo - 1;
+      if (b >= 0) {
+        const int t0 = p.row_start[b], t1 = p.row_start[b + 1];
+        if (starts_ordered(t0, t1, p.n_rows) && r < t1) {
+          const long long j = (long long)(p.first ? p.first[b] : 0) + (r - t0);
+          if (j < 0 || j >= (long long)p.g.max_pages << p.g.page_shift) {
+            atomicOr(p.errflag, kDevErrPosRange);
+          } else {
+            const int* table = p.page_table + (int64_t)b * p.g.max_pages;
+            code = paged_offset(table, (int)j, p.g, p.errflag);
+            if (code >= 0) scale = paged8_scale(table, (int)j, p.g);
+          }
+        }
+      }
+    }
+    s_code[tid] = code;
+    s_scale[tid] = scale;
+  }
+  __syncthreads();
+  const int per_row = p.g.nkv * C;  // of K, and as many of V
+  for (int x = tid; x < kReadRows * 2 * per_row; x += kReadThreads) {
+    const int side = x / per_row, i = side >> 1, kv = side & 1, y = x - side * per_row;
+    const int h = y / C, c = y - h * C;
+    void* out = kv ? p.v_out : p.k_out;
+    const int64_t code = s_code[i];
+    if (out == nullptr || code == -2) continue;
+    uint4 w = make_uint4(0, 0, 0, 0);
+    float scale = 0.f;
+    if (code >= 0) {
+      w = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(kv ? p.v_pages : p.k_pages) +
+                                               code + (int64_t)h * p.g.head_stride + c * 16));
+      scale = __ldg((&p.scales[s_scale[i] + ((int64_t)h << p.g.page_shift)].x) + kv);
+    }
+    scale *= kCodeUnit<CODE>;
+    const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+    uint32_t o[8];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      uint32_t even, odd;
+      code_halves<CODE>(v[e], even, odd);
+      const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&even));
+      const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&odd));
+      o[2 * e] = pack2<T>(a.x * scale, b.x * scale);
+      o[2 * e + 1] = pack2<T>(a.y * scale, b.y * scale);
+    }
+    uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(out) + (int64_t)(r0 + i) * p.out_stride +
+                                          h * D + c * 16);
+    dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+    dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+  }
+}
+
+template <typename T, int D>
+const void* read_fn(int code) {
+  return code == CF_CODE_INT8 ? (const void*)&paged8_read_kernel<T, D, CF_CODE_INT8>
+                              : (const void*)&paged8_read_kernel<T, D, CF_CODE_E4M3>;
+}
+
+}  // namespace
+
+bool cf::paged8_read_launch(int dtype, int code, const Paged8ReadParams& p, int sm_count,
+                            cudaStream_t st) {
+  const void* fn = dtype == CF_F16 ? (p.g.D == 64 ? read_fn<__half, 64>(code)
+                                                  : read_fn<__half, 128>(code))
+                                   : (p.g.D == 64 ? read_fn<__nv_bfloat16, 64>(code)
+                                                  : read_fn<__nv_bfloat16, 128>(code));
+  Paged8ReadParams pp = p;
+  void* args[] = {&pp};
+  return launch_pdl(fn, dim3((p.n_rows + kReadRows - 1) / kReadRows), kReadThreads, 0, st, args);
+}
