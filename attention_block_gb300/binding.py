@@ -60,6 +60,11 @@ class CfPaged8Config(ctypes.Structure):
     _fields_ = [("cache", CfPagedConfig), ("code", ctypes.c_int32)]
 
 
+class CfW4Config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "in_features", "out_features", "group", "zeros", "max_rows", "dtype")]
+
+
 class CfLaunchInfo(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in (
         "cluster_size", "batch_tile", "group", "rows_per_wtile", "pos_per_ktile",
@@ -138,6 +143,11 @@ SIGNATURES = {
                        + [ctypes.c_int64, _vp]),
     "cf_paged8_get_status": (ctypes.c_int, [_vp]),
     "cf_paged8_destroy": (None, [_vp]),
+    "cf_w4_create": (ctypes.c_int, [ctypes.POINTER(CfW4Config), ctypes.POINTER(_vp)]),
+    "cf_w4_packed_bytes": (ctypes.c_size_t, [_vp]),
+    "cf_w4_pack": (ctypes.c_int, [_vp] * 6),
+    "cf_w4_matvec": (ctypes.c_int, [_vp, ctypes.c_int32, _vp, ctypes.c_int64] + [_vp] * 4),
+    "cf_w4_destroy": (None, [_vp]),
 }
 
 TIMELINE_SLOTS = 32
@@ -816,3 +826,110 @@ class Paged8Kv(PagedKv):
         if getattr(self, "handle", None):
             lib().cf_paged8_destroy(self.handle)
             self.handle = None
+
+
+# ------------------------------------------------------- weights of 4 bits --
+def cf_w4_create_rc(cfg: CfW4Config | None) -> tuple[int, int | None]:
+    """Return code and handle without raising (boundary tests)."""
+    h = _vp()
+    rc = lib().cf_w4_create(ctypes.byref(cfg) if cfg is not None else None, ctypes.byref(h))
+    return rc, h.value
+
+
+def make_w4_config(in_features, out_features, group=128, zeros=False, max_rows=1,
+                   dtype=CF_F16) -> CfW4Config:
+    if isinstance(dtype, str):
+        dtype = {"f32": CF_F32, "f16": CF_F16, "bf16": CF_BF16}[dtype]
+    return CfW4Config(int(in_features), int(out_features), int(group), int(zeros), int(max_rows),
+                      int(dtype))
+
+
+class W4Matvec:
+    """Owns one cf_w4_handle (include/cf_w4.h): products of up to max_rows rows
+    with weights of 4 bits, of any number of matrices of one shape.  Raises
+    CfError on any non-zero return code.
+
+    Tensors are checked for dtype, device, shape and dense rows; raw addresses
+    are taken as they are."""
+
+    def __init__(self, **cfg):
+        self.cfg = c = make_w4_config(**cfg)
+        rc, h = cf_w4_create_rc(c)
+        if rc != CF_OK:
+            raise CfError(rc, "cf_w4_create")
+        self.handle = h
+        import torch
+        self._dtype = {CF_F32: torch.float32, CF_F16: torch.float16, CF_BF16: torch.bfloat16}[
+            c.dtype]
+        self._dev = torch.cuda.current_device()
+        self._raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda d: torch.cuda.current_stream(d).cuda_stream)
+        self._matvec = lib().cf_w4_matvec
+        self.packed_bytes = lib().cf_w4_packed_bytes(h)
+
+    # Address of a dense tensor [at least n, cols] after checking it.
+    def _at(self, x, dtype, n, cols, what):
+        if x is None or isinstance(x, int):
+            return x
+        if x.dtype is dtype and x.get_device() == self._dev and x.is_contiguous() and \
+                x.dim() == 2 and x.shape[0] >= n and x.shape[1] == cols:
+            return x.data_ptr()
+        raise CfError(CF_ERR_INVALID_ARG, f"{what}: {x.dtype} {tuple(x.shape)} on {x.device}")
+
+    def _on(self, stream):
+        return self._raw_stream(self._dev) if stream is None else _stream(stream)
+
+    def pack(self, codes, scales, zeros=None, packed=None, stream=None):
+        """Lays out codes uint8 [K, N / 2], scales [K / group, N] and zeros uint8
+        [K / group, N] (cf_w4_pack); returns the packed weights, a uint8 tensor."""
+        import torch
+        c, u8 = self.cfg, torch.uint8
+        groups = c.in_features // c.group
+        if packed is None:
+            packed = torch.empty(self.packed_bytes, dtype=u8, device=f"cuda:{self._dev}")
+        rc = lib().cf_w4_pack(
+            self.handle, self._at(codes, u8, c.in_features, c.out_features // 2, "codes"),
+            self._at(scales, self._dtype, groups, c.out_features, "scales"),
+            self._at(zeros, u8, groups, c.out_features, "zeros"), self._packed(packed),
+            self._on(stream))
+        if rc != CF_OK:
+            raise CfError(rc, "cf_w4_pack")
+        return packed
+
+    def _packed(self, x):
+        if isinstance(x, int):
+            return x
+        if x.get_device() == self._dev and x.is_contiguous() and \
+                x.numel() * x.element_size() >= self.packed_bytes:
+            return x.data_ptr()
+        raise CfError(CF_ERR_INVALID_ARG, f"packed: {x.dtype} {tuple(x.shape)} on {x.device}")
+
+    def __call__(self, rows, x, packed, out, residual=None, x_stride=None, stream=None):
+        """out = x W (+ residual) for the first `rows` rows (cf_w4_matvec)."""
+        c = self.cfg
+        if not isinstance(x, int):
+            if x.dtype is not self._dtype or x.get_device() != self._dev or x.dim() != 2 or \
+                    x.shape[0] < rows or x.shape[1] != c.in_features or x.stride(1) != 1:
+                raise CfError(CF_ERR_INVALID_ARG, f"x: {x.dtype} {tuple(x.shape)} on {x.device}")
+            if not x_stride:  # the stride of a single row says nothing
+                x_stride = x.stride(0) if x.shape[0] > 1 else c.in_features
+            x = x.data_ptr()
+        rc = self._matvec(self.handle, rows, x, int(x_stride or c.in_features),
+                          self._packed(packed),
+                          self._at(residual, self._dtype, rows, c.out_features, "residual"),
+                          self._at(out, self._dtype, rows, c.out_features, "out"),
+                          self._on(stream))
+        if rc != CF_OK:
+            raise CfError(rc, "cf_w4_matvec")
+        return out
+
+    def close(self) -> None:
+        if getattr(self, "handle", None):
+            lib().cf_w4_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
