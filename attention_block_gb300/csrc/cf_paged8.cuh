@@ -93,4 +93,11 @@ bool paged8_read_launch(int dtype, int code, const Paged8ReadParams& p, int sm_c
                         cudaStream_t st);
 bool paged8_rows_launch(int dtype, int code, const PagedAttnParams& p, cudaStream_t st);
 
+// The kernel for few rows (tokens x grouped heads, at most kFewRows).  grid:
+// resident blocks, 0 on failure; its parts take as many rows as
+// paged_few_part_rows says.
+int paged8_few_grid(int dtype, int code, int head_dim, int sm_count);
+bool paged8_few_launch(int dtype, int code, const PagedAttnParams& p, const PagedSplit& ws,
+                       cudaStream_t st);
+
 }  // namespace cf

@@ -15,6 +15,7 @@ struct cf_paged8_handle : PagedHost {
   int code = 0;
   void* ws = nullptr;
   int* errflag = nullptr;
+  PagedSplit few;
 };
 
 extern "C" {
@@ -36,13 +37,29 @@ int cf_paged8_create(const cf_paged8_config* cfg, cf_paged8_handle** out) {
   if (rc != CF_OK) return fail(rc);
   h->code = cfg->code;
   size_t bytes = 256;
+  auto take = [&](size_t n) {
+    const size_t at = bytes;
+    bytes += (n + 255) & ~(size_t)255;
+    return at;
+  };
+  // The words that start at zero, then the states of split items.
+  const cf_paged_config& c = h->cfg;
+  h->few.grid = paged8_few_grid(c.dtype, h->code, c.head_dim, h->sm_count);
+  if (h->few.grid == 0) return fail(CF_ERR_CUDA);
+  const size_t tickets = take(4 * (size_t)c.max_batch * c.n_kv_heads);
+  const size_t zero = bytes;
+  const long long rows = paged_few_part_rows(h->few.grid);
+  const size_t at_o = take((size_t)rows * c.head_dim * 4), at_ml = take((size_t)rows * 8);
   if (cudaMalloc(&h->ws, bytes) != cudaSuccess) {
     cudaGetLastError();
     h->ws = nullptr;
     return fail(CF_ERR_CUDA);
   }
-  if (!clear(h->ws, bytes)) return fail(CF_ERR_CUDA);
-  h->errflag = static_cast<int*>(h->ws);
+  if (!clear(h->ws, zero)) return fail(CF_ERR_CUDA);
+  uint8_t* ws = static_cast<uint8_t*>(h->ws);
+  h->errflag = reinterpret_cast<int*>(ws);
+  h->few.parts = {reinterpret_cast<float*>(ws + at_o), reinterpret_cast<float2*>(ws + at_ml), rows, 0};
+  h->few.tickets = reinterpret_cast<int*>(ws + tickets);
   *out = h;
   return CF_OK;
 }
@@ -81,7 +98,10 @@ int cf_paged8_attention(cf_paged8_handle* h, int32_t batch, int32_t n_tokens, in
                                       kv_len, page_table, nullptr, 0, k_pages, v_pages, scales,
                                       window, n_sinks, out, lse, p);
   if (rc != CF_OK || p.n_tokens == 0) return rc;
-  if (!paged8_rows_launch(h->cfg.dtype, h->code, p, static_cast<cudaStream_t>(stream))) {
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (!((int64_t)p.max_q * p.g.G <= kFewRows
+            ? paged8_few_launch(h->cfg.dtype, h->code, p, h->few, st)
+            : paged8_rows_launch(h->cfg.dtype, h->code, p, st))) {
     cudaGetLastError();
     return CF_ERR_CUDA;
   }
