@@ -56,10 +56,7 @@ __device__ __forceinline__ void quantise_head(const float (&f)[16], float& scale
 }
 
 // Four codes as two words of fp16 values: of codes 0 and 2, and of 1 and 3.
-// int8: whole.  e4m3: 2^-8 of the value (kCodeUnit), by moving the bits: the
-// subnormal codes become subnormal fp16 values, and none a NaN or infinity.
-template <int CODE>
-constexpr float kCodeUnit = CODE == CF_CODE_INT8 ? 1.f : 256.f;
+// Both are exact; an e4m3 NaN becomes a NaN.
 template <int CODE>
 __device__ __forceinline__ void code_halves(uint32_t w, uint32_t& even, uint32_t& odd) {
   if constexpr (CODE == CF_CODE_INT8) {
@@ -72,10 +69,43 @@ __device__ __forceinline__ void code_halves(uint32_t w, uint32_t& even, uint32_t
     even = *reinterpret_cast<const uint32_t*>(&a);
     odd = *reinterpret_cast<const uint32_t*>(&b);
   } else {
-    // seeeemmm -> s0eeeemm m0000000
-    even = ((w << 8) & 0x80008000u) | ((w << 7) & 0x3f803f80u);
-    odd = (w & 0x80008000u) | ((w >> 1) & 0x3f803f80u);
+    const uint32_t t = __byte_perm(w, 0u, 0x3120);
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, lo;\n\tcvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
+        : "=r"(even), "=r"(odd)
+        : "r"(t));
   }
+}
+
+// The same of codes 0 and 1, and of 2 and 3.
+template <int CODE>
+__device__ __forceinline__ void code_row4(uint32_t w, uint32_t& first, uint32_t& last) {
+  if constexpr (CODE == CF_CODE_INT8) {
+    const uint32_t u = w ^ 0x80808080u;
+    const __half2 bias = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
+    const uint32_t e = __byte_perm(u, 0x64646464u, 0x4140), o = __byte_perm(u, 0x64646464u, 0x4342);
+    const __half2 a = __hsub2(*reinterpret_cast<const __half2*>(&e), bias);
+    const __half2 b = __hsub2(*reinterpret_cast<const __half2*>(&o), bias);
+    first = *reinterpret_cast<const uint32_t*>(&a);
+    last = *reinterpret_cast<const uint32_t*>(&b);
+  } else {
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %2;\n\t"
+        "cvt.rn.f16x2.e4m3x2 %0, lo;\n\tcvt.rn.f16x2.e4m3x2 %1, hi;\n\t}"
+        : "=r"(first), "=r"(last)
+        : "r"(w));
+  }
+}
+
+// log2 x and 1 / x, off by a few ulp (log2 by 2^-22 near 1).
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 // Host launchers; false: the launch failed.
@@ -91,7 +121,6 @@ struct Paged8ReadParams {
 };
 bool paged8_read_launch(int dtype, int code, const Paged8ReadParams& p, int sm_count,
                         cudaStream_t st);
-bool paged8_rows_launch(int dtype, int code, const PagedAttnParams& p, cudaStream_t st);
 
 // The kernel for few rows (tokens x grouped heads, at most kFewRows).  grid:
 // resident blocks, 0 on failure; its parts take as many rows as
@@ -99,5 +128,13 @@ bool paged8_rows_launch(int dtype, int code, const PagedAttnParams& p, cudaStrea
 int paged8_few_grid(int dtype, int code, int head_dim, int sm_count);
 bool paged8_few_launch(int dtype, int code, const PagedAttnParams& p, const PagedSplit& ws,
                        cudaStream_t st);
+
+
+// The kernel for many rows; its parts take as many rows as paged_tc_part_rows
+// says, and its list of items paged8_tc_list_bytes.
+int paged8_tc_grid(int dtype, int code, int head_dim, int sm_count);
+size_t paged8_tc_list_bytes(int grid);
+bool paged8_tc_launch(int dtype, int code, const PagedAttnParams& p, const PagedSplit& ws,
+                      cudaStream_t st);
 
 }  // namespace cf

@@ -15,7 +15,7 @@ struct cf_paged8_handle : PagedHost {
   int code = 0;
   void* ws = nullptr;
   int* errflag = nullptr;
-  PagedSplit few;
+  PagedSplit few, tc;
 };
 
 extern "C" {
@@ -48,7 +48,14 @@ int cf_paged8_create(const cf_paged8_config* cfg, cf_paged8_handle** out) {
   if (h->few.grid == 0) return fail(CF_ERR_CUDA);
   const size_t tickets = take(4 * (size_t)c.max_batch * c.n_kv_heads);
   const size_t zero = bytes;
-  const long long rows = paged_few_part_rows(h->few.grid);
+  long long rows = paged_few_part_rows(h->few.grid);
+  size_t list = 0;
+  if ((int64_t)c.max_tokens * h->geom.G > kFewRows) {
+    h->tc.grid = paged8_tc_grid(c.dtype, h->code, c.head_dim, h->sm_count);
+    if (h->tc.grid == 0) return fail(CF_ERR_CUDA);
+    list = take(paged8_tc_list_bytes(h->tc.grid));
+    rows = std::max(rows, paged_tc_part_rows(h->tc.grid));
+  }
   const size_t at_o = take((size_t)rows * c.head_dim * 4), at_ml = take((size_t)rows * 8);
   if (cudaMalloc(&h->ws, bytes) != cudaSuccess) {
     cudaGetLastError();
@@ -58,7 +65,9 @@ int cf_paged8_create(const cf_paged8_config* cfg, cf_paged8_handle** out) {
   if (!clear(h->ws, zero)) return fail(CF_ERR_CUDA);
   uint8_t* ws = static_cast<uint8_t*>(h->ws);
   h->errflag = reinterpret_cast<int*>(ws);
-  h->few.parts = {reinterpret_cast<float*>(ws + at_o), reinterpret_cast<float2*>(ws + at_ml), rows, 0};
+  h->few.parts = h->tc.parts = {reinterpret_cast<float*>(ws + at_o),
+                                reinterpret_cast<float2*>(ws + at_ml), rows, 0};
+  h->tc.list = ws + list;
   h->few.tickets = reinterpret_cast<int*>(ws + tickets);
   *out = h;
   return CF_OK;
@@ -101,7 +110,7 @@ int cf_paged8_attention(cf_paged8_handle* h, int32_t batch, int32_t n_tokens, in
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (!((int64_t)p.max_q * p.g.G <= kFewRows
             ? paged8_few_launch(h->cfg.dtype, h->code, p, h->few, st)
-            : paged8_rows_launch(h->cfg.dtype, h->code, p, st))) {
+            : paged8_tc_launch(h->cfg.dtype, h->code, p, h->tc, st))) {
     cudaGetLastError();
     return CF_ERR_CUDA;
   }

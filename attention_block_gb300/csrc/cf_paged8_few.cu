@@ -34,19 +34,20 @@ using namespace cf;
 
 namespace {
 
-constexpr int kFew8Warps = 8;  // one block per SM
-constexpr int kFew8Threads = kFew8Warps * 32;
-constexpr int KS = 32;         // positions of a unit
+constexpr int KS = 32;  // positions of a unit
 
+// One block per SM.
 template <int D, int NT>
 struct Shape8 {
+  static constexpr int WARPS = NT == 1 ? 12 : 8, THREADS = 32 * WARPS;
   static constexpr int SLOT = KS * D;              // bytes of a unit's K or V
-  static constexpr int PAIRS = D == 128 ? 2 : 4;   // units whose K and V are on their way
+  static constexpr int PAIRS = D == 128 ? NT : 2;   // units whose K and V are on their way
   static constexpr int SCALES = KS * 8;
-  static constexpr int RING = PAIRS * (2 * SLOT + SCALES);
+  static constexpr int PREP = KS * 16;             // what the weights take of a unit's scales
+  static constexpr int RING = PAIRS * (2 * SLOT + SCALES) + PREP;
   static constexpr int ROWS = 8 * NT * D * 4;      // o of a part
   static constexpr int WARP = RING + ROWS;
-  static constexpr int SMEM = kFew8Warps * WARP;
+  static constexpr int SMEM = WARPS * WARP;
   static_assert(ROWS <= PAIRS * 2 * SLOT && SMEM <= 220 * 1024, "shared memory");
 };
 
@@ -57,16 +58,6 @@ struct Few8Args {
   int row_limit;  // rows per item, at most
 };
 
-__device__ __forceinline__ float lg2(float x) {
-  float y;
-  asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-__device__ __forceinline__ float rcp(float x) {
-  float y;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 __device__ __forceinline__ uint4 lds16(uint32_t at) {
   uint4 w;
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
@@ -82,27 +73,29 @@ __device__ __forceinline__ void cp8(uint32_t dst, const void* src, bool there) {
 }
 
 template <typename T, int D, int CODE, int NT>
-__global__ void __launch_bounds__(kFew8Threads, 1)
+__global__ void __launch_bounds__(Shape8<D, NT>::THREADS, 1)
     paged8_few_kernel(const __grid_constant__ Few8Args a) {
   using S = Shape8<D, NT>;
   using M = MmaKind<__half>;
   constexpr int MT = KS / 16;     // key tiles of a unit
   constexpr int NH = D / 64;      // 64-element pieces of a head
   constexpr int NJ = D / 16;      // 16-column tiles of o
-  constexpr int PAIRS = S::PAIRS;
+  constexpr int PAIRS = S::PAIRS, WARPS = S::WARPS, THREADS = S::THREADS;
   constexpr int LIFT = weight_lift<__half>(0);
   const PagedAttnParams& p = a.p;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ long long s_first[kFew8Threads];  // first unit of each thread's sequences
-  __shared__ long long s_scan[kFew8Warps];
-  __shared__ int s_top[kFew8Warps];
-  __shared__ uint32_t s_valid[kFew8Warps][PAIRS];
+  __shared__ long long s_first[THREADS];  // first unit of each thread's sequences
+  __shared__ long long s_scan[WARPS];
+  __shared__ int s_top[WARPS];
   // per warp: the part of an item that began before its run (F), and of one
   // that goes on behind it (L; if it also began before, there is no F)
-  __shared__ FewItem s_item[2][kFew8Warps];
-  __shared__ float2 s_ml[2][kFew8Warps][kFewRows];
-  __shared__ int s_has[2][kFew8Warps];
+  __shared__ FewItem s_item[2][WARPS];
+  __shared__ float2 s_ml[2][WARPS][kFewRows];
+  __shared__ int s_has[2][WARPS];
   __shared__ int s_last[2];
+  // each warp's place, and that of its copies, ahead of it: too much for
+  // registers.  One lane moves them on.
+  __shared__ Cursor<KS, false> s_cur[WARPS], s_ld[WARPS];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int gq = lane >> 2, tq = lane & 3;
 
@@ -111,7 +104,7 @@ __global__ void __launch_bounds__(kFew8Threads, 1)
 
   // Units of every sequence, summed up over the batch: each thread has a run
   // of sequences.
-  const int per = (p.batch + kFew8Threads - 1) / kFew8Threads;
+  const int per = (p.batch + THREADS - 1) / THREADS;
   long long mine = 0;
   int top = 0;  // units of the longest item
   for (int b = tid * per; b < min(p.batch, (tid + 1) * per); ++b) {
@@ -133,14 +126,14 @@ __global__ void __launch_bounds__(kFew8Threads, 1)
   __syncthreads();
   long long before = incl - mine, total = 0;
 #pragma unroll
-  for (int w = 0; w < kFew8Warps; ++w) {
+  for (int w = 0; w < WARPS; ++w) {
     if (w < warp) before += s_scan[w];
     total += s_scan[w];
     top = max(top, s_top[w]);
   }
   s_first[tid] = before;
   const long long block_upc =
-      div_units(total + gridDim.x * kFew8Warps - 1, gridDim.x * kFew8Warps) * kFew8Warps;
+      div_units(total + gridDim.x * WARPS - 1, gridDim.x * WARPS) * WARPS;
   if (lane == 0) s_has[0][warp] = s_has[1][warp] = 0;
   __syncthreads();
 
@@ -149,7 +142,7 @@ __global__ void __launch_bounds__(kFew8Threads, 1)
     // the last run of sequences that begins at or before unit u
     int n = 0;
 #pragma unroll
-    for (int i = 0; i < kFew8Threads / 32; ++i)
+    for (int i = 0; i < THREADS / 32; ++i)
       n += __popc(__ballot_sync(~0u, s_first[i * 32 + lane] <= u));
     long long at = s_first[n - 1];
     int b = (n - 1) * per;
@@ -170,42 +163,46 @@ __global__ void __launch_bounds__(kFew8Threads, 1)
   // This block's units.  Where items are short, by themselves or beside a
   // block's share, a block takes the items that begin in its share, whole:
   // one item more at most, and nothing to join across blocks.
-  Cursor<KS, false> cur;
+  Cursor<KS, false> at;
   long long lo = min(total, blockIdx.x * block_upc), hi = min(total, lo + block_upc);
   const bool snap =
       block_upc >= 3LL * top && (top <= 16 + 2 * a.row_limit || block_upc >= 8LL * top);
   if (snap) {
     if (lo < total) {
-      locate(cur, lo);
-      if (cur.tile) lo = cur.i0 + cur.w.tiles;
+      locate(at, lo);
+      if (at.tile) lo = at.i0 + at.w.tiles;
     }
     if (hi < total) {
-      locate(cur, hi);
-      if (cur.tile) hi = cur.i0 + cur.w.tiles;
+      locate(at, hi);
+      if (at.tile) hi = at.i0 + at.w.tiles;
     }
   }
   if (lo >= hi) return;
   // and this warp's run of them
-  const int run = (int)((hi - lo + kFew8Warps - 1) / kFew8Warps);
-  cur.u = lo + (long long)warp * run;
-  cur.end = min(hi, cur.u + run);
-  if (cur.u < cur.end) locate(cur, cur.u);
+  const int run = (int)((hi - lo + WARPS - 1) / WARPS);
+  at.u = lo + (long long)warp * run;
+  at.end = min(hi, at.u + run);
+  if (at.u < at.end) locate(at, at.u);
+  Cursor<KS, false>&cur = s_cur[warp], &ld = s_ld[warp];
+  if (lane == 0) cur = ld = at;
+  __syncwarp();
 
-  const char* kbase = static_cast<const char*>(p.k_pages);
-  const char* vbase = static_cast<const char*>(p.v_pages);
   uint8_t* mem = smem + warp * S::WARP;
   const uint32_t ring_s = smem_u32(mem);
-  const uint32_t scale_s = ring_s + PAIRS * 2 * S::SLOT;
+  const uint32_t scale_s = ring_s + PAIRS * 2 * S::SLOT, prep_s = scale_s + PAIRS * S::SCALES;
 
-  Cursor<KS, false> ld = cur;  // runs ahead of cur
-
-  // The page of this lane's position in the tile that ld stands on, fetched
-  // one tile before its copies are issued.
+  // The unit whose copies are next: ld stands on its item's first one in this
+  // run or on the one itself, ld_tile and ld_left say which, and how many units
+  // of the item are left to this run.
+  int ld_tile = ld.tile, ld_left = 0;
+  if (ld.u < ld.end) ld_left = (int)min((long long)(ld.w.tiles - ld.tile), ld.end - ld.u);
+  // The page of this lane's position in it, fetched one unit before its copies
+  // are issued.
   int ld_pos = -1, ld_page = -1;
   auto fetch_page = [&]() {
     ld_pos = -1;
-    if (ld.u >= ld.end) return;
-    const int j = ld.w.base(ld.tile) + lane;
+    if (ld_left == 0) return;
+    const int j = ld.w.base(ld_tile) + lane;
     if (!ld.w.sees(j)) return;
     ld_pos = j;
     ld_page = __ldg(p.page_table + (int64_t)ld.b * p.g.max_pages + (j >> p.g.page_shift));
@@ -216,29 +213,29 @@ __global__ void __launch_bounds__(kFew8Threads, 1)
   constexpr int C = D / 16;   // chunks of a row
   constexpr int RP = 32 / C;  // rows of one copy instruction
   const int r0 = lane / C, c0 = lane % C;
-  const uint32_t k0 = r0 * D + ((D == 128 ? c0 ^ ((r0 & 1) << 2) : c0) << 4);
-  const uint32_t v0 = r0 * D + ((D == 128 ? c0 ^ r0 : c0 ^ ((r0 >> 1) & 3)) << 4);
-  const int64_t ss = p.g.slot_stride;
+  const uint32_t k0 = ring_s + r0 * D + ((D == 128 ? c0 ^ ((r0 & 1) << 2) : c0) << 4);
+  const uint32_t v0 =
+      ring_s + S::SLOT + r0 * D + ((D == 128 ? c0 ^ r0 : c0 ^ ((r0 >> 1) & 3)) << 4);
+  const char* kbase = static_cast<const char*>(p.k_pages);
+  const char* vbase = static_cast<const char*>(p.v_pages);
+  const int64_t step = RP * p.g.slot_stride, own = r0 * p.g.slot_stride + c0 * 16;
   const bool octets = p.g.page_shift >= 3;
   auto copy = [&](uint32_t d, bool values, const char* src, int64_t off) {
     // the swizzle of a later row of the same lane (D = 128: rows 4 apart)
-    auto turn = [&](int row) { return values && D == 128 ? (uint32_t)((row & 4) << 4) : 0u; };
+    const uint32_t d4 = values && D == 128 ? d ^ 64u : d;
     if (octets && __all_sync(~0u, off >= 0)) {
       // eight consecutive positions lie in one page: one lookup serves them
 #pragma unroll
       for (int y = 0; y < KS / 8; ++y) {
-        const char* at = src + __shfl_sync(~0u, off, 8 * y) + r0 * ss + c0 * 16;
-#pragma unroll
-        for (int z = 0; z < 8 / RP; ++z) {
-          cp16((d + (8 * y + z * RP) * D) ^ turn(z * RP), at);
-          at += RP * ss;
-        }
+        const char* at = src + (__shfl_sync(~0u, off, 8 * y) + own);
+        cp16(d + 8 * y * D, at);
+        if constexpr (RP == 4) cp16(d4 + (8 * y + 4) * D, at + step);
       }
     } else {
 #pragma unroll
       for (int i = 0; i < KS / RP; ++i) {
         const int64_t o = __shfl_sync(~0u, off, i * RP + r0);
-        cp16((d + i * RP * D) ^ turn(i * RP), src + (o >= 0 ? o + c0 * 16 : 0), o >= 0);
+        cp16((i * RP & 4 ? d4 : d) + i * RP * D, src + (o >= 0 ? o + c0 * 16 : 0), o >= 0);
       }
     }
   };
@@ -246,7 +243,7 @@ __global__ void __launch_bounds__(kFew8Threads, 1)
   bool v_some = false;
   auto issue_k = [&](int pair) {
     v_some = false;
-    if (ld.u < ld.end) {
+    if (ld_left) {
       v_off = -1;  // no copy: zeros
       int64_t sc = 0;
       if (ld_pos >= 0) {
@@ -259,17 +256,31 @@ __global__ void __launch_bounds__(kFew8Threads, 1)
           sc = (((int64_t)ld_page * p.g.nkv + ld.h) << p.g.page_shift) + slot;
         }
       }
-      const uint32_t valid = __ballot_sync(~0u, ld_pos >= 0);
-      if (lane == 0) s_valid[warp][pair] = valid;
-      v_some = valid != 0;
-      const int ob = ld.b, oh = ld.h;
-      ld.next(p);
+      v_some = ld.w.hi > ld.w.lo;  // (a sequence without keys has one tile)
+      bool other = false;
+      if (--ld_left) {
+        ++ld_tile;
+      } else {
+        __syncwarp();
+        if (lane == 0) {
+          const int passed = ld_tile - ld.tile;
+          ld.u += passed;
+          ld.tile = ld_tile;
+          ld.next(p);
+        }
+        __syncwarp();
+        if (ld.u < ld.end) {
+          ld_tile = ld.tile;
+          ld_left = (int)min((long long)(ld.w.tiles - ld.tile), ld.end - ld.u);
+          other = true;
+        }
+      }
       fetch_page();
       if (v_some) {
         cp8(scale_s + pair * S::SCALES + lane * 8, p.scales + sc, v_off >= 0);
-        copy(ring_s + 2 * pair * S::SLOT + k0, false, kbase, v_off);
+        copy(k0 + 2 * pair * S::SLOT, false, kbase, v_off);
       }
-      if (ld.u < ld.end && (ld.b != ob || ld.h != oh)) {  // the next item's queries
+      if (other) {  // the next item's queries
         const int row = lane * 64 / D, i = row / p.g.G;
         if (row < ld.w.n * p.g.G)
           prefetch_line(static_cast<const T*>(p.q) + (int64_t)(ld.w.t0 + i) * p.q_stride +
@@ -279,7 +290,7 @@ __global__ void __launch_bounds__(kFew8Threads, 1)
     cp_commit();
   };
   auto issue_v = [&](int pair) {
-    if (v_some) copy(ring_s + (2 * pair + 1) * S::SLOT + v0, true, vbase, v_off);
+    if (v_some) copy(v0 + 2 * pair * S::SLOT, true, vbase, v_off);
     cp_commit();
   };
 
@@ -295,13 +306,13 @@ __global__ void __launch_bounds__(kFew8Threads, 1)
   float o[NT][NJ][4], m[NT][2], l[NT][2];
   int pos[NT][2];  // positions of rows 8 nt + 2 tq and + 1: this thread's
   float qk = 0.f;  // what q.k is multiplied by beside the key's scale
-  bool fresh = true;
-  int first_tile = cur.tile;
+  int tile = 0, left = 0;  // of the item: the unit in work, units left to this run
 
   while (cur.u < cur.end) {
     const int nrows = cur.w.n * p.g.G;
-    if (fresh) {
-      fresh = false;
+    if (left == 0) {
+      tile = cur.tile;
+      left = (int)min((long long)(cur.w.tiles - tile), cur.end - cur.u);
       uint32_t top2 = 0;  // bf16: largest finite magnitude of the rows, as bits
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
@@ -359,26 +370,37 @@ __global__ void __launch_bounds__(kFew8Threads, 1)
               qf[nt][k][x] = pack2<__half>(f[0] * up, f[1] * up);
             }
       }
-      qk = back * p.scale_log2 * kCodeUnit<CODE>;
+      qk = back * p.scale_log2;
     }
     cp_wait<2 * PAIRS - 1>();  // K and the scales have landed
     __syncwarp();
-    const uint32_t valid = s_valid[warp][pair];
+    const bool some = cur.w.hi > cur.w.lo;
     const uint32_t ks = ring_s + 2 * pair * S::SLOT, vs = ks + S::SLOT;
+    const int j0 = cur.w.base(tile);
     float c[MT][NT][4];
-    float2 sc[MT][2];  // scales of keys gq and gq + 8 of a tile
-    if (valid) {
+    uint32_t odd = 0;  // positions with a value scale of NaN
+    if (some) {
+      {  // each lane's position: a, b, 1 / vs
+        const bool there = cur.w.sees(j0 + lane);
+        float k, v;
+        asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];"
+                     : "=f"(k), "=f"(v)
+                     : "r"(scale_s + pair * S::SCALES + lane * 8));
+        odd = __ballot_sync(~0u, there && v != v);
+        // (zero: the codes are zero too, and any scale will do; fmaxf takes a
+        // NaN for the bound)
+        const float vv = v == 0.f ? 0x1p-7f : fmaxf(v, 0x1p-60f);
+        const float ak = there ? k * qk : 0.f, bk = there ? lg2(vv) : -INFINITY;
+        asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(prep_s + lane * 16), "f"(ak),
+                     "f"(bk), "f"(rcp(vv)), "f"(0.f)
+                     : "memory");
+      }
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 4; ++e) c[mt][nt][e] = 0.f;
-#pragma unroll
-        for (int r = 0; r < 2; ++r)
-          asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];"
-                       : "=f"(sc[mt][r].x), "=f"(sc[mt][r].y)
-                       : "r"(scale_s + pair * S::SCALES + (mt * 16 + 8 * r + gq) * 8));
 #pragma unroll
         for (int hf = 0; hf < NH; ++hf) {
           const uint32_t at = ks + (mt * 16 + gq) * D +
@@ -400,14 +422,12 @@ __global__ void __launch_bounds__(kFew8Threads, 1)
     __syncwarp();  // K and the scales are read before their next copies are issued
     issue_k(pair);
     uint32_t pf[MT][NT][2];
-    if (valid) {
+    if (some) {
       // mask, running maximum
-      const int j0 = cur.w.base(cur.tile);
       const bool edge =  // do the rows see different parts of this tile?
           cur.w.n > 1 && (j0 + KS - 1 > cur.w.p0 ||
                           (p.window != 0 && cur.w.p0 + cur.w.n - 1 - j0 >= p.window));
       float inv[MT][2];  // 1 / vs
-      bool odd = false;  // a value scale of NaN
       float mx[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
@@ -419,22 +439,16 @@ __global__ void __launch_bounds__(kFew8Threads, 1)
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           const int jj = mt * 16 + 8 * r + gq;
-          const bool there = (valid >> jj) & 1;
-          const float v = sc[mt][r].y;
-          odd |= there && v != v;
-          // (zero: the codes are zero too, and any scale will do; fmaxf takes a
-          // NaN for the bound)
-          const float vv = v == 0.f ? 0x1p-7f : fmaxf(v, 0x1p-60f);
-          const float ak = sc[mt][r].x * qk, bk = lg2(vv);
-          inv[mt][r] = rcp(vv);
+          const uint4 w = lds16(prep_s + jj * 16);
+          const float ak = __uint_as_float(w.x), bk = __uint_as_float(w.y);
+          inv[mt][r] = __uint_as_float(w.z);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              bool see = there;
-              if (edge) see = see && paged_visible(pos[nt][e], j0 + jj, p.window, p.n_sinks);
               float& x = c[mt][nt][2 * r + e];
-              x = see ? fmaf(x, ak, bk) : -INFINITY;
+              x = fmaf(x, ak, bk);
+              if (edge && !paged_visible(pos[nt][e], j0 + jj, p.window, p.n_sinks)) x = -INFINITY;
               mx[nt][e] = fmaxf(mx[nt][e], x);
             }
         }
@@ -473,13 +487,13 @@ __global__ void __launch_bounds__(kFew8Threads, 1)
             x = ex2(x - mx[nt][e & 1]);
             l[nt][e & 1] = fmaf(x, inv[mt][e >> 1], l[nt][e & 1]);
           }
-      if (__any_sync(~0u, odd)) {  // a value of NaN: for the rows that see it
+      if (odd) {  // a value of NaN: for the rows that see it
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
             const int jj = mt * 16 + 8 * r + gq;
-            if (!((valid >> jj) & 1) || sc[mt][r].y == sc[mt][r].y) continue;
+            if (!((odd >> jj) & 1)) continue;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -499,7 +513,7 @@ __global__ void __launch_bounds__(kFew8Threads, 1)
     }
     cp_wait<2 * PAIRS - 1>();  // V has landed
     __syncwarp();
-    if (valid) {
+    if (some) {
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -524,14 +538,13 @@ __global__ void __launch_bounds__(kFew8Threads, 1)
     issue_v(pair);
     if (++pair == PAIRS) pair = 0;
 
-    const bool item_done = cur.tile + 1 == cur.w.tiles;
-    if (!item_done && cur.u + 1 < cur.end) {
-      cur.next(p);
+    if (--left) {
+      ++tile;
       continue;
     }
 
     // ---- the warp's part of the item is complete
-    const bool begins = first_tile == 0;
+    const bool begins = cur.tile == 0, item_done = tile + 1 == cur.w.tiles;
     constexpr float back = 1.f / (1 << LIFT);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -544,7 +557,7 @@ __global__ void __launch_bounds__(kFew8Threads, 1)
 #pragma unroll
       for (int k = 0; k < NJ; ++k)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[nt][k][e] *= back * kCodeUnit<CODE>;
+        for (int e = 0; e < 4; ++e) o[nt][k][e] *= back;
     }
     FewItem it;
     it.i0 = cur.i0;
@@ -601,9 +614,13 @@ __global__ void __launch_bounds__(kFew8Threads, 1)
         paged_store4<T, D>(none, p.out, p.lse, out_row(p, it, x / (D / 4)), x % (D / 4) * 4);
       }
     }
-    cur.next(p);
-    fresh = true;
-    first_tile = cur.tile;
+    __syncwarp();
+    if (lane == 0) {
+      cur.u += tile - cur.tile;
+      cur.tile = tile;
+      cur.next(p);
+    }
+    __syncwarp();
   }
   cp_wait<0>();
   __syncthreads();
@@ -615,7 +632,7 @@ __global__ void __launch_bounds__(kFew8Threads, 1)
   FewItem cut[2];                 // items that go on in other blocks: the first's, the last's
   bool has_cut[2] = {false, false};
   int task = 0;
-  for (int w0 = 0, k0 = 0; w0 < kFew8Warps;) {
+  for (int w0 = 0, k0 = 0; w0 < WARPS;) {
     if (!s_has[k0][w0]) {
       w0 += k0;
       k0 ^= 1;
@@ -623,7 +640,7 @@ __global__ void __launch_bounds__(kFew8Threads, 1)
     }
     const FewItem it = s_item[k0][w0];
     int last = w0, kind = k0;  // of the item's last part in this block
-    while (kind == 1 && last + 1 < kFew8Warps) {
+    while (kind == 1 && last + 1 < WARPS) {
       ++last;
       kind = s_has[0][last] ? 0 : 1;
     }
@@ -633,7 +650,7 @@ __global__ void __launch_bounds__(kFew8Threads, 1)
     const int nrows = it.n * p.g.G, col = (lane % C4) * 4;
     for (int row0 = 0; row0 < nrows; row0 += 32 / C4, ++task) {
       const int row = row0 + lane / C4;
-      if (task % kFew8Warps != warp || row >= nrows) continue;
+      if (task % WARPS != warp || row >= nrows) continue;
       PagedState4 s{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
       for (int w = w0; w <= last; ++w) {
         const int k = w == last ? kind : 1;
@@ -654,7 +671,7 @@ __global__ void __launch_bounds__(kFew8Threads, 1)
       has_cut[here ? 1 : 0] = true;
     }
     // on to what follows that part: after an F its warp's L, if any
-    w0 = kind == 0 ? last : kFew8Warps;
+    w0 = kind == 0 ? last : WARPS;
     k0 = 1;
   }
   if (!(has_cut[0] || has_cut[1])) return;
@@ -675,7 +692,7 @@ __global__ void __launch_bounds__(kFew8Threads, 1)
   for (int i = 0; i < 2; ++i) {
     if (!s_last[i]) continue;
     const PagedItemParts parts(cut[i].i0, cut[i].tiles, block_upc);
-    for (int x = tid; x < cut[i].n * p.g.G * C4; x += kFew8Threads) {
+    for (int x = tid; x < cut[i].n * p.g.G * C4; x += THREADS) {
       const int row = x / C4, col = (x - row * C4) * 4;
       PagedState4 s{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
       paged_join_row<D>(s, a.ws.o, a.ws.ml, PagedRowParts(parts, kFewRows, row, -1), col);
@@ -686,14 +703,14 @@ __global__ void __launch_bounds__(kFew8Threads, 1)
 
 struct Few8Fn {
   const void* main;
-  int smem;
+  int threads, smem;
 };
 template <typename T, int D, int NT>
 Few8Fn few8_code(int code) {
   return Few8Fn{code == CF_CODE_INT8
                     ? (const void*)&paged8_few_kernel<T, D, CF_CODE_INT8, NT>
                     : (const void*)&paged8_few_kernel<T, D, CF_CODE_E4M3, NT>,
-                Shape8<D, NT>::SMEM};
+                Shape8<D, NT>::THREADS, Shape8<D, NT>::SMEM};
 }
 template <typename T>
 Few8Fn few8_d(int code, int d, int rows) {
@@ -728,5 +745,5 @@ bool cf::paged8_few_launch(int dtype, int code, const PagedAttnParams& p, const 
   a.row_limit = std::min(kFewRows, p.max_q * p.g.G);
   const Few8Fn f = few8_fn(dtype, code, p.g.D, a.row_limit);
   void* args[] = {&a};
-  return launch_pdl(f.main, dim3(ws.grid), kFew8Threads, f.smem, st, args);
+  return launch_pdl(f.main, dim3(ws.grid), f.threads, f.smem, st, args);
 }

@@ -77,8 +77,7 @@ __global__ void __launch_bounds__(kReadThreads)
                                                code + (int64_t)h * p.g.head_stride + c * 16));
       scale = __ldg((&p.scales[s_scale[i] + ((int64_t)h << p.g.page_shift)].x) + kv);
     }
-    scale *= kCodeUnit<CODE>;
-    const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+      const uint32_t v[4] = {w.x, w.y, w.z, w.w};
     uint32_t o[8];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
