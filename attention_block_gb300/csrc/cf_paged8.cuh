@@ -108,6 +108,13 @@ __device__ __forceinline__ float rcp(float x) {
   return y;
 }
 
+// 8 bytes global -> shared, asynchronously; zeros where there is no source.
+__device__ __forceinline__ void cp8(uint32_t dst, const void* src, bool there) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src),
+               "r"(there ? 8 : 0)
+               : "memory");
+}
+
 // Host launchers; false: the launch failed.
 struct Paged8ReadParams {
   PagedGeom g;

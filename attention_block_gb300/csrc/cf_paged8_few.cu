@@ -65,13 +65,6 @@ __device__ __forceinline__ uint4 lds16(uint32_t at) {
                : "r"(at));
   return w;
 }
-// 8 bytes global -> shared, asynchronously; zeros where there is no source.
-__device__ __forceinline__ void cp8(uint32_t dst, const void* src, bool there) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src),
-               "r"(there ? 8 : 0)
-               : "memory");
-}
-
 template <typename T, int D, int CODE, int NT>
 __global__ void __launch_bounds__(Shape8<D, NT>::THREADS, 1)
     paged8_few_kernel(const __grid_constant__ Few8Args a) {

@@ -13,15 +13,24 @@
 //
 // Roles of a block's 16 warps:
 //   0-3, 4-7  softmax of half 0 / 1, a thread per row
-//   8-11      codes of K and V: from global memory into registers, a tile
-//             ahead, then as fp16 into the swizzled tiles; a, b, c of a tile's
-//             positions
+//   8-11      codes of K and V: copied into shared memory ahead (cp.async, each
+//             thread what it will read itself), then as fp16 into the swizzled
+//             tiles; a, b, c of a tile's positions
 //   12        one thread issues S = Q K^T and O += P V
 //   13-15     queries: copied, and where they are bf16 turned into fp16 in
 //             place, a row that would leave fp16's range times a power of two
 // What a row does not see gets a weight of exactly 0, and codes are finite, so
 // nothing that lies in a slot reaches a row that does not see it; a NaN among
 // a tile's value scales is set in the weights of the rows that see it.
+//
+// 512 tokens behind 15872 (32 / 8 heads of 128): 180 us, 750 TFLOP/s; 4 chunks of
+// 257-1024 tokens behind 0-2049, 32 heads: 222.  Bound by the softmax: it is busy
+// for 4000 of a unit's 6100 cycles (2050 of them products), waiting on shared
+// memory for the positions' a, b, c.  Accumulator fragments, with which a thread
+// needs a quarter of them, take 186 and 316 us (205 and 272 in two passes of 32
+// columns each): their chains are longer.  code x scale rounded to fp16 as
+// operand, with powers of two alone in the softmax, takes 163 and 215, but puts
+// 2.7 times the error of an fp16 result on it.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -37,12 +46,15 @@ namespace {
 template <int D>
 struct Tc8Shape {
   static constexpr int TILE = kBN * D * 2;         // bytes of a K, V or Q tile
-  static constexpr int SLOTS = D == 128 ? 4 : 8;   // K and V tiles
-  static constexpr int SMEM = (2 + SLOTS) * TILE;  // 1024-aligned
-  // The scales of a tile are written when its K gets a slot, SLOTS / 2 tiles
-  // after the one that had it.  That one's scores are complete then, and so is
-  // the softmax of the tile in front of it.
-  static constexpr int BUFS = SLOTS / 2 + 1;
+  static constexpr int SLOTS = D == 128 ? 3 : 7;  // K and V tiles
+  static constexpr int RAW = D == 128 ? 3 : 6;    // tiles of codes on their way
+  static constexpr int SMEM = (2 + SLOTS) * TILE + RAW * kBN * D;  // 1024-aligned
+  // The scales of tile j are written when its K has a slot.  With an odd number
+  // of slots that was V's of tile j - (SLOTS + 1) / 2: the products with it are
+  // complete, and so is that tile's softmax.
+  static constexpr int BUFS = (SLOTS + 1) / 2;
+  static_assert(SLOTS % 2 == 1, "K takes V's slot");
+  static constexpr int AHEAD = RAW / 2 + 2;  // units whose scales are on their way
   static constexpr uint32_t S_COL = 0, O_COL = 2 * kBN;  // TMEM columns
 };
 
@@ -84,6 +96,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   __shared__ __align__(8) uint64_t s_sfull[2], s_pfull[2], s_ofull[2];
   __shared__ uint32_t s_tmem;
   __shared__ __align__(16) Tc8Scales s_scale[S::BUFS];
+  __shared__ __align__(8) float2 s_raw[S::AHEAD][kBN];  // scales on their way
   __shared__ float s_qf[2][2 * kHalf];  // what a row's queries were divided by; items take turns
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t sq = smem_u32(sm);                   // Q, two tiles
@@ -431,23 +444,34 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const uint32_t x0 = (uint32_t)((2 * c0) & 7);
     const char* kbase = static_cast<const char*>(p.k_pages) + c0 * 16;
     const char* vbase = static_cast<const char*>(p.v_pages) + c0 * 16;
-    uint4 w[NP];  // pieces on their way
-    // Loads piece i of the rows that lie at the lanes' offsets; -1: zeros.
-    auto load = [&](int i, const char* src, int64_t off) {
-      const int64_t o = __shfl_sync(~0u, off, i * RP + r0);
-      w[i] = make_uint4(0, 0, 0, 0);
-      if (o >= 0) w[i] = __ldg(reinterpret_cast<const uint4*>(src + o));
+    // A ring of tiles of codes.  A thread reads what it copied itself: its own
+    // groups of copies are all that it waits for.
+    const uint32_t raw = skv + S::SLOTS * S::TILE + (tid - 256) * 16;
+    // Copies the pieces of the rows that lie at the lanes' offsets; -1: zeros.
+    auto load = [&](int r, const char* src, int64_t off) {
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        const int64_t o = __shfl_sync(~0u, off, i * RP + r0);
+        cp16(raw + (r * NP + i) * (kCopyThreads * 16), src + (o >= 0 ? o : 0), o >= 0);
+      }
     };
-    auto store = [&](int i, uint32_t slot) {
-      uint32_t h[8];
-      code_row4<CODE>(w[i].x, h[0], h[1]);
-      code_row4<CODE>(w[i].y, h[2], h[3]);
-      code_row4<CODE>(w[i].z, h[4], h[5]);
-      code_row4<CODE>(w[i].w, h[6], h[7]);
-      const uint32_t row = d0 + slot * S::TILE + i * RP * 128, sw = (uint32_t)((i * RP + r0) & 7);
-      const uint32_t lo = row + ((x0 ^ sw) << 4), hi = row + (((x0 + 1) ^ sw) << 4);
-      sts16(lo, h[0], h[1], h[2], h[3]);
-      sts16(hi, h[4], h[5], h[6], h[7]);
+    auto convert = [&](int r, uint32_t slot) {
+      uint32_t c[NP][4];  // all of them first: a store might be to what a load behind it reads
+#pragma unroll
+      for (int i = 0; i < NP; ++i)
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(c[i][0]), "=r"(c[i][1]), "=r"(c[i][2]), "=r"(c[i][3])
+                     : "r"(raw + (r * NP + i) * (kCopyThreads * 16)));
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        uint32_t h[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) code_row4<CODE>(c[i][e], h[2 * e], h[2 * e + 1]);
+        const uint32_t row = d0 + slot * S::TILE + i * RP * 128;
+        const uint32_t sw = (uint32_t)((i * RP + r0) & 7);
+        sts16(row + ((x0 ^ sw) << 4), h[0], h[1], h[2], h[3]);
+        sts16(row + (((x0 + 1) ^ sw) << 4), h[4], h[5], h[6], h[7]);
+      }
     };
     // The page of this lane's position, looked up one tile ahead of its loads.
     int f_pos = -1, f_page = 0;
@@ -459,56 +483,62 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       f_pos = j;
       f_page = __ldg(p.page_table + (int64_t)cur.t.b * p.g.max_pages + (j >> p.g.page_shift));
     };
-    // This lane's offset in the pools and its scales, of the unit that cur
-    // stands on; then cur moves on.
-    int64_t off = -1;
-    float2 scale = make_float2(0.f, 0.f);
-    auto place = [&]() {
-      off = -1;
-      scale = make_float2(0.f, 0.f);
-      if (f_pos >= 0) {
-        if ((unsigned)f_page >= (unsigned)p.g.num_pages) {
-          atomicOr(err, kDevErrPosRange);
-        } else {
-          const int slot = f_pos & p.g.page_mask;
-          off = (int64_t)f_page * p.g.page_stride + (int64_t)slot * p.g.slot_stride +
-                (int64_t)cur.h * p.g.head_stride;
-          scale = __ldg(p.scales + ((((int64_t)f_page * p.g.nkv + cur.h) << p.g.page_shift) + slot));
+    // K and V of the units in turn, RAW tiles ahead of their conversion; cur runs
+    // with the copies.
+    int64_t off = -1;     // of this lane's position in the unit whose copies are next
+    bool value = false;   // its V is next
+    int in = 0, in_unit = 0, left = 0;  // ring places; tiles to be converted
+    const int row = lw * 32 + lane;
+    auto issue = [&]() {
+      if (value) {
+        load(in, vbase, off);
+        value = false;
+        ++left;
+        if (++in == S::RAW) in = 0;
+      } else if (cur.u < u1) {
+        off = -1;
+        const float2* scale = p.scales;
+        if (f_pos >= 0) {
+          if ((unsigned)f_page >= (unsigned)p.g.num_pages) {
+            atomicOr(err, kDevErrPosRange);
+          } else {
+            const int slot = f_pos & p.g.page_mask;
+            off = (int64_t)f_page * p.g.page_stride + (int64_t)slot * p.g.slot_stride +
+                  (int64_t)cur.h * p.g.head_stride;
+            scale += (((int64_t)f_page * p.g.nkv + cur.h) << p.g.page_shift) + slot;
+          }
         }
+        __syncwarp();
+        if (lane == 0) cur.next(p, u1);
+        __syncwarp();
+        look_up();
+        cp8(smem_u32(&s_raw[in_unit][row]), scale, off >= 0);
+        if (++in_unit == S::AHEAD) in_unit = 0;
+        load(in, kbase, off);
+        value = true;
+        ++left;
+        if (++in == S::RAW) in = 0;
       }
-      __syncwarp();
-      if (lane == 0) cur.next(p, u1);
-      __syncwarp();
-      look_up();
+      cp_commit();
     };
     RingPos ring(0, S::SLOTS);
     uint32_t use = 0;  // slots taken so far
-    int buf = 0;
-    auto slot_free = [&]() {
+    int buf = 0, out = 0, out_unit = 0;
+    look_up();
+#pragma unroll 1
+    for (int i = 0; i < S::RAW; ++i) issue();
+#pragma unroll 1
+    for (bool key = true; left > 0; key = !key) {
+      cp_wait<S::RAW - 1>();
       if (use >= S::SLOTS) wait_bar(&s_empty[ring.slot], ring.phase ^ 1u, err);
       ++use;
-    };
-    auto slot_full = [&]() {
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&s_full[ring.slot]);
-      ring.next(S::SLOTS);
-    };
-    bool more = cur.u < u1;
-    look_up();
-    if (more) {
-      place();
-#pragma unroll
-      for (int i = 0; i < NP; ++i) load(i, kbase, off);
-    }
-    while (more) {
-      slot_free();
-      {
+      if (key) {
         // (zero: the codes are zero too, and any scale will do; fmaxf takes a
         // NaN for the bound)
+        const float2 scale = s_raw[out_unit][row];
+        if (++out_unit == S::AHEAD) out_unit = 0;
         const float v = scale.y, vv = v == 0.f ? 0x1p-7f : fmaxf(v, 0x1p-60f);
         Tc8Scales& sc = s_scale[buf];
-        const int row = lw * 32 + lane;
         sc.a[row] = scale.x * p.scale_log2;
         sc.b[row] = lg2(vv);
         sc.c[row] = rcp(vv);
@@ -516,22 +546,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (lane == 0) sc.odd[lw] = odd;
         if (++buf == S::BUFS) buf = 0;
       }
-#pragma unroll
-      for (int i = 0; i < NP; ++i) {
-        store(i, ring.slot);
-        load(i, vbase, off);
-      }
-      slot_full();
-      more = cur.u < u1;  // a unit behind this one
-      slot_free();
-      if (more) place();
-#pragma unroll
-      for (int i = 0; i < NP; ++i) {
-        store(i, ring.slot);
-        if (more) load(i, kbase, off);
-      }
-      slot_full();
+      convert(out, ring.slot);
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s_full[ring.slot]);
+      ring.next(S::SLOTS);
+      if (++out == S::RAW) out = 0;
+      --left;
+      issue();
     }
+    cp_wait<0>();
   } else if (warp > 12) {
     // ------------------------------------------------------------ queries --
     set_regs_down<56>();
