@@ -147,6 +147,7 @@ SIGNATURES = {
     "cf_w4_packed_bytes": (ctypes.c_size_t, [_vp]),
     "cf_w4_pack": (ctypes.c_int, [_vp] * 6),
     "cf_w4_matvec": (ctypes.c_int, [_vp, ctypes.c_int32, _vp, ctypes.c_int64] + [_vp] * 4),
+    "cf_w4_get_status": (ctypes.c_int, [_vp]),
     "cf_w4_destroy": (None, [_vp]),
 }
 
@@ -922,6 +923,11 @@ class W4Matvec:
         if rc != CF_OK:
             raise CfError(rc, "cf_w4_matvec")
         return out
+
+    def status(self) -> int:
+        import torch
+        torch.cuda.synchronize(self._dev)
+        return lib().cf_w4_get_status(self.handle)
 
     def close(self) -> None:
         if getattr(self, "handle", None):

@@ -21,8 +21,8 @@
  * Conventions: CF_OK or a negative CF_ERR_* code of cf.h, nothing is printed;
  * calls enqueue work on `stream` and return, never allocate or synchronize, and
  * may be captured in a CUDA graph.  The device current at cf_w4_create must be
- * current at every call.  A handle holds its sizes and no state of a call: one
- * handle serves any number of matrices of its shape, streams and threads.
+ * current at every call.  A handle holds its sizes, an error word and no state of a
+ * call: one handle serves any number of matrices of its shape, streams and threads.
  */
 #ifndef CF_W4_H
 #define CF_W4_H
@@ -70,6 +70,10 @@ int cf_w4_pack(cf_w4_handle* h, const uint8_t* codes, const void* scales, const 
  *   out       [rows, N]  dense; must not overlap another input (CF_ERR_ALIAS) */
 int cf_w4_matvec(cf_w4_handle* h, int32_t rows, const void* x, int64_t x_stride,
                  const void* packed, const void* residual, void* out, void* stream);
+
+/* Read and clear the device-side error word (synchronize the stream first):
+ * CF_OK, CF_ERR_DEVICE_TIMEOUT (a wait that ran out) or CF_ERR_CUDA. */
+int cf_w4_get_status(cf_w4_handle* h);
 
 /* NULL is a no-op. */
 void cf_w4_destroy(cf_w4_handle* h);

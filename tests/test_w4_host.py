@@ -16,7 +16,8 @@ def test_every_declared_function_is_exported_and_bound():
     text = open(os.path.join(ROOT, "include", "cf_w4.h")).read()
     text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
     names = set(re.findall(r"\b(cf_w4_[a-z_]+)\s*\(", text))
-    assert {"cf_w4_create", "cf_w4_packed_bytes", "cf_w4_pack", "cf_w4_matvec", "cf_w4_destroy"} == names
+    assert {"cf_w4_create", "cf_w4_packed_bytes", "cf_w4_pack", "cf_w4_matvec", "cf_w4_get_status",
+            "cf_w4_destroy"} == names
     for n in names:
         assert hasattr(binding.lib(), n) and n in binding.SIGNATURES
 
@@ -38,4 +39,5 @@ def test_null_arguments():
     assert lib.cf_w4_packed_bytes(None) == 0
     assert lib.cf_w4_pack(*([None] * 6)) == INVALID
     assert lib.cf_w4_matvec(None, 1, None, 0, *([None] * 4)) == INVALID
+    assert lib.cf_w4_get_status(None) == INVALID
     lib.cf_w4_destroy(None)
