@@ -7,23 +7,25 @@
 // 128 + c (bf16) by setting bits, and c - zero by one exact subtraction; a
 // group's sum is scaled in fp32.
 //
-// A record holds 64 columns x 128 elements of k.  Its codes: for each block of
-// 16 columns and each 64 of k, a 16-byte vector per lane, word s the A fragment
-// of step s.  Lane (g, t) of step s stands for columns g and g + 8 and for
-// k = 32 (s / 2) + 8 t + 4 (s % 2) + 0..3: any order of k will do as long as x
-// follows it, and in this one a lane's x are 16-byte vectors and no step mixes
-// two groups.  Of a word, nibble i and nibble i + 4 are the two halves of the
-// fragment's register i.  Behind the codes the groups' scales, then their
-// zeros, columns g and g + 8 of a block side by side.
+// A record holds 16 columns x 128 elements of k.  Its codes: for each 64 of k a
+// 16-byte vector per lane, word s the A fragment of step s.  Lane (g, t) of step
+// s stands for columns g and g + 8 and for k = 32 (s / 2) + 8 t + 4 (s % 2) + 0..3:
+// any order of k will do as long as x follows it, and in this one a lane's x are
+// 16-byte vectors and no step mixes two groups.  Of a word, nibble i and nibble
+// i + 4 are the two halves of the fragment's register i.  Behind the codes the
+// groups' scales, then what is subtracted for their zeros, as 16-bit floats,
+// columns g and g + 8 side by side.  Records of
+// neighbouring columns lie one after another, then the next 128 of k.
 //
-// Bound by the weights' bytes for few rows.  A block takes a tile of 64 columns,
-// or a part of its k; its eight warps take the records in turn, each through a
-// ring of its own that bulk copies fill (records lie one after another), so no
-// warp waits for another before the sums are joined.  Within a record a warp has
-// four independent chains of products, and its x serve four blocks of columns.
-// Where tiles are few, k is split over the blocks of a cluster, which exchange
-// their sums through distributed shared memory; all sums are joined in a fixed
-// order.
+// Bound by the weights' bytes for few rows.  The columns, in blocks of 16, are
+// shared evenly over as many thread blocks as the SMs hold, so all of them end at
+// about one time; one takes its columns four blocks at a time.  Its eight warps
+// take k in turn, each through a ring of its own that bulk copies fill ahead, over
+// the next columns too, so no warp waits for another before the sums are joined.
+// Within a step a warp has up to four independent chains of products, and its x
+// serve them all.  Where columns are few, k is split over the blocks of a
+// cluster, which exchange their sums through distributed shared memory; all sums
+// are joined in a fixed order.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -41,31 +43,39 @@ using namespace cf;
 namespace {
 
 constexpr int kUnitK = 128;   // elements of k of a record
-constexpr int kTileN = 64;    // columns of a record
-constexpr int kCodeBytes = kUnitK * kTileN / 2;
+constexpr int kBlockN = 16;   // columns of a record
+constexpr int kCodeBytes = kUnitK * kBlockN / 2;
 constexpr int kW4Threads = 256;
 
 struct W4Shape {
   int K, N, group, zeros, es;
-  int units, tiles;       // records along k and along n
+  int half;               // fp16 operands, else bf16
+  int units, blocks;      // records along k and along n
   int record;             // bytes
   __host__ __device__ int groups() const { return kUnitK / group; }  // of a record
 };
 
 // ------------------------------------------------------------------- layout --
-__global__ void __launch_bounds__(kW4Threads)
+// The 16-bit float that is subtracted from a code of a column with this zero:
+// fp16, columns g (0) and g + 8 (1) of a block, or bf16.
+__host__ __device__ constexpr uint32_t zero_half(bool half, uint32_t zero, int column) {
+  return !half ? 0x4300u + zero : column == 0 ? 0x6400u + zero : 0x5400u + (zero << 4);
+}
+
+constexpr int kPackThreads = 128;
+__global__ void __launch_bounds__(kPackThreads)
     w4_pack_kernel(W4Shape s, const uint8_t* codes, const uint8_t* scales, const uint8_t* zeros,
                    uint8_t* packed) {
-  const int unit = blockIdx.x % s.units, tile = blockIdx.x / s.units;
+  const int unit = blockIdx.x / s.blocks, block = blockIdx.x - unit * s.blocks;
   uint8_t* out = packed + (int64_t)blockIdx.x * s.record;
   pdl_wait();
-  for (int w = threadIdx.x; w < kCodeBytes / 4; w += kW4Threads) {
-    const int step = w & 3, lane = (w >> 2) & 31, half = (w >> 7) & 1, block = w >> 8;
+  for (int w = threadIdx.x; w < kCodeBytes / 4; w += kPackThreads) {
+    const int step = w & 3, lane = (w >> 2) & 31, half = w >> 7;
     const int g = lane >> 2, t = lane & 3;
     uint32_t word = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {  // register i & 3, its low (i < 4) or high half
-      const int n = tile * kTileN + block * 16 + g + 8 * (i & 1);
+      const int n = block * kBlockN + g + 8 * (i & 1);
       const int k = unit * kUnitK + half * 64 + 32 * (step >> 1) + 8 * t + 4 * (step & 1) +
                     2 * ((i >> 1) & 1) + (i >> 2);
       uint32_t c = 0;
@@ -74,12 +84,12 @@ __global__ void __launch_bounds__(kW4Threads)
     }
     reinterpret_cast<uint32_t*>(out)[w] = word;
   }
-  // scales and zeros: place x of a group is column (x / 16) * 16 + (x % 16) / 2 + 8 (x % 2)
-  const int places = s.groups() * kTileN;
-  for (int e = threadIdx.x; e < places; e += kW4Threads) {
-    const int x = e % kTileN;
-    const int n = tile * kTileN + (x & ~15) + ((x & 15) >> 1) + 8 * (x & 1);
-    const int k = unit * kUnitK + (e / kTileN) * s.group;
+  // scales and zeros: place x of a group is column x / 2 + 8 (x % 2)
+  const int places = s.groups() * kBlockN;
+  for (int e = threadIdx.x; e < places; e += kPackThreads) {
+    const int x = e % kBlockN;
+    const int n = block * kBlockN + (x >> 1) + 8 * (x & 1);
+    const int k = unit * kUnitK + (e / kBlockN) * s.group;
     const bool there = n < s.N && k < s.K;
     const int64_t at = (int64_t)(k / s.group) * s.N + n;
     if (s.es == 2)
@@ -88,7 +98,9 @@ __global__ void __launch_bounds__(kW4Threads)
     else
       reinterpret_cast<uint32_t*>(out + kCodeBytes)[e] =
           there ? reinterpret_cast<const uint32_t*>(scales)[at] : 0u;
-    if (s.zeros) out[kCodeBytes + places * s.es + e] = there ? zeros[at] & 15u : 0;
+    if (s.zeros)
+      reinterpret_cast<uint16_t*>(out + kCodeBytes + places * s.es)[e] =
+          (uint16_t)zero_half(s.half, there ? zeros[at] & 15u : 0u, x & 1);
   }
 }
 
@@ -99,8 +111,36 @@ struct W4Type;
 template <>
 struct W4Type<__half> {
   using M = MmaKind<__half>;
+  // M::mma onto zero
+  static __device__ __forceinline__ void first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                               uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+  }
   static constexpr uint32_t kBias = 0x64006400u;  // 1024, ulp 1
   static constexpr int PARTS = 1;
+  // The fragment of a word; z: bias + zero of columns g and g + 8.  Nibbles 1
+  // and 3 stay four bits up, as 1024 + 16 c, and one fused operation takes the
+  // sixteenth and subtracts.
+  static __device__ __forceinline__ void fragment(uint32_t w, const uint32_t (&z)[2],
+                                                  uint32_t (&A)[4]) {
+    const uint32_t v = w >> 8;
+    A[0] = sub((w & 0x000f000fu) | kBias, z[0]);
+    A[1] = sub16((w & 0x00f000f0u) | kBias, z[1]);
+    A[2] = sub((v & 0x000f000fu) | kBias, z[0]);
+    A[3] = sub16((v & 0x00f000f0u) | kBias, z[1]);
+  }
+  static constexpr bool kHalf = true;
+  static __device__ __forceinline__ uint32_t sub16(uint32_t a, uint32_t b) {
+    const uint32_t sixteenth = 0x2c002c00u;
+    const __half2 r = __hfma2(*reinterpret_cast<__half2*>(&a),
+                              *reinterpret_cast<const __half2*>(&sixteenth),
+                              __hneg2(*reinterpret_cast<__half2*>(&b)));
+    return *reinterpret_cast<const uint32_t*>(&r);
+  }
   static __device__ __forceinline__ uint32_t sub(uint32_t a, uint32_t b) {
     const __half2 r = __hsub2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
     return *reinterpret_cast<const uint32_t*>(&r);
@@ -109,8 +149,22 @@ struct W4Type<__half> {
 template <>
 struct W4Type<__nv_bfloat16> {
   using M = MmaKind<__nv_bfloat16>;
+  static __device__ __forceinline__ void first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0,
+                                               uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+        "{%8, %9}, {%10, %10, %10, %10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+  }
   static constexpr uint32_t kBias = 0x43004300u;  // 128, ulp 1
   static constexpr int PARTS = 1;
+  static __device__ __forceinline__ void fragment(uint32_t w, const uint32_t (&z)[2],
+                                                  uint32_t (&A)[4]) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) A[e] = sub(((w >> (4 * e)) & 0x000f000fu) | kBias, z[e & 1]);
+  }
+  static constexpr bool kHalf = false;
   static __device__ __forceinline__ uint32_t sub(uint32_t a, uint32_t b) {
     const __nv_bfloat162 r =
         __hsub2(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&b));
@@ -130,6 +184,7 @@ struct W4Args {
   int64_t x_stride;
   int* errflag;
   int rows, split;
+  int shares;  // column shares: blocks of the grid without the split
 };
 
 // Two neighbouring elements in fp32.
@@ -148,9 +203,10 @@ __device__ __forceinline__ void load_cvt2(const T* p, float (&f)[2]) {
 template <typename T>
 struct XFrag {
   uint32_t w[W4Type<T>::PARTS][4];
-  __device__ __forceinline__ void load(const T* at, bool there) {
+  __device__ __forceinline__ void load(const T* at, bool there = true) {
     if constexpr (sizeof(T) == 2) {
-      const uint4 v = there ? *reinterpret_cast<const uint4*>(at) : make_uint4(0, 0, 0, 0);
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (there) v = __ldg(reinterpret_cast<const uint4*>(at));
       w[0][0] = v.x;
       w[0][1] = v.y;
       w[0][2] = v.z;
@@ -159,7 +215,8 @@ struct XFrag {
       float f[8];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const float4 v = there ? reinterpret_cast<const float4*>(at)[i] : make_float4(0, 0, 0, 0);
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (there) v = __ldg(reinterpret_cast<const float4*>(at) + i);
         f[4 * i] = v.x;
         f[4 * i + 1] = v.y;
         f[4 * i + 2] = v.z;
@@ -186,7 +243,6 @@ struct XFrag {
 constexpr int kWarps = kW4Threads / 32;
 constexpr int kStages = 2;     // records of a warp's ring
 constexpr int kMaxSplit = 8;
-constexpr int kPitch = kTileN + 4;  // of a row of sums
 
 // Asks for n bytes (a multiple of 16) to be brought to L2.
 __device__ __forceinline__ void prefetch_l2(const void* at, uint32_t n) {
@@ -198,192 +254,233 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr) {
   return v;
 }
 
-// Block `blockIdx.x % split` of its cluster takes its share of the records of
-// tile blockIdx.x / split.  With 64 rows the sums of a tile are too many for a
-// warp: two warps share a record, each with two blocks of columns.
+// How many thread blocks of w4_kernel<T, NT> an SM holds, and how many blocks of
+// columns a warp has sums of at a time.
 template <typename T, int NT>
-__global__ void __launch_bounds__(kW4Threads, NT * W4Type<T>::PARTS <= 2 ? 2 : 1)
+constexpr int kPerSm = NT * W4Type<T>::PARTS <= 2 ? 2 : 1;
+template <int NT>
+constexpr int kWide = NT <= 4 ? 4 : 2;
+
+// Block `blockIdx.x % split` of its cluster takes its share of k for column
+// share blockIdx.x / split.
+template <typename T, int NT>
+__global__ void __launch_bounds__(kW4Threads, kPerSm<T, NT>)
     w4_kernel(const __grid_constant__ W4Args a) {
   using W = W4Type<T>;
-  constexpr int BL = NT <= 4 ? 4 : 2;          // blocks of columns of a warp
-  constexpr int STREAMS = kWarps * BL / 4;     // records that are in work
-  constexpr bool AHEAD = NT * W::PARTS <= 2;   // there are registers for x ahead
+  constexpr int BL = kWide<NT>;
+  constexpr bool AHEAD = NT * W::PARTS <= 2;  // there are registers for x ahead
+  constexpr int kPitch = BL * kBlockN + 4;    // of a row of sums
+  constexpr int kRows = 8 * NT;
   extern __shared__ __align__(128) uint8_t ring[];
   __shared__ __align__(8) uint64_t s_full[kWarps][kStages];
   const W4Shape& s = a.s;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-  const int tile = blockIdx.x / a.split, part = blockIdx.x - tile * a.split;
-  const int u0 = (int)((long long)s.units * part / a.split);
+  const int share = blockIdx.x / a.split, part = blockIdx.x - share * a.split;
+  const int u0 = (int)((long long)s.units * part / a.split) + warp;
   const int u1 = (int)((long long)s.units * (part + 1) / a.split);
-  const int first = u0 + warp % STREAMS;                    // this warp's records
-  const int n = first < u1 ? (u1 - first + STREAMS - 1) / STREAMS : 0;
-  const int b0 = BL == 4 ? 0 : warp / STREAMS * BL;         // and blocks
-  constexpr int kPart = BL * 1024;                          // bytes of their codes
-  const int extra = s.record - kCodeBytes;                  // of scales and zeros
-  const int slot_bytes = kPart + extra;
-  const uint8_t* stream = a.packed + ((int64_t)tile * s.units + first) * s.record;
+  const int n = u0 < u1 ? (u1 - u0 + kWarps - 1) / kWarps : 0;  // this warp's steps along k
+  const int c0 = (int)((long long)s.blocks * share / a.shares);
+  const int c1 = (int)((long long)s.blocks * (share + 1) / a.shares);
+  // the columns in passes of nearly equal width
+  const int passes = (c1 - c0 + BL - 1) / BL;
+  auto pass_at = [&](int i) { return c0 + (c1 - c0) * i / passes; };
+  const int slot_bytes = BL * s.record;
   uint8_t* mem = ring + warp * kStages * slot_bytes;
-  const int64_t stride = (int64_t)STREAMS * s.record;
+  float* sums = reinterpret_cast<float*>(ring + kWarps * kStages * slot_bytes);
+  const int64_t stride = (int64_t)s.blocks * s.record;  // from a unit to the next
+  const uint64_t policy = policy_evict_first();
+
+  // Copies run ahead of the products: the next one's pass and step, its records,
+  // and which of the ring's slots it takes.
+  int in_pass = 0, in_step = 0, in = 0, in_bytes;
+  const uint8_t* in_at;
+  auto in_begin = [&]() {
+    const int b = pass_at(in_pass);
+    in_bytes = (pass_at(in_pass + 1) - b) * s.record;
+    in_at = a.packed + u0 * stride + (int64_t)b * s.record;
+  };
+  auto copy = [&](bool hint) {  // by one lane
+    if (hint) {
+      prefetch_l2(in_at, in_bytes);
+    } else {
+      mbar_arrive_expect_tx(&s_full[warp][in], in_bytes);
+      bulk_load_1d(mem + in * slot_bytes, in_at, in_bytes, &s_full[warp][in], policy);
+      if (++in == kStages) in = 0;
+    }
+    in_at += kWarps * stride;
+    if (++in_step == n) {
+      in_step = 0;
+      if (++in_pass < passes) in_begin();
+    }
+  };
+  const int total = n * passes;
   if (lane == 0) {
     for (int i = 0; i < kStages; ++i) mbar_init(&s_full[warp][i], 1);
     fence_mbar_init_cluster();
     // what lies in L2 is what memory holds: this may run ahead of the launch in front
-    if (b0 == 0)
-      for (int i = 0; i < min(n, 2 * kStages); ++i) prefetch_l2(stream + i * stride, s.record);
+    in_begin();
+    for (int i = 0; i < min(total, 2 * kStages); ++i) copy(true);
+    in_pass = in_step = 0;
+    in_begin();
   }
   __syncwarp();
   pdl_wait();
   pdl_trigger();
-  const uint64_t policy = policy_evict_first();
-  auto copy = [&](int i) {  // by one lane
-    const int slot = i % kStages;
-    const uint8_t* rec = stream + i * stride;
-    mbar_arrive_expect_tx(&s_full[warp][slot], slot_bytes);
-    if (BL == 4) {
-      bulk_load_1d(mem + slot * slot_bytes, rec, slot_bytes, &s_full[warp][slot], policy);
-    } else {
-      bulk_load_1d(mem + slot * slot_bytes, rec + b0 * 1024, kPart, &s_full[warp][slot], policy);
-      bulk_load_1d(mem + slot * slot_bytes + kPart, rec + kCodeBytes, extra, &s_full[warp][slot],
-                   policy);
-    }
-  };
   if (lane == 0)
-    for (int i = 0; i < min(n, kStages); ++i) copy(i);
+    for (int i = 0; i < min(total, kStages); ++i) copy(false);
 
   // x of this lane for half a record: rows g + 8 j, k = 32 q + 8 t
   struct Half {
     XFrag<T> f[NT][2];
   };
-  auto load_x = [&](Half& x, int i, int half) {
-    const int k = (first + i * STREAMS) * kUnitK + half * 64 + t * 8;
+  // (a row behind the last gives columns that nobody reads: any row will do)
+  const T* row[NT];
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
+  for (int j = 0; j < NT; ++j)
+    row[j] = static_cast<const T*>(a.x) + (int64_t)min(j * 8 + g, a.rows - 1) * a.x_stride + t * 8;
+  auto load_x = [&](Half& x, int step, int half) {
+    const int k = (u0 + step * kWarps) * kUnitK + half * 64;
+    if (k + 64 <= s.K) {
 #pragma unroll
-      for (int q = 0; q < 2; ++q)
-        x.f[j][q].load(static_cast<const T*>(a.x) + (int64_t)(j * 8 + g) * a.x_stride + k + q * 32,
-                       j * 8 + g < a.rows && k + q * 32 < s.K);
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int q = 0; q < 2; ++q) x.f[j][q].load(row[j] + k + q * 32);
+    } else {
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int q = 0; q < 2; ++q) x.f[j][q].load(row[j] + k + q * 32, k + q * 32 < s.K);
+    }
   };
-  float y[BL][NT][4];
-#pragma unroll
-  for (int b = 0; b < BL; ++b)
-#pragma unroll
-    for (int j = 0; j < NT; ++j)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) y[b][j][e] = 0.f;
-  const bool fine = s.group == 32;
-  const int shift = s.group == 128 ? 1 : 0;  // groups of a record's half: 1 / 2, 1, 2
-  const int places = s.groups() * kTileN;
+  // A record's half has two groups (fine), one, or half of one.  Where its
+  // scales and zeros begin for this lane, and how far the second half's are.
+  const bool fine = s.group == 32, zeros = s.zeros != 0;
+  const int places = s.groups() * kBlockN;
+  const int half_at = fine ? 2 * kBlockN : s.group == 64 ? kBlockN : 0;
+  const uint8_t* scale0 = mem + kCodeBytes + 2 * g * (int)sizeof(T);
+  const uint8_t* zero0 = mem + kCodeBytes + places * (int)sizeof(T) + 4 * g;
   Half x[AHEAD ? 2 : 1];
   if (AHEAD && n > 0) load_x(x[0], 0, 0);
-  for (int i = 0; i < n; ++i) {
-    const int slot = i % kStages;
-    if (!AHEAD) load_x(x[0], i, 0);
-    mbar_wait(&s_full[warp][slot], (i / kStages) & 1, a.errflag);
-    const uint8_t* rec = mem + slot * slot_bytes;
+  int slot = 0, phase = 0;
+  for (int pass = 0; pass < passes; ++pass) {
+    const int first = pass_at(pass), wide = pass_at(pass + 1) - first;
+    float y[BL][NT][4];
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      if constexpr (AHEAD) {
-        if (half == 0)
-          load_x(x[1], i, 1);
-        else if (i + 1 < n)
-          load_x(x[0], i + 1, 0);
-      } else if (half == 1) {
-        load_x(x[0], i, 1);
-      }
-      const Half& h = x[AHEAD ? half : 0];
-      const int gr = fine ? 2 * half : half >> shift;
+    for (int b = 0; b < BL; ++b)
 #pragma unroll
-      for (int b = 0; b < BL; ++b) {
-        const uint4 c = *reinterpret_cast<const uint4*>(rec + ((b * 2 + half) * 32 + lane) * 16);
-        const uint32_t cw[4] = {c.x, c.y, c.z, c.w};
-        float sc[2];
-        uint32_t z[2] = {W::kBias + 0x00080008u, W::kBias + 0x00080008u};
-        auto scales = [&](int gr) {
-          const int place = gr * kTileN + (b0 + b) * 16 + 2 * g;
-          load_cvt2(reinterpret_cast<const T*>(rec + kPart) + place, sc);
-          if (s.zeros) {
-            const uint32_t zz =
-                *reinterpret_cast<const uint16_t*>(rec + kPart + places * s.es + place);
-            z[0] = W::kBias + (zz & 0xffu) * 0x00010001u;
-            z[1] = W::kBias + (zz >> 8) * 0x00010001u;
-          }
-        };
-        scales(gr);
-        float acc[NT][4];
+      for (int j = 0; j < NT; ++j)
 #pragma unroll
-        for (int q = 0; q < 2; ++q) {
-          if (q == 1 && fine) scales(gr + 1);
-          if (q == 0 || fine) {
+        for (int e = 0; e < 4; ++e) y[b][j][e] = 0.f;
+    for (int i = 0; i < n; ++i) {
+      if (!AHEAD) load_x(x[0], i, 0);
+      mbar_wait(&s_full[warp][slot], phase, a.errflag);
+      const uint8_t* rec = mem + slot * slot_bytes;
 #pragma unroll
-            for (int j = 0; j < NT; ++j)
+      for (int half = 0; half < 2; ++half) {
+        if constexpr (AHEAD) {
+          if (half == 0)
+            load_x(x[1], i, 1);
+          else
+            load_x(x[0], i + 1 < n ? i + 1 : 0, 0);  // (behind the last: the next pass)
+        } else if (half == 1) {
+          load_x(x[0], i, 1);
+        }
+        const Half& h = x[AHEAD ? half : 0];
+        const uint8_t* scale = scale0 + slot * slot_bytes + half * half_at * (int)sizeof(T);
+        const uint8_t* zero = zero0 + slot * slot_bytes + half * half_at * 2;
 #pragma unroll
-              for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
-          }
+        for (int b = 0; b < BL; ++b) {
+          if (b >= wide) break;
+          const uint4 c =
+              *reinterpret_cast<const uint4*>(rec + b * s.record + (half * 32 + lane) * 16);
+          const uint32_t cw[4] = {c.x, c.y, c.z, c.w};
+          float sc[2];
+          uint32_t z[2] = {zero_half(W::kHalf, 8, 0) * 0x00010001u,
+                           zero_half(W::kHalf, 8, 1) * 0x00010001u};
+          auto scales = [&](int group) {  // of the half
+            load_cvt2(reinterpret_cast<const T*>(scale + b * s.record) + group * kBlockN, sc);
+            if (zeros) {
+              const uint32_t zz =
+                  *reinterpret_cast<const uint32_t*>(zero + b * s.record + group * 2 * kBlockN);
+              z[0] = __byte_perm(zz, 0u, 0x1010);
+              z[1] = __byte_perm(zz, 0u, 0x3232);
+            }
+          };
+          scales(0);
+          float acc[NT][4];
 #pragma unroll
-          for (int st = 0; st < 2; ++st) {
-            uint32_t A[4];
+          for (int q = 0; q < 2; ++q) {
+            if (q == 1 && fine) scales(1);
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              A[e] = W::sub(((cw[2 * q + st] >> (4 * e)) & 0x000f000fu) | W::kBias, z[e & 1]);
+            for (int st = 0; st < 2; ++st) {
+              uint32_t A[4];
+              W::fragment(cw[2 * q + st], z, A);
 #pragma unroll
-            for (int j = 0; j < NT; ++j)
+              for (int j = 0; j < NT; ++j)
 #pragma unroll
-              for (int w = 0; w < W::PARTS; ++w)
-                W::M::mma(acc[j], A, h.f[j][q].w[w][2 * st], h.f[j][q].w[w][2 * st + 1]);
-          }
-          if (q == 1 || fine) {
+                for (int w = 0; w < W::PARTS; ++w)
+                  if (st == 0 && w == 0 && (q == 0 || fine))
+                    W::first(acc[j], A, h.f[j][q].w[w][0], h.f[j][q].w[w][1]);
+                  else
+                    W::M::mma(acc[j], A, h.f[j][q].w[w][2 * st], h.f[j][q].w[w][2 * st + 1]);
+            }
+            if (q == 1 || fine) {
 #pragma unroll
-            for (int j = 0; j < NT; ++j)
+              for (int j = 0; j < NT; ++j)
 #pragma unroll
-              for (int e = 0; e < 4; ++e) y[b][j][e] = fmaf(acc[j][e], sc[e >> 1], y[b][j][e]);
+                for (int e = 0; e < 4; ++e) y[b][j][e] = fmaf(acc[j][e], sc[e >> 1], y[b][j][e]);
+            }
           }
         }
       }
+      __syncwarp();  // the slot is read
+      if (lane == 0 && pass * n + i + kStages < total) copy(false);
+      if (++slot == kStages) {
+        slot = 0;
+        phase ^= 1;
+      }
     }
-    __syncwarp();  // the slot is read
-    if (lane == 0 && i + kStages < n) copy(i + kStages);
-  }
-  __syncthreads();  // every record is read: the rings take the sums
 
-  // [stream][row][column of the tile]
-  float* sums = reinterpret_cast<float*>(ring);
-  constexpr int kRows = 8 * NT;
+    // ---- the warps' sums, [warp][row][column]
+    if (pass > 0) __syncthreads();  // the last pass's are read
 #pragma unroll
-  for (int b = 0; b < BL; ++b)
+    for (int b = 0; b < BL; ++b)
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
+      for (int j = 0; j < NT; ++j)
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        sums[(warp % STREAMS * kRows + j * 8 + 2 * t + (e & 1)) * kPitch + (b0 + b) * 16 + g +
-             8 * (e >> 1)] = y[b][j][e];
-  __syncthreads();
-  auto finish = [&](int row, int col, float v) {
-    const int n0 = tile * kTileN + col;
-    if (n0 >= s.N) return;
-    const int64_t o = (int64_t)row * s.N + n0;
-    if (a.residual) v += Elem<T>::to_f(static_cast<const T*>(a.residual)[o]);
-    static_cast<T*>(a.out)[o] = Elem<T>::from_f(v);
-  };
-  for (int e = tid; e < a.rows * kTileN; e += kW4Threads) {
-    const int row = e / kTileN, col = e - row * kTileN, at = row * kPitch + col;
-    float v = 0.f;
+        for (int e = 0; e < 4; ++e)
+          sums[(warp * kRows + j * 8 + 2 * t + (e & 1)) * kPitch + b * kBlockN + g + 8 * (e >> 1)] =
+              y[b][j][e];
+    __syncthreads();
+    const int columns = wide * kBlockN, outputs = a.rows * columns;
+    auto finish = [&](int r, int col, float v) {
+      const int at = first * kBlockN + col;
+      if (at >= s.N) return;
+      const int64_t o = (int64_t)r * s.N + at;
+      if (a.residual) v += Elem<T>::to_f(static_cast<const T*>(a.residual)[o]);
+      static_cast<T*>(a.out)[o] = Elem<T>::from_f(v);
+    };
+    for (int e = tid; e < outputs; e += kW4Threads) {
+      const int r = e / columns, col = e - r * columns, at = r * kPitch + col;
+      float v = 0.f;
 #pragma unroll
-    for (int w = 0; w < STREAMS; ++w) v += sums[w * kRows * kPitch + at];
-    if (a.split == 1)
-      finish(row, col, v);
-    else
-      sums[at] = v;
+      for (int w = 0; w < kWarps; ++w) v += sums[w * kRows * kPitch + at];
+      if (a.split == 1)
+        finish(r, col, v);
+      else
+        sums[at] = v;
+    }
+    if (a.split == 1) continue;
+    cluster_sync_all();
+    const uint32_t base = smem_u32(sums);
+    for (int e = part * kW4Threads + tid; e < outputs; e += a.split * kW4Threads) {
+      const int r = e / columns, col = e - r * columns;
+      float v = 0.f;
+      for (int q = 0; q < a.split; ++q) v += ld_cluster(mapa(base, q) + (r * kPitch + col) * 4);
+      finish(r, col, v);
+    }
+    cluster_sync_all();  // the sums are read: they may be overwritten, and the block may end
   }
-  if (a.split == 1) return;
-  cluster_sync_all();
-  const uint32_t base = smem_u32(sums);
-  for (int e = part * kW4Threads + tid; e < a.rows * kTileN; e += a.split * kW4Threads) {
-    const int row = e / kTileN, col = e - row * kTileN;
-    float v = 0.f;
-    for (int r = 0; r < a.split; ++r) v += ld_cluster(mapa(base, r) + (row * kPitch + col) * 4);
-    finish(row, col, v);
-  }
-  cluster_sync_all();  // no block leaves while its sums are read
 }
 
 // Rows of a launch, at most: fp32 x as three values of 64 rows leave no registers.
@@ -402,11 +499,37 @@ const void* w4_fn_of(int dtype, int rows) {
          : dtype == CF_F16 ? w4_fn<__half>(rows)
                            : w4_fn<__nv_bfloat16>(rows);
 }
-// Shared memory of a launch: the rings, then the sums.
-int w4_smem(const W4Shape& s, int rows) {
-  const int nt = rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 32 ? 4 : 8, bl = nt <= 4 ? 4 : 2;
-  const int ring = kWarps * kStages * (bl * 1024 + s.record - kCodeBytes);
-  return std::max(ring, kWarps * bl / 4 * 8 * nt * kPitch * 4);
+// What a launch of `rows` rows takes: n-tiles of 8 rows, blocks of columns of a
+// pass, thread blocks on an SM, shared memory (rings and sums).
+struct W4Plan {
+  int nt, wide, per_sm, smem, split, shares;
+};
+constexpr int kMaxSmem = 160 * 1024;  // fp32, groups of 32, zeros, 32 rows: 156 KB
+W4Plan w4_plan(const W4Shape& s, int dtype, int rows, int sms) {
+  W4Plan p;
+  p.nt = rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 32 ? 4 : 8;
+  p.wide = p.nt <= 4 ? 4 : 2;
+  p.per_sm = p.nt * (dtype == CF_F32 ? 3 : 1) <= 2 ? 2 : 1;
+  p.smem = kWarps * (kStages * p.wide * s.record + 8 * p.nt * (p.wide * kBlockN + 4) * 4);
+  // Splitting k shortens the steps of a warp where columns are too few for the
+  // SMs, and costs the exchange.  In cycles: a step's x and loop 150 and 50 more
+  // for each 8 rows, a block of columns 200 and 60; an exchange 2500.
+  const int slots = p.per_sm * sms;
+  long long best = -1;
+  for (int split = 1; split <= kMaxSplit && split <= s.units; split *= 2) {
+    const int shares = std::max(1, std::min(s.blocks, slots / split));
+    const long long blocks = (s.blocks + shares - 1) / shares;
+    const long long passes = (blocks + p.wide - 1) / p.wide;
+    const long long steps = ((s.units + split - 1) / split + kWarps - 1) / kWarps;
+    const long long cost = steps * (passes * (150 + 50 * p.nt) + blocks * (200 + 60 * p.nt)) +
+                           (split > 1 ? 2500 * passes : 0);
+    if (best < 0 || cost < best) {
+      best = cost;
+      p.split = split;
+      p.shares = shares;
+    }
+  }
+  return p;
 }
 
 bool overlap(const void* a, size_t na, const void* b, size_t nb) {
@@ -421,8 +544,7 @@ bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p
 struct cf_w4_handle {
   cf_w4_config cfg;
   W4Shape s;
-  int device = 0;
-  int split = 1;  // blocks of a cluster
+  int device = 0, sm_count = 0;
   int* errflag = nullptr;
 };
 
@@ -463,14 +585,14 @@ int cf_w4_create(const cf_w4_config* cfg, cf_w4_handle** out) {
   s.group = c.group;
   s.zeros = c.zeros;
   s.es = c.dtype == CF_F32 ? 4 : 2;
+  s.half = c.dtype == CF_F16;
   s.units = (s.K + kUnitK - 1) / kUnitK;
-  s.tiles = (s.N + kTileN - 1) / kTileN;
-  s.record = kCodeBytes + s.groups() * kTileN * (s.es + s.zeros);
-  if ((int64_t)s.units * s.tiles > INT32_MAX) {  // the grid of the layout's kernel
+  s.blocks = (s.N + kBlockN - 1) / kBlockN;
+  s.record = kCodeBytes + s.groups() * kBlockN * (s.es + 2 * s.zeros);
+  if ((int64_t)s.units * s.blocks > INT32_MAX) {  // the grid of the layout's kernel
     delete h;
     return CF_ERR_INVALID_ARG;
   }
-  int sms = 0;
   auto fail = [&]() {
     cudaGetLastError();
     if (h->errflag) cudaFree(h->errflag);
@@ -478,15 +600,12 @@ int cf_w4_create(const cf_w4_config* cfg, cf_w4_handle** out) {
     return CF_ERR_CUDA;
   };
   if (cudaGetDevice(&h->device) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, h->device) != cudaSuccess)
+      cudaDeviceGetAttribute(&h->sm_count, cudaDevAttrMultiProcessorCount, h->device) !=
+          cudaSuccess)
     return fail();
-  // Few tiles leave SMs without one: k is split until there are three blocks to
-  // two SMs (two fit on each), or a block has four records left.
-  while (h->split < kMaxSplit && s.tiles * h->split * 2 < 3 * sms && s.units >= 8 * h->split)
-    h->split *= 2;
   for (int rows = 8; rows <= launch_rows(c.dtype); rows *= 2)
     if (cudaFuncSetAttribute(w4_fn_of(c.dtype, rows), cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             100 * 1024) != cudaSuccess)
+                             kMaxSmem) != cudaSuccess)
       return fail();
   if (cudaMalloc(&h->errflag, sizeof(int)) != cudaSuccess ||
       cudaMemset(h->errflag, 0, sizeof(int)) != cudaSuccess ||
@@ -497,7 +616,7 @@ int cf_w4_create(const cf_w4_config* cfg, cf_w4_handle** out) {
 }
 
 size_t cf_w4_packed_bytes(const cf_w4_handle* h) {
-  return h == nullptr ? 0 : (size_t)h->s.units * h->s.tiles * h->s.record;
+  return h == nullptr ? 0 : (size_t)h->s.units * h->s.blocks * h->s.record;
 }
 
 int cf_w4_pack(cf_w4_handle* h, const uint8_t* codes, const void* scales, const uint8_t* zeros,
@@ -517,7 +636,7 @@ int cf_w4_pack(cf_w4_handle* h, const uint8_t* codes, const void* scales, const 
   const uint8_t* sc = static_cast<const uint8_t*>(scales);
   uint8_t* pk = static_cast<uint8_t*>(packed);
   void* args[] = {&sh, &codes, &sc, &zeros, &pk};
-  if (!launch_pdl((const void*)&w4_pack_kernel, dim3((unsigned)(s.units * s.tiles)), kW4Threads, 0,
+  if (!launch_pdl((const void*)&w4_pack_kernel, dim3((unsigned)(s.units * s.blocks)), kPackThreads, 0,
                   static_cast<cudaStream_t>(stream), args)) {
     cudaGetLastError();
     return CF_ERR_CUDA;
@@ -546,20 +665,16 @@ int cf_w4_matvec(cf_w4_handle* h, int32_t rows, const void* x, int64_t x_stride,
   a.packed = static_cast<const uint8_t*>(packed);
   a.x_stride = x_stride;
   a.errflag = h->errflag;
-  a.split = h->split;
   void* args[] = {&a};
   cudaLaunchConfig_t lc = {};
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = (unsigned)h->split;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-  lc.gridDim = dim3((unsigned)(s.tiles * h->split));
   lc.blockDim = dim3(kW4Threads);
   lc.stream = static_cast<cudaStream_t>(stream);
   lc.attrs = attr;
-  lc.numAttrs = h->split > 1 ? 2 : 1;
   const int step = launch_rows(h->cfg.dtype);
   for (int r0 = 0; r0 < rows; r0 += step) {
     a.rows = std::min(step, rows - r0);
@@ -567,7 +682,13 @@ int cf_w4_matvec(cf_w4_handle* h, int32_t rows, const void* x, int64_t x_stride,
     a.out = static_cast<uint8_t*>(out) + (int64_t)r0 * s.N * s.es;
     a.residual = residual ? static_cast<const uint8_t*>(residual) + (int64_t)r0 * s.N * s.es
                           : nullptr;
-    lc.dynamicSmemBytes = w4_smem(s, a.rows);
+    const W4Plan plan = w4_plan(s, h->cfg.dtype, a.rows, h->sm_count);
+    a.split = plan.split;
+    a.shares = plan.shares;
+    attr[1].val.clusterDim.x = (unsigned)plan.split;
+    lc.gridDim = dim3((unsigned)(plan.shares * plan.split));
+    lc.dynamicSmemBytes = plan.smem;
+    lc.numAttrs = plan.split > 1 ? 2 : 1;
     if (cudaLaunchKernelExC(&lc, w4_fn_of(h->cfg.dtype, a.rows), args) != cudaSuccess) {
       cudaGetLastError();
       return CF_ERR_CUDA;

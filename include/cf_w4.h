@@ -15,7 +15,7 @@
  * gives the same bits.
  *
  * Weights are laid out once, by cf_w4_pack, in the order in which the kernel
- * streams them: for each 64 columns and 128 elements of k one record of 4 KB of
+ * streams them: for each 128 elements of k and 16 columns one record of 1 KB of
  * codes with their scales and zeros.
  *
  * Conventions: CF_OK or a negative CF_ERR_* code of cf.h, nothing is printed;
