@@ -499,10 +499,7 @@ inline bool launch_pdl(const void* fn, dim3 grid, int threads, int smem, cudaStr
 }
 
 // Host launchers (one translation unit each); false: the launch failed.
-// code: what the pages hold, kCodeNone (values) or a cf_code of cf_paged8.h.
-constexpr int kCodeNone = -1;
-bool paged_append_launch(int dtype, int code, const PagedAppendParams& p, int sm_count,
-                         cudaStream_t st);
+bool paged_append_launch(int dtype, const PagedAppendParams& p, int sm_count, cudaStream_t st);
 
 // The fp32 kernel.  grid: resident blocks, 0 on failure; part_rows: workspace;
 // a ticket per resident block and a word more.

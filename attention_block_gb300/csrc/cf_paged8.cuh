@@ -116,6 +116,8 @@ __device__ __forceinline__ void cp8(uint32_t dst, const void* src, bool there) {
 }
 
 // Host launchers; false: the launch failed.
+bool paged8_append_launch(int dtype, int code, const PagedAppendParams& p, int sm_count,
+                          cudaStream_t st);
 struct Paged8ReadParams {
   PagedGeom g;
   const void *k_pages, *v_pages;

@@ -86,8 +86,8 @@ int cf_paged8_append(cf_paged8_handle* h, int32_t batch, int32_t n_tokens, const
                                    q_start, kv_len, rope_pos, page_table, k_pages, v_pages, scales,
                                    q_out, q_out_stride, p);
   if (rc != CF_OK || p.n_tokens == 0) return rc;
-  if (!paged_append_launch(h->cfg.dtype, h->code, p, h->sm_count,
-                           static_cast<cudaStream_t>(stream))) {
+  if (!paged8_append_launch(h->cfg.dtype, h->code, p, h->sm_count,
+                            static_cast<cudaStream_t>(stream))) {
     cudaGetLastError();
     return CF_ERR_CUDA;
   }

@@ -16,7 +16,8 @@ using namespace cf;
 namespace {
 
 constexpr int kReadThreads = 256;
-constexpr int kReadRows = 16;  // of a block
+constexpr int kReadRows = 8;  // of a block
+constexpr int kReadAhead = 4;  // loads of a thread on their way
 
 template <typename T, int D, int CODE>
 __global__ void __launch_bounds__(kReadThreads)
@@ -63,35 +64,61 @@ __global__ void __launch_bounds__(kReadThreads)
     s_scale[tid] = scale;
   }
   __syncthreads();
-  const int per_row = p.g.nkv * C;  // of K, and as many of V
-  for (int x = tid; x < kReadRows * 2 * per_row; x += kReadThreads) {
-    const int side = x / per_row, i = side >> 1, kv = side & 1, y = x - side * per_row;
-    const int h = y / C, c = y - h * C;
-    void* out = kv ? p.v_out : p.k_out;
-    const int64_t code = s_code[i];
-    if (out == nullptr || code == -2) continue;
-    uint4 w = make_uint4(0, 0, 0, 0);
-    float scale = 0.f;
-    if (code >= 0) {
-      w = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(kv ? p.v_pages : p.k_pages) +
-                                               code + (int64_t)h * p.g.head_stride + c * 16));
-      scale = __ldg((&p.scales[s_scale[i] + ((int64_t)h << p.g.page_shift)].x) + kv);
+  // A thread keeps to one piece of a head and walks over the heads of the rows'
+  // keys and values, with several loads on their way.
+  const int c = tid % C;
+  constexpr int step = kReadThreads / C;  // heads of one step of the block
+  int side = 0, h = tid / C;              // 2 * row, + 1: its values
+  auto fit = [&]() {
+    while (h >= p.g.nkv) {
+      h -= p.g.nkv;
+      ++side;
     }
-      const uint32_t v[4] = {w.x, w.y, w.z, w.w};
-    uint32_t o[8];
+  };
+  fit();
+  while (side < 2 * kReadRows) {
+    uint4 w[kReadAhead];
+    float scale[kReadAhead];
+    void* to[kReadAhead];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      uint32_t even, odd;
-      code_halves<CODE>(v[e], even, odd);
-      const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&even));
-      const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&odd));
-      o[2 * e] = pack2<T>(a.x * scale, b.x * scale);
-      o[2 * e + 1] = pack2<T>(a.y * scale, b.y * scale);
+    for (int i = 0; i < kReadAhead; ++i) {
+      to[i] = nullptr;
+      if (side < 2 * kReadRows) {
+        const int row = side >> 1, kv = side & 1;
+        void* out = kv ? p.v_out : p.k_out;
+        const int64_t code = s_code[row];
+        if (out != nullptr && code != -2)
+          to[i] = static_cast<T*>(out) + (int64_t)(r0 + row) * p.out_stride + h * D + c * 16;
+        w[i] = make_uint4(0, 0, 0, 0);
+        scale[i] = 0.f;
+        if (to[i] != nullptr && code >= 0) {
+          const uint8_t* pool = static_cast<const uint8_t*>(kv ? p.v_pages : p.k_pages);
+          w[i] = __ldcs(reinterpret_cast<const uint4*>(pool + code + (int64_t)h * p.g.head_stride +
+                                                       c * 16));
+          scale[i] = __ldg((&p.scales[s_scale[row] + ((int64_t)h << p.g.page_shift)].x) + kv);
+        }
+      }
+      h += step;
+      fit();
     }
-    uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(out) + (int64_t)(r0 + i) * p.out_stride +
-                                          h * D + c * 16);
-    dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
-    dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+#pragma unroll
+    for (int i = 0; i < kReadAhead; ++i) {
+      if (to[i] == nullptr) continue;
+      const uint32_t v[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+      uint32_t o[8];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        uint32_t first, last;
+        code_row4<CODE>(v[e], first, last);
+        const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&first));
+        const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&last));
+        o[2 * e] = pack2<T>(a.x * scale[i], a.y * scale[i]);
+        o[2 * e + 1] = pack2<T>(b.x * scale[i], b.y * scale[i]);
+      }
+      uint4* dst = static_cast<uint4*>(to[i]);
+      dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+      dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    }
   }
 }
 

@@ -160,7 +160,7 @@ int cf_paged_append(cf_paged_handle* h, int32_t batch, int32_t n_tokens, const v
                                    q_start, kv_len, rope_pos, page_table, k_pages, v_pages, nullptr,
                                    q_out, q_out_stride, p);
   if (rc != CF_OK || p.n_tokens == 0) return rc;
-  if (!paged_append_launch(h->cfg.dtype, kCodeNone, p, h->sm_count, static_cast<cudaStream_t>(stream))) {
+  if (!paged_append_launch(h->cfg.dtype, p, h->sm_count, static_cast<cudaStream_t>(stream))) {
     cudaGetLastError();
     return CF_ERR_CUDA;
   }

@@ -1,6 +1,5 @@
 // cf_paged_append.cu -- rotate new keys and queries and write keys and values
-// to their pages (cf_paged_append), or their 8-bit codes and scales
-// (cf_paged8_append).
+// to their pages (cf_paged_append).
 //
 // The rotation angle is kept as a fraction of a turn in 64-bit fixed point:
 // pos * turn_i mod 2^64 is the exact fraction of pos times the host's
@@ -17,13 +16,9 @@
 // the heads of the block's tokens; the first loads are under way before the
 // block knows where its tokens go (sequence, length, page: loads that depend on
 // one another).
-//
-// Codes: the threads of a head hold all of it, find its largest magnitude by
-// shuffles and write 8-byte pieces of codes, the first of them the scale.
 #include <cuda_runtime.h>
 
 #include "cf_paged.cuh"
-#include "cf_paged8.cuh"
 
 using namespace cf;
 
@@ -36,21 +31,7 @@ constexpr int kAppendThreads = 256;
 template <int TPB>
 constexpr int kBatch = TPB == 1 ? 3 : 1;
 
-// (sin, cos) of f / 2^64 turns.  Behind a quarter turn's reduction the float
-// that sincospif takes is off by 2^-28 of a turn, for codes: an error there
-// moves more of them over a border than those of the arithmetic do.
-__device__ __forceinline__ float2 turn_fine(uint64_t f) {
-  const uint32_t hi = (uint32_t)(f >> 32);
-  const uint32_t quarter = (hi + 0x20000000u) >> 30;
-  const float part = (float)(int32_t)(hi - (quarter << 30)) * 0x1p-32f;
-  float s, c;
-  sincospif(2.0f * part, &s, &c);
-  const bool swap = quarter & 1u;
-  const float x = swap ? s : c, y = swap ? c : s;
-  return make_float2(quarter == 1 || quarter == 2 ? -x : x, quarter >= 2 ? -y : y);
-}
-
-template <typename T, int D, int TPB, int CODE>
+template <typename T, int D, int TPB>
 __global__ void __launch_bounds__(kAppendThreads, TPB == 1 ? 4 : 8)
     paged_append_kernel(const __grid_constant__ PagedAppendParams p) {
   constexpr int NB = kBatch<TPB>;
@@ -58,7 +39,7 @@ __global__ void __launch_bounds__(kAppendThreads, TPB == 1 ? 4 : 8)
   constexpr int RPI = kAppendThreads / UPH;             // heads per step of the block
   __shared__ float2 s_cs[TPB][kMaxPairs];
   __shared__ int s_seq[TPB], s_pos[TPB];
-  __shared__ int64_t s_slot[TPB], s_scale[TPB];
+  __shared__ int64_t s_slot[TPB];
   const int tid = threadIdx.x, c = tid % UPH;
   const int t_lo = blockIdx.x * TPB;
   const int nt = min(TPB, p.n_tokens - t_lo);
@@ -140,8 +121,6 @@ __global__ void __launch_bounds__(kAppendThreads, TPB == 1 ? 4 : 8)
         atomicOr(p.errflag, kDevErrPosRange);
       else
         slot = paged_offset(p.page_table + (int64_t)b * p.g.max_pages, pos, p.g, p.errflag);
-      if (CODE != kCodeNone && slot >= 0)
-        s_scale[tid] = paged8_scale(p.page_table + (int64_t)b * p.g.max_pages, pos, p.g);
     }
     s_slot[tid] = slot;
     s_pos[tid] = pos;
@@ -152,13 +131,9 @@ __global__ void __launch_bounds__(kAppendThreads, TPB == 1 ? 4 : 8)
     const int P =
         p.rope_pos ? p.rope_pos[(int64_t)p.axis[j] * p.n_tokens + t_lo + t] : s_pos[t];
     const uint64_t f = (uint64_t)(int64_t)P * p.turn[j];
+    const float turns = (float)(int32_t)(uint32_t)(f >> 32) * 0x1p-32f;
     float2 cs;
-    if constexpr (CODE == kCodeNone) {
-      const float turns = (float)(int32_t)(uint32_t)(f >> 32) * 0x1p-32f;
-      sincospif(2.0f * turns, &cs.y, &cs.x);
-    } else {
-      cs = turn_fine(f);
-    }
+    sincospif(2.0f * turns, &cs.y, &cs.x);
     s_cs[t][j] = cs;
   }
   __syncthreads();
@@ -168,46 +143,33 @@ __global__ void __launch_bounds__(kAppendThreads, TPB == 1 ? 4 : 8)
     for (int i = 0; i < NB; ++i) {
       if (bt[i] < 0 || s_slot[bt[i]] < 0) continue;
       const int64_t t = t_lo + bt[i];
-      const bool query = bh[i] < p.g.nq, value = bh[i] >= p.g.nq + p.g.nkv;
-      const int kvh = bh[i] - p.g.nq - (value ? p.g.nkv : 0);
-      const bool turn = rot && !value;
-      const int e0 = value ? c * W : r0, e1 = value ? e0 + D / 2 : r1;
-      float o[2 * W];  // the two vectors in fp32 (a copy needs none)
-      if (turn || (CODE != kCodeNone && !query)) {
-        Elem<T>::words(reinterpret_cast<const uint32_t*>(&x[i]), 4, o);
-        Elem<T>::words(reinterpret_cast<const uint32_t*>(&y[i]), 4, o + W);
+      T* dst;
+      int e0 = r0, e1 = r1;
+      bool turn = rot;
+      if (bh[i] < p.g.nq) {
+        dst = static_cast<T*>(p.q_out) + t * p.q_out_stride + (int64_t)bh[i] * D;
+      } else if (bh[i] < p.g.nq + p.g.nkv) {
+        dst = static_cast<T*>(p.k_pages) + s_slot[bt[i]] + (bh[i] - p.g.nq) * p.g.head_stride;
+      } else {
+        dst = static_cast<T*>(p.v_pages) + s_slot[bt[i]] +
+              (bh[i] - p.g.nq - p.g.nkv) * p.g.head_stride;
+        e0 = c * W;
+        e1 = e0 + D / 2;
+        turn = false;
       }
       if (turn) {
+        float a[W], b[W];
+        Elem<T>::words(reinterpret_cast<const uint32_t*>(&x[i]), 4, a);
+        Elem<T>::words(reinterpret_cast<const uint32_t*>(&y[i]), 4, b);
+        T o0[W], o1[W];
 #pragma unroll
         for (int e = 0; e < W; ++e) {
           const float2 cs = s_cs[bt[i]][c * W + e];
-          const float a = o[e], b = o[W + e];
-          o[e] = a * cs.x - b * cs.y;
-          o[W + e] = b * cs.x + a * cs.y;
+          o0[e] = Elem<T>::from_f(a[e] * cs.x - b[e] * cs.y);
+          o1[e] = Elem<T>::from_f(b[e] * cs.x + a[e] * cs.y);
         }
-      }
-      if constexpr (CODE != kCodeNone) {
-        if (!query) {
-          float scale;
-          uint2 w[2];
-          quantise_head<CODE, UPH>(o, scale, w);
-          uint8_t* dst = static_cast<uint8_t*>(value ? p.v_pages : p.k_pages) + s_slot[bt[i]] +
-                         (int64_t)kvh * p.g.head_stride;
-          *reinterpret_cast<uint2*>(dst + e0) = w[0];
-          *reinterpret_cast<uint2*>(dst + e1) = w[1];
-          if (c == 0) (&p.scales[s_scale[bt[i]] + ((int64_t)kvh << p.g.page_shift)].x)[value] = scale;
-          continue;
-        }
-      }
-      T* dst = query ? static_cast<T*>(p.q_out) + t * p.q_out_stride + (int64_t)bh[i] * D
-                     : static_cast<T*>(value ? p.v_pages : p.k_pages) + s_slot[bt[i]] +
-                           kvh * p.g.head_stride;
-      if (turn) {
-        T v[2 * W];
-#pragma unroll
-        for (int e = 0; e < 2 * W; ++e) v[e] = Elem<T>::from_f(o[e]);
-        x[i] = *reinterpret_cast<const uint4*>(v);
-        y[i] = *reinterpret_cast<const uint4*>(v + W);
+        x[i] = *reinterpret_cast<const uint4*>(o0);
+        y[i] = *reinterpret_cast<const uint4*>(o1);
       }
       *reinterpret_cast<uint4*>(dst + e0) = x[i];
       *reinterpret_cast<uint4*>(dst + e1) = y[i];
@@ -217,42 +179,35 @@ __global__ void __launch_bounds__(kAppendThreads, TPB == 1 ? 4 : 8)
   }
 }
 
-template <typename T, int D, int CODE, int TPB>
+template <typename T, int D, int TPB>
 bool launch_n(const PagedAppendParams& p, int gy, cudaStream_t st) {
   PagedAppendParams pp = p;
   void* args[] = {&pp};
-  return launch_pdl((const void*)&paged_append_kernel<T, D, TPB, CODE>,
+  return launch_pdl((const void*)&paged_append_kernel<T, D, TPB>,
                     dim3((p.n_tokens + TPB - 1) / TPB, gy, 1), kAppendThreads, 0, st, args);
 }
 
-template <typename T, int D, int CODE>
+template <typename T, int D>
 bool launch(const PagedAppendParams& p, int sm_count, cudaStream_t st) {
   // Few tokens: one per block, its heads over several blocks of one step each
   // while the GPU has room.  Many: four per block.
-  if (p.n_tokens >= 8 * sm_count) return launch_n<T, D, CODE, 4>(p, 1, st);
+  if (p.n_tokens >= 8 * sm_count) return launch_n<T, D, 4>(p, 1, st);
   constexpr int RPI = kAppendThreads / (D / (2 * (16 / (int)sizeof(T))));
   const int steps = (p.g.nq + 2 * p.g.nkv + RPI - 1) / RPI;
-  return launch_n<T, D, CODE, 1>(
-      p, p.n_tokens <= sm_count ? steps : (steps + kBatch<1> - 1) / kBatch<1>, st);
-}
-template <typename T, int CODE = kCodeNone>
-bool launch_d(const PagedAppendParams& p, int sm_count, cudaStream_t st) {
-  return p.g.D == 64 ? launch<T, 64, CODE>(p, sm_count, st) : launch<T, 128, CODE>(p, sm_count, st);
+  return launch_n<T, D, 1>(p, p.n_tokens <= sm_count ? steps : (steps + kBatch<1> - 1) / kBatch<1>, st);
 }
 template <typename T>
-bool launch_code(int code, const PagedAppendParams& p, int sm_count, cudaStream_t st) {
-  return code == CF_CODE_INT8   ? launch_d<T, CF_CODE_INT8>(p, sm_count, st)
-         : code == CF_CODE_E4M3 ? launch_d<T, CF_CODE_E4M3>(p, sm_count, st)
-                                : launch_d<T>(p, sm_count, st);
+bool launch_d(const PagedAppendParams& p, int sm_count, cudaStream_t st) {
+  return p.g.D == 64 ? launch<T, 64>(p, sm_count, st) : launch<T, 128>(p, sm_count, st);
 }
 
 }  // namespace
 
-bool cf::paged_append_launch(int dtype, int code, const PagedAppendParams& p, int sm_count,
+bool cf::paged_append_launch(int dtype, const PagedAppendParams& p, int sm_count,
                              cudaStream_t st) {
   switch (dtype) {
     case CF_F32: return launch_d<float>(p, sm_count, st);
-    case CF_F16: return launch_code<__half>(code, p, sm_count, st);
-    default: return launch_code<__nv_bfloat16>(code, p, sm_count, st);
+    case CF_F16: return launch_d<__half>(p, sm_count, st);
+    default: return launch_d<__nv_bfloat16>(p, sm_count, st);
   }
 }

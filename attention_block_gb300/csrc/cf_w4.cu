@@ -108,6 +108,23 @@ __global__ void __launch_bounds__(kPackThreads)
 // How codes and x enter the tensor core.
 template <typename T>
 struct W4Type;
+
+// (w & mask) | bias in one instruction: both from registers, as the compiler
+// takes two with constants.
+struct W4Mask {
+  uint32_t low, high, bias;
+  __device__ __forceinline__ explicit W4Mask(uint32_t b) {
+    asm("mov.b32 %0, 0x000f000f;" : "=r"(low));
+    asm("mov.b32 %0, 0x00f000f0;" : "=r"(high));
+    asm("mov.b32 %0, %1;" : "=r"(bias) : "r"(b));
+  }
+  static __device__ __forceinline__ uint32_t take(uint32_t w, uint32_t mask, uint32_t bias) {
+    uint32_t d;
+    asm("lop3.b32 %0, %1, %2, %3, 0xea;" : "=r"(d) : "r"(w), "r"(mask), "r"(bias));
+    return d;
+  }
+};
+
 template <>
 struct W4Type<__half> {
   using M = MmaKind<__half>;
@@ -125,13 +142,13 @@ struct W4Type<__half> {
   // The fragment of a word; z: bias + zero of columns g and g + 8.  Nibbles 1
   // and 3 stay four bits up, as 1024 + 16 c, and one fused operation takes the
   // sixteenth and subtracts.
-  static __device__ __forceinline__ void fragment(uint32_t w, const uint32_t (&z)[2],
-                                                  uint32_t (&A)[4]) {
+  static __device__ __forceinline__ void fragment(uint32_t w, const W4Mask& m,
+                                                  const uint32_t (&z)[2], uint32_t (&A)[4]) {
     const uint32_t v = w >> 8;
-    A[0] = sub((w & 0x000f000fu) | kBias, z[0]);
-    A[1] = sub16((w & 0x00f000f0u) | kBias, z[1]);
-    A[2] = sub((v & 0x000f000fu) | kBias, z[0]);
-    A[3] = sub16((v & 0x00f000f0u) | kBias, z[1]);
+    A[0] = sub(W4Mask::take(w, m.low, m.bias), z[0]);
+    A[1] = sub16(W4Mask::take(w, m.high, m.bias), z[1]);
+    A[2] = sub(W4Mask::take(v, m.low, m.bias), z[0]);
+    A[3] = sub16(W4Mask::take(v, m.high, m.bias), z[1]);
   }
   static constexpr bool kHalf = true;
   static __device__ __forceinline__ uint32_t sub16(uint32_t a, uint32_t b) {
@@ -159,10 +176,11 @@ struct W4Type<__nv_bfloat16> {
   }
   static constexpr uint32_t kBias = 0x43004300u;  // 128, ulp 1
   static constexpr int PARTS = 1;
-  static __device__ __forceinline__ void fragment(uint32_t w, const uint32_t (&z)[2],
-                                                  uint32_t (&A)[4]) {
+  static __device__ __forceinline__ void fragment(uint32_t w, const W4Mask& m,
+                                                  const uint32_t (&z)[2], uint32_t (&A)[4]) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) A[e] = sub(((w >> (4 * e)) & 0x000f000fu) | kBias, z[e & 1]);
+    for (int e = 0; e < 4; ++e)
+      A[e] = sub(W4Mask::take(w >> (4 * e), m.low, m.bias), z[e & 1]);
   }
   static constexpr bool kHalf = false;
   static __device__ __forceinline__ uint32_t sub(uint32_t a, uint32_t b) {
@@ -359,6 +377,7 @@ __global__ void __launch_bounds__(kW4Threads, kPerSm<T, NT>)
   const int half_at = fine ? 2 * kBlockN : s.group == 64 ? kBlockN : 0;
   const uint8_t* scale0 = mem + kCodeBytes + 2 * g * (int)sizeof(T);
   const uint8_t* zero0 = mem + kCodeBytes + places * (int)sizeof(T) + 4 * g;
+  const W4Mask mask(W::kBias);
   Half x[AHEAD ? 2 : 1];
   if (AHEAD && n > 0) load_x(x[0], 0, 0);
   int slot = 0, phase = 0;
@@ -414,7 +433,7 @@ __global__ void __launch_bounds__(kW4Threads, kPerSm<T, NT>)
 #pragma unroll
             for (int st = 0; st < 2; ++st) {
               uint32_t A[4];
-              W::fragment(cw[2 * q + st], z, A);
+              W::fragment(cw[2 * q + st], mask, z, A);
 #pragma unroll
               for (int j = 0; j < NT; ++j)
 #pragma unroll
