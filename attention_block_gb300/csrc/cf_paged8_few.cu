@@ -95,12 +95,14 @@ __global__ void __launch_bounds__(Shape8<D, NT>::THREADS, 1)
   pdl_wait();
   pdl_trigger();
 
-  // Units of every sequence, summed up over the batch: each thread has a run
-  // of sequences.
-  const int per = (p.batch + THREADS - 1) / THREADS;
+  // Units of every sequence, summed up over the batch: each lane of every warp
+  // has one or, with more than 32, each thread a run of them.
+  const bool small = p.batch <= 32;
+  const int per = small ? 1 : (p.batch + THREADS - 1) / THREADS;
+  const int mine0 = small ? lane : tid * per;
   long long mine = 0;
   int top = 0;  // units of the longest item
-  for (int b = tid * per; b < min(p.batch, (tid + 1) * per); ++b) {
+  for (int b = mine0; b < min(p.batch, mine0 + per); ++b) {
     const int t = work_of<KS, false>(p, b).tiles;
     mine += (long long)t * p.g.nkv;
     top = max(top, t);
@@ -112,32 +114,40 @@ __global__ void __launch_bounds__(Shape8<D, NT>::THREADS, 1)
     const long long v = __shfl_up_sync(~0u, incl, o);
     if (lane >= o) incl += v;
   }
-  if (lane == 31) {
-    s_scan[warp] = incl;
-    s_top[warp] = top;
-  }
-  __syncthreads();
-  long long before = incl - mine, total = 0;
+  long long before = incl - mine, total = __shfl_sync(~0u, incl, 31);
+  if (!small) {
+    if (lane == 31) {
+      s_scan[warp] = incl;
+      s_top[warp] = top;
+    }
+    __syncthreads();
+    total = 0;
 #pragma unroll
-  for (int w = 0; w < WARPS; ++w) {
-    if (w < warp) before += s_scan[w];
-    total += s_scan[w];
-    top = max(top, s_top[w]);
+    for (int w = 0; w < WARPS; ++w) {
+      if (w < warp) before += s_scan[w];
+      total += s_scan[w];
+      top = max(top, s_top[w]);
+    }
+    s_first[tid] = before;
   }
-  s_first[tid] = before;
-  const long long block_upc =
-      div_units(total + gridDim.x * WARPS - 1, gridDim.x * WARPS) * WARPS;
+  const long long block_upc = div_units(total + gridDim.x * WARPS - 1, gridDim.x * WARPS) * WARPS;
   if (lane == 0) s_has[0][warp] = s_has[1][warp] = 0;
-  __syncthreads();
+  if (!small) __syncthreads();
 
   // A cursor at unit u of the line.
   auto locate = [&](Cursor<KS, false>& c, long long u) {
     // the last run of sequences that begins at or before unit u
     int n = 0;
+    long long at;
+    if (small) {
+      n = __popc(__ballot_sync(~0u, lane < p.batch && before <= u));
+      at = __shfl_sync(~0u, before, n - 1);
+    } else {
 #pragma unroll
-    for (int i = 0; i < THREADS / 32; ++i)
-      n += __popc(__ballot_sync(~0u, s_first[i * 32 + lane] <= u));
-    long long at = s_first[n - 1];
+      for (int i = 0; i < THREADS / 32; ++i)
+        n += __popc(__ballot_sync(~0u, s_first[i * 32 + lane] <= u));
+      at = s_first[n - 1];
+    }
     int b = (n - 1) * per;
     while (true) {
       c.w = work_of<KS, false>(p, b);
@@ -209,9 +219,9 @@ __global__ void __launch_bounds__(Shape8<D, NT>::THREADS, 1)
   const uint32_t k0 = ring_s + r0 * D + ((D == 128 ? c0 ^ ((r0 & 1) << 2) : c0) << 4);
   const uint32_t v0 =
       ring_s + S::SLOT + r0 * D + ((D == 128 ? c0 ^ r0 : c0 ^ ((r0 >> 1) & 3)) << 4);
-  const char* kbase = static_cast<const char*>(p.k_pages);
-  const char* vbase = static_cast<const char*>(p.v_pages);
-  const int64_t step = RP * p.g.slot_stride, own = r0 * p.g.slot_stride + c0 * 16;
+  const char* kbase = static_cast<const char*>(p.k_pages) + c0 * 16;
+  const char* vbase = static_cast<const char*>(p.v_pages) + c0 * 16;
+  const int64_t step = RP * p.g.slot_stride, own = r0 * p.g.slot_stride;
   const bool octets = p.g.page_shift >= 3;
   auto copy = [&](uint32_t d, bool values, const char* src, int64_t off) {
     // the swizzle of a later row of the same lane (D = 128: rows 4 apart)
@@ -220,7 +230,7 @@ __global__ void __launch_bounds__(Shape8<D, NT>::THREADS, 1)
       // eight consecutive positions lie in one page: one lookup serves them
 #pragma unroll
       for (int y = 0; y < KS / 8; ++y) {
-        const char* at = src + (__shfl_sync(~0u, off, 8 * y) + own);
+        const char* at = src + own + __shfl_sync(~0u, off, 8 * y);
         cp16(d + 8 * y * D, at);
         if constexpr (RP == 4) cp16(d4 + (8 * y + 4) * D, at + step);
       }
@@ -228,7 +238,7 @@ __global__ void __launch_bounds__(Shape8<D, NT>::THREADS, 1)
 #pragma unroll
       for (int i = 0; i < KS / RP; ++i) {
         const int64_t o = __shfl_sync(~0u, off, i * RP + r0);
-        cp16((i * RP & 4 ? d4 : d) + i * RP * D, src + (o >= 0 ? o + c0 * 16 : 0), o >= 0);
+        cp16((i * RP & 4 ? d4 : d) + i * RP * D, src + (o >= 0 ? o : 0), o >= 0);
       }
     }
   };
@@ -294,6 +304,12 @@ __global__ void __launch_bounds__(Shape8<D, NT>::THREADS, 1)
     issue_v(s);
   }
 
+  // where this lane's pieces of K (of key gq) and V (of position lane % 16) lie;
+  // their swizzles are whole in the bits that a piece's number is put to by ^
+  const uint32_t k_lane = ring_s + gq * D + ((D == 128 ? tq ^ ((gq & 1) << 2) : tq) << 4);
+  const uint32_t v_lane =
+      ring_s + S::SLOT + (lane & 15) * D +
+      (((lane >> 4) ^ (D == 128 ? lane & 7 : (lane >> 1) & 3)) << 4);
   int pair = 0;
   uint32_t qf[NT][D / 16][2];
   float o[NT][NJ][4], m[NT][2], l[NT][2];
@@ -317,10 +333,10 @@ __global__ void __launch_bounds__(Shape8<D, NT>::THREADS, 1)
           const uint4 w = row < nrows
                               ? *reinterpret_cast<const uint4*>(src + (k >> 1) * 64 + (k & 1) * 8)
                               : make_uint4(0, 0, 0, 0);
-          qf[nt][2 * k][0] = __byte_perm(w.x, w.y, 0x5410);
-          qf[nt][2 * k][1] = __byte_perm(w.x, w.y, 0x7632);
-          qf[nt][2 * k + 1][0] = __byte_perm(w.z, w.w, 0x5410);
-          qf[nt][2 * k + 1][1] = __byte_perm(w.z, w.w, 0x7632);
+          qf[nt][2 * k][0] = w.x;
+          qf[nt][2 * k][1] = w.y;
+          qf[nt][2 * k + 1][0] = w.z;
+          qf[nt][2 * k + 1][1] = w.w;
         }
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
@@ -368,7 +384,7 @@ __global__ void __launch_bounds__(Shape8<D, NT>::THREADS, 1)
     cp_wait<2 * PAIRS - 1>();  // K and the scales have landed
     __syncwarp();
     const bool some = cur.w.hi > cur.w.lo;
-    const uint32_t ks = ring_s + 2 * pair * S::SLOT, vs = ks + S::SLOT;
+    const uint32_t k_at = k_lane + 2 * pair * S::SLOT, v_at = v_lane + 2 * pair * S::SLOT;
     const int j0 = cur.w.base(tile);
     float c[MT][NT][4];
     uint32_t odd = 0;  // positions with a value scale of NaN
@@ -396,15 +412,14 @@ __global__ void __launch_bounds__(Shape8<D, NT>::THREADS, 1)
           for (int e = 0; e < 4; ++e) c[mt][nt][e] = 0.f;
 #pragma unroll
         for (int hf = 0; hf < NH; ++hf) {
-          const uint32_t at = ks + (mt * 16 + gq) * D +
-                              ((D == 128 ? (hf * 4 + tq) ^ ((gq & 1) << 2) : tq) << 4);
+          const uint32_t at = (k_at ^ (hf << 6)) + mt * 16 * D;
           const uint4 x = lds16(at), y = lds16(at + 8 * D);
           const uint32_t xw[4] = {x.x, x.y, x.z, x.w}, yw[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
           for (int w = 0; w < 4; ++w) {
             uint32_t f[4];
-            code_halves<CODE>(xw[w], f[0], f[2]);
-            code_halves<CODE>(yw[w], f[1], f[3]);
+            code_row4<CODE>(xw[w], f[0], f[2]);
+            code_row4<CODE>(yw[w], f[1], f[3]);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
               M::mma(c[mt][nt], f, qf[nt][hf * 4 + w][0], qf[nt][hf * 4 + w][1]);
@@ -511,11 +526,8 @@ __global__ void __launch_bounds__(Shape8<D, NT>::THREADS, 1)
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int j = 0; j < NJ; j += 2) {
-          const int row = mt * 16 + (lane & 15), ch = j + (lane >> 4);
           uint32_t w[4];
-          ldsm_x4_trans(w[0], w[1], w[2], w[3],
-                        vs + row * D +
-                            ((D == 128 ? ch ^ (row & 7) : ch ^ ((row >> 1) & 3)) << 4));
+          ldsm_x4_trans(w[0], w[1], w[2], w[3], (v_at ^ (j << 4)) + mt * 16 * D);
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             uint32_t f[4];
@@ -645,11 +657,20 @@ __global__ void __launch_bounds__(Shape8<D, NT>::THREADS, 1)
       const int row = row0 + lane / C4;
       if (task % WARPS != warp || row >= nrows) continue;
       PagedState4 s{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+      for (int w = w0; w <= last; ++w) s.m = fmaxf(s.m, s_ml[w == last ? kind : 1][w][row].x);
+      const float ref = s.m == -INFINITY ? 0.f : s.m;
+#pragma unroll 4
       for (int w = w0; w <= last; ++w) {
         const int k = w == last ? kind : 1;
-        const float* src =
-            reinterpret_cast<const float*>(smem + w * S::WARP + (k ? 0 : S::RING)) + row * D + col;
-        s.join(s_ml[k][w][row].x, s_ml[k][w][row].y, *reinterpret_cast<const float4*>(src));
+        const float2 ml = s_ml[k][w][row];
+        const float4 o4 = *reinterpret_cast<const float4*>(
+            reinterpret_cast<const float*>(smem + w * S::WARP + (k ? 0 : S::RING)) + row * D + col);
+        const float x = ex2(ml.x - ref);
+        s.l = fmaf(ml.y, x, s.l);
+        s.o.x = fmaf(o4.x, x, s.o.x);
+        s.o.y = fmaf(o4.y, x, s.o.y);
+        s.o.z = fmaf(o4.z, x, s.o.z);
+        s.o.w = fmaf(o4.w, x, s.o.w);
       }
       if (here && kind == 0) {
         paged_store4<T, D>(s, p.out, p.lse, out_row(p, it, row), col);
