@@ -396,9 +396,9 @@ __global__ void __launch_bounds__(Shape8<D, NT>::THREADS, 1)
                      : "=f"(k), "=f"(v)
                      : "r"(scale_s + pair * S::SCALES + lane * 8));
         odd = __ballot_sync(~0u, there && v != v);
-        // (zero: the codes are zero too, and any scale will do; fmaxf takes a
-        // NaN for the bound)
-        const float vv = v == 0.f ? 0x1p-7f : fmaxf(v, 0x1p-60f);
+        // (zero: the codes are zero too, and any scale will do: a small one, which
+        // does not raise the row's maximum; fmaxf takes a NaN for the bound)
+        const float vv = v == 0.f ? 0x1p-30f : fmaxf(v, 0x1p-60f);
         const float ak = there ? k * qk : 0.f, bk = there ? lg2(vv) : -INFINITY;
         asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(prep_s + lane * 16), "f"(ak),
                      "f"(bk), "f"(rcp(vv)), "f"(0.f)

@@ -533,11 +533,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if (use >= S::SLOTS) wait_bar(&s_empty[ring.slot], ring.phase ^ 1u, err);
       ++use;
       if (key) {
-        // (zero: the codes are zero too, and any scale will do; fmaxf takes a
-        // NaN for the bound)
+        // (zero: the codes are zero too, and any scale will do: a small one, which
+        // does not raise the row's maximum; fmaxf takes a NaN for the bound)
         const float2 scale = s_raw[out_unit][row];
         if (++out_unit == S::AHEAD) out_unit = 0;
-        const float v = scale.y, vv = v == 0.f ? 0x1p-7f : fmaxf(v, 0x1p-60f);
+        const float v = scale.y, vv = v == 0.f ? 0x1p-30f : fmaxf(v, 0x1p-60f);
         Tc8Scales& sc = s_scale[buf];
         sc.a[row] = scale.x * p.scale_log2;
         sc.b[row] = lg2(vv);

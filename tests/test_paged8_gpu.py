@@ -364,3 +364,317 @@ def test_read_reports_what_lies_outside():
     k, v = rows([0, 5, 8, 10], [0, 0, 0], bad)
     assert kv.status() == RANGE and (k[:5] == 0).all() and (v[:5] == 0).all()
     assert kv.status() == OK
+
+
+# ------------------------------------------------- what the device reports --
+def with_starts(starts, kv_len, tokens, heads, **kw):
+    """A problem whose q_start is given as it is: malformed entries have no tokens."""
+    q_len = [b - a if 0 <= a <= b <= tokens else 0 for a, b in zip(starts, starts[1:])]
+    pr = Problem8(q_len, kv_len, *heads, extra_tokens=tokens - sum(q_len), **kw)
+    pr.starts = list(starts)
+    pr.q_start = torch.tensor(starts, dtype=torch.int32, device="cuda")
+    return pr
+
+
+@pytest.mark.parametrize("code", CODES)
+@pytest.mark.parametrize("starts,kv_len,tokens,heads", [
+    ([0, 64, 2000, 128, 192, 256, 320, 384, 448], [1000, 5, 5, 3000, 100, 64, 80, 90], 512, (8, 2)),
+    ([300, 400, 200, 300, 100, 200, 0, 100], [400, 1, 300, 1, 250, 1, 700], 400, (4, 2)),
+    ([8, 12, 0, 4], [20, 9, 30], 12, (1, 1)),
+    ([t if t not in (100, 170) else (-3, 10 ** 9)[t > 100] for t in range(251)],
+     [1 + 3 * (b % 50) for b in range(250)], 250, (8, 2)),
+    ([3 * t if t != 31 else 2 ** 31 - 1 for t in range(61)], [9 + b for b in range(60)], 180, (16, 1)),
+    ([5, 4, 3, 2, 1, 0], [5, 4, 3, 2, 1], 5, (8, 2)),
+    ([-2 ** 31, 2 ** 31 - 1, -2 ** 31, 2 ** 31 - 1], [50, 40, 30], 70, (8, 2)),
+], ids=["far", "falling", "swapped", "singles", "drafts", "none", "limits"])
+def test_sequences_beside_malformed_starts(code, starts, kv_len, tokens, heads):
+    pr = with_starts(starts, kv_len, tokens, heads, code=code, d=64)
+    r = Run8(pr)
+    want = ref_attention8(pr)
+    for _ in range(2):
+        r.out.fill_(NAN), r.lse.fill_(NAN)
+        r.attend()
+        assert r.kv.status() == RANGE
+        close(r.out, want[0], want[1], "out")
+        close(r.lse, want[2], want[3], "lse")
+
+
+@pytest.mark.parametrize("n", [3, 70])
+def test_tokens_claimed_twice_leave_the_rest_alone(n):
+    batch = 41
+    pr = Problem8([n] + [0] * (batch - 1), [n + 40 + 3 * b for b in range(batch)], 8, 2, d=64, extra_tokens=2)
+    r = Run8(pr)
+    good = pr.q_start.clone()
+    big = torch.full((3 * pr.tokens, pr.nq, pr.d), 7.0, dtype=r.out.dtype, device="cuda")
+    big_lse = torch.full((3 * pr.tokens, pr.nq), 7.0, device="cuda")
+    r.out, r.lse = big[pr.tokens:2 * pr.tokens], big_lse[pr.tokens:2 * pr.tokens]
+    for _ in range(3):
+        pr.q_start.copy_(torch.tensor([n * (b % 2) for b in range(batch + 1)], dtype=torch.int32))
+        r.attend()
+        assert r.kv.status() == RANGE
+        pr.q_start.copy_(good)
+        r.out.fill_(NAN), r.lse.fill_(NAN)
+        r.attend()
+        r.check()
+    for x in (big, big_lse):
+        assert (x[:pr.tokens] == 7).all() and (x[2 * pr.tokens:] == 7).all()
+
+
+@pytest.mark.parametrize("q_len", [[1, 2, 1, 1], [60, 70, 1, 40]], ids=str)
+def test_bad_lengths_and_pages_are_reported_and_stay_in_bounds(q_len):
+    pr = Problem8(q_len, [80, 90, 40, 93], 4, 2, max_pages=9)
+    r = Run8(pr)
+    good = ref_attention8(pr)
+    lens, table = pr.lens.clone(), pr.table.clone()
+    pr.lens[0] = -1
+    pr.lens[1] = pr.max_pages * pr.page + 1
+    pr.table[2, 1] = pr.num_pages  # positions 16..31 of sequence 2 have no page
+    r.attend()
+    assert r.kv.status() == RANGE and r.kv.status() == OK
+    n = pr.starts[2]
+    assert (r.out[:n] == 0).all() and torch.isinf(r.lse[:n]).all()
+    close(r.out[n + 1:], good[0][n + 1:], good[1][n + 1:], "the good sequence")
+    # zeros stand for the lost positions: as if their scales were zero
+    pr.table.copy_(table), pr.lens.copy_(lens)
+    ids = pr.table[2, 1].long()
+    pr.scales[ids] = 0
+    for pool in (pr.k_pages, pr.v_pages):
+        pool.view(torch.uint8)[ids] = 0
+    want = ref_attention8(pr)
+    close(r.out[n], want[0][n], want[1][n], "the sequence with a lost page")
+    close(r.lse[n], want[2][n], want[3][n], "the sequence with a lost page")
+
+
+@pytest.mark.parametrize("q_len,max_q", [([2, 3, 1], 2), ([70, 3, 40], 69)], ids=str)
+def test_more_tokens_than_max_q_are_reported(q_len, max_q):
+    pr = Problem8(q_len, [90, 30, 40], 4, 2)
+    r = Run8(pr)
+    good = ref_attention8(pr)
+    r.attend(max_q=max_q)
+    assert r.kv.status() == RANGE
+    for b in range(3):
+        rows = slice(pr.starts[b], pr.starts[b + 1])
+        if q_len[b] > max_q:
+            assert (r.out[rows] == 0).all() and torch.isinf(r.lse[rows]).all()
+        else:
+            close(r.out[rows], good[0][rows], good[1][rows], "a good sequence")
+
+
+# -------------------------------------------------------------- refusals --
+def test_refusals():
+    pr = Problem8([1, 2], [20, 30], 4, 2)
+    r = Run8(pr)
+    kv, INV, ALIAS = r.kv, binding.CF_ERR_INVALID_ARG, binding.CF_ERR_ALIAS
+    L, s = binding.lib(), torch.cuda.current_stream().cuda_stream
+    qp, kp, vp, sp, op = (x.data_ptr() for x in (pr.q, pr.k_pages, pr.v_pages, pr.scales, r.out))
+    base = dict(h=kv.handle, batch=2, n=3, max_q=2, q=qp, qs=512, st=pr.q_start.data_ptr(), kl=pr.lens.data_ptr(),
+                tab=pr.table.data_ptr(), k=kp, v=vp, sc=sp, w=0, sk=0, out=op, lse=None, stream=s)
+
+    def att(**kw):
+        return L.cf_paged8_attention(*dict(base, **kw).values())
+
+    for kw in (dict(batch=3), dict(n=4), dict(max_q=0), dict(max_q=4), dict(q=None), dict(q=qp + 2), dict(qs=511),
+               dict(qs=2 ** 62), dict(st=None), dict(kl=None), dict(tab=None), dict(k=None), dict(v=vp + 8), dict(sc=None),
+               dict(sc=sp + 4), dict(w=-1), dict(sk=-1), dict(out=None), dict(lse=r.lse.data_ptr() + 2)):
+        assert att(**kw) == INV, kw
+    for kw in (dict(out=qp), dict(out=kp), dict(out=vp), dict(out=sp), dict(lse=sp + 8), dict(lse=op),
+               dict(lse=pr.table.data_ptr())):
+        assert att(**kw) == ALIAS, kw
+    assert att(batch=0) == OK and att(n=0) == OK
+    ap = dict(h=kv.handle, b=2, n=3, q=qp, k=pr.k.data_ptr(), v=pr.v.data_ptr(), qs=512, ks=256, st=base["st"],
+              kl=base["kl"], rp=None, tab=base["tab"], kp=kp, vp=vp, sc=sp, qo=op, qos=512, stream=s)
+
+    def app(**kw):
+        return L.cf_paged8_append(*dict(ap, **kw).values())
+
+    for kw in (dict(b=3), dict(n=4), dict(st=None), dict(q=None), dict(qo=None), dict(k=None), dict(ks=255),
+               dict(qos=8), dict(kp=None), dict(vp=vp + 4), dict(sc=None), dict(sc=sp + 4), dict(rp=base["st"] + 2)):
+        assert app(**kw) == INV, kw
+    for kw in (dict(qo=qp, qos=520), dict(qo=ap["k"]), dict(qo=kp), dict(qo=sp), dict(k=kp), dict(v=vp), dict(vp=kp),
+               dict(tab=kp), dict(sc=kp), dict(sc=vp + 64), dict(k=sp)):
+        assert app(**kw) == ALIAS, kw
+    assert app(n=0) == OK
+    out = torch.empty(2, 8, pr.nkv, pr.d, dtype=torch.bfloat16, device="cuda")
+    rs = torch.tensor([0, 4, 8], dtype=torch.int32, device="cuda")
+    rd = dict(h=kv.handle, b=2, n=8, rs=rs.data_ptr(), first=None, tab=base["tab"], kp=kp, vp=vp, sc=sp,
+              ko=out[0].data_ptr(), vo=out[1].data_ptr(), os=256, stream=s)
+
+    def read(**kw):
+        return L.cf_paged8_read(*dict(rd, **kw).values())
+
+    for kw in (dict(b=3), dict(b=-1), dict(n=-1), dict(n=2 ** 30 + 1), dict(rs=None), dict(rs=rs.data_ptr() + 1),
+               dict(first=rs.data_ptr() + 2), dict(tab=None), dict(kp=None), dict(vp=vp + 8), dict(sc=None),
+               dict(sc=sp + 4), dict(ko=None, vo=None), dict(ko=rd["ko"] + 8), dict(os=255), dict(os=260)):
+        assert read(**kw) == INV, kw
+    for kw in (dict(ko=kp), dict(vo=vp), dict(ko=sp), dict(vo=rd["ko"]), dict(vo=rd["ko"] + 16), dict(ko=base["tab"] & ~15)):
+        assert read(**kw) == ALIAS, kw
+    assert read(n=0) == OK and read() == OK
+    assert kv.status() == OK
+    args = (2, 3, 2, pr.q, pr.q_start, pr.lens, pr.table, pr.k_pages, pr.v_pages, pr.scales, r.out)
+    for at, bad in ((3, pr.q.float()), (3, pr.q.cpu()), (3, pr.q[:2]), (4, pr.q_start.long()), (6, pr.table[:, :1].contiguous()),
+                    (7, pr.k_pages[1:]), (7, pr.k_pages.view(torch.int8)), (8, pr.v_pages.bfloat16()),
+                    (9, pr.scales[1:]), (9, pr.scales.double()), (9, pr.scales.transpose(0, 1)), (10, r.out[:2])):
+        with pytest.raises(binding.CfError):
+            kv.attention(*args[:at], bad, *args[at + 1:])
+    with pytest.raises(binding.CfError):
+        kv.prefix_attention(*args)
+    torch.cuda.synchronize()
+    assert r.out.isnan().all()
+
+
+# ------------------------------------------- streams, graphs, whole runs --
+def test_offsets_past_32_bits():
+    """Pools of more than 2^32 codes, scales of more than 2^31 bytes; the sequence's pages lie at their end."""
+    nkv, d, page = 8, 64, 64
+    num = 2 ** 32 // (nkv * d * page) + 1 << 1
+    if torch.cuda.mem_get_info()[0] < 4 * num * page * nkv * d:
+        pytest.skip("needs 35 GB of device memory")
+    g = torch.Generator(device="cuda").manual_seed(60)
+    kp, vp = (torch.zeros(num, page, nkv, d, dtype=torch.int8, device="cuda") for _ in range(2))
+    scales = torch.zeros(num, nkv, page, 2, device="cuda")
+    kv = binding.Paged8Kv(n_q_heads=8, n_kv_heads=nkv, head_dim=d, page_size=page, num_pages=num, max_pages=4,
+                          max_batch=2, max_tokens=300, dtype="f16", code="int8")
+    table = torch.tensor([[num - 1, num - 5, num - 9, num - 2], [0, 1, 2, num - 3]], dtype=torch.int32, device="cuda")
+    for n in ((200, 100), (1, 1)):
+        lens = torch.tensor([250, 256], dtype=torch.int32, device="cuda")
+        T = sum(n)
+        st = torch.tensor([0, n[0], T], dtype=torch.int32, device="cuda")
+        q, k, v = (torch.randn(T, 8, d, generator=g, device="cuda").half() for _ in range(3))
+        qr, o = torch.empty_like(q), torch.empty_like(q)
+        kv.append(2, T, q, k, v, st, lens, table, kp, vp, scales, qr)
+        kv.attention(2, T, max(n), qr, st, lens, table, kp, vp, scales, o)
+        rows = torch.tensor([0, 250, 506], dtype=torch.int32, device="cuda")
+        K, V = (torch.empty(506, nkv, d, dtype=torch.float16, device="cuda") for _ in range(2))
+        kv.read(2, 506, rows, None, table, kp, vp, scales, K, V)
+        assert kv.status() == OK
+        for b in range(2):
+            Kb, Vb = (x[int(rows[b]):int(rows[b + 1])].double() for x in (K, V))
+            new = v[int(st[b]):int(st[b + 1])].double()
+            assert ((Vb[int(lens[b]) - n[b]:] - new).abs() <= new.abs().amax(-1, keepdim=True) * (0.5 / 127 + 2.0 ** -10)).all()
+            s = torch.einsum("nhd,shd->hns", qr[int(st[b]):int(st[b + 1])].double(), Kb) / math.sqrt(d)
+            p = torch.arange(int(lens[b]) - n[b], int(lens[b]), device="cuda")[:, None]
+            s.masked_fill_(torch.arange(int(lens[b]), device="cuda")[None] > p, -math.inf)
+            want = torch.einsum("hns,shd->nhd", s.softmax(-1), Vb)
+            # keys and values are read back in fp16, half a step off each
+            err = (o[int(st[b]):int(st[b + 1])].double() - want).norm() / want.norm()
+            assert err <= 8 * 2.0 ** -11, err
+
+
+@pytest.mark.parametrize("code", CODES)
+@pytest.mark.parametrize("q_len", [[1], [3], [40]], ids=str)
+def test_flat_tails_far_below_the_largest_weight_count(code, q_len):
+    """One key of weight 1 and a value of 0, 20000 of 2^-26 and values of 1: the product has the tail as the sum has it.
+    Scores of 0 and 18 are off by (64 + 4) 2^-23 18 at most, and by 3 2^-23 (26 + 30 + 4) with the scales' logarithms,
+    weights relatively by twice that.  A weight of 2^-26 is held to 2^-33 (40 tokens) or 2^-41 of the largest."""
+    n, d = q_len[0], 64
+    pr = Problem8(q_len, [20000], 8, 2, d=d, page=64, code=code, dtype="f16")
+    top = CODE[code][1]
+    pr.k_pages.view(torch.uint8).zero_()
+    ones = torch.full((1,), top, device="cuda").to(CODE[code][0]).view(torch.uint8)
+    pr.v_pages.view(torch.uint8).fill_(int(ones))
+    pr.scales[..., 0] = 0
+    pr.scales[..., 1] = 1 / top
+    pr.q.zero_()
+    pr.q[..., 0] = 16.0
+    ids = pr.table[0, 0].long()
+    pr.k_pages.view(torch.uint8)[ids, 7, :, 0] = ones
+    pr.scales[ids, :, 7, 0] = 26 * math.log(2) * 8 / 16 / top
+    pr.v_pages.view(torch.uint8)[ids, 7] = 0
+    pr.scales[ids, :, 7, 1] = 0
+    r = Run8(pr, poison=False).attend()
+    assert r.kv.status() == OK
+    s = float(pr.scales[ids, 0, 7, 0]) * top * 16 / 8
+    w = math.exp(-s)
+    seen = torch.arange(20000 - n, 20000, dtype=torch.float64, device="cuda")
+    want = (seen * w / (1 + seen * w))[:, None, None].expand(r.out.shape)
+    ds, db = 68 * 2.0 ** -23 * s, 3 * 2.0 ** -23 * 60
+    held = 2.0 ** -11 + (2.0 ** -34 if n * 4 > 16 else 2.0 ** -42) / w
+    tol = want * (2.0 ** -11 + held + 2 * ds + 2 * db + 20008 * 2.0 ** -23) + 2.0 ** -25
+    close(r.out, want, tol, "out")
+
+
+@pytest.mark.parametrize("code", CODES)
+def test_calls_of_every_kind_repeat_their_bits_and_graphs_replay_with_other_lengths(code):
+    prs = [Problem8(q, kv, 8, 2, code=code, max_pages=40, spare=3) for q, kv in
+           (([1] * 5, [600, 3, 17, 250, 1]), ([4, 2, 0, 3], [500, 90, 5, 77]), ([200, 3, 90], [600, 30, 90]))]
+    runs = [Run8(p) for p in prs]
+    first = []
+    for r in runs:
+        r.attend().check()
+        first.append((r.out.clone(), r.lse.clone()))
+    for _ in range(4):
+        for r, f in zip(runs, first):
+            r.out.fill_(NAN)
+            r.attend()
+            assert torch.equal(r.out, f[0]) and torch.equal(r.lse, f[1])
+    graphs, streams = [], []
+    for r in runs:
+        s, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(g, stream=s):
+            r.attend()
+        graphs.append(g), streams.append(s)
+    for cut in (0, 1, 0):  # the graphs at once, each on its own handle and stream
+        for p, r in zip(prs, runs):
+            p.lens.copy_(torch.tensor([max(n - cut * 7, q) for n, q in zip(p.kv_len, p.q_len)], dtype=torch.int32))
+            r.out.fill_(NAN)
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for p, r, f in zip(prs, runs, first):
+            if cut == 0:
+                assert torch.equal(r.out, f[0])
+            else:
+                out, tol, lse, ltol = ref_attention8(p, kv_len=[int(x) for x in p.lens])
+                close(r.out, out, tol, "out")
+
+
+def test_current_stream_and_a_stream_that_is_given():
+    pr = Problem8([1, 1], [300, 17], 4, 2)
+    r = Run8(pr)
+    want = ref_attention8(pr)
+    s = torch.cuda.Stream()
+    for how in ("current", "given", "raw"):
+        r.out.fill_(NAN)
+        s.wait_stream(torch.cuda.current_stream())
+        if how == "current":
+            with torch.cuda.stream(s):
+                r.attend()
+        else:
+            r.attend(stream=s if how == "given" else s.cuda_stream)
+        s.synchronize()
+        close(r.out, want[0], want[1], how)
+
+
+@pytest.mark.parametrize("code,dtype", [("e4m3", "bf16"), ("int8", "f16")])
+def test_prompt_in_chunks_then_steps(code, dtype):
+    """A prompt appended and attended in chunks of 1, 7, 64 and 200 tokens, then steps: the cache holds the same codes
+    as after one append of everything, and each row is what the reference makes of that cache."""
+    n = 330
+    one = Problem8([n], [n], 8, 2, code=code, dtype=dtype, max_pages=32, spare=12)
+    q_rot = append(one)
+    whole = [one.k_pages.clone(), one.v_pages.clone(), one.scales.clone()]
+    kv = binding.Paged8Kv(**one.config())
+    one.k_pages.view(torch.uint8).zero_(), one.v_pages.view(torch.uint8).zero_(), one.scales.zero_()
+    out = torch.full_like(one.q, NAN)
+    at = 0
+    for c in (200, 64, 7, 1, 50, 1, 1, 1, 5):
+        rows = slice(at, at + c)
+        at += c
+        lens = torch.tensor([at], dtype=torch.int32, device="cuda")
+        st = torch.tensor([0, c], dtype=torch.int32, device="cuda")
+        qr = torch.empty_like(one.q[rows])
+        kv.append(1, c, one.q[rows], one.k[rows], one.v[rows], st, lens, one.table, one.k_pages, one.v_pages, one.scales, qr)
+        assert torch.equal(qr, q_rot[rows])
+        kv.attention(1, c, c, qr, st, lens, one.table, one.k_pages, one.v_pages, one.scales, out[rows])
+    assert at == n and kv.status() == OK
+    held = one.held(0, 0, n)
+    for i, pool in enumerate((one.k_pages, one.v_pages)):
+        ids = one.table[0, :-(-n // one.page)].long()
+        assert torch.equal(pool.view(torch.uint8)[ids][:n // one.page], whole[i].view(torch.uint8)[ids][:n // one.page])
+    assert all(torch.isfinite(x).all() for x in held)
+    one.q = q_rot
+    want, tol, _, _ = ref_attention8(one)
+    close(out, want, tol, "out")
