@@ -31,6 +31,7 @@
 #include <algorithm>
 #include <cstring>
 #include <new>
+#include <type_traits>
 
 #include "cf_cluster.cuh"
 #include "cf_common.cuh"
@@ -277,7 +278,7 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr) {
 template <typename T, int NT>
 constexpr int kPerSm = NT * W4Type<T>::PARTS <= 2 ? 2 : 1;
 template <int NT>
-constexpr int kWide = NT <= 4 ? 4 : 2;
+constexpr int kWide = NT == 1 || NT == 4 ? 4 : 2;
 
 // Block `blockIdx.x % split` of its cluster takes its share of k for column
 // share blockIdx.x / split.
@@ -390,9 +391,11 @@ __global__ void __launch_bounds__(kW4Threads, kPerSm<T, NT>)
       for (int j = 0; j < NT; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e) y[b][j][e] = 0.f;
-    for (int i = 0; i < n; ++i) {
-      if (!AHEAD) load_x(x[0], i, 0);
-      mbar_wait(&s_full[warp][slot], phase, a.errflag);
+    // One step for a number of blocks that is known when this is compiled: their
+    // chains of products then run side by side (one row, 4096 x 22016: 15.3 ->
+    // 14.5 us).  With more rows the copies of the code spill, and it is asked.
+    auto products = [&](auto width, int i) {
+      constexpr int WIDE = decltype(width)::value;
       const uint8_t* rec = mem + slot * slot_bytes;
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
@@ -408,8 +411,8 @@ __global__ void __launch_bounds__(kW4Threads, kPerSm<T, NT>)
         const uint8_t* scale = scale0 + slot * slot_bytes + half * half_at * (int)sizeof(T);
         const uint8_t* zero = zero0 + slot * slot_bytes + half * half_at * 2;
 #pragma unroll
-        for (int b = 0; b < BL; ++b) {
-          if (b >= wide) break;
+        for (int b = 0; b < WIDE; ++b) {
+          if (NT > 2 && b >= wide) break;
           const uint4 c =
               *reinterpret_cast<const uint4*>(rec + b * s.record + (half * 32 + lane) * 16);
           const uint32_t cw[4] = {c.x, c.y, c.z, c.w};
@@ -451,6 +454,20 @@ __global__ void __launch_bounds__(kW4Threads, kPerSm<T, NT>)
             }
           }
         }
+      }
+    };
+    for (int i = 0; i < n; ++i) {
+      if (!AHEAD) load_x(x[0], i, 0);
+      mbar_wait(&s_full[warp][slot], phase, a.errflag);
+      if (NT > 2 || wide == BL)
+        products(std::integral_constant<int, BL>(), i);
+      else if (wide == 1)
+        products(std::integral_constant<int, 1>(), i);
+      else if constexpr (BL == 4) {
+        if (wide == 2)
+          products(std::integral_constant<int, 2>(), i);
+        else
+          products(std::integral_constant<int, 3>(), i);
       }
       __syncwarp();  // the slot is read
       if (lane == 0 && pass * n + i + kStages < total) copy(false);
@@ -527,7 +544,7 @@ constexpr int kMaxSmem = 160 * 1024;  // fp32, groups of 32, zeros, 32 rows: 156
 W4Plan w4_plan(const W4Shape& s, int dtype, int rows, int sms) {
   W4Plan p;
   p.nt = rows <= 8 ? 1 : rows <= 16 ? 2 : rows <= 32 ? 4 : 8;
-  p.wide = p.nt <= 4 ? 4 : 2;
+  p.wide = p.nt == 1 ? kWide<1> : p.nt == 2 ? kWide<2> : p.nt == 4 ? kWide<4> : kWide<8>;
   p.per_sm = p.nt * (dtype == CF_F32 ? 3 : 1) <= 2 ? 2 : 1;
   p.smem = kWarps * (kStages * p.wide * s.record + 8 * p.nt * (p.wide * kBlockN + 4) * 4);
   // Splitting k shortens the steps of a warp where columns are too few for the
