@@ -547,18 +547,23 @@ W4Plan w4_plan(const W4Shape& s, int dtype, int rows, int sms) {
   p.wide = p.nt == 1 ? kWide<1> : p.nt == 2 ? kWide<2> : p.nt == 4 ? kWide<4> : kWide<8>;
   p.per_sm = p.nt * (dtype == CF_F32 ? 3 : 1) <= 2 ? 2 : 1;
   p.smem = kWarps * (kStages * p.wide * s.record + 8 * p.nt * (p.wide * kBlockN + 4) * 4);
-  // Splitting k shortens the steps of a warp where columns are too few for the
-  // SMs, and costs the exchange.  In cycles: a step's x and loop 150 and 50 more
-  // for each 8 rows, a block of columns 200 and 60; an exchange 2500.
-  const int slots = p.per_sm * sms;
+  // Splitting k shortens a warp's way along it where columns are too few for the
+  // SMs, and costs the exchange.  In cycles, roughly: a step's x and loop 500 and
+  // 100 more for each 8 rows, a block of columns 550 and 100; an exchange 1500,
+  // twice that with two blocks to an SM.  Clusters do not fill the SMs: seven
+  // eighths of the places, with eight blocks half of them.  One row, us with 1, 2,
+  // 4, 8: 14336 x 256 9.9, 6.5, 4.7, 3.9; 14336 x 4096 12.4, 11.4, 16.3, 21.2;
+  // 4096 x 12288 8.6, 11.2.
+  const int places = p.per_sm * sms;
   long long best = -1;
   for (int split = 1; split <= kMaxSplit && split <= s.units; split *= 2) {
+    const int slots = split == 1 ? places : split == 8 ? places / 2 : places * 7 / 8;
     const int shares = std::max(1, std::min(s.blocks, slots / split));
     const long long blocks = (s.blocks + shares - 1) / shares;
     const long long passes = (blocks + p.wide - 1) / p.wide;
     const long long steps = ((s.units + split - 1) / split + kWarps - 1) / kWarps;
-    const long long cost = steps * (passes * (150 + 50 * p.nt) + blocks * (200 + 60 * p.nt)) +
-                           (split > 1 ? 2500 * passes : 0);
+    long long cost = steps * (passes * (500 + 100 * p.nt) + blocks * (550 + 100 * p.nt));
+    if (split > 1) cost += passes * (shares * split > sms ? 3000 : 1500);
     if (best < 0 || cost < best) {
       best = cost;
       p.split = split;
