@@ -2,8 +2,10 @@
 // rows per KV head: single tokens and short drafts (tokens x grouped heads <=
 // 16).
 //
-// Bound by the cache's bytes, with half as many of them to the arithmetic of
-// the 16-bit cache: the work per byte decides the form.  Keys and values are
+// 16 sequences of 4097 positions, 32 / 8 heads of 128: 36 us, 3.9 TB/s (the 16-bit
+// cache: 54); 32 of 2048-32768: 199, 5.8 TB/s; one of 1025, 32 heads: 12; 4 draft
+// tokens of 32 sequences of 1005-4100 (16 rows): 61.  Half the bytes to the
+// arithmetic of the 16-bit cache: the work per byte decides the form.  Keys and values are
 // the A operand of mma.sync m16n8k16 and the rows its B operand, in octets:
 // S^T = K Q^T (16 keys x 8 rows) and O^T = V^T P^T (16 columns x 8 rows), so
 // up to 8 rows cost half the products, exponentials and registers of a 16-row
@@ -16,6 +18,12 @@
 // value j is exp(s_j) vs_j = 2^(a_j q.k_j + b_j), so one fused product, one
 // maximum and one exponential serve the weights, whatever the scales are; the
 // sum of exp(s_j) takes the weight times 1 / vs_j.
+//
+// A unit of 32 positions takes a warp 820 instructions (e4m3, 8 rows), 55 % of the
+// SM's issue slots at the copy rate, but 5500 cycles: with three warps to a
+// scheduler the chains are not hidden.  16 warps of 128 registers spill (40 us for
+// 36), 10 with two units on their way have fewer to switch between (41).  A fixed
+// 10-12 us are the schedule, the first loads and the joins.
 //
 // The cut of the work, rings and joins are those of cf_paged_few.cu: the key
 // tiles of all (sequence, KV head) items are one line that the warps share
@@ -37,6 +45,8 @@ namespace {
 constexpr int KS = 32;  // positions of a unit
 
 // One block per SM.
+// NT octets of rows: with one the kernel takes 36 us for 4 rows (16 sequences of
+// 4097 positions), with two 44.
 template <int D, int NT>
 struct Shape8 {
   static constexpr int WARPS = NT == 1 ? 12 : 8, THREADS = 32 * WARPS;

@@ -31,15 +31,16 @@
  *
  * Arithmetic: codes are whole in the products, which run on the tensor cores
  * as fp16 x fp16 with fp32 sums.  The query enters as fp16: bf16 queries are
- * multiplied by a power of two, the same for the rows that share a tile, and
- * lose only what is below 2^-32 of the tile's largest element.  Scales and
- * softmax statistics are fp32; weights exp(s_j) vs_j enter the second product
- * in fp16, held down to 2^-32 of the row's largest; the sum of exp(s_j) is
- * taken before that rounding.  Scales that are read must be NaN or from 0 to
- * 2^60, value scales other than 0 at least 2^-60; e4m3 codes must not be NaN
- * (0x7f, 0xff: they count as +-480).  Appending fp16 keeps to both, and so does
- * bf16 between 2^-50 and 2^60.  Outputs are rounded once.  The same call on
- * the same data gives the same bits.
+ * multiplied by a power of two, the same for the rows that share a tile (with
+ * max_q * nq/nkv above 16: for rows whose largest element is not between 2^-10
+ * and 2^15), and lose only what is below 2^-32 of the tile's largest element, or
+ * of 1.  Scales and softmax statistics are fp32; weights exp(s_j) vs_j enter the
+ * second product in fp16, held down to 2^-32 of the row's largest; the sum of
+ * exp(s_j) is taken before that rounding.  Scales that are read must be NaN or
+ * from 0 to 2^60, value scales other than 0 at least 2^-60 (appending fp16 keeps
+ * to that, and so does bf16 between 2^-50 and 2^60), and e4m3 codes not NaN (0x7f,
+ * 0xff; none is appended).  Outputs are rounded once.  The same call on the same
+ * data gives the same bits.
  *
  * Conventions, and what the device records (cf_paged8_get_status), are those
  * of cf_paged.h; scales are 8-byte aligned.
