@@ -117,13 +117,17 @@ __global__ void __launch_bounds__(Shape8<D, NT>::THREADS, 1)
     mine += (long long)t * p.g.nkv;
     top = max(top, t);
   }
+  const int own_tiles = top;  // (of the lane's one sequence)
   top = __reduce_max_sync(~0u, top);
-  long long incl = mine;
+  auto scan = [&](long long x) {  // sums up to each lane's
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long v = __shfl_up_sync(~0u, incl, o);
-    if (lane >= o) incl += v;
-  }
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(~0u, x, o);
+      if (lane >= o) x += v;
+    }
+    return x;
+  };
+  long long incl = scan(mine);
   long long before = incl - mine, total = __shfl_sync(~0u, incl, 31);
   if (!small) {
     if (lane == 31) {
@@ -143,6 +147,22 @@ __global__ void __launch_bounds__(Shape8<D, NT>::THREADS, 1)
   const long long block_upc = div_units(total + gridDim.x * WARPS - 1, gridDim.x * WARPS) * WARPS;
   if (lane == 0) s_has[0][warp] = s_has[1][warp] = 0;
   if (!small) __syncthreads();
+  // Where there is little work, an item takes whole blocks: it is cut into fewer
+  // parts, and no block has parts of two (one sequence of 4097 positions, 32 / 8
+  // heads of 128: 14.0 us without, 12.7 with; of 101: 10.0 and 8.4).
+  int pad = 0;
+  if (small && block_upc <= 4 * WARPS) {
+    const int n = (int)block_upc, wide = (own_tiles + n - 1) / n * n;
+    const long long padded = scan((long long)wide * p.g.nkv);
+    const long long all = __shfl_sync(~0u, padded, 31);
+    if (all <= gridDim.x * block_upc) {
+      pad = n;
+      mine = (long long)wide * p.g.nkv;
+      before = padded - mine;
+      total = all;
+    }
+  }
+  auto units = [&](int tiles) { return pad ? (tiles + pad - 1) / pad * pad : tiles; };
 
   // A cursor at unit u of the line.
   auto locate = [&](Cursor<KS, false>& c, long long u) {
@@ -161,15 +181,16 @@ __global__ void __launch_bounds__(Shape8<D, NT>::THREADS, 1)
     int b = (n - 1) * per;
     while (true) {
       c.w = work_of<KS, false>(p, b);
-      const long long len = (long long)c.w.tiles * p.g.nkv;
+      const long long len = (long long)units(c.w.tiles) * p.g.nkv;
       if (u < at + len || b + 1 >= p.batch) break;
       at += len;
       ++b;
     }
     c.b = b;
     const long long off = u - at;
-    c.h = (int)div_units(off, max(c.w.tiles, 1));
-    c.tile = (int)(off - (long long)c.h * c.w.tiles);
+    const int wide = units(c.w.tiles);
+    c.h = (int)div_units(off, max(wide, 1));
+    c.tile = (int)(off - (long long)c.h * wide);
     c.i0 = u - c.tile;
     c.u = u;
   };
@@ -179,7 +200,7 @@ __global__ void __launch_bounds__(Shape8<D, NT>::THREADS, 1)
   Cursor<KS, false> at;
   long long lo = min(total, blockIdx.x * block_upc), hi = min(total, lo + block_upc);
   const bool snap =
-      block_upc >= 3LL * top && (top <= 16 + 2 * a.row_limit || block_upc >= 8LL * top);
+      !pad && block_upc >= 3LL * top && (top <= 16 + 2 * a.row_limit || block_upc >= 8LL * top);
   if (snap) {
     if (lo < total) {
       locate(at, lo);
@@ -191,6 +212,10 @@ __global__ void __launch_bounds__(Shape8<D, NT>::THREADS, 1)
     }
   }
   if (lo >= hi) return;
+  if (pad) {  // without what only fills the last block
+    locate(at, lo);
+    hi = min(hi, at.i0 + at.w.tiles);
+  }
   // and this warp's run of them
   const int run = (int)((hi - lo + WARPS - 1) / WARPS);
   at.u = lo + (long long)warp * run;
