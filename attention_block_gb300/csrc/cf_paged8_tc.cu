@@ -23,14 +23,18 @@
 // nothing that lies in a slot reaches a row that does not see it; a NaN among
 // a tile's value scales is set in the weights of the rows that see it.
 //
-// 512 tokens behind 15872 (32 / 8 heads of 128): 180 us, 750 TFLOP/s; 4 chunks of
-// 257-1024 tokens behind 0-2049, 32 heads: 222.  Bound by the softmax: it is busy
-// for 4000 of a unit's 6100 cycles (2050 of them products), waiting on shared
-// memory for the positions' a, b, c.  Accumulator fragments, with which a thread
-// needs a quarter of them, take 186 and 316 us (205 and 272 in two passes of 32
-// columns each): their chains are longer.  code x scale rounded to fp16 as
-// operand, with powers of two alone in the softmax, takes 163 and 215, but puts
-// 2.7 times the error of an fp16 result on it.
+// 512 tokens behind 15872 (32 / 8 heads of 128): 178 us, 760 TFLOP/s; 4 chunks of
+// 820-1024 tokens behind 195-1752, 32 heads: 207.  A half's tiles are a chain: 3450
+// cycles softmax, 1950 until the next scores are there (products of both halves
+// 2050).  Of the softmax, reading the positions' a, b, c takes up to a sixth: without
+// them 150 and 205 us.  Accumulator fragments, with which a thread needs a quarter of
+// them, take 186 and 316 (205 and 272 in two passes of 32 columns each): their chains
+// are longer.  code x scale rounded to fp16 as operand, with powers of two alone
+// in the softmax, takes 163 and 215, but puts 2.7 times the error of an fp16
+// result on it.  An item's result takes 5500-7500 cycles, its queries 8000 (bf16:
+// 18000), some behind the last tiles.  Queries by halves, and half 1's last product
+// behind the next item's first scores, let the halves fall out of step: 4 chunks of
+// bf16, GQA, 199 us for 190.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -64,6 +68,12 @@ struct Tc8Scales {
   uint32_t odd[kBN / 32];
 };
 
+// What an item costs apart from its tiles, in tiles: its queries, its result, the
+// halves out of step.  4 chunks of 820-1024 tokens, 32 heads: 207 us with 4, 210
+// with 5, 211 with 6; one chunk of 512 behind 15872: 178, 182, 182.
+constexpr int kItemCost8 = 4;
+using Cursor = TcCursor<false, kItemCost8>;
+
 struct Tc8Args {
   PagedAttnParams p;
   PagedParts ws;
@@ -80,6 +90,12 @@ __device__ __forceinline__ void sts16(uint32_t at, uint32_t x, uint32_t y, uint3
                : "memory");
 }
 
+// Maxima of the 16-bit halves.
+__device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
+  asm("max.u16x2 %0, %0, %1;" : "+r"(a) : "r"(b));
+  return a;
+}
+
 template <typename T, int D, int CODE>
 __global__ void __launch_bounds__(kTcThreads, 1)
     paged8_tc_kernel(const __grid_constant__ Tc8Args a) {
@@ -89,8 +105,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const PagedAttnParams& p = a.p;
   extern __shared__ __align__(1024) uint8_t sm[];
   __shared__ long long s_scan[kTcThreads / 32];
-  __shared__ TcCursor<false> s_cur;
-  __shared__ TcCursor<false> s_wcur[16];  // each warp's place: too much for registers
+  __shared__ Cursor s_cur;
+  __shared__ Cursor s_wcur[16];  // each warp's place: too much for registers
   __shared__ __align__(8) uint64_t s_full[S::SLOTS], s_empty[S::SLOTS];
   __shared__ __align__(8) uint64_t s_qfull, s_qempty, s_done;
   __shared__ __align__(8) uint64_t s_sfull[2], s_pfull[2], s_ofull[2];
@@ -138,7 +154,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   while (true) {
     mine = 0;
     share.walk(p, [&](const RowTile& t) {
-      mine += (long long)(t.tiles + kItemCost) * p.g.nkv;
+      mine += (long long)(t.tiles + kItemCost8) * p.g.nkv;
       mine_t = t;
       return false;
     });
@@ -184,13 +200,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
   if (warp < 8) {
     // ------------------------------------------------------------ softmax --
+    // 72 for the others: the codes do not spill, and the two below less than with 56
+    // (4 chunks, 32 heads: 211 us, with 88 and 56 214); softmax of 176 spills (221).
     set_regs_up<184>();
     const int hf = warp >> 2;                   // half
     const int r = (warp & 3) * 32 + lane;       // row of the half = TMEM lane
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lanes + S::S_COL + hf * kBN;
     const uint32_t to = tmem + lanes + S::O_COL + hf * D;
-    TcCursor<false>& cur = s_wcur[warp];
+    Cursor& cur = s_wcur[warp];
     if (lane == 0) cur = s_cur;
     __syncwarp();
     uint32_t n_tiles = 0;  // active tiles so far: parity of the barriers
@@ -428,9 +446,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
   } else if (warp < 12) {
     // -------------------------------------------------------------- codes --
-    set_regs_down<88>();
+    set_regs_down<72>();
     const int lw = warp - 8;  // rows 32 lw .. 32 lw + 31 of every tile
-    TcCursor<false>& cur = s_wcur[warp];
+    Cursor& cur = s_wcur[warp];
     if (lane == 0) cur = s_cur;
     __syncwarp();
     constexpr int C = D / 16;    // 16-byte pieces of a row's codes
@@ -558,9 +576,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     cp_wait<0>();
   } else if (warp > 12) {
     // ------------------------------------------------------------ queries --
-    set_regs_down<56>();
+    set_regs_down<72>();
     const int qw = warp - 13;
-    TcCursor<false>& cur = s_wcur[warp];
+    Cursor& cur = s_wcur[warp];
     if (lane == 0) cur = s_cur;
     __syncwarp();
     constexpr int C = D / 8;    // 16-byte chunks of a row
@@ -572,52 +590,83 @@ __global__ void __launch_bounds__(kTcThreads, 1)
              (uint32_t)((c0 >> 3) * (kBN * 128) + (row & (kHalf - 1)) * 128 +
                         (((c0 & 7) ^ (row & 7)) << 4));
     };
+    // x / G for a row's place behind the first token of its tile
+    const uint32_t over = 0xffffffffu / (uint32_t)p.g.G + 1u;
+    constexpr int U = 4;  // copies, and rows' chunks in work, at a time
     uint32_t items = 0;
     while (cur.u < u1) {
       const RowTile& t = cur.t;
       const int count = (int)min((long long)(t.tiles - cur.tile), u1 - cur.u);
+      // in registers: the next item's first products wait for its queries
+      const int gr0 = t.j * 2 * kHalf, i0 = gr0 / p.g.G, rem = gr0 - i0 * p.g.G;
+      const int left = t.rows - gr0;
+      const T* q = static_cast<const T*>(p.q) + (int64_t)(t.t0 + i0) * p.q_stride +
+                   (int64_t)cur.h * p.g.G * D + c0 * 8;
       if (items) wait_bar(&s_qempty, (items - 1) & 1, err);
-      for (int g = qw; g < NG; g += 3) {
-        const int row = g * RP + r0, gr = t.j * 2 * kHalf + row, i = gr / p.g.G;
-        const T* src = static_cast<const T*>(p.q) + (int64_t)(t.t0 + i) * p.q_stride +
-                       (int64_t)(cur.h * p.g.G + gr - i * p.g.G) * D + c0 * 8;
-        cp16(chunk(row), gr < t.rows ? src : static_cast<const T*>(p.q), gr < t.rows);
+#pragma unroll 1
+      for (int g0 = qw; g0 < NG; g0 += 3 * U) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int g = g0 + 3 * u, row = g * RP + r0;
+          if (g >= NG) break;
+          const int x = rem + row, i = p.g.G == 1 ? x : (int)__umulhi(x, over);
+          const T* src = q + i * p.q_stride + (x - i * p.g.G) * D;
+          cp16(chunk(row), row < left ? src : static_cast<const T*>(p.q), row < left);
+        }
       }
       cp_commit();
       cp_wait<0>();
       if constexpr (kIsBf16<T>) {
         // a thread's own chunks, in place
-        for (int g = qw; g < NG; g += 3) {
-          const int row = g * RP + r0;
-          uint32_t x[4];
-          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                       : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
-                       : "r"(chunk(row)));
-          uint32_t top = 0;  // largest finite magnitudes of the row, as bits
+#pragma unroll 1
+        for (int g0 = qw; g0 < NG; g0 += 3 * U) {
+          uint32_t x[U][4], top[U];  // largest finite magnitudes of the rows, as bits
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint32_t y = x[e] & 0x7fffu, z = (x[e] >> 16) & 0x7fffu;
-            if (y < 0x7f80u) top = max(top, y);
-            if (z < 0x7f80u) top = max(top, z);
+          for (int u = 0; u < U; ++u)  // (behind the last chunk: the first again)
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(x[u][0]), "=r"(x[u][1]), "=r"(x[u][2]), "=r"(x[u][3])
+                         : "r"(chunk((g0 + 3 * u < NG ? g0 + 3 * u : g0) * RP + r0)));
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            uint32_t y = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y = max2(y, x[u][e] & 0x7fff7fffu);
+            top[u] = max(y & 0xffffu, y >> 16);
+            if (top[u] >= 0x7f80u) {  // infinities and NaN do not count
+              top[u] = 0;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const uint32_t lo = x[u][e] & 0x7fffu, hi = (x[u][e] >> 16) & 0x7fffu;
+                if (lo < 0x7f80u) top[u] = max(top[u], lo);
+                if (hi < 0x7f80u) top[u] = max(top[u], hi);
+              }
+            }
           }
 #pragma unroll
-          for (int d = C / 2; d >= 1; d >>= 1) top = max(top, __shfl_xor_sync(~0u, top, d));
-          // exponents -10 .. 14 of the largest stay: what is lost then is below 2^-25
-          const int e = (int)(top >> 7) - 127;
-          float up = 1.f, down = 1.f;
-          if (top != 0 && (e > 14 || e < -10)) {
-            const int s = min(max(14 - e, -113), 113);
-            up = __uint_as_float((uint32_t)(127 + s) << 23);
-            down = __uint_as_float((uint32_t)(127 - s) << 23);
-          }
+          for (int d = C / 2; d >= 1; d >>= 1)
 #pragma unroll
-          for (int e2 = 0; e2 < 4; ++e2) {
-            float f[2];
-            Elem<T>::words(&x[e2], 1, f);
-            x[e2] = pack2<__half>(f[0] * up, f[1] * up);
+            for (int u = 0; u < U; ++u) top[u] = max(top[u], __shfl_xor_sync(~0u, top[u], d));
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const int g = g0 + 3 * u, row = g * RP + r0;
+            if (g >= NG) break;
+            // exponents -10 .. 14 of the largest stay: what is lost then is below 2^-25
+            const int e = (int)(top[u] >> 7) - 127;
+            float up = 1.f, down = 1.f;
+            if (top[u] != 0 && (e > 14 || e < -10)) {
+              const int s = min(max(14 - e, -113), 113);
+              up = __uint_as_float((uint32_t)(127 + s) << 23);
+              down = __uint_as_float((uint32_t)(127 - s) << 23);
+            }
+#pragma unroll
+            for (int e2 = 0; e2 < 4; ++e2) {
+              float f[2];
+              Elem<T>::words(&x[u][e2], 1, f);
+              x[u][e2] = pack2<__half>(f[0] * up, f[1] * up);
+            }
+            sts16(chunk(row), x[u][0], x[u][1], x[u][2], x[u][3]);
+            if (c0 == 0) s_qf[items & 1][row] = down;
           }
-          sts16(chunk(row), x[0], x[1], x[2], x[3]);
-          if (c0 == 0) s_qf[items & 1][row] = down;
         }
       }
       fence_proxy_async_smem();
@@ -633,13 +682,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
   } else {
     // ---------------------------------------------------------------- mma --
-    set_regs_down<56>();
+    set_regs_down<72>();
     // The whole warp walks (its operands then lie in uniform registers); one
     // elected thread issues.
     {
       constexpr uint32_t id_s = idesc_kind_f16(false, kHalf, kBN);
       constexpr uint32_t id_o = idesc_kind_f16(false, kHalf, D) | (1u << 16);  // B is N-major
-      TcCursor<false>& cur = s_wcur[12];
+      Cursor& cur = s_wcur[12];
       if (lane == 0) cur = s_cur;
       __syncwarp();
       const bool leader = elect_one();
@@ -680,6 +729,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const TileCheck<false> tc(cur.t);
         const int ns = cur.t.ns, skip = cur.t.skip, first = cur.tile;
         const int count = (int)min((long long)(cur.t.tiles - first), u1 - cur.u);
+        // the tiles that both halves see whole, but for the run's last
+        int mid_lo, mid_hi;
+        tc.middle(p, first, first + count - 1, ns, skip, mid_lo, mid_hi);
         wait_bar(&s_qfull, items & 1, err);
         ++items;
         tc05_fence_after();
@@ -725,9 +777,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             __syncwarp();
           }
         };
-        // the tiles that both halves see whole, but for the run's last
-        int mid_lo, mid_hi;
-        tc.middle(p, first, first + count - 1, ns, skip, mid_lo, mid_hi);
 #pragma unroll 1
         for (int tile = first; tile < first + count; ++tile) {
           if (tile == mid_lo && mid_lo < mid_hi) {

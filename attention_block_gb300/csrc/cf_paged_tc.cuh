@@ -258,9 +258,9 @@ struct TileCheck {
 };
 
 // A walk over a block's units: row tiles, KV heads, key tiles.  On the line of
-// units an item has kItemCost empty ones before its tiles, so that blocks with
+// units an item has COST empty ones before its tiles, so that blocks with
 // many small items get fewer of them.
-template <bool PRE>
+template <bool PRE, int COST = kItemCost>
 struct TcCursor {
   RowTile t;
   int h, tile;
@@ -270,7 +270,7 @@ struct TcCursor {
     ++u;
     if (++tile < t.tiles) return u >= end;
     tile = 0;
-    u += kItemCost;
+    u += COST;
     i0 = u;
     if (++h < p.g.nkv) return true;
     h = 0;
@@ -350,10 +350,10 @@ struct TcShare {
 
 // Sets c to unit u of the line if that lies in the row tile t, whose units
 // begin at `at`; else at moves on behind the row tile.
-template <bool PRE>
+template <bool PRE, int COST>
 CF_HOST_DEVICE bool start_in(const PagedAttnParams& p, const RowTile& t, long long u, long long& at,
-                             TcCursor<PRE>& c) {
-  const int len = t.tiles + kItemCost;
+                             TcCursor<PRE, COST>& c) {
+  const int len = t.tiles + COST;
   const long long n = (long long)len * p.g.nkv;
   if (u >= at + n) {
     at += n;
@@ -361,7 +361,7 @@ CF_HOST_DEVICE bool start_in(const PagedAttnParams& p, const RowTile& t, long lo
   }
   c.t = t;
   c.h = (int)div_units(u - at, len);
-  c.i0 = at + (long long)c.h * len + kItemCost;
+  c.i0 = at + (long long)c.h * len + COST;
   c.tile = u > c.i0 ? (int)(u - c.i0) : 0;
   c.u = c.i0 + c.tile;
   return true;
