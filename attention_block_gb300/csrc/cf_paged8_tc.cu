@@ -19,11 +19,12 @@
 //   12        one thread issues S = Q K^T and O += P V
 //   13-15     queries: copied, and where they are bf16 turned into fp16 in
 //             place, a row that would leave fp16's range times a power of two
+//             (of the first item together with the softmax warps)
 // What a row does not see gets a weight of exactly 0, and codes are finite, so
 // nothing that lies in a slot reaches a row that does not see it; a NaN among
 // a tile's value scales is set in the weights of the rows that see it.
 //
-// 512 tokens behind 15872 (32 / 8 heads of 128): 178 us, 760 TFLOP/s; 4 chunks of
+// 512 tokens behind 15872 (32 / 8 heads of 128): 171 us, 790 TFLOP/s; 4 chunks of
 // 820-1024 tokens behind 195-1752, 32 heads: 207.  A half's tiles are a chain: 3450
 // cycles softmax, 1950 until the next scores are there (products of both halves
 // 2050).  Of the softmax, reading the positions' a, b, c takes up to a sixth: without
@@ -102,13 +103,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   using S = Tc8Shape<D>;
   constexpr int LIFT = weight_lift<__half>(kGrow);
   constexpr float BACK = 1.f / (1 << LIFT);
+  // Warps that bring the first item's queries: turning them takes longer than the
+  // softmax warps' help costs (bf16, 512 behind 15872 171 us, with 3 178; fp16, 4
+  // chunks 210, with 3 208).
+  constexpr int FIRST = kIsBf16<T> ? 11 : 3;
   const PagedAttnParams& p = a.p;
   extern __shared__ __align__(1024) uint8_t sm[];
   __shared__ long long s_scan[kTcThreads / 32];
   __shared__ Cursor s_cur;
   __shared__ Cursor s_wcur[16];  // each warp's place: too much for registers
   __shared__ __align__(8) uint64_t s_full[S::SLOTS], s_empty[S::SLOTS];
-  __shared__ __align__(8) uint64_t s_qfull, s_qempty, s_done;
+  __shared__ __align__(8) uint64_t s_qfirst, s_qfull, s_qempty, s_done;
   __shared__ __align__(8) uint64_t s_sfull[2], s_pfull[2], s_ofull[2];
   __shared__ uint32_t s_tmem;
   __shared__ __align__(16) Tc8Scales s_scale[S::BUFS];
@@ -128,6 +133,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       mbar_init(&s_full[i], 4);
       mbar_init(&s_empty[i], 1);
     }
+    mbar_init(&s_qfirst, FIRST);  // of the first item
     mbar_init(&s_qfull, 3);
     mbar_init(&s_qempty, 1);
     mbar_init(&s_done, 1);
@@ -198,6 +204,97 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   tc05_fence_after();
   const uint32_t tmem = s_tmem;
 
+  // The queries of cur's item: this warp's part of them, every `warps`th group of
+  // rows from `first` on.
+  constexpr int C = D / 8;    // 16-byte chunks of a row
+  constexpr int RP = 32 / C;  // rows of one copy
+  constexpr int NG = 2 * kHalf / RP;
+  const int r0 = lane / C, c0 = lane % C;
+  auto chunk = [&](int row) {
+    return sq + (row >= kHalf ? S::TILE : 0) +
+           (uint32_t)((c0 >> 3) * (kBN * 128) + (row & (kHalf - 1)) * 128 +
+                      (((c0 & 7) ^ (row & 7)) << 4));
+  };
+  // x / G for a row's place behind the first token of its tile
+  const uint32_t over = 0xffffffffu / (uint32_t)p.g.G + 1u;
+  constexpr int U = 4;  // copies, and rows' chunks in work, at a time
+  auto queries = [&](const Cursor& cur, uint32_t turn, int first, int warps) {
+    const RowTile& t = cur.t;
+    // in registers: the first products wait for the queries
+    const int gr0 = t.j * 2 * kHalf, i0 = gr0 / p.g.G, rem = gr0 - i0 * p.g.G;
+    const int left = t.rows - gr0;
+    const T* q = static_cast<const T*>(p.q) + (int64_t)(t.t0 + i0) * p.q_stride +
+                 (int64_t)cur.h * p.g.G * D + c0 * 8;
+#pragma unroll 1
+    for (int g0 = first; g0 < NG; g0 += warps * U) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int g = g0 + warps * u, row = g * RP + r0;
+        if (g >= NG) break;
+        const int x = rem + row, i = p.g.G == 1 ? x : (int)__umulhi(x, over);
+        const T* src = q + i * p.q_stride + (x - i * p.g.G) * D;
+        cp16(chunk(row), row < left ? src : static_cast<const T*>(p.q), row < left);
+      }
+    }
+    cp_commit();
+    cp_wait<0>();
+    if constexpr (kIsBf16<T>) {
+      // a thread's own chunks, in place
+#pragma unroll 1
+      for (int g0 = first; g0 < NG; g0 += warps * U) {
+        uint32_t x[U][4], top[U];  // largest finite magnitudes of the rows, as bits
+#pragma unroll
+        for (int u = 0; u < U; ++u)  // (behind the last chunk: the first again)
+          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(x[u][0]), "=r"(x[u][1]), "=r"(x[u][2]), "=r"(x[u][3])
+                       : "r"(chunk((g0 + warps * u < NG ? g0 + warps * u : g0) * RP + r0)));
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          uint32_t y = 0;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) y = max2(y, x[u][e] & 0x7fff7fffu);
+          top[u] = max(y & 0xffffu, y >> 16);
+          if (top[u] >= 0x7f80u) {  // infinities and NaN do not count
+            top[u] = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t lo = x[u][e] & 0x7fffu, hi = (x[u][e] >> 16) & 0x7fffu;
+              if (lo < 0x7f80u) top[u] = max(top[u], lo);
+              if (hi < 0x7f80u) top[u] = max(top[u], hi);
+            }
+          }
+        }
+#pragma unroll
+        for (int d = C / 2; d >= 1; d >>= 1)
+#pragma unroll
+          for (int u = 0; u < U; ++u) top[u] = max(top[u], __shfl_xor_sync(~0u, top[u], d));
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int g = g0 + warps * u, row = g * RP + r0;
+          if (g >= NG) break;
+          // exponents -10 .. 14 of the largest stay: what is lost then is below 2^-25
+          const int e = (int)(top[u] >> 7) - 127;
+          float up = 1.f, down = 1.f;
+          if (top[u] != 0 && (e > 14 || e < -10)) {
+            const int s = min(max(14 - e, -113), 113);
+            up = __uint_as_float((uint32_t)(127 + s) << 23);
+            down = __uint_as_float((uint32_t)(127 - s) << 23);
+          }
+#pragma unroll
+          for (int e2 = 0; e2 < 4; ++e2) {
+            float f[2];
+            Elem<T>::words(&x[u][e2], 1, f);
+            x[u][e2] = pack2<__half>(f[0] * up, f[1] * up);
+          }
+          sts16(chunk(row), x[u][0], x[u][1], x[u][2], x[u][3]);
+          if (c0 == 0) s_qf[turn][row] = down;
+        }
+      }
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+  };
+
   if (warp < 8) {
     // ------------------------------------------------------------ softmax --
     // 72 for the others: the codes do not spill, and the two below less than with 56
@@ -211,6 +308,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     Cursor& cur = s_wcur[warp];
     if (lane == 0) cur = s_cur;
     __syncwarp();
+    if constexpr (kIsBf16<T>) {  // nothing else to do before the first scores
+      if (cur.u < u1) {
+        queries(cur, 0, 3 + warp, FIRST);
+        if (lane == 0) mbar_arrive(&s_qfirst);
+      }
+    }
     uint32_t n_tiles = 0;  // active tiles so far: parity of the barriers
     uint32_t items = 0;
     int buf = S::BUFS - 1;  // of the tile's scales
@@ -581,98 +684,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     Cursor& cur = s_wcur[warp];
     if (lane == 0) cur = s_cur;
     __syncwarp();
-    constexpr int C = D / 8;    // 16-byte chunks of a row
-    constexpr int RP = 32 / C;  // rows of one copy
-    constexpr int NG = 2 * kHalf / RP;
-    const int r0 = lane / C, c0 = lane % C;
-    auto chunk = [&](int row) {
-      return sq + (row >= kHalf ? S::TILE : 0) +
-             (uint32_t)((c0 >> 3) * (kBN * 128) + (row & (kHalf - 1)) * 128 +
-                        (((c0 & 7) ^ (row & 7)) << 4));
-    };
-    // x / G for a row's place behind the first token of its tile
-    const uint32_t over = 0xffffffffu / (uint32_t)p.g.G + 1u;
-    constexpr int U = 4;  // copies, and rows' chunks in work, at a time
     uint32_t items = 0;
     while (cur.u < u1) {
-      const RowTile& t = cur.t;
-      const int count = (int)min((long long)(t.tiles - cur.tile), u1 - cur.u);
-      // in registers: the next item's first products wait for its queries
-      const int gr0 = t.j * 2 * kHalf, i0 = gr0 / p.g.G, rem = gr0 - i0 * p.g.G;
-      const int left = t.rows - gr0;
-      const T* q = static_cast<const T*>(p.q) + (int64_t)(t.t0 + i0) * p.q_stride +
-                   (int64_t)cur.h * p.g.G * D + c0 * 8;
+      const int count = (int)min((long long)(cur.t.tiles - cur.tile), u1 - cur.u);
       if (items) wait_bar(&s_qempty, (items - 1) & 1, err);
-#pragma unroll 1
-      for (int g0 = qw; g0 < NG; g0 += 3 * U) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-          const int g = g0 + 3 * u, row = g * RP + r0;
-          if (g >= NG) break;
-          const int x = rem + row, i = p.g.G == 1 ? x : (int)__umulhi(x, over);
-          const T* src = q + i * p.q_stride + (x - i * p.g.G) * D;
-          cp16(chunk(row), row < left ? src : static_cast<const T*>(p.q), row < left);
-        }
-      }
-      cp_commit();
-      cp_wait<0>();
-      if constexpr (kIsBf16<T>) {
-        // a thread's own chunks, in place
-#pragma unroll 1
-        for (int g0 = qw; g0 < NG; g0 += 3 * U) {
-          uint32_t x[U][4], top[U];  // largest finite magnitudes of the rows, as bits
-#pragma unroll
-          for (int u = 0; u < U; ++u)  // (behind the last chunk: the first again)
-            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(x[u][0]), "=r"(x[u][1]), "=r"(x[u][2]), "=r"(x[u][3])
-                         : "r"(chunk((g0 + 3 * u < NG ? g0 + 3 * u : g0) * RP + r0)));
-#pragma unroll
-          for (int u = 0; u < U; ++u) {
-            uint32_t y = 0;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) y = max2(y, x[u][e] & 0x7fff7fffu);
-            top[u] = max(y & 0xffffu, y >> 16);
-            if (top[u] >= 0x7f80u) {  // infinities and NaN do not count
-              top[u] = 0;
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const uint32_t lo = x[u][e] & 0x7fffu, hi = (x[u][e] >> 16) & 0x7fffu;
-                if (lo < 0x7f80u) top[u] = max(top[u], lo);
-                if (hi < 0x7f80u) top[u] = max(top[u], hi);
-              }
-            }
-          }
-#pragma unroll
-          for (int d = C / 2; d >= 1; d >>= 1)
-#pragma unroll
-            for (int u = 0; u < U; ++u) top[u] = max(top[u], __shfl_xor_sync(~0u, top[u], d));
-#pragma unroll
-          for (int u = 0; u < U; ++u) {
-            const int g = g0 + 3 * u, row = g * RP + r0;
-            if (g >= NG) break;
-            // exponents -10 .. 14 of the largest stay: what is lost then is below 2^-25
-            const int e = (int)(top[u] >> 7) - 127;
-            float up = 1.f, down = 1.f;
-            if (top[u] != 0 && (e > 14 || e < -10)) {
-              const int s = min(max(14 - e, -113), 113);
-              up = __uint_as_float((uint32_t)(127 + s) << 23);
-              down = __uint_as_float((uint32_t)(127 - s) << 23);
-            }
-#pragma unroll
-            for (int e2 = 0; e2 < 4; ++e2) {
-              float f[2];
-              Elem<T>::words(&x[u][e2], 1, f);
-              x[u][e2] = pack2<__half>(f[0] * up, f[1] * up);
-            }
-            sts16(chunk(row), x[u][0], x[u][1], x[u][2], x[u][3]);
-            if (c0 == 0) s_qf[items & 1][row] = down;
-          }
-        }
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
+      queries(cur, items & 1, qw, items ? 3 : FIRST);
       if (lane == 0) {
-        mbar_arrive(&s_qfull);
+        mbar_arrive(items ? &s_qfull : &s_qfirst);
         cur.u += count - 1;
         cur.tile += count - 1;
         cur.next(p, u1);
@@ -732,7 +750,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         // the tiles that both halves see whole, but for the run's last
         int mid_lo, mid_hi;
         tc.middle(p, first, first + count - 1, ns, skip, mid_lo, mid_hi);
-        wait_bar(&s_qfull, items & 1, err);
+        wait_bar(items ? &s_qfull : &s_qfirst, items ? (items - 1) & 1 : 0, err);
         ++items;
         tc05_fence_after();
         bool acc0 = false, acc1 = false;
