@@ -124,6 +124,28 @@ def test_large_and_small_queries_share_a_tile(code, dtype):
     both(pr)
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("q_len,kv_len", [([4, 1], [90, 33]), ([300, 700, 40], [500, 700, 2000])], ids=str)
+def test_queries_that_are_not_finite_stay_in_their_rows(dtype, q_len, kv_len):
+    pr = Problem8(q_len, kv_len, 8, 2, dtype=dtype)
+    if dtype == "bf16":  # a power of two of its own for this row, beside the others
+        pr.q[2] *= 2.0 ** 20
+        pr.scales[..., 0] /= 2.0 ** 20
+    out, tol, lse, ltol = ref_attention8(pr)
+    q = pr.q.clone()
+    q[0, 3, 5] = NAN
+    q[1, 6, 0] = float("inf")
+    q[pr.tokens - 1, 0, pr.d - 1] = -float("inf")
+    r = Run8(pr).attend(q=q)
+    assert r.kv.status() == OK
+    assert r.out[0, 3].isnan().all() and r.lse[0, 3].isnan()
+    for t, h in ((0, 3), (1, 6), (pr.tokens - 1, 0)):
+        out[t, h], tol[t, h] = r.out[t, h].to(out), 0
+        lse[t, h], ltol[t, h] = r.lse[t, h].to(lse), 0
+    close(r.out, out, tol, "out")
+    close(r.lse, lse, ltol, "lse")
+
+
 @pytest.mark.parametrize("code", CODES)
 @pytest.mark.parametrize("q_len", [[1, 1, 1], [3, 2, 1], [100, 40, 17]], ids=str)
 def test_scales_of_many_sizes_and_zero(code, q_len):
