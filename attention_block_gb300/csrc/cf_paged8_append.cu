@@ -23,15 +23,21 @@ constexpr int kAppendThreads = 256;
 template <int TPB>
 constexpr int kBatch = TPB == 1 ? 3 : 1;
 
-// (sin, cos) of f / 2^64 turns.  Behind a quarter turn's reduction the float
-// that sincospif takes is off by 2^-28 of a turn, for codes: an error there
-// moves more of them over a border than those of the arithmetic do.
+// (cos, sin) of f / 2^64 turns, reduced by quarter turns.  What the float that
+// sincospif takes rounds off, up to 2^-28 of a turn, is put back by a step of its
+// derivative: such errors move more codes over a border than those of the
+// rotation's arithmetic do.
 __device__ __forceinline__ float2 turn_fine(uint64_t f) {
-  const uint32_t hi = (uint32_t)(f >> 32);
+  const uint32_t hi = (uint32_t)((f + 0x80000000u) >> 32);
   const uint32_t quarter = (hi + 0x20000000u) >> 30;
-  const float part = (float)(int32_t)(hi - (quarter << 30)) * 0x1p-32f;
+  const int32_t n = (int32_t)(hi - (quarter << 30));
+  const float r = (float)n;
+  const float rest = (float)(n - (int32_t)r) * 1.4629180793e-9f;  // 2 pi / 2^32
   float s, c;
-  sincospif(2.0f * part, &s, &c);
+  sincospif(r * 0x1p-31f, &s, &c);
+  const float s0 = s;
+  s = fmaf(rest, c, s);
+  c = fmaf(-rest, s0, c);
   const bool swap = quarter & 1u;
   const float x = swap ? s : c, y = swap ? c : s;
   return make_float2(quarter == 1 || quarter == 2 ? -x : x, quarter >= 2 ? -y : y);
