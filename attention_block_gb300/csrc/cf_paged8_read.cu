@@ -96,7 +96,9 @@ __global__ void __launch_bounds__(kReadThreads)
           const uint8_t* pool = static_cast<const uint8_t*>(kv ? p.v_pages : p.k_pages);
           w[i] = __ldcs(reinterpret_cast<const uint4*>(pool + code + (int64_t)h * p.g.head_stride +
                                                        c * 16));
-          scale[i] = __ldg((&p.scales[s_scale[row] + ((int64_t)h << p.g.page_shift)].x) + kv);
+          // (coherent, like the codes' load: the append in front may have begun to write them
+          // when this launch was here already)
+          scale[i] = (&p.scales[s_scale[row] + ((int64_t)h << p.g.page_shift)].x)[kv];
         }
       }
       h += step;

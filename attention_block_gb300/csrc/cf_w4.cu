@@ -226,14 +226,15 @@ __device__ __forceinline__ void load_cvt2(const T* p, float (&f)[2]) {
 }
 
 // x of one lane for the two steps of 32 elements of k: words [step][half]
-// (PARTS of them).
+// (PARTS of them).  Coherent loads: the launch in front, which may still have been
+// writing x when this one began, has to be seen.
 template <typename T>
 struct XFrag {
   uint32_t w[W4Type<T>::PARTS][4];
   __device__ __forceinline__ void load(const T* at, bool there = true) {
     if constexpr (sizeof(T) == 2) {
       uint4 v = make_uint4(0, 0, 0, 0);
-      if (there) v = __ldg(reinterpret_cast<const uint4*>(at));
+      if (there) v = *reinterpret_cast<const uint4*>(at);
       w[0][0] = v.x;
       w[0][1] = v.y;
       w[0][2] = v.z;
@@ -243,7 +244,7 @@ struct XFrag {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (there) v = __ldg(reinterpret_cast<const float4*>(at) + i);
+        if (there) v = reinterpret_cast<const float4*>(at)[i];
         f[4 * i] = v.x;
         f[4 * i + 1] = v.y;
         f[4 * i + 2] = v.z;
