@@ -850,8 +850,10 @@ class W4Matvec:
     with weights of 4 bits, of any number of matrices of one shape.  Raises
     CfError on any non-zero return code.
 
-    Tensors are checked for dtype, device, shape and dense rows; raw addresses
-    are taken as they are."""
+    Rows of x may be strided: a tensor's stride along dim 0 is used, a raw
+    address counts as dense unless the stride is given.  Tensors are checked for
+    dtype, device, shape and dense rows, and that a stride that is given ends
+    within them; raw addresses are taken as they are."""
 
     def __init__(self, **cfg):
         self.cfg = c = make_w4_config(**cfg)
@@ -913,9 +915,13 @@ class W4Matvec:
                     x.shape[0] < rows or x.shape[1] != c.in_features or x.stride(1) != 1:
                 raise CfError(CF_ERR_INVALID_ARG, f"x: {x.dtype} {tuple(x.shape)} on {x.device}")
             if not x_stride:  # the stride of a single row says nothing
-                x_stride = x.stride(0) if x.shape[0] > 1 else c.in_features
+                x_stride = x.stride(0) if rows > 1 else c.in_features
+            elif (rows - 1) * x_stride > (x.shape[0] - 1) * x.stride(0):
+                raise CfError(CF_ERR_INVALID_ARG, f"x: rows {x_stride} apart of {tuple(x.shape)}")
             x = x.data_ptr()
-        rc = self._matvec(self.handle, rows, x, int(x_stride or c.in_features),
+        elif not x_stride:
+            x_stride = c.in_features
+        rc = self._matvec(self.handle, rows, x, int(x_stride),
                           self._packed(packed),
                           self._at(residual, self._dtype, rows, c.out_features, "residual"),
                           self._at(out, self._dtype, rows, c.out_features, "out"),
