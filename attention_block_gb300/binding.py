@@ -561,8 +561,9 @@ class PagedKv:
     Rows of q, k, v and q_out may be strided: a tensor's stride along dim 0 is
     used, a raw address counts as dense unless the stride is given.  Tensors
     are checked for dtype, device, dense inner dimensions and, page tables and
-    positions of three axes, for the width they are read by; raw addresses are
-    taken as they are."""
+    positions of three axes, for the width they are read by; a stride that is
+    given for a tensor has to end within it; raw addresses are taken as they
+    are."""
 
     def __init__(self, **cfg):
         self.cfg = c = make_paged_config(**cfg)
@@ -611,7 +612,8 @@ class PagedKv:
         shape, st = x.shape, x.stride()
         if x.dtype is self._dtype and x.get_device() == self._dev and shape[0] >= n and \
                 st[-1] == 1 and (shape[1] == row if len(shape) == 2 else len(shape) == 3 and
-                                 shape[1] * shape[2] == row and st[1] == shape[2]):
+                                 shape[1] * shape[2] == row and st[1] == shape[2]) and \
+                (not stride or (n - 1) * stride <= (shape[0] - 1) * st[0]):
             # the stride of a single row says nothing
             return x.data_ptr(), int(stride) if stride else (st[0] if shape[0] > 1 else row)
         raise CfError(CF_ERR_INVALID_ARG,
