@@ -266,8 +266,9 @@ struct PagedState4 {
 // Joins a row's states into s: the D / 4 lanes that share the row call it
 // together, each for its 4 columns at `col`.  Each lane fetches one part's
 // maximum and sum, and the parts' values come B at a time, the first ones
-// together with the maxima.
-template <int D, int B = 8>
+// together with the maxima.  HALVES: what a sum is multiplied by can be below 2^-126
+// and the sum still count, as the maxima hold value scales that lie far apart.
+template <int D, int B = 8, bool HALVES = false>
 __device__ __forceinline__ void paged_join_row(PagedState4& s, const float* o, const float2* ml,
                                                const PagedRowParts& x, int col) {
   constexpr int W = D / 4;
@@ -289,12 +290,24 @@ __device__ __forceinline__ void paged_join_row(PagedState4& s, const float* o, c
 #pragma unroll
     for (int d = W / 2; d >= 1; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(mask, mx, d));
     const float mn = fmaxf(s.m, mx), ref = mn == -INFINITY ? 0.f : mn;
-    const float a = exp2f(s.m - ref), w = exp2f(v.x - ref);
-    float l = v.y * w;
+    float a, w, l, ha = 1.f;
+    if constexpr (HALVES) {
+      const float hw = exp2f(0.5f * (v.x - ref));
+      ha = exp2f(0.5f * (s.m - ref));
+      a = ha * ha;
+      w = hw * hw;
+      l = v.y * hw * hw;
+    } else {
+      a = exp2f(s.m - ref), w = exp2f(v.x - ref);
+      l = v.y * w;
+    }
 #pragma unroll
     for (int d = W / 2; d >= 1; d >>= 1) l += __shfl_xor_sync(mask, l, d);
     s.m = mn;
-    s.l = s.l * a + l;
+    if constexpr (HALVES)
+      s.l = s.l * ha * ha + l;
+    else
+      s.l = s.l * a + l;
     s.o = make_float4(s.o.x * a, s.o.y * a, s.o.z * a, s.o.w * a);
     for (int k = 0; k < n; k += B) {
       if (k) fetch(k);

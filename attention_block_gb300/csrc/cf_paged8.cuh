@@ -108,6 +108,27 @@ __device__ __forceinline__ float rcp(float x) {
   return y;
 }
 
+// Value scales in the weights.  A position's weight takes log2 vs into its
+// exponent; the sum of exp(s) takes the weight times 1 / vs.  That is exact enough
+// while 1 / vs is below 2^19: with a maximum that holds a scale of 2^60, the most
+// that there is, a weight is flushed where exp(s) is below 2^-54 of the largest,
+// so that 2^30 of them lose 2^-24 of the sum.  Positions with a smaller scale, or
+// one of zero, are added to the sum apart, as 2^(s - reference).  A scale of zero
+// enters the weights' exponent as 2^-80: the codes are zero, so it only has to be
+// too small to raise the maximum (20 octaves below the least scale) and to leave
+// 2^(s - reference) room for a sum of 2^30 (2^(80 + 15 + 30) at most).
+struct ValueScale {
+  float log2;   // of what stands for the scale in the exponent
+  float inv;    // 1 / that: what the sum multiplies a weight by
+  bool apart;
+  __device__ __forceinline__ explicit ValueScale(float v) {
+    const float vv = v == 0.f ? 0x1p-80f : fmaxf(v, 0x1p-60f);  // (of a NaN: the bound)
+    log2 = lg2(vv);
+    inv = rcp(vv);
+    apart = !(v >= 0x1p-19f);
+  }
+};
+
 // 8 bytes global -> shared, asynchronously; zeros where there is no source.
 __device__ __forceinline__ void cp8(uint32_t dst, const void* src, bool there) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src),

@@ -17,7 +17,8 @@
 // Scales: with a_j = scale ks_j log2(e) and b_j = log2 vs_j, the weight of
 // value j is exp(s_j) vs_j = 2^(a_j q.k_j + b_j), so one fused product, one
 // maximum and one exponential serve the weights, whatever the scales are; the
-// sum of exp(s_j) takes the weight times 1 / vs_j.
+// sum of exp(s_j) takes the weight times 1 / vs_j, or where vs_j is small or zero
+// an exponential of its own (ValueScale).
 //
 // A unit of 32 positions takes a warp 820 instructions (e4m3, 8 rows), 55 % of the
 // SM's issue slots at the copy rate, but 5500 cycles: with three warps to a
@@ -422,7 +423,7 @@ __global__ void __launch_bounds__(Shape8<D, NT>::THREADS, 1)
     const uint32_t k_at = k_lane + 2 * pair * S::SLOT, v_at = v_lane + 2 * pair * S::SLOT;
     const int j0 = cur.w.base(tile);
     float c[MT][NT][4];
-    uint32_t odd = 0;  // positions with a value scale of NaN
+    uint32_t apart = 0;  // positions that the sum takes apart (ValueScale)
     if (some) {
       {  // each lane's position: a, b, 1 / vs
         const bool there = cur.w.sees(j0 + lane);
@@ -430,13 +431,11 @@ __global__ void __launch_bounds__(Shape8<D, NT>::THREADS, 1)
         asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];"
                      : "=f"(k), "=f"(v)
                      : "r"(scale_s + pair * S::SCALES + lane * 8));
-        odd = __ballot_sync(~0u, there && v != v);
-        // (zero: the codes are zero too, and any scale will do: a small one, which
-        // does not raise the row's maximum; fmaxf takes a NaN for the bound)
-        const float vv = v == 0.f ? 0x1p-30f : fmaxf(v, 0x1p-60f);
-        const float ak = there ? k * qk : 0.f, bk = there ? lg2(vv) : -INFINITY;
+        const ValueScale vs(v);
+        apart = __ballot_sync(~0u, there && vs.apart);
+        const float ak = there ? k * qk : 0.f, bk = there ? vs.log2 : -INFINITY;
         asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(prep_s + lane * 16), "f"(ak),
-                     "f"(bk), "f"(rcp(vv)), "f"(0.f)
+                     "f"(bk), "f"(vs.apart ? 0.f : vs.inv), "f"(there ? v : 0.f)
                      : "memory");
       }
 #pragma unroll
@@ -495,8 +494,8 @@ __global__ void __launch_bounds__(Shape8<D, NT>::THREADS, 1)
               mx[nt][e] = fmaxf(mx[nt][e], x);
             }
         }
-      float corr[NT][2];
-      bool moved = false;
+      float corr[NT][2];  // at first the square roots
+      bool moved = apart != 0;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -505,19 +504,57 @@ __global__ void __launch_bounds__(Shape8<D, NT>::THREADS, 1)
           for (int d = 4; d <= 16; d <<= 1)
             mx[nt][e] = fmaxf(mx[nt][e], __shfl_xor_sync(~0u, mx[nt][e], d));
           const float ref = mx[nt][e] == -INFINITY ? 0.f : mx[nt][e];
-          corr[nt][e] = ex2(m[nt][e] - ref);
+          // (by halves: with value scales far apart, what the sum is multiplied by can be
+          // below 2^-126 and the sum still count)
+          corr[nt][e] = ex2(0.5f * (m[nt][e] - ref));
           moved |= corr[nt][e] != 1.f;
           m[nt][e] = mx[nt][e];
           mx[nt][e] = ref - LIFT;
-          l[nt][e] *= corr[nt][e];
         }
       if (__any_sync(~0u, moved)) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            l[nt][e] = l[nt][e] * corr[nt][e] * corr[nt][e];
+            corr[nt][e] *= corr[nt][e];
+          }
 #pragma unroll
           for (int k = 0; k < NJ; ++k)
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[nt][k][e] *= corr[nt][e & 1];
+        }
+        if (apart) {  // 2^(s - reference) of those positions (decode at d = 64 28.9 -> 29.2 us)
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              const int jj = mt * 16 + 8 * r + gq;
+              if (!((apart >> jj) & 1)) continue;
+              const float b = __uint_as_float(lds16(prep_s + jj * 16).y);
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) l[nt][e] += ex2(c[mt][nt][2 * r + e] - b - mx[nt][e]);
+            }
+          // a value of NaN: o of the rows that see it
+          const float v = __uint_as_float(lds16(prep_s + lane * 16).w);
+          const uint32_t odd = __ballot_sync(~0u, v != v);
+          if (odd) {
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                bool hit = !edge;
+                for (uint32_t w = odd; w; w &= w - 1)
+                  hit |= paged_visible(pos[nt][e], j0 + __ffs(w) - 1, p.window, p.n_sinks);
+                if (!hit) continue;
+#pragma unroll
+                for (int k = 0; k < NJ; ++k)
+                  o[nt][k][e] = o[nt][k][e + 2] = __uint_as_float(0x7fc00000u);
+              }
+          }
+        }
       }
       // weights, and their sums without the value scales
 #pragma unroll
@@ -530,21 +567,6 @@ __global__ void __launch_bounds__(Shape8<D, NT>::THREADS, 1)
             x = ex2(x - mx[nt][e & 1]);
             l[nt][e & 1] = fmaf(x, inv[mt][e >> 1], l[nt][e & 1]);
           }
-      if (odd) {  // a value of NaN: for the rows that see it
-#pragma unroll
-        for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            const int jj = mt * 16 + 8 * r + gq;
-            if (!((odd >> jj) & 1)) continue;
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-              for (int e = 0; e < 2; ++e)
-                if (!edge || paged_visible(pos[nt][e], j0 + jj, p.window, p.n_sinks))
-                  c[mt][nt][2 * r + e] = __uint_as_float(0x7fc00000u);
-          }
-      }
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -700,8 +722,8 @@ __global__ void __launch_bounds__(Shape8<D, NT>::THREADS, 1)
         const float2 ml = s_ml[k][w][row];
         const float4 o4 = *reinterpret_cast<const float4*>(
             reinterpret_cast<const float*>(smem + w * S::WARP + (k ? 0 : S::RING)) + row * D + col);
-        const float x = ex2(ml.x - ref);
-        s.l = fmaf(ml.y, x, s.l);
+        const float half = ex2(0.5f * (ml.x - ref)), x = half * half;
+        s.l = fmaf(ml.y * half, half, s.l);
         s.o.x = fmaf(o4.x, x, s.o.x);
         s.o.y = fmaf(o4.y, x, s.o.y);
         s.o.z = fmaf(o4.z, x, s.o.z);
@@ -744,7 +766,7 @@ __global__ void __launch_bounds__(Shape8<D, NT>::THREADS, 1)
     for (int x = tid; x < cut[i].n * p.g.G * C4; x += THREADS) {
       const int row = x / C4, col = (x - row * C4) * 4;
       PagedState4 s{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-      paged_join_row<D>(s, a.ws.o, a.ws.ml, PagedRowParts(parts, kFewRows, row, -1), col);
+      paged_join_row<D, 8, true>(s, a.ws.o, a.ws.ml, PagedRowParts(parts, kFewRows, row, -1), col);
       paged_store4<T, D>(s, p.out, p.lse, out_row(p, cut[i], row), col);
     }
   }

@@ -9,7 +9,8 @@
 // are fp16 x fp16; a code is exact in fp16, and scales do not touch the
 // operands: with a_j = scale ks_j log2(e) and b_j = log2 vs_j the weight of
 // value j is 2^(a_j q.k_j + b_j), and the sum of exp(s_j) takes that weight
-// times c_j = 1 / vs_j.
+// times c_j = 1 / vs_j, or where vs_j is small or zero an exponential of its own
+// (ValueScale).
 //
 // Roles of a block's 16 warps:
 //   0-3, 4-7  softmax of half 0 / 1, a thread per row
@@ -48,6 +49,10 @@ using namespace cf;
 
 namespace {
 
+// Scales of what no row of an item sees: masked, and nothing for the sum to take
+// apart.  (A page outside the pool reads as zeros.)
+__device__ const float2 kUnseen = {0.f, 1.f};
+
 template <int D>
 struct Tc8Shape {
   static constexpr int TILE = kBN * D * 2;         // bytes of a K, V or Q tile
@@ -63,10 +68,11 @@ struct Tc8Shape {
   static constexpr uint32_t S_COL = 0, O_COL = 2 * kBN;  // TMEM columns
 };
 
-// Of a tile's positions: a, b, c; and which value scales are NaN.
+// Of a tile's positions: a, b, c; which the sum takes apart (ValueScale), and
+// which of those have a value scale of NaN.
 struct Tc8Scales {
   float a[kBN], b[kBN], c[kBN];
-  uint32_t odd[kBN / 32];
+  uint32_t apart[kBN / 32], odd[kBN / 32];
 };
 
 // What an item costs apart from its tiles, in tiles: its queries, its result, the
@@ -339,11 +345,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 #pragma unroll
           for (int k = 0; k < kBN / 32; ++k) tmem_ld32(ts + 32 * k, s + 32 * k);
           tmem_wait_ld();
+          float qf = 1.f;
           if constexpr (kIsBf16<T>) {  // rows whose queries were brought into fp16's range
-            const float f = s_qf[items & 1][hf * kHalf + r];
-            if (__any_sync(~0u, f != 1.f)) {
+            qf = s_qf[items & 1][hf * kHalf + r];
+            if (__any_sync(~0u, qf != 1.f)) {
 #pragma unroll
-              for (int k = 0; k < kBN; ++k) s[k] *= f;
+              for (int k = 0; k < kBN; ++k) s[k] *= qf;
             }
           }
 #pragma unroll
@@ -385,9 +392,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           for (int e = 0; e < 4; ++e) mx4[e] = fmaxf(mx4[e], s[kBN - 4 + e]);
           const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
           const float m_new = fmaxf(m, mx);
-          const bool grow = m_new - m > (float)kGrow;  // also from -inf
+          // (one question for both: another branch on every tile's way costs 2-6 %)
+          const bool apart = (sc.apart[0] | sc.apart[1] | sc.apart[2] | sc.apart[3]) != 0;
+          const bool grow = m_new - m > (float)kGrow || apart;  // also from -inf
+          float l_apart = 0.f;
           if (__any_sync(~0u, grow)) {
-            const float corr = m_new == -INFINITY ? 1.f : ex2(m - m_new);
+            // (by halves: with value scales far apart, what the sum is multiplied by can be
+            // below 2^-126 and the sum still count)
+            const float half = m_new == -INFINITY ? 1.f : ex2(0.5f * (m - m_new));
+            const float corr = half * half;
             if (some) {
               wait_bar(&s_ofull[hf], (n_tiles - 1) & 1, err);
               tc05_fence_after();
@@ -401,12 +414,36 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 tmem_st16(to + c, o);
               }
             }
-            l *= corr;
+            l = l * half * half;
             m = m_new;
+            if (apart) {  // the sum over this tile as 2^(s - reference)
+              const float at = (m == -INFINITY ? 0.f : m) - LIFT;
+              l_apart = l;
+#pragma unroll 1
+              for (int c = 0; c < kBN; c += 16) {
+                const uint32_t see = sees(base + c);
+                uint32_t x[16];
+                tmem_ld_32x32b_x16_nowait(ts + c, x);
+                tmem_wait_ld();
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                  if ((see >> e) & 1u)
+                    l_apart += ex2(fmaf(__uint_as_float(x[e]) * qf, sc.a[c + e], -at));
+              }
+              // values of NaN: for the rows that see them
+              if ((sc.odd[0] | sc.odd[1] | sc.odd[2] | sc.odd[3]) != 0) {
+#pragma unroll
+                for (int k = 0; k < kBN / 32; ++k) {
+                  const uint32_t hit = sc.odd[k] & sees(base + 32 * k);
+#pragma unroll
+                  for (int e = 0; e < 32; ++e)
+                    if ((hit >> e) & 1u) s[32 * k + e] = __uint_as_float(0x7fc00000u);
+                }
+              }
+            }
           }
           const float ref = (m == -INFINITY ? 0.f : m) - LIFT;
           const float2 ref2 = make_float2(-ref, -ref);
-          const bool odd = (sc.odd[0] | sc.odd[1] | sc.odd[2] | sc.odd[3]) != 0;
           float2 sum[2] = {make_float2(l, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
           for (int k = 0; k < kBN / 32; ++k) {
@@ -424,21 +461,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 w[e + x2] = pack2<__half>(x.x, x.y);
               }
             }
-            if (odd) {  // values of NaN: for the rows that see them
-              const uint32_t hit = sc.odd[k] & sees(base + 32 * k);
-#pragma unroll
-              for (int e = 0; e < 16; ++e) {
-                if ((hit >> (2 * e)) & 1u) w[e] |= 0x7fffu;
-                if ((hit >> (2 * e + 1)) & 1u) w[e] |= 0x7fff0000u;
-              }
-            }
             tmem_st16(ts + 16 * k, w);
           }
           tmem_wait_st();
           tc05_fence_before();
           __syncwarp();
           if (lane == 0) mbar_arrive(&s_pfull[hf]);
-          l = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+          l = apart ? l_apart : (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
           some = true;
           ++n_tiles;
         }
@@ -618,22 +647,23 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (++in == S::RAW) in = 0;
       } else if (cur.u < u1) {
         off = -1;
-        const float2* scale = p.scales;
-        if (f_pos >= 0) {
+        const float2* scale = &kUnseen;
+        const bool seen = f_pos >= 0;
+        if (seen) {
           if ((unsigned)f_page >= (unsigned)p.g.num_pages) {
             atomicOr(err, kDevErrPosRange);
           } else {
             const int slot = f_pos & p.g.page_mask;
             off = (int64_t)f_page * p.g.page_stride + (int64_t)slot * p.g.slot_stride +
                   (int64_t)cur.h * p.g.head_stride;
-            scale += (((int64_t)f_page * p.g.nkv + cur.h) << p.g.page_shift) + slot;
+            scale = p.scales + (((int64_t)f_page * p.g.nkv + cur.h) << p.g.page_shift) + slot;
           }
         }
         __syncwarp();
         if (lane == 0) cur.next(p, u1);
         __syncwarp();
         look_up();
-        cp8(smem_u32(&s_raw[in_unit][row]), scale, off >= 0);
+        cp8(smem_u32(&s_raw[in_unit][row]), scale, off >= 0 || !seen);
         if (++in_unit == S::AHEAD) in_unit = 0;
         load(in, kbase, off);
         value = true;
@@ -654,17 +684,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if (use >= S::SLOTS) wait_bar(&s_empty[ring.slot], ring.phase ^ 1u, err);
       ++use;
       if (key) {
-        // (zero: the codes are zero too, and any scale will do: a small one, which
-        // does not raise the row's maximum; fmaxf takes a NaN for the bound)
         const float2 scale = s_raw[out_unit][row];
         if (++out_unit == S::AHEAD) out_unit = 0;
-        const float v = scale.y, vv = v == 0.f ? 0x1p-30f : fmaxf(v, 0x1p-60f);
+        const ValueScale vs(scale.y);
         Tc8Scales& sc = s_scale[buf];
         sc.a[row] = scale.x * p.scale_log2;
-        sc.b[row] = lg2(vv);
-        sc.c[row] = rcp(vv);
-        const uint32_t odd = __ballot_sync(~0u, v != v);
-        if (lane == 0) sc.odd[lw] = odd;
+        sc.b[row] = vs.log2;
+        sc.c[row] = vs.inv;
+        const uint32_t apart = __ballot_sync(~0u, vs.apart);
+        const uint32_t odd = __ballot_sync(~0u, scale.y != scale.y);
+        if (lane == 0) {
+          sc.apart[lw] = apart;
+          sc.odd[lw] = odd;
+        }
         if (++buf == S::BUFS) buf = 0;
       }
       convert(out, ring.slot);
@@ -840,7 +872,7 @@ __global__ void __launch_bounds__(256, 4) paged8_tc_join_kernel(const __grid_con
       PagedState4 s{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
       const int gr = x.j * 2 * kHalf + r, i = gr / p.g.G, g = gr - i * p.g.G;
       const long long row = ((long long)x.t0 + i) * p.g.nq + x.h * p.g.G + g;
-      paged_join_row<D, 4>(s, a.ws.o, a.ws.ml, PagedRowParts(parts, 2 * kHalf, r, -1), col);
+      paged_join_row<D, 4, true>(s, a.ws.o, a.ws.ml, PagedRowParts(parts, 2 * kHalf, r, -1), col);
       paged_store4<T, D>(s, p.out, p.lse, row, col);
     }
   }

@@ -35,8 +35,9 @@
  * max_q * nq/nkv above 16: for rows whose largest element is not between 2^-10
  * and 2^15), and lose only what is below 2^-32 of the tile's largest element, or
  * of 1.  Scales and softmax statistics are fp32; weights exp(s_j) vs_j enter the
- * second product in fp16, held down to 2^-32 of the row's largest; the sum of
- * exp(s_j) is taken before that rounding.  Scales that are read must be NaN or
+ * second product in fp16, held down to 2^-32 of the row's largest (a scale of 0
+ * counts as 2^-80 there); the sum of exp(s_j) is taken before that rounding and
+ * whatever the value scales are.  Scales that are read must be NaN or
  * from 0 to 2^60, value scales other than 0 at least 2^-60 (appending fp16 keeps
  * to that, and so does bf16 between 2^-50 and 2^60), and e4m3 codes not NaN (0x7f,
  * 0xff; none is appended).  Outputs are rounded once.  The same call on the same

@@ -4,6 +4,7 @@ import torch
 
 from attention_block_gb300 import binding
 from paged8_util import DT, Problem8
+from test_paged8_gpu import both
 
 pytestmark = pytest.mark.gpu
 OK, RANGE = binding.CF_OK, binding.CF_ERR_DEVICE_POS_RANGE
@@ -41,3 +42,59 @@ def test_reading_back_sees_the_append_in_front(code, q_len):
     for _ in range(3):
         assert torch.equal(run(False), want)
     assert kv.status() == OK
+
+
+# ------------------------------------------------------------- value scales --
+def set_values(pr, scale, zero=None):
+    """Value scales [num_pages, nkv, page]; heads in `zero` are held as zeros."""
+    pr.scales[..., 1] = scale
+    if zero is not None:
+        pr.scales[..., 1][zero] = 0
+        z = zero.transpose(1, 2) if pr.layout == 0 else zero
+        pr.v_pages.view(torch.uint8)[z] = 0
+
+
+@pytest.mark.parametrize("code", CODES)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("log2", [-60, -45, -30, -19, 0, 40, 60])
+@pytest.mark.parametrize("q_len", [[1, 1], [3, 4], [60, 130]], ids=str)
+def test_zero_heads_beside_value_scales_of_any_size(code, d, log2, q_len):
+    """A head of zeros weighs in the sum as exp(s), and takes nothing from the others' weights."""
+    pr = Problem8(q_len, [300, 190], 4, 2, d=d, code=code)
+    g = torch.Generator(device="cuda").manual_seed(7)
+    shape = pr.scales.shape[:-1]
+    set_values(pr, 2.0 ** log2 * (1 + torch.rand(shape, generator=g, device="cuda")) / 2 ** (log2 > 0),
+               torch.rand(shape, generator=g, device="cuda") < 0.2)
+    both(pr)
+
+
+@pytest.mark.parametrize("code", CODES)
+@pytest.mark.parametrize("log2", [-60, -45, -9])
+@pytest.mark.parametrize("ahead", [3, 12, 18])
+@pytest.mark.parametrize("q_len", [[1], [4], [70]], ids=str)
+def test_a_first_position_of_zeros_that_takes_most_of_the_weight(code, log2, ahead, q_len):
+    """Position 0 holds a value of zeros and scores some `ahead` octaves above the others."""
+    pr = Problem8(q_len, [700], 4, 2, code=code)
+    pr.q[..., 0] = 8.0
+    at = int(pr.table[0, 0])
+    top = 127.0 if code == "int8" else 448.0
+    pr.k_pages.view(torch.uint8)[at, 0] = 0
+    pr.k_pages[at, 0, :, 0] = int(top) if code == "int8" else torch.tensor(top).to(pr.k_pages.dtype)
+    pr.scales[at, :, 0, 0] = ahead * 0.6931 * pr.d ** 0.5 / (8 * top)
+    zero = torch.zeros(pr.scales.shape[:-1], dtype=torch.bool, device="cuda")
+    zero[at, :, 0] = True
+    set_values(pr, 2.0 ** log2, zero)
+    both(pr)
+
+
+@pytest.mark.parametrize("code", CODES)
+@pytest.mark.parametrize("q_len", [[1], [4], [70]], ids=str)
+@pytest.mark.parametrize("low,high", [(-60, 60), (-60, -9), (-33, 9), (-19, 60), (-20, 60)], ids=str)
+def test_one_large_value_scale_beside_many_small_ones(code, q_len, low, high):
+    """Most of exp(s) lies at positions whose values are 2^-(high - low) of the largest: they count in the sum."""
+    pr = Problem8(q_len, [20000], 4, 2, code=code, page=64, q_scale=0.5)
+    scale = torch.full(pr.scales.shape[:-1], 2.0 ** low, device="cuda")
+    scale[int(pr.table[0, 100]), :, 5] = 2.0 ** high
+    set_values(pr, scale)
+    pr.scales[int(pr.table[0, 100]), :, 5, 0] = 0.5
+    both(pr)
