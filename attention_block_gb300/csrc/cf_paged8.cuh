@@ -117,17 +117,25 @@ __device__ __forceinline__ float rcp(float x) {
 // enters the weights' exponent as 2^-80: the codes are zero, so it only has to be
 // too small to raise the maximum (20 octaves below the least scale) and to leave
 // 2^(s - reference) room for a sum of 2^30 (2^(80 + 15 + 30) at most).
+//
+// What lies outside the scales that are read: below 2^-60 a value scale counts as 0
+// (its codes may be other than zero: what 2^-80 of them adds is below 2^-70); above
+// 2^60 or below 0 a scale counts as NaN.
 struct ValueScale {
-  float log2;   // of what stands for the scale in the exponent
-  float inv;    // 1 / that: what the sum multiplies a weight by
+  float log2;      // of what stands for the scale in the exponent
+  float inv;       // 1 / that: what the sum multiplies a weight by
   bool apart;
   __device__ __forceinline__ explicit ValueScale(float v) {
-    const float vv = v == 0.f ? 0x1p-80f : fmaxf(v, 0x1p-60f);  // (of a NaN: the bound)
+    const float vv = v >= 0x1p-60f ? fminf(v, 0x1p60f) : 0x1p-80f;
     log2 = lg2(vv);
     inv = rcp(vv);
-    apart = !(v >= 0x1p-19f);
+    apart = !(v >= 0x1p-19f && v <= 0x1p60f);
   }
 };
+__device__ __forceinline__ bool scale_is_read(float v) { return v >= 0.f && v <= 0x1p60f; }
+__device__ __forceinline__ float key_scale(float k) {
+  return scale_is_read(k) ? k : __uint_as_float(0x7fc00000u);
+}
 
 // 8 bytes global -> shared, asynchronously; zeros where there is no source.
 __device__ __forceinline__ void cp8(uint32_t dst, const void* src, bool there) {

@@ -433,7 +433,7 @@ __global__ void __launch_bounds__(Shape8<D, NT>::THREADS, 1)
                      : "r"(scale_s + pair * S::SCALES + lane * 8));
         const ValueScale vs(v);
         apart = __ballot_sync(~0u, there && vs.apart);
-        const float ak = there ? k * qk : 0.f, bk = there ? vs.log2 : -INFINITY;
+        const float ak = there ? key_scale(k) * qk : 0.f, bk = there ? vs.log2 : -INFINITY;
         asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(prep_s + lane * 16), "f"(ak),
                      "f"(bk), "f"(vs.apart ? 0.f : vs.inv), "f"(there ? v : 0.f)
                      : "memory");
@@ -539,7 +539,7 @@ __global__ void __launch_bounds__(Shape8<D, NT>::THREADS, 1)
             }
           // a value of NaN: o of the rows that see it
           const float v = __uint_as_float(lds16(prep_s + lane * 16).w);
-          const uint32_t odd = __ballot_sync(~0u, v != v);
+          const uint32_t odd = __ballot_sync(~0u, !scale_is_read(v));
           if (odd) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)

@@ -688,11 +688,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (++out_unit == S::AHEAD) out_unit = 0;
         const ValueScale vs(scale.y);
         Tc8Scales& sc = s_scale[buf];
-        sc.a[row] = scale.x * p.scale_log2;
+        sc.a[row] = key_scale(scale.x) * p.scale_log2;
         sc.b[row] = vs.log2;
         sc.c[row] = vs.inv;
         const uint32_t apart = __ballot_sync(~0u, vs.apart);
-        const uint32_t odd = __ballot_sync(~0u, scale.y != scale.y);
+        const uint32_t odd = __ballot_sync(~0u, !scale_is_read(scale.y));
         if (lane == 0) {
           sc.apart[lw] = apart;
           sc.odd[lw] = odd;

@@ -37,9 +37,11 @@
  * of 1.  Scales and softmax statistics are fp32; weights exp(s_j) vs_j enter the
  * second product in fp16, held down to 2^-32 of the row's largest (a scale of 0
  * counts as 2^-80 there); the sum of exp(s_j) is taken before that rounding and
- * whatever the value scales are.  Scales that are read must be NaN or
- * from 0 to 2^60, value scales other than 0 at least 2^-60 (appending fp16 keeps
- * to that, and so does bf16 between 2^-50 and 2^60), and e4m3 codes not NaN (0x7f,
+ * whatever the value scales are.  Scales are read from 0 to 2^60, value scales
+ * from 2^-60 on: a smaller one counts as 0 (what it adds to o is below 2^-70),
+ * and a scale above 2^60 or below 0 as NaN.  Appending fp16 stays within that, and
+ * so does bf16 between 2^-51 and 2^66; a head of smaller values can be read back
+ * (cf_paged8_read) and adds nothing to o.  E4m3 codes must not be NaN (0x7f,
  * 0xff; none is appended).  Outputs are rounded once.  The same call on the same
  * data gives the same bits.
  *

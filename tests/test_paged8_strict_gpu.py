@@ -3,8 +3,8 @@ import pytest
 import torch
 
 from attention_block_gb300 import binding
-from paged8_util import DT, Problem8
-from test_paged8_gpu import both
+from paged8_util import DT, Problem8, ref_attention8
+from test_paged8_gpu import Run8, both
 
 pytestmark = pytest.mark.gpu
 OK, RANGE = binding.CF_OK, binding.CF_ERR_DEVICE_POS_RANGE
@@ -98,3 +98,62 @@ def test_one_large_value_scale_beside_many_small_ones(code, q_len, low, high):
     set_values(pr, scale)
     pr.scales[int(pr.table[0, 100]), :, 5, 0] = 0.5
     both(pr)
+
+
+@pytest.mark.parametrize("code", CODES)
+@pytest.mark.parametrize("q_len", [[1, 2], [60, 130]], ids=str)
+def test_scales_outside_what_is_read(code, q_len):
+    """A value scale below 2^-60 counts as 0; one above 2^60 or below 0, of a key or a value, as NaN."""
+    pr = Problem8(q_len, [200, 190], 4, 2, code=code)
+    ids, slot = pr.table[:, 2].long(), 3  # position 35 of both sequences
+    pr.scales[ids[0], 0, slot, 1] = 2.0 ** -61
+    pr.scales[ids[0], 1, slot, 1] = 2.0 ** -108
+    want = Problem8(q_len, [200, 190], 4, 2, code=code)
+    want.scales[ids[0], :, slot, 1] = 0
+    want.v_pages.view(torch.uint8)[ids[0], slot] = 0
+    r = Run8(pr).attend()
+    out, tol, lse, ltol = ref_attention8(want)
+    rows = slice(0, q_len[0])
+    assert ((r.out[rows].double() - out[rows]).abs() <= tol[rows]).all()
+    assert ((r.lse[rows].double() - lse[rows]).abs() <= ltol[rows]).all()
+    G, rows = pr.nq // pr.nkv, slice(q_len[0], sum(q_len))
+    for side, bad in ((0, 2.0 ** 61), (0, -1.0), (0, float("inf")), (1, 2.0 ** 61), (1, -2.0 ** -70), (1, float("inf"))):
+        kept = pr.scales.clone()
+        pr.scales[ids[1], 1, slot, side] = bad
+        r.attend()
+        pr.scales.copy_(kept)
+        assert r.kv.status() == OK
+        assert r.out[rows, G:].isnan().all() and not r.out[rows, :G].isnan().any(), (side, bad)
+        assert r.lse[rows, G:].isnan().all() == (side == 0) and not r.lse[rows, :G].isnan().any(), (side, bad)
+        assert not r.out[:q_len[0]].isnan().any()
+
+
+@pytest.mark.parametrize("code", CODES)
+@pytest.mark.parametrize("q_len", [[1], [4], [70]], ids=str)
+@pytest.mark.parametrize("log2", [-99, -70, -53, -49, 65], ids=str)
+def test_heads_of_any_size_are_appended_and_attended(code, q_len, log2):
+    """bf16 values of one size, from where append holds them to the largest that attention reads: o is what is read back,
+    or 0 where the scales lie below 2^-60."""
+    n = 100
+    pr = Problem8(q_len, [n], 4, 2, code=code)
+    ap = Problem8([n], [n], 4, 2, code=code)
+    ap.v = (ap.v.double().clamp(-1.9, 1.9) * 2.0 ** log2).bfloat16()
+    pr.table, pr.k_pages, pr.v_pages, pr.scales = ap.table, ap.k_pages, ap.v_pages, ap.scales
+    pr.num_pages = ap.num_pages
+    kv = binding.Paged8Kv(**ap.config())
+    kv.append(1, n, ap.q, ap.k, ap.v, ap.q_start, ap.lens, ap.table, ap.k_pages, ap.v_pages, ap.scales, ap.q)
+    K, V, ks, vs = pr.held(0, 0, n)
+    back = torch.full((n, 2, pr.d), NAN, dtype=torch.bfloat16, device="cuda")
+    kv.read(1, n, ap.q_start, None, ap.table, ap.k_pages, ap.v_pages, ap.scales, None, back)
+    want = V * vs[..., None]
+    assert kv.status() == OK and want.abs().amax() > 2.0 ** log2
+    assert ((back.double() - want).abs() <= 2.0 ** -8 * want.abs()).all()
+    low = vs < 2.0 ** -60
+    assert low.all() or not low.any()
+    if low.any():
+        r = Run8(pr, poison=False).attend()
+        assert (r.out.double().abs() <= 2.0 ** -70).all()
+        _, _, lse, ltol = ref_attention8(pr)
+        assert ((r.lse.double() - lse).abs() <= ltol).all()
+    else:
+        both(pr)
