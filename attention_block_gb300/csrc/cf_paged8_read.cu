@@ -25,6 +25,7 @@ __global__ void __launch_bounds__(kReadThreads)
     paged8_read_kernel(const __grid_constant__ Paged8ReadParams p) {
   constexpr int C = D / 16;  // 16-byte pieces of a head's codes
   __shared__ int64_t s_code[kReadRows], s_scale[kReadRows];  // -1: zeros, -2: not a row
+  __shared__ int s_seq[kReadRows];
   const int tid = threadIdx.x, r0 = blockIdx.x * kReadRows;
   pdl_wait();
   pdl_trigger();
@@ -32,9 +33,30 @@ __global__ void __launch_bounds__(kReadThreads)
     for (int b = tid; b < p.batch; b += kReadThreads)
       if (!starts_ordered(p.row_start[b], p.row_start[b + 1], p.n_rows))
         atomicOr(p.errflag, kDevErrPosRange);
+  // Whether sequence b has the row r.
+  auto has = [&](int b, int r) {
+    const int t0 = p.row_start[b], t1 = p.row_start[b + 1];
+    return starts_ordered(t0, t1, p.n_rows) && t0 <= r && r < t1;
+  };
+  // Where row r0 + tid of sequence b lies.
+  auto look_up = [&](int b) {
+    int64_t code = -2, scale = -2;
+    const long long j = (long long)(p.first ? p.first[b] : 0) + (r0 + tid - p.row_start[b]);
+    if (j < 0 || j >= (long long)p.g.max_pages << p.g.page_shift) {
+      atomicOr(p.errflag, kDevErrPosRange);
+    } else {
+      const int* table = p.page_table + (int64_t)b * p.g.max_pages;
+      code = paged_offset(table, (int)j, p.g, p.errflag);
+      if (code >= 0) scale = paged8_scale(table, (int)j, p.g);
+    }
+    s_code[tid] = code;
+    s_scale[tid] = scale;
+  };
+  bool lost = false;  // the bisection finds no sequence for this thread's row
   if (tid < kReadRows) {
     const int r = r0 + tid;
-    int64_t code = -2, scale = -2;
+    s_code[tid] = -2;
+    s_seq[tid] = -1;
     if (r < p.n_rows) {
       // the last sequence whose start is at or before the row: those behind it
       // begin later
@@ -46,25 +68,22 @@ __global__ void __launch_bounds__(kReadThreads)
         else
           hi = mid;
       }
-      const int b = lo - 1;
-      if (b >= 0) {
-        const int t0 = p.row_start[b], t1 = p.row_start[b + 1];
-        if (starts_ordered(t0, t1, p.n_rows) && r < t1) {
-          const long long j = (long long)(p.first ? p.first[b] : 0) + (r - t0);
-          if (j < 0 || j >= (long long)p.g.max_pages << p.g.page_shift) {
-            atomicOr(p.errflag, kDevErrPosRange);
-          } else {
-            const int* table = p.page_table + (int64_t)b * p.g.max_pages;
-            code = paged_offset(table, (int)j, p.g, p.errflag);
-            if (code >= 0) scale = paged8_scale(table, (int)j, p.g);
-          }
-        }
-      }
+      lost = lo == 0 || !has(lo - 1, r);
+      if (!lost) look_up(lo - 1);
     }
-    s_code[tid] = code;
-    s_scale[tid] = scale;
   }
-  __syncthreads();
+  if (__syncthreads_or(lost)) {
+    // A row of no sequence or, where starts are out of order, of one that the
+    // bisection passed by: all are asked.
+    for (int b = tid; b < p.batch; b += kReadThreads) {
+      const int t0 = p.row_start[b], t1 = p.row_start[b + 1];
+      if (starts_ordered(t0, t1, p.n_rows))
+        for (int r = max(t0, r0); r < min(t1, r0 + kReadRows); ++r) atomicMax(&s_seq[r - r0], b);
+    }
+    __syncthreads();
+    if (lost && s_seq[tid] >= 0) look_up(s_seq[tid]);
+    __syncthreads();
+  }
   // A thread keeps to one piece of a head and walks over the heads of the rows'
   // keys and values, with several loads on their way.
   const int c = tid % C;

@@ -3,8 +3,8 @@ import pytest
 import torch
 
 from attention_block_gb300 import binding
-from paged8_util import DT, Problem8, ref_attention8
-from test_paged8_gpu import Run8, both
+from paged8_util import DT, Problem8, half_step, ref_attention8
+from test_paged8_gpu import Run8, both, close
 
 pytestmark = pytest.mark.gpu
 OK, RANGE = binding.CF_OK, binding.CF_ERR_DEVICE_POS_RANGE
@@ -157,3 +157,31 @@ def test_heads_of_any_size_are_appended_and_attended(code, q_len, log2):
         assert ((r.lse.double() - lse).abs() <= ltol).all()
     else:
         both(pr)
+
+
+# ------------------------------------------------------------- reading back --
+@pytest.mark.parametrize("start,rows", [
+    ([0, 100, 8, 10], 10), ([0, 5, 3, 10], 10), ([9, 30, -1, 4, 9, 6, 9, 30], 30), ([40, 0, 20, 40], 40),
+    ([0] + [2 ** 31 - 1] * 3 + [4, 9, 17], 20), ([t if t % 7 else 1000 for t in range(301)], 300),
+    ([3, 3, 3, 7, 7, 20], 23)], ids=["far", "falling", "mixed", "swapped", "limit", "many", "in order"])
+def test_rows_beside_malformed_starts_are_read(start, rows):
+    """A sequence whose starts decrease or leave the rows has none, the others have theirs."""
+    batch = len(start) - 1
+    pr = Problem8([1] * batch, [30 + 3 * (b % 9) for b in range(batch)], 4, 2, d=64, max_pages=4)
+    kv = binding.Paged8Kv(**pr.config())
+    k, v = (torch.full((rows, 2, 64), 99.0, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    kv.read(batch, rows, torch.tensor(start, dtype=torch.int32, device="cuda"), None, pr.table, pr.k_pages, pr.v_pages,
+            pr.scales, k, v)
+    ordered = all(0 <= a <= b <= rows for a, b in zip(start, start[1:]))
+    assert kv.status() == (OK if ordered else RANGE)
+    want = [torch.full((rows, 2, 64), 99.0, dtype=torch.float64, device="cuda") for _ in range(2)]
+    twice = torch.zeros(rows, dtype=torch.int32, device="cuda")
+    for b, (a, e) in enumerate(zip(start, start[1:])):
+        if 0 <= a <= e <= rows and e - a <= pr.kv_len[b]:
+            K, V, ks, vs = pr.held(b, 0, e - a)
+            want[0][a:e], want[1][a:e] = K * ks[..., None], V * vs[..., None]
+            twice[a:e] += 1
+    assert (twice == 1).any()
+    for got, w in zip((k, v), want):
+        one = twice < 2  # what a row holds that two claim is unspecified
+        close(got[one], w[one], half_step("bf16") * (1 + 2.0 ** -10) * w[one].abs(), "rows")
