@@ -254,7 +254,8 @@ struct XFrag {
       for (int part = 0; part < 3; ++part)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          // cut off, not rounded: what is left is exact, and an infinity leaves nothing
+          // cut off, not rounded: what is left is exact; an infinity leaves nothing, and
+          // a NaN, whose upper half may be an infinity's, a NaN
           const uint32_t a = __float_as_uint(f[2 * i]), b = __float_as_uint(f[2 * i + 1]);
           w[part][i] = __byte_perm(a, b, 0x7632);
           f[2 * i] = rest(f[2 * i]);
@@ -264,7 +265,7 @@ struct XFrag {
   }
   static __device__ __forceinline__ float rest(float f) {
     const float hi = __uint_as_float(__float_as_uint(f) & 0xffff0000u);
-    return fabsf(f) < INFINITY ? f - hi : 0.f;
+    return fabsf(f) == INFINITY ? 0.f : f - hi;
   }
 };
 

@@ -33,3 +33,19 @@ def test_a_product_reads_what_the_launches_in_front_wrote(dtype, rows):
     for _ in range(3):
         assert torch.equal(run(False), want)
     assert first.mv.status() == binding.CF_OK and second.mv.status() == binding.CF_OK
+
+
+@pytest.mark.parametrize("bits", [0x7f800001, 0x7f80ffff, 0xff800001, 0xff801234, 0x7fc00000])
+@pytest.mark.parametrize("rows", [2, 20])
+def test_every_nan_of_32_bits_makes_its_row_nan(bits, rows):
+    m = Mat(384, 140, 128, True, "f32", rows)
+    m.codes[77], m.zeros[0] = 0xff, 3  # all of the same sign, and none zero
+    m.scales.abs_()
+    m.packed = m.mv.pack(m.codes, m.scales, m.zeros)
+    clean = torch.empty(rows, 140, device="cuda")
+    m.mv(rows, m.x, m.packed, clean)
+    m.x.view(torch.int32)[1, 77] = bits - (1 << 32 if bits >> 31 else 0)
+    out = torch.empty_like(clean)
+    m.mv(rows, m.x, m.packed, out)
+    assert out[1].isnan().all()
+    assert torch.equal(out[0], clean[0]) and torch.equal(out[2:], clean[2:])
