@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(Shape8<D, NT>::THREADS, 1)
   // parts, and no block has parts of two (one sequence of 4097 positions, 32 / 8
   // heads of 128: 14.0 us without, 12.7 with; of 101: 10.0 and 8.4).
   int pad = 0;
-  if (small && block_upc <= 4 * WARPS) {
+  if (small && total > 0 && block_upc <= 4 * WARPS) {
     const int n = (int)block_upc, wide = (own_tiles + n - 1) / n * n;
     const long long padded = scan((long long)wide * p.g.nkv);
     const long long all = __shfl_sync(~0u, padded, 31);

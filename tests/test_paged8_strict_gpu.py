@@ -185,3 +185,23 @@ def test_rows_beside_malformed_starts_are_read(start, rows):
     for got, w in zip((k, v), want):
         one = twice < 2  # what a row holds that two claim is unspecified
         close(got[one], w[one], half_step("bf16") * (1 + 2.0 ** -10) * w[one].abs(), "rows")
+
+
+# ------------------------------------------------------ calls without tokens --
+@pytest.mark.parametrize("batch", [1, 32, 33, 300])
+@pytest.mark.parametrize("max_q", [1, 40])
+def test_tokens_of_no_sequence_are_left_alone(batch, max_q):
+    """A padded call: n_tokens rows, none of which belongs to a sequence."""
+    pr = Problem8([0] * batch, [30 + b % 7 for b in range(batch)], 8, 2, d=64, extra_tokens=50)
+    r = Run8(pr)
+    before = [pr.k_pages.clone(), pr.v_pages.clone(), pr.scales.clone()]
+    q_out = torch.full_like(pr.q, 7.0)
+    r.out.fill_(7), r.lse.fill_(7)
+    for _ in range(2):
+        r.attend(max_q=max_q)
+        r.kv.append(batch, pr.tokens, pr.q, pr.k, pr.v, pr.q_start, pr.lens, pr.table, pr.k_pages, pr.v_pages, pr.scales, q_out)
+        assert r.kv.status() == OK
+    for x in (r.out, r.lse, q_out):
+        assert (x == 7).all()
+    for x, y in zip(before, (pr.k_pages, pr.v_pages, pr.scales)):
+        assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
