@@ -45,6 +45,7 @@
 #include "cf_common.cuh"
 #include "cf_mma.cuh"
 #include "cf_paged.cuh"
+#include "cf_paged_host.h"
 #include "cf_w4.h"
 
 using namespace cf;
@@ -583,13 +584,6 @@ W4Plan w4_plan(const W4Shape& s, int dtype, int rows, int sms) {
   return p;
 }
 
-bool overlap(const void* a, size_t na, const void* b, size_t nb) {
-  if (a == nullptr || b == nullptr || na == 0 || nb == 0) return false;
-  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return x < y + nb && y < x + na;
-}
-bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
-
 }  // namespace
 
 struct cf_w4_handle {
@@ -658,9 +652,7 @@ int cf_w4_create(const cf_w4_config* cfg, cf_w4_handle** out) {
     if (cudaFuncSetAttribute(w4_fn_of(c.dtype, rows), cudaFuncAttributeMaxDynamicSharedMemorySize,
                              kMaxSmem) != cudaSuccess)
       return fail();
-  if (cudaMalloc(&h->errflag, sizeof(int)) != cudaSuccess ||
-      cudaMemset(h->errflag, 0, sizeof(int)) != cudaSuccess ||
-      cudaStreamSynchronize(nullptr) != cudaSuccess)
+  if (cudaMalloc(&h->errflag, sizeof(int)) != cudaSuccess || !clear(h->errflag, sizeof(int)))
     return fail();
   *out = h;
   return CF_OK;
@@ -753,7 +745,7 @@ int cf_w4_get_status(cf_w4_handle* h) {
   int flag = 0;
   if (cudaMemcpy(&flag, h->errflag, sizeof(int), cudaMemcpyDeviceToHost) != cudaSuccess)
     return CF_ERR_CUDA;
-  if (flag != 0 && cudaMemset(h->errflag, 0, sizeof(int)) != cudaSuccess) return CF_ERR_CUDA;
+  if (flag != 0 && !clear(h->errflag, sizeof(int))) return CF_ERR_CUDA;
   return flag != 0 ? CF_ERR_DEVICE_TIMEOUT : CF_OK;
 }
 
