@@ -852,8 +852,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   if (warp == 12) tmem_dealloc(tmem, 512);
 }
 
-// Joins the states of split items: a row per D / 4 lanes, gridDim.y blocks to
-// an item (cf_paged_tc.cu).
+// Joins the states of split items, one to a block of the main kernel at most: a row
+// per D / 4 lanes, gridDim.y blocks to an item.
 constexpr int kTc8JoinY = 16;
 template <typename T, int D>
 __global__ void __launch_bounds__(256, 4) paged8_tc_join_kernel(const __grid_constant__ Tc8Args a) {
@@ -861,20 +861,18 @@ __global__ void __launch_bounds__(256, 4) paged8_tc_join_kernel(const __grid_con
   constexpr int C4 = D / 4;
   pdl_wait();
   pdl_trigger();
-  for (int item = blockIdx.x; item < a.grid; item += gridDim.x) {
-    const TcMeta x = a.meta[item];
-    // (an item that ends behind the line: lengths changed under the call)
-    if (x.tiles == 0 || x.i0 + x.tiles > x.upc * a.grid) continue;
-    const int rows = min(2 * kHalf, x.rows - x.j * 2 * kHalf);
-    const PagedItemParts parts(x.i0, x.tiles, x.upc);
-    for (int e = blockIdx.y * 256 + threadIdx.x; e < rows * C4; e += gridDim.y * 256) {
-      const int r = e / C4, col = (e - r * C4) * 4;
-      PagedState4 s{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-      const int gr = x.j * 2 * kHalf + r, i = gr / p.g.G, g = gr - i * p.g.G;
-      const long long row = ((long long)x.t0 + i) * p.g.nq + x.h * p.g.G + g;
-      paged_join_row<D, 4, true>(s, a.ws.o, a.ws.ml, PagedRowParts(parts, 2 * kHalf, r, -1), col);
-      paged_store4<T, D>(s, p.out, p.lse, row, col);
-    }
+  const TcMeta x = a.meta[blockIdx.x];
+  // (an item that ends behind the line: lengths changed under the call)
+  if (x.tiles == 0 || x.i0 + x.tiles > x.upc * a.grid) return;
+  const int rows = min(2 * kHalf, x.rows - x.j * 2 * kHalf);
+  const PagedItemParts parts(x.i0, x.tiles, x.upc);
+  for (int e = blockIdx.y * 256 + threadIdx.x; e < rows * C4; e += gridDim.y * 256) {
+    const int r = e / C4, col = (e - r * C4) * 4;
+    PagedState4 s{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+    const int gr = x.j * 2 * kHalf + r, i = gr / p.g.G, g = gr - i * p.g.G;
+    const long long row = ((long long)x.t0 + i) * p.g.nq + x.h * p.g.G + g;
+    paged_join_row<D, 4, true>(s, a.ws.o, a.ws.ml, PagedRowParts(parts, 2 * kHalf, r, -1), col);
+    paged_store4<T, D>(s, p.out, p.lse, row, col);
   }
 }
 
@@ -921,5 +919,5 @@ bool cf::paged8_tc_launch(int dtype, int code, const PagedAttnParams& p, const P
   // fewer blocks to an item where its rows are fewer
   const long long rows = std::min<long long>(kTcRows, (long long)p.max_q * p.g.G);
   const int y = (int)std::min<long long>(kTc8JoinY, (rows * (p.g.D / 4) + 255) / 256);
-  return launch_pdl(f.join, dim3(ws.grid * (kTc8JoinY / y), y), 256, 0, st, args);
+  return launch_pdl(f.join, dim3(ws.grid, y), 256, 0, st, args);
 }
