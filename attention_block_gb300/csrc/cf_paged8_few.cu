@@ -148,19 +148,21 @@ __global__ void __launch_bounds__(Shape8<D, NT>::THREADS, 1)
   const long long block_upc = div_units(total + gridDim.x * WARPS - 1, gridDim.x * WARPS) * WARPS;
   if (lane == 0) s_has[0][warp] = s_has[1][warp] = 0;
   if (!small) __syncthreads();
-  // Where there is little work, an item takes whole blocks: it is cut into fewer
-  // parts, and no block has parts of two (one sequence of 4097 positions, 32 / 8
-  // heads of 128: 14.0 us without, 12.7 with; of 101: 10.0 and 8.4).
+  // Where there is little work and the blocks are enough for it, an item takes whole
+  // ones: it is cut into fewer parts, and no block has parts of two.  Without and
+  // with, us: one sequence of 4097 positions, 32 / 8 heads of 128, 14.1 and 12.8, of
+  // 101 10.1 and 8.4; 24 of 301, 16 / 4 heads, 13.0 and 9.3; 2 of 8001, 32 heads, 34.3
+  // and 34.3.  Where they are not enough, the question costs 0.1 (32 heads, 8 of
+  // 301-901, 19.7 and 19.8; 4 of 501-2001, 21.4 and 21.6).
   int pad = 0;
   if (small && total > 0 && block_upc <= 4 * WARPS) {
-    const int n = (int)block_upc, wide = (own_tiles + n - 1) / n * n;
-    const long long padded = scan((long long)wide * p.g.nkv);
-    const long long all = __shfl_sync(~0u, padded, 31);
-    if (all <= gridDim.x * block_upc) {
+    const int n = (int)block_upc, blocks = (own_tiles + n - 1) / n * p.g.nkv;
+    const uint32_t all = __reduce_add_sync(~0u, (uint32_t)blocks);
+    if (all <= gridDim.x) {
       pad = n;
-      mine = (long long)wide * p.g.nkv;
-      before = padded - mine;
-      total = all;
+      mine = (long long)blocks * n;
+      before = scan(mine) - mine;
+      total = (long long)all * n;
     }
   }
   auto units = [&](int tiles) { return pad ? (tiles + pad - 1) / pad * pad : tiles; };
