@@ -31,19 +31,21 @@
  *
  * Arithmetic: codes are whole in the products, which run on the tensor cores
  * as fp16 x fp16 with fp32 sums.  The query enters as fp16: bf16 queries are
- * multiplied by a power of two, the same for the rows that share a tile (with
- * max_q * nq/nkv above 16: for rows whose largest element is not between 2^-10
- * and 2^15), and lose only what is below 2^-32 of the tile's largest element, or
- * of 1.  Scales and softmax statistics are fp32; weights exp(s_j) vs_j enter the
- * second product in fp16, held down to 2^-32 of the row's largest (a scale of 0
- * counts as 2^-80 there); the sum of exp(s_j) is taken before that rounding and
- * whatever the value scales are.  Scales are read from 0 to 2^60, value scales
- * from 2^-60 on: a smaller one counts as 0 (what it adds to o is below 2^-70),
- * and a scale above 2^60 or below 0 as NaN.  Appending fp16 stays within that, and
- * so does bf16 between 2^-51 and 2^66; a head of smaller values can be read back
- * (cf_paged8_read) and adds nothing to o.  E4m3 codes must not be NaN (0x7f,
- * 0xff; none is appended).  Outputs are rounded once.  The same call on the same
- * data gives the same bits.
+ * multiplied by a power of two where they need it.  With max_q * nq/nkv of 16 at
+ * most that is the same for the rows that share a tile (a sequence's, of one KV
+ * head), and an element is off by 2^-39 of the largest of them at most; with more
+ * by 2^-25 in a row whose largest lies between 2^-10 and 2^15, else by 2^-39 of
+ * that (or by 2^-138).  Scales and softmax statistics are fp32; weights
+ * exp(s_j) vs_j enter the second product in fp16, held down to 2^-32 of the row's
+ * largest (a scale of 0 counts as 2^-80 there); the sum of exp(s_j) is taken before
+ * that rounding and whatever the value scales are.  Outputs are rounded once.  The
+ * same call on the same data gives the same bits.
+ *
+ * Scales are read from 0 to 2^60, value scales from 2^-60 on: a smaller one counts
+ * as 0 (what it adds to o is below 2^-70), and a scale above 2^60 or below 0 as
+ * NaN.  Appending fp16 stays within that, and so does bf16 between 2^-51 and 2^66;
+ * a head of smaller values can be read back (cf_paged8_read) and adds nothing to o.
+ * E4m3 codes must not be NaN (0x7f, 0xff; none is appended).
  *
  * Conventions, and what the device records (cf_paged8_get_status), are those
  * of cf_paged.h; scales are 8-byte aligned.

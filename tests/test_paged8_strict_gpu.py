@@ -159,6 +159,25 @@ def test_heads_of_any_size_are_appended_and_attended(code, q_len, log2):
         both(pr)
 
 
+# ----------------------------------------------------------------- queries --
+@pytest.mark.parametrize("code", CODES)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("q_len", [[1], [4], [70]], ids=str)
+@pytest.mark.parametrize("log2", [-30, -11, -10, 0, 20])
+def test_elements_of_bf16_queries_far_below_the_largest(code, d, q_len, log2):
+    """A row's largest element meets keys of zero; the scores come from elements 2^-15 of it.  They count whole but in the
+    many-row kernel where the largest lies between 2^-10 and 2^15: there they are multiples of 2^-24."""
+    pr = Problem8(q_len, [300], 4, 2, d=d, code=code)
+    pr.q = (pr.q.double() * 2.0 ** (log2 - 16)).bfloat16()
+    pr.q[..., 0] = 1.5 * 2.0 ** log2
+    pr.k_pages.view(torch.uint8)[..., 0] = 0
+    pr.scales[..., 0] *= 2.0 ** (15 - log2)
+    r = Run8(pr).attend()
+    if q_len[0] * 2 > 16 and -10 <= log2 < 15:
+        pr.q = pr.q.half().double()
+    r.check()
+
+
 # ------------------------------------------------------------- reading back --
 @pytest.mark.parametrize("start,rows", [
     ([0, 100, 8, 10], 10), ([0, 5, 3, 10], 10), ([9, 30, -1, 4, 9, 6, 9, 30], 30), ([40, 0, 20, 40], 40),
