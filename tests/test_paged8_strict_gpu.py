@@ -178,6 +178,37 @@ def test_elements_of_bf16_queries_far_below_the_largest(code, d, q_len, log2):
     r.check()
 
 
+# ------------------------------------------------------------------- append --
+@pytest.mark.parametrize("code", CODES)
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_appends_of_any_size_leave_the_same_codes_and_scales(code, dtype, d):
+    """A sequence appended at once, by a call of one token to a block or of four, and in chunks down to single tokens: codes
+    and scales of every position, the last page's among them, and the rotated queries are the same bits."""
+    n = 1301
+    pr = Problem8([n], [n], 8, 2, d=d, code=code, dtype=dtype, max_pages=90, spare=20)
+    kv = binding.Paged8Kv(**pr.config())
+
+    def appended(chunks):
+        pr.k_pages.view(torch.uint8).fill_(9), pr.v_pages.view(torch.uint8).fill_(9), pr.scales.fill_(NAN)
+        q_out = torch.full_like(pr.q, NAN)
+        at = 0
+        for c in chunks:
+            rows = slice(at, at + c)
+            at += c
+            lens = torch.tensor([at], dtype=torch.int32, device="cuda")
+            st = torch.tensor([0, c], dtype=torch.int32, device="cuda")
+            kv.append(1, c, pr.q[rows], pr.k[rows], pr.v[rows], st, lens, pr.table, pr.k_pages, pr.v_pages, pr.scales, q_out[rows])
+        assert at == n and kv.status() == OK
+        return [q_out] + list(pr.held(0, 0, n)) + [pr.k_pages.clone(), pr.v_pages.clone(), pr.scales.clone()]
+
+    want = appended([n])
+    assert all(torch.isfinite(x).all() for x in want[:5])
+    for chunks in ([1221, 64, 1, 7, 1, 1, 5, 1], [400, 1, 900], [1] * 21 + [1280]):
+        for a, b in zip(appended(chunks), want):
+            assert torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8))
+
+
 # ------------------------------------------------------------- reading back --
 @pytest.mark.parametrize("start,rows", [
     ([0, 100, 8, 10], 10), ([0, 5, 3, 10], 10), ([9, 30, -1, 4, 9, 6, 9, 30], 30), ([40, 0, 20, 40], 40),
