@@ -157,8 +157,7 @@ struct Paged8ReadParams {
   int* errflag;
   int batch, n_rows;
 };
-bool paged8_read_launch(int dtype, int code, const Paged8ReadParams& p, int sm_count,
-                        cudaStream_t st);
+bool paged8_read_launch(int dtype, int code, const Paged8ReadParams& p, cudaStream_t st);
 
 // The kernel for few rows (tokens x grouped heads, at most kFewRows).  grid:
 // resident blocks, 0 on failure; its parts take as many rows as
@@ -166,7 +165,6 @@ bool paged8_read_launch(int dtype, int code, const Paged8ReadParams& p, int sm_c
 int paged8_few_grid(int dtype, int code, int head_dim, int sm_count);
 bool paged8_few_launch(int dtype, int code, const PagedAttnParams& p, const PagedSplit& ws,
                        cudaStream_t st);
-
 
 // The kernel for many rows; its parts take as many rows as paged_tc_part_rows
 // says, and its list of items paged8_tc_list_bytes.

@@ -173,7 +173,7 @@ int cf_paged8_read(cf_paged8_handle* h, int32_t batch, int32_t n_rows, const int
   p.errflag = h->errflag;
   p.batch = batch;
   p.n_rows = n_rows;
-  if (!paged8_read_launch(c.dtype, h->code, p, h->sm_count, static_cast<cudaStream_t>(stream))) {
+  if (!paged8_read_launch(c.dtype, h->code, p, static_cast<cudaStream_t>(stream))) {
     cudaGetLastError();
     return CF_ERR_CUDA;
   }

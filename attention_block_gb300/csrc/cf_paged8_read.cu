@@ -152,8 +152,7 @@ const void* read_fn(int code) {
 
 }  // namespace
 
-bool cf::paged8_read_launch(int dtype, int code, const Paged8ReadParams& p, int sm_count,
-                            cudaStream_t st) {
+bool cf::paged8_read_launch(int dtype, int code, const Paged8ReadParams& p, cudaStream_t st) {
   const void* fn = dtype == CF_F16 ? (p.g.D == 64 ? read_fn<__half, 64>(code)
                                                   : read_fn<__half, 128>(code))
                                    : (p.g.D == 64 ? read_fn<__nv_bfloat16, 64>(code)
