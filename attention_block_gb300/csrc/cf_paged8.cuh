@@ -56,7 +56,9 @@ __device__ __forceinline__ void quantise_head(const float (&f)[16], float& scale
 }
 
 // Four codes as two words of fp16 values: of codes 0 and 2, and of 1 and 3.
-// Both are exact; an e4m3 NaN becomes a NaN.
+// Both are exact; an e4m3 NaN becomes a NaN.  (Whole numbers set into the mantissa of
+// a power of two, which is then subtracted: a published way with weights of 8 and 4
+// bits, Kim et al., 2022; the constants follow from the format.)
 template <int CODE>
 __device__ __forceinline__ void code_halves(uint32_t w, uint32_t& even, uint32_t& odd) {
   if constexpr (CODE == CF_CODE_INT8) {

@@ -5,10 +5,11 @@
 // head hold all of it, 16 elements each, find its largest magnitude by shuffles
 // and write 8-byte pieces of codes; the first of them writes the scale.
 //
-// Bound by memory, with the arithmetic close behind: 9600 tokens, 32 + 2 x 8
-// heads of 128: 40 us, 4.5 TB/s, with five blocks on an SM (48 registers; 62 us
-// with the eight of cf_paged_append.cu, which spill, 43 with four); a single
-// token: 3 us, the launch.
+// Bound by the reads that are on their way, with issue at half of what it can: 8063
+// tokens, 32 + 2 x 8 heads of 128: 41 us, 4.5 TB/s, with five blocks on an SM (48
+// registers; half as long again with the eight of cf_paged_append.cu, which spill,
+// 43 for 40 with four); a single token: 3 us, the launch.  The source is not shared
+// with cf_paged_append.cu: that one took 45 us for 36 when it was.
 #include <cuda_runtime.h>
 
 #include "cf_paged.cuh"

@@ -2,9 +2,9 @@
 // rows per KV head: single tokens and short drafts (tokens x grouped heads <=
 // 16).
 //
-// 16 sequences of 4097 positions, 32 / 8 heads of 128: 36 us, 3.9 TB/s (the 16-bit
-// cache: 54); 32 of 2048-32768: 199, 5.8 TB/s; one of 1025, 32 heads: 12; 4 draft
-// tokens of 32 sequences of 1005-4100 (16 rows): 61.  Half the bytes to the
+// 16 sequences of 4097 positions, 32 / 8 heads of 128: 35 us, 4.0 TB/s (the 16-bit
+// cache: 54); 32 of 2383-32504: 186-200, 5.8-6.2 TB/s; one of 1025, 32 heads: 12; 4
+// draft tokens of 32 sequences of 1070-4093 (16 rows): 63.  Half the bytes to the
 // arithmetic of the 16-bit cache: the work per byte decides the form.  Keys and values are
 // the A operand of mma.sync m16n8k16 and the rows its B operand, in octets:
 // S^T = K Q^T (16 keys x 8 rows) and O^T = V^T P^T (16 columns x 8 rows), so
@@ -18,7 +18,10 @@
 // value j is exp(s_j) vs_j = 2^(a_j q.k_j + b_j), so one fused product, one
 // maximum and one exponential serve the weights, whatever the scales are; the
 // sum of exp(s_j) takes the weight times 1 / vs_j, or where vs_j is small or zero
-// an exponential of its own (ValueScale).
+// an exponential of its own (ValueScale).  Weights enter the second product as one
+// fp16 value: a relative 2^-12 each, by which results in fp16 are off 2.2e-4 of their
+// norm for the 2.1e-4 of their own rounding; a second value for the rest would double
+// that product.
 //
 // A unit of 32 positions takes a warp 820 instructions (e4m3, 8 rows), 55 % of the
 // SM's issue slots at the copy rate, but 5500 cycles: with three warps to a

@@ -4,8 +4,8 @@
 // Bound by memory: per head d codes and a scale read, 2 d bytes written.  A
 // block takes eight rows: a thread per row looks up where it lies (sequence by
 // bisection of the starts, page), then 16 codes at a time are expanded by
-// neighbouring threads, four loads ahead.  24,600 positions of 32 heads of 64: 57
-// us, 5.3 TB/s (16 rows to a block 59, 32: 68; eight loads ahead 74, two 66).
+// neighbouring threads, four loads ahead.  25,299 positions of 32 heads of 64: 56
+// us, 5.6 TB/s (16 rows to a block 59, 32: 68; eight loads ahead 74, two 66).
 #include <cuda_runtime.h>
 
 #include <algorithm>

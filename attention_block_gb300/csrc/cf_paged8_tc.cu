@@ -23,20 +23,29 @@
 //             (of the first item together with the softmax warps)
 // What a row does not see gets a weight of exactly 0, and codes are finite, so
 // nothing that lies in a slot reaches a row that does not see it; a NaN among
-// a tile's value scales is set in the weights of the rows that see it.
+// a tile's value scales is set in the scores of the rows that see it.  Weights
+// enter the second product as one fp16 value (cf_paged8_few.cu); over short contexts
+// results in fp16 are off 2.8e-4 of their norm, 2.1e-4 of it their own rounding.
 //
-// 512 tokens behind 15872 (32 / 8 heads of 128): 171 us, 790 TFLOP/s; 4 chunks of
-// 820-1024 tokens behind 195-1752, 32 heads: 207.  A half's tiles are a chain: 3450
-// cycles softmax, 1950 until the next scores are there (products of both halves
-// 2050).  Of the softmax, reading the positions' a, b, c takes up to a sixth: without
-// them 150 and 205 us.  Accumulator fragments, with which a thread needs a quarter of
-// them, take 186 and 316 (205 and 272 in two passes of 32 columns each): their chains
-// are longer.  code x scale rounded to fp16 as operand, with powers of two alone
-// in the softmax, takes 163 and 215, but puts 2.7 times the error of an fp16
-// result on it.  An item's result takes 5500-7500 cycles, its queries 8000 (bf16:
-// 18000), some behind the last tiles.  Queries by halves, and half 1's last product
-// behind the next item's first scores, let the halves fall out of step: 4 chunks of
-// bf16, GQA, 199 us for 190.
+// 512 tokens behind 15872 (32 / 8 heads of 128): 160 us, 845 TFLOP/s; 4 chunks of
+// 820-1024 tokens behind 195-1752, 32 heads: 194; one prompt of 8192 647.  The 16-bit
+// cache takes 113, 153 and 402 for the same: its kernel loads tiles as they are, this
+// one expands each again for every 256 rows, through three slots for five (what each
+// of these costs is not measured).
+//
+// A half's tiles are a chain: when they took 171 and 207 us, 3450 cycles softmax and
+// 1950 until the next scores were there (products of both halves 2050).  A branch for
+// NaN behind each 32 columns was 11-13 us of that: what is rare stands in the block
+// that the maximum's growth enters (in blocks of its own 172-190 and 214-233).
+// Measured before that was found: reading the positions' a, b, c takes up to a sixth
+// of the softmax (without them 150 and 205 of 171 and 207).  Accumulator fragments,
+// with which a thread needs a quarter of them, take 186 and 316 (205 and 272 in two
+// passes of 32 columns each): their chains are longer.  code x scale rounded to fp16
+// as operand, with powers of two alone in the softmax, takes 163 and 215, but puts
+// 2.7 times the error of an fp16 result on it.  An item's result takes 5500-7500
+// cycles, its queries 8000 (bf16: 18000), some behind the last tiles.  Queries by
+// halves, and half 1's last product behind the next item's first scores, let the
+// halves fall out of step: 4 chunks of bf16, GQA, 199 us for 190.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -76,8 +85,9 @@ struct Tc8Scales {
 };
 
 // What an item costs apart from its tiles, in tiles: its queries, its result, the
-// halves out of step.  4 chunks of 820-1024 tokens, 32 heads: 207 us with 4, 210
-// with 5, 211 with 6; one chunk of 512 behind 15872: 178, 182, 182.
+// halves out of step.  4 chunks of 820-1024 tokens, 32 heads: 194.5 us with 3, 193.8
+// with 4, 196.4 with 5; one chunk of 512 behind 15872: 161.5, 159.6, 161.5; one prompt
+// of 8192: 726, 647, 644.
 constexpr int kItemCost8 = 4;
 using Cursor = TcCursor<false, kItemCost8>;
 
@@ -110,8 +120,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   constexpr int LIFT = weight_lift<__half>(kGrow);
   constexpr float BACK = 1.f / (1 << LIFT);
   // Warps that bring the first item's queries: turning them takes longer than the
-  // softmax warps' help costs (bf16, 512 behind 15872 171 us, with 3 178; fp16, 4
-  // chunks 210, with 3 208).
+  // softmax warps' help costs (bf16, 512 behind 15872 159.6 us, with 3 163.1; fp16, 4
+  // chunks 195.7, with 3 193.8).
   constexpr int FIRST = kIsBf16<T> ? 11 : 3;
   const PagedAttnParams& p = a.p;
   extern __shared__ __align__(1024) uint8_t sm[];
@@ -303,8 +313,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
   if (warp < 8) {
     // ------------------------------------------------------------ softmax --
-    // 72 for the others: the codes do not spill, and the two below less than with 56
-    // (4 chunks, 32 heads: 211 us, with 88 and 56 214); softmax of 176 spills (221).
+    // 72 for the others (4 chunks, 32 heads, 193.8 us, 512 behind 15872 159.6; with 88 for
+    // the codes and 56 for the rest 194.1 and 157.9; with 176 here and 80 there 190.8 and
+    // 166.9).
     set_regs_up<184>();
     const int hf = warp >> 2;                   // half
     const int r = (warp & 3) * 32 + lane;       // row of the half = TMEM lane

@@ -4,8 +4,8 @@
 // The weights are the tensor core's A operand (16 columns of W by 16 elements
 // of k), the rows of x its B operand (8 rows), so one row costs as many
 // instructions as eight.  A code c becomes the 16-bit float 1024 + c (fp16) or
-// 128 + c (bf16) by setting bits, and c - zero by one exact subtraction; a
-// group's sum is scaled in fp32.
+// 128 + c (bf16) by setting bits, and c - zero by one exact subtraction (a published
+// way with weights of few bits, Kim et al., 2022); a group's sum is scaled in fp32.
 //
 // A record holds 16 columns x 128 elements of k.  Its codes: for each 64 of k a
 // 16-byte vector per lane, word s the A fragment of step s.  Lane (g, t) of step
@@ -27,13 +27,14 @@
 // cluster, which exchange their sums through distributed shared memory; all sums
 // are joined in a fixed order.
 //
-// One row, 4096 x 12288 in fp16: 8.5 us with the weights in DRAM, 3.1 TB/s; 4096 x
+// One row, 4096 x 12288 in fp16: 8.1-8.5 us with the weights in DRAM, 3.1 TB/s; 4096 x
 // 22016 in bf16: 14.3, 3.3 TB/s; 16 rows, 11008 x 4096: 12.4.  2-3 us of it are the
-// launch, the first records and the sums; the rest is bound by the integer pipe,
-// two cycles an instruction (a word of eight codes takes 4 masks and 3 shifts in
-// bf16, 4 and 1 in fp16), at about half of what it can issue: 16 warps on an SM do
-// not hide all of the chains from copy to product.  From 32 rows on the products
-// themselves (mma.sync) take longer than the weights: 64 rows 64 us.
+// launch, the first records and the sums.  Of the rest no pipe is full (one row and 16
+// rows: integer 38 and 27 %, issue 48 and 35, DRAM 26 and 17, tensor cores 18): a
+// warp's steps are chains from copy over unpacking (a word of eight codes takes 4
+// masks and 3 shifts in bf16, 4 and 1 in fp16) to product and scale, and 16 warps on
+// an SM do not hide them.  With more rows x and the products (mma.sync) grow, the
+// weights' share falls: 4096 x 12288, 32 rows 23, 64 rows 41.
 #include <cuda_runtime.h>
 
 #include <algorithm>

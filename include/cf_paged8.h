@@ -72,9 +72,9 @@ typedef struct cf_paged8_config {
 typedef struct cf_paged8_handle cf_paged8_handle; /* opaque */
 
 /* Validate cfg and allocate the handle's workspace on the current device: an
- * error word and partial results of split sequences (up to 160,000 * (d + 2)
- * fp32 values, 81 MB for d = 128).  On failure nothing stays allocated and
- * *out is NULL.  Errors: INVALID_ARG, UNSUPPORTED (head_dim, page_size, fp32),
+ * error word, a word for each sequence and KV head, and partial results of split
+ * sequences (with 152 SMs up to (d + 2) * 77,824 fp32 values, 40 MB for d = 128).
+ * On failure nothing stays allocated and *out is NULL.  Errors: INVALID_ARG, UNSUPPORTED (head_dim, page_size, fp32),
  * CUDA. */
 int cf_paged8_create(const cf_paged8_config* cfg, cf_paged8_handle** out);
 
@@ -96,7 +96,8 @@ int cf_paged8_attention(cf_paged8_handle* h, int32_t batch, int32_t n_tokens, in
                         const void* v_pages, const float* scales, int32_t window, int32_t n_sinks,
                         void* out, float* lse, void* stream);
 
-/* Read positions back into rows of the storage type, code * scale rounded once.
+/* Read positions back into rows of the storage type: code * scale in fp32, then
+ * rounded to it.
  *   row_start [batch+1] int32: sequence b has the rows row_start[b] ..
  *             row_start[b+1]-1; rows from row_start[batch] on stay as they are
  *   first     [batch] int32, the position of each sequence's first row, or
