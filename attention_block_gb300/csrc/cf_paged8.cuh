@@ -111,28 +111,32 @@ __device__ __forceinline__ float rcp(float x) {
 }
 
 // Value scales in the weights.  A position's weight takes log2 vs into its
-// exponent; the sum of exp(s) takes the weight times 1 / vs.  That is exact enough
-// while 1 / vs is below 2^19: with a maximum that holds a scale of 2^60, the most
-// that there is, a weight is flushed where exp(s) is below 2^-54 of the largest,
-// so that 2^30 of them lose 2^-24 of the sum.  Positions with a smaller scale, or
-// one of zero, are added to the sum apart, as 2^(s - reference).  A scale of zero
-// enters the weights' exponent as 2^-80: the codes are zero, so it only has to be
-// too small to raise the maximum (20 octaves below the least scale) and to leave
+// exponent; the sum of exp(s) takes the weight times 1 / vs.  That is whole while the
+// scales of a row lie within 2^79 of one another: what is flushed then has an exp(s)
+// below 2^-54 of the largest, and 2^30 of them are 2^-24 of the sum.  So it is from
+// 2^-80 to 2^-1 (values of 63 with int8, 224 with e4m3), and from 2^-19 to the largest
+// scale, 2^60.  Where an item has shown a scale above 2^-1 (high), the positions with
+// one below 2^-19 (low) are added to the sum apart, as 2^(s - reference).
+//
+// A scale of zero enters the exponent as 2^-80: the codes are zero, so it only has to
+// be too small to raise the maximum (20 octaves below the least scale), and leaves
 // 2^(s - reference) room for a sum of 2^30 (2^(80 + 15 + 30) at most).
 //
 // What lies outside the scales that are read: below 2^-60 a value scale counts as 0
 // (its codes may be other than zero: what 2^-80 of them adds is below 2^-70); above
-// 2^60 or below 0 a scale counts as NaN.
+// 2^60 or below 0 a scale counts as NaN (odd).
 struct ValueScale {
   float log2;      // of what stands for the scale in the exponent
   float inv;       // 1 / that: what the sum multiplies a weight by
-  bool apart;
+  bool plain;      // neither low nor high nor odd
   __device__ __forceinline__ explicit ValueScale(float v) {
     const float vv = v >= 0x1p-60f ? fminf(v, 0x1p60f) : 0x1p-80f;
     log2 = lg2(vv);
     inv = rcp(vv);
-    apart = !(v >= 0x1p-19f && v <= 0x1p60f);
+    plain = v >= 0x1p-19f && v <= 0.5f;
   }
+  static __device__ __forceinline__ bool low(float v) { return v < 0x1p-19f; }
+  static __device__ __forceinline__ bool high(float v) { return v > 0.5f; }
 };
 __device__ __forceinline__ bool scale_is_read(float v) { return v >= 0.f && v <= 0x1p60f; }
 __device__ __forceinline__ float key_scale(float k) {

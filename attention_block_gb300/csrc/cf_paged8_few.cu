@@ -17,8 +17,8 @@
 // Scales: with a_j = scale ks_j log2(e) and b_j = log2 vs_j, the weight of
 // value j is exp(s_j) vs_j = 2^(a_j q.k_j + b_j), so one fused product, one
 // maximum and one exponential serve the weights, whatever the scales are; the
-// sum of exp(s_j) takes the weight times 1 / vs_j, or where vs_j is small or zero
-// an exponential of its own (ValueScale).  Weights enter the second product as one
+// sum of exp(s_j) takes the weight times 1 / vs_j, or where scales lie far apart an
+// exponential of its own (ValueScale).  Weights enter the second product as one
 // fp16 value: a relative 2^-12 each, by which results in fp16 are off 2.2e-4 of their
 // norm for the 2.1e-4 of their own rounding; a second value for the rest would double
 // that product.
@@ -357,12 +357,14 @@ __global__ void __launch_bounds__(Shape8<D, NT>::THREADS, 1)
   int pos[NT][2];  // positions of rows 8 nt + 2 tq and + 1: this thread's
   float qk = 0.f;  // what q.k is multiplied by beside the key's scale
   int tile = 0, left = 0;  // of the item: the unit in work, units left to this run
+  bool high = false;       // has it shown a high value scale (ValueScale)?
 
   while (cur.u < cur.end) {
     const int nrows = cur.w.n * p.g.G;
     if (left == 0) {
       tile = cur.tile;
       left = (int)min((long long)(cur.w.tiles - tile), cur.end - cur.u);
+      high = false;
       uint32_t top2 = 0;  // bf16: largest finite magnitude of the rows, as bits
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
@@ -437,10 +439,15 @@ __global__ void __launch_bounds__(Shape8<D, NT>::THREADS, 1)
                      : "=f"(k), "=f"(v)
                      : "r"(scale_s + pair * S::SCALES + lane * 8));
         const ValueScale vs(v);
-        apart = __ballot_sync(~0u, there && vs.apart);
+        bool alone = false;
+        if (__any_sync(~0u, there && !vs.plain)) {
+          high |= __any_sync(~0u, there && ValueScale::high(v));
+          alone = there && ((ValueScale::low(v) && high) || !scale_is_read(v));
+          apart = __ballot_sync(~0u, alone);
+        }
         const float ak = there ? key_scale(k) * qk : 0.f, bk = there ? vs.log2 : -INFINITY;
         asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(prep_s + lane * 16), "f"(ak),
-                     "f"(bk), "f"(vs.apart ? 0.f : vs.inv), "f"(there ? v : 0.f)
+                     "f"(bk), "f"(alone ? 0.f : vs.inv), "f"(there ? v : 0.f)
                      : "memory");
       }
 #pragma unroll
@@ -529,7 +536,7 @@ __global__ void __launch_bounds__(Shape8<D, NT>::THREADS, 1)
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[nt][k][e] *= corr[nt][e & 1];
         }
-        if (apart) {  // 2^(s - reference) of those positions (decode at d = 64 28.9 -> 29.2 us)
+        if (apart) {  // 2^(s - reference) of those positions
 #pragma unroll
           for (int mt = 0; mt < MT; ++mt)
 #pragma unroll

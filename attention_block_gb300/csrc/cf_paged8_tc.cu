@@ -9,7 +9,7 @@
 // are fp16 x fp16; a code is exact in fp16, and scales do not touch the
 // operands: with a_j = scale ks_j log2(e) and b_j = log2 vs_j the weight of
 // value j is 2^(a_j q.k_j + b_j), and the sum of exp(s_j) takes that weight
-// times c_j = 1 / vs_j, or where vs_j is small or zero an exponential of its own
+// times c_j = 1 / vs_j, or where scales lie far apart an exponential of its own
 // (ValueScale).
 //
 // Roles of a block's 16 warps:
@@ -77,11 +77,11 @@ struct Tc8Shape {
   static constexpr uint32_t S_COL = 0, O_COL = 2 * kBN;  // TMEM columns
 };
 
-// Of a tile's positions: a, b, c; which the sum takes apart (ValueScale), and
-// which of those have a value scale of NaN.
+// Of a tile's positions: a, b, c; whether 32 of them have low (1), high (2) or odd
+// (4) value scales (ValueScale), and which are odd.
 struct Tc8Scales {
   float a[kBN], b[kBN], c[kBN];
-  uint32_t apart[kBN / 32], odd[kBN / 32];
+  uint32_t kinds[kBN / 32], odd[kBN / 32];
 };
 
 // What an item costs apart from its tiles, in tiles: its queries, its result, the
@@ -344,6 +344,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const int ns = t.ns, skip = t.skip;
       float m = -INFINITY, l = 0.f;
       bool some = false;  // O holds something
+      uint32_t ask = 4;   // kinds of value scales for which the sum is taken apart
 #pragma unroll 1
       for (int tile = first; tile < first + count; ++tile) {
         const int base = (tile < ns ? tile : tile + skip) * kBN;
@@ -404,7 +405,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
           const float m_new = fmaxf(m, mx);
           // (one question for both: another branch on every tile's way costs 2-6 %)
-          const bool apart = (sc.apart[0] | sc.apart[1] | sc.apart[2] | sc.apart[3]) != 0;
+          const uint4 kd = *reinterpret_cast<const uint4*>(sc.kinds);
+          const uint32_t kinds = kd.x | kd.y | kd.z | kd.w;
+          ask |= (kinds >> 1) & 1u;  // low ones count from the first high one on
+          const bool apart = (kinds & ask) != 0;
           const bool grow = m_new - m > (float)kGrow || apart;  // also from -inf
           float l_apart = 0.f;
           if (__any_sync(~0u, grow)) {
@@ -437,9 +441,15 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 tmem_ld_32x32b_x16_nowait(ts + c, x);
                 tmem_wait_ld();
 #pragma unroll
-                for (int e = 0; e < 16; ++e)
-                  if ((see >> e) & 1u)
-                    l_apart += ex2(fmaf(__uint_as_float(x[e]) * qf, sc.a[c + e], -at));
+                for (int e = 0; e < 16; e += 4) {
+                  const float4 av = lds4(sc.a + c + e);
+                  const float y[4] = {av.x, av.y, av.z, av.w};
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) {
+                    const float s2 = fmaf(__uint_as_float(x[e + i]) * qf, y[i], -at);
+                    l_apart += ex2((see >> (e + i)) & 1u ? s2 : -INFINITY);
+                  }
+                }
               }
               // values of NaN: for the rows that see them
               if ((sc.odd[0] | sc.odd[1] | sc.odd[2] | sc.odd[3]) != 0) {
@@ -702,10 +712,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         sc.a[row] = key_scale(scale.x) * p.scale_log2;
         sc.b[row] = vs.log2;
         sc.c[row] = vs.inv;
-        const uint32_t apart = __ballot_sync(~0u, vs.apart);
-        const uint32_t odd = __ballot_sync(~0u, !scale_is_read(scale.y));
+        uint32_t kinds = 0, odd = 0;
+        if (__any_sync(~0u, !vs.plain)) {
+          odd = __ballot_sync(~0u, !scale_is_read(scale.y));
+          kinds = (__any_sync(~0u, ValueScale::low(scale.y)) ? 1u : 0u) |
+                  (__any_sync(~0u, ValueScale::high(scale.y)) ? 2u : 0u) | (odd ? 4u : 0u);
+        }
         if (lane == 0) {
-          sc.apart[lw] = apart;
+          sc.kinds[lw] = kinds;
           sc.odd[lw] = odd;
         }
         if (++buf == S::BUFS) buf = 0;

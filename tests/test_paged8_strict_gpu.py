@@ -101,6 +101,39 @@ def test_one_large_value_scale_beside_many_small_ones(code, q_len, low, high):
 
 
 @pytest.mark.parametrize("code", CODES)
+@pytest.mark.parametrize("q_len,window", [([1, 1], 0), ([4, 3], 0), ([70, 200], 0), ([70, 200], 150)], ids=str)
+@pytest.mark.parametrize("order", ["up", "down", "mixed", "small"])
+def test_value_scales_that_grow_fall_and_mix_along_a_sequence(code, q_len, window, order):
+    """Scales from 2^-50 to 2^50, zeros among them, and NaN heads behind them; all of them small in the last case."""
+    pr = Problem8(q_len, [1500, 900], 4, 2, code=code)
+    g = torch.Generator(device="cuda").manual_seed(11)
+    zero = torch.rand(pr.scales.shape[:-1], generator=g, device="cuda") < 0.05
+    log2 = torch.randint(-50, 51, pr.scales.shape[:-1], generator=g, device="cuda").float()
+    if order == "small":
+        log2 = -40 - log2.abs() / 5
+    for b in range(2):
+        if order in ("up", "down"):
+            j = torch.arange(pr.kv_len[b], device="cuda")
+            x = -50 + 100 * j / (pr.kv_len[b] - 1)
+            log2[pr.table[b][j // pr.page].long(), :, j % pr.page] = (x if order == "up" else -x)[:, None]
+    set_values(pr, log2.exp2(), zero)
+    both(pr, window)
+    for b, h in ((0, 1), (1, 0)):
+        pr.scales[pr.table[b, 40].long(), h, 5, 1] = NAN  # position 645
+    r = Run8(pr).attend(window)
+    out, tol, lse, ltol = ref_attention8(pr, window)
+    for b in range(2):
+        p = torch.arange(pr.kv_len[b] - q_len[b], pr.kv_len[b], device="cuda")
+        hit = (p >= 645) & (p - 645 < (window or 10 ** 6))
+        rows = slice(pr.starts[b], pr.starts[b + 1])
+        sick = torch.zeros(q_len[b], 4, dtype=torch.bool, device="cuda")
+        sick[:, 2 - 2 * b:4 - 2 * b] = hit[:, None]
+        assert (r.out[rows].isnan().all(-1) == sick).all() and (r.out[rows].isnan().any(-1) == sick).all()
+        assert ((r.out[rows].double() - out[rows]).abs() <= tol[rows])[~sick].all()
+    assert ((r.lse.double() - lse).abs() <= ltol).all()
+
+
+@pytest.mark.parametrize("code", CODES)
 @pytest.mark.parametrize("q_len", [[1, 2], [60, 130]], ids=str)
 def test_scales_outside_what_is_read(code, q_len):
     """A value scale below 2^-60 counts as 0; one above 2^60 or below 0, of a key or a value, as NaN."""
@@ -255,3 +288,9 @@ def test_tokens_of_no_sequence_are_left_alone(batch, max_q):
         assert (x == 7).all()
     for x, y in zip(before, (pr.k_pages, pr.v_pages, pr.scales)):
         assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+
+
+@pytest.mark.parametrize("code,dtype", [("e4m3", "bf16"), ("int8", "f16")])
+@pytest.mark.parametrize("heads", [(300, 1), (257, 1), (514, 2), (1000, 1)], ids=str)
+def test_more_grouped_heads_than_a_tile_has_rows(code, dtype, heads):
+    both(Problem8([1, 3, 2], [40, 70, 2], *heads, d=64, dtype=dtype, code=code))
