@@ -110,7 +110,7 @@ int cf_paged8_attention(cf_paged8_handle* h, int32_t batch, int32_t n_tokens, in
   if (rc != CF_OK || p.n_tokens == 0) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   // Up to 16 rows per KV head (tokens of one sequence x grouped heads) go to the
-  // few-row kernel; more to the many-row kernel, which takes 98 us for 36 with 4
+  // few-row kernel; more to the many-row kernel, which takes 99 us for 35 with 4
   // rows (16 sequences of 4097 positions) and 117 for 63 with 16 (32 of 1070-4093).
   if (!((int64_t)p.max_q * p.g.G <= kFewRows
             ? paged8_few_launch(h->cfg.dtype, h->code, p, h->few, st)

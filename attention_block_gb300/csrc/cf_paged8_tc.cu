@@ -28,14 +28,14 @@
 // results in fp16 are off 2.8e-4 of their norm, 2.1e-4 of it their own rounding.
 //
 // 512 tokens behind 15872 (32 / 8 heads of 128): 160 us, 845 TFLOP/s; 4 chunks of
-// 820-1024 tokens behind 195-1752, 32 heads: 194; one prompt of 8192 647.  The 16-bit
-// cache takes 113, 153 and 402 for the same: its kernel loads tiles as they are, this
+// 820-1024 tokens behind 195-1752, 32 heads: 186; one prompt of 8192 638.  The 16-bit
+// cache takes 113, 154 and 402 for the same: its kernel loads tiles as they are, this
 // one expands each again for every 256 rows, through three slots for five (what each
 // of these costs is not measured).
 //
 // A half's tiles are a chain: when they took 171 and 207 us, 3450 cycles softmax and
 // 1950 until the next scores were there (products of both halves 2050).  A branch for
-// NaN behind each 32 columns was 11-13 us of that: what is rare stands in the block
+// NaN behind each 32 columns was 11-20 us of that: what is rare stands in the block
 // that the maximum's growth enters (in blocks of its own 172-190 and 214-233).
 // Measured before that was found: reading the positions' a, b, c takes up to a sixth
 // of the softmax (without them 150 and 205 of 171 and 207).  Accumulator fragments,
@@ -85,9 +85,9 @@ struct Tc8Scales {
 };
 
 // What an item costs apart from its tiles, in tiles: its queries, its result, the
-// halves out of step.  4 chunks of 820-1024 tokens, 32 heads: 194.5 us with 3, 193.8
-// with 4, 196.4 with 5; one chunk of 512 behind 15872: 161.5, 159.6, 161.5; one prompt
-// of 8192: 726, 647, 644.
+// halves out of step.  4 chunks of 820-1024 tokens, 32 heads: 186.3 us with 3, 186.2
+// with 4, 189.1 with 5; one chunk of 512 behind 15872: 161.2, 159.3, 161.3; one prompt
+// of 8192: 724, 639, 635.
 constexpr int kItemCost8 = 4;
 using Cursor = TcCursor<false, kItemCost8>;
 
@@ -120,8 +120,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   constexpr int LIFT = weight_lift<__half>(kGrow);
   constexpr float BACK = 1.f / (1 << LIFT);
   // Warps that bring the first item's queries: turning them takes longer than the
-  // softmax warps' help costs (bf16, 512 behind 15872 159.6 us, with 3 163.1; fp16, 4
-  // chunks 195.7, with 3 193.8).
+  // softmax warps' help costs (bf16, 512 behind 15872 159.3 us, with 3 161.5; fp16, 4
+  // chunks 189.1, with 3 186.2).
   constexpr int FIRST = kIsBf16<T> ? 11 : 3;
   const PagedAttnParams& p = a.p;
   extern __shared__ __align__(1024) uint8_t sm[];
@@ -313,9 +313,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
   if (warp < 8) {
     // ------------------------------------------------------------ softmax --
-    // 72 for the others (4 chunks, 32 heads, 193.8 us, 512 behind 15872 159.6; with 88 for
-    // the codes and 56 for the rest 194.1 and 157.9; with 176 here and 80 there 190.8 and
-    // 166.9).
+    // 72 for the others (512 behind 15872 159.3 us, 4 chunks, 32 heads, 186.2, 32 of 8
+    // tokens 109.9; with 88 for the codes and 56 for the rest 157.8, 185.6 and 111.9; with
+    // 176 here and 80 there 164.8, 181.9 and 106.6).
     set_regs_up<184>();
     const int hf = warp >> 2;                   // half
     const int r = (warp & 3) * 32 + lane;       // row of the half = TMEM lane
@@ -404,7 +404,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           for (int e = 0; e < 4; ++e) mx4[e] = fmaxf(mx4[e], s[kBN - 4 + e]);
           const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
           const float m_new = fmaxf(m, mx);
-          // (one question for both: another branch on every tile's way costs 2-6 %)
+          // (one question for both: another branch on every tile's way costs 2-11 %)
           const uint4 kd = *reinterpret_cast<const uint4*>(sc.kinds);
           const uint32_t kinds = kd.x | kd.y | kd.z | kd.w;
           ask |= (kinds >> 1) & 1u;  // low ones count from the first high one on
