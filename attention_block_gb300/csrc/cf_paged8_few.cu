@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(Shape8<D, NT>::THREADS, 1)
   int ld_tile = ld.tile, ld_left = 0;
   if (ld.u < ld.end) ld_left = (int)min((long long)(ld.w.tiles - ld.tile), ld.end - ld.u);
   // The page of this lane's position in it, fetched one unit before its copies
-  // are issued.
+  // are issued (a coherent load: the launch in front may have written the table).
   int ld_pos = -1, ld_page = -1;
   auto fetch_page = [&]() {
     ld_pos = -1;
@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(Shape8<D, NT>::THREADS, 1)
     const int j = ld.w.base(ld_tile) + lane;
     if (!ld.w.sees(j)) return;
     ld_pos = j;
-    ld_page = __ldg(p.page_table + (int64_t)ld.b * p.g.max_pages + (j >> p.g.page_shift));
+    ld_page = p.page_table[(int64_t)ld.b * p.g.max_pages + (j >> p.g.page_shift)];
   };
   // Copies a unit's K or V into a slot; lane i holds position i's byte offset,
   // or -1 (zeros).  Chunks of 16 bytes are swizzled so that the reads below

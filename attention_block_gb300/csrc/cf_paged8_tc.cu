@@ -644,7 +644,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         sts16(row + (((x0 + 1) ^ sw) << 4), h[4], h[5], h[6], h[7]);
       }
     };
-    // The page of this lane's position, looked up one tile ahead of its loads.
+    // The page of this lane's position, looked up one tile ahead of its loads (a coherent
+    // load: the launch in front may have written the table).
     int f_pos = -1, f_page = 0;
     auto look_up = [&]() {
       f_pos = -1;
@@ -652,7 +653,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const int j = cur.t.base(cur.tile) + lw * 32 + lane;
       if (!cur.t.sees(j)) return;
       f_pos = j;
-      f_page = __ldg(p.page_table + (int64_t)cur.t.b * p.g.max_pages + (j >> p.g.page_shift));
+      f_page = p.page_table[(int64_t)cur.t.b * p.g.max_pages + (j >> p.g.page_shift)];
     };
     // K and V of the units in turn, RAW tiles ahead of their conversion; cur runs
     // with the copies.

@@ -44,6 +44,38 @@ def test_reading_back_sees_the_append_in_front(code, q_len):
     assert kv.status() == OK
 
 
+@pytest.mark.parametrize("q_len", [[1, 1, 1], [40, 3, 90]], ids=str)
+def test_page_tables_and_lengths_written_right_in_front(q_len):
+    """The page table and the lengths change on the device between calls, without a pause."""
+    pr = Problem8(q_len, [300, 400, 500], 8, 2)
+    other = Problem8(q_len, [290, 410, 470], 8, 2, seed=1, max_pages=pr.max_pages)
+    n = pr.num_pages
+    pr.k_pages, pr.v_pages = (torch.cat([a.view(torch.uint8), b.view(torch.uint8)]).view(a.dtype) for a, b in
+                              ((pr.k_pages, other.k_pages), (pr.v_pages, other.v_pages)))
+    pr.scales, pr.num_pages = torch.cat([pr.scales, other.scales]), n + other.num_pages
+    inputs = [(pr.table.clone(), pr.lens.clone()), (torch.where(other.table >= 0, other.table + n, -7), other.lens)]
+    r = Run8(pr, poison=False)
+
+    def run(pause):
+        out = []
+        for i in range(40):
+            pr.table.copy_(inputs[i % 2][0])
+            pr.lens.copy_(inputs[i % 2][1])
+            if pause:
+                torch.cuda.synchronize()
+            r.attend()
+            if pause:
+                torch.cuda.synchronize()
+            out.append(r.out.clone())
+        return torch.stack(out)
+
+    want = run(True)
+    assert not torch.equal(want[0], want[1])
+    for _ in range(3):
+        assert torch.equal(run(False), want)
+    assert r.kv.status() == OK
+
+
 # ------------------------------------------------------------- value scales --
 def set_values(pr, scale, zero=None):
     """Value scales [num_pages, nkv, page]; heads in `zero` are held as zeros."""
